@@ -33,7 +33,12 @@ PROBE_LIB_PATH = os.path.join(_PKG, "libgemm_relu_probe.so")
 
 EXPORTS = ("gemm_relu", "gemm_relu_strerror", "gemm_relu_configs", "gemm_relu_plan",
            "gemm_relu_ws", "gemm_relu_workspace_size", "gemm_relu_ws_plan", "gemm_relu_noalloc",
-           "gemm_relu_mx", "gemm_relu_mx_plan", "gemm_relu_sp", "gemm_relu_sp_plan")
+           "gemm_relu_mx", "gemm_relu_mx_plan", "gemm_relu_sp", "gemm_relu_sp_plan",
+           "gemm_relu_layer_norm", "gemm_relu_layer_norm_backward",
+           "gemm_relu_layer_norm_backward_workspace", "gemm_relu_gated", "gemm_relu_gated_plan",
+           "gemm_relu_gated_backward", "gemm_relu_gated_backward_workspace",
+           "gemm_relu_gated_backward_plan", "gemm_relu_quantize_rows", "gemm_relu_i8",
+           "gemm_relu_i8_plan")
 
 _lib = None
 
@@ -91,6 +96,8 @@ def library():
     lib.gemm_relu_sp_plan.argtypes = [vp, vp, vp, vp, i64, i64, i64, ctypes.c_int, ctypes.c_int,
                                       ctypes.c_int]
     lib.gemm_relu_sp_plan.restype = ctypes.c_char_p
+    from . import ffn
+    ffn.declare(lib)
     _lib = lib
     return lib
 
@@ -277,3 +284,8 @@ def matmul_relu(A, B, transB=False, out_dtype=None, out=None, stream=None):
     gemm_relu(A, B, out, M, N, K, _torch_dtype_code(A.dtype), _torch_dtype_code(out.dtype),
               1 if transB else 0, stream)
     return out
+
+
+# Operators of a feed-forward half layer (include/gemm_relu_ffn.h).
+from .ffn import (ACTIVATIONS, layer_norm, layer_norm_backward, matmul_gated,  # noqa: E402,F401
+                  matmul_gated_backward, matmul_i8, quantize_rows)

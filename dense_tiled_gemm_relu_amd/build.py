@@ -1,7 +1,7 @@
 """Build the HIP libraries of the package for gfx950.
 
-* ``libgemm_relu.so``       — the product: C-ABI gemm_relu / gemm_relu_strerror /
-                              gemm_relu_plan (include/gemm_relu.h);
+* ``libgemm_relu.so``       — the product: the C-ABI of include/gemm_relu.h and of
+                              include/gemm_relu_ffn.h;
 * ``libgemm_relu_probe.so`` — test-only lane-layout probes and the MFMA-rate
   diagnostic (MFMA-only throughput on random operands).
 
@@ -27,10 +27,11 @@ LIB_SOURCES = ["gemm_relu_api.hip", "inst_f16_nn.hip", "inst_f16_nt.hip",
                "inst_bf16_nn.hip", "inst_bf16_nt.hip", "inst_f8e4m3_nn.hip",
                "inst_f8e4m3_nt.hip", "inst_f8e5m2_nn.hip", "inst_f8e5m2_nt.hip",
                "inst_mx_e4m3.hip", "inst_mx_e5m2.hip", "inst_mx_e2m1.hip", "inst_sp.hip",
-               "inst_i16.hip"]
+               "inst_i16.hip", "ffn_api.hip", "ffn_rows.hip", "inst_ffn.hip"]
 PROBE_SOURCES = ["probe_layouts.hip", "probe_mfma_rate.hip", "probe_mfma16.hip", "probe_fp8.hip",
                  "probe_sparse.hip"]
-HEADERS = ["gemm_relu_kernel.hpp", "configs.hpp", "gemm_sp_relu_kernel.hpp"]
+HEADERS = ["gemm_relu_kernel.hpp", "configs.hpp", "gemm_sp_relu_kernel.hpp", "api_common.hpp",
+           "ffn.hpp"]
 
 # gfx950 only.  Packed fp32 ALU ops are switched off: the compiler otherwise
 # forms v_pk_* fp32 instructions from ordinary float code.
@@ -45,6 +46,7 @@ HIP_FLAGS = ["--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC",
 # form of the matrix instructions leaves the main loop spill-free.
 EXTRA_FLAGS = {"inst_sp.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
                "inst_i16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+               "inst_ffn.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
                "probe_mfma16.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 
@@ -67,7 +69,7 @@ def _config_flags():
 def _compile(src, force, verbose):
     obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
     deps = [os.path.join(CSRC, src)] + [os.path.join(CSRC, h) for h in HEADERS] + \
-        [os.path.join(INCLUDE, "gemm_relu.h")]
+        [os.path.join(INCLUDE, h) for h in ("gemm_relu.h", "gemm_relu_ffn.h")]
     if force or _newer(obj, deps):
         cmd = [HIPCC] + HIP_FLAGS + _config_flags() + EXTRA_FLAGS.get(src, []) + \
             ["-c", os.path.join(CSRC, src), "-o", obj]

@@ -1,0 +1,70 @@
+// Launch interface of the feed-forward operators' kernels, between the C-ABI
+// unit (ffn_api.hip) and the kernel units.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "gemm_relu_kernel.hpp"
+
+namespace gemm_relu_hip {
+
+// ---- matrix products (inst_ffn.hip)
+enum LinearConfig : int { LIN_G64 = 0, LIN_COUNT };
+
+struct LinearInfo {
+    const char* name;
+    int bm, bn;
+};
+
+inline const LinearInfo& linear_info(int cfg)
+{
+    static const LinearInfo table[LIN_COUNT] = {
+        {"g64x64x64", 64, 64},
+    };
+    return table[cfg];
+}
+
+typedef hipError_t (*LinearLaunchFn)(const KernelArgs& args, int grid, hipStream_t stream);
+LinearLaunchFn launcher_gated(int dt, int cfg);                // B stored (N,K)
+LinearLaunchFn launcher_cast(int dt, int cfg);                 // B stored (K,N), C of type dt
+LinearLaunchFn launcher_i8(int out_dt, int cfg);               // B stored (N,K)
+
+// ---- rows and element-wise work (ffn_rows.hip)
+struct NormArgs {
+    const void* x;
+    const void* w;
+    const void* b;          // null: zero
+    void* y;
+    float* mean;            // null: not wanted (forward)
+    float* rstd;
+    const void* dy;         // backward
+    void* dx;
+    void* dw;
+    void* db;               // null: not wanted
+    float* partial;         // backward: per strip, cols sums for dw, then cols for db
+    int64_t x_stride, dy_stride;
+    int rows, cols;
+    float eps;
+};
+hipError_t launch_layer_norm(const NormArgs& a, int dt, int wdt, hipStream_t stream);
+// strips of rows the backward pass sums on their own before joining them
+int layer_norm_strips(int64_t rows);
+hipError_t launch_layer_norm_backward(const NormArgs& a, int dt, int wdt, hipStream_t stream);
+
+struct GatedGradArgs {
+    const float* gu;        // (rows, 2 hidden)
+    const void* dh;
+    void* dgu;              // (rows, 2 hidden), rows ld apart
+    void* dgu_t;            // (2 hidden, rows), rows ld_t apart
+    int64_t dh_stride;
+    int ld, ld_t;
+    int rows, hidden, act;
+};
+hipError_t launch_gated_grad(const GatedGradArgs& a, int dt, hipStream_t stream);
+
+hipError_t launch_quantize_rows(const void* x, int64_t x_stride, signed char* q, float* scale, int rows,
+                                int cols, int dt, hipStream_t stream);
+
+}  // namespace gemm_relu_hip

@@ -1,0 +1,330 @@
+// C-ABI of the feed-forward operators (include/gemm_relu_ffn.h): argument checks,
+// configuration choice, launch.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstdlib>
+#include <cstring>
+
+#include "api_common.hpp"
+#include "ffn.hpp"
+#include "gemm_relu_ffn.h"
+
+using namespace gemm_relu_hip;
+
+namespace {
+
+constexpr int64_t kLim = INT32_MAX;
+
+int elem_bytes(int dt) { return dt == GEMM_RELU_F32 ? 4 : dt == DT_I8 ? 1 : 2; }
+bool is_16bit(int dt) { return dt == GEMM_RELU_F16 || dt == GEMM_RELU_BF16; }
+bool is_float(int dt) { return is_16bit(dt) || dt == GEMM_RELU_F32; }
+bool size_ok(int64_t n) { return n >= 0 && n <= kLim; }
+
+// A matrix argument: rows x cols elements of `bytes` bytes, rows `stride` apart.
+struct Mat {
+    const void* p;
+    int64_t rows, cols, stride;
+    int bytes;
+    uintptr_t at() const { return reinterpret_cast<uintptr_t>(p); }
+    uint64_t span() const
+    {
+        return rows == 0 || cols == 0 ? 0 : (uint64_t(rows - 1) * uint64_t(stride) + uint64_t(cols)) * uint64_t(bytes);
+    }
+    bool ok() const { return stride >= cols && stride <= kLim && !(span() && !p) && !(at() & uintptr_t(bytes - 1)); }
+};
+Mat dense(const void* p, int64_t rows, int64_t cols, int bytes) { return Mat{p, rows, cols, cols, bytes}; }
+
+// Whether every matrix is well formed and no output (the first `outs`)
+// overlaps another matrix.
+template <size_t N> bool mats_ok(const Mat (&m)[N], size_t outs)
+{
+    for (size_t i = 0; i < N; ++i)
+        if (!m[i].ok()) return false;
+    for (size_t i = 0; i < outs; ++i)
+        for (size_t j = i + 1; j < N; ++j)
+            if (m[i].p && m[j].p && overlaps(m[i].at(), m[i].span(), m[j].at(), m[j].span())) return false;
+    return true;
+}
+
+// A workspace as a matrix of bytes (256-byte alignment is checked apart).
+Mat bytes_of(const void* p, uint64_t n) { return Mat{p, int64_t(n), 1, 1, 1}; }
+bool workspace_ok(const void* ws, uint64_t have, uint64_t need)
+{
+    return need == 0 || (ws && have >= need && !(reinterpret_cast<uintptr_t>(ws) & 255));
+}
+
+int finish(hipError_t e, hipStream_t st)
+{
+    if (e != hipSuccess) return GEMM_RELU_EHIP;
+    const char* s = std::getenv("GEMM_RELU_SYNC");
+    if (s && s[0] == '1') {
+        if (hipStreamSynchronize(st) != hipSuccess) return GEMM_RELU_EHIP;
+        if (hipGetLastError() != hipSuccess) return GEMM_RELU_EHIP;
+    }
+    return GEMM_RELU_OK;
+}
+
+// ---- matrix products
+struct LinearPlan {
+    int cfg;
+    int64_t tiles_m, tiles_n;
+};
+
+// N counts columns of the tile's own width (gated: both projections).
+LinearPlan plan_linear(int64_t M, int64_t N)
+{
+    LinearPlan p;
+    p.cfg = LIN_G64;
+    p.tiles_m = ceil_div(M, linear_info(p.cfg).bm);
+    p.tiles_n = ceil_div(N, linear_info(p.cfg).bn);
+    return p;
+}
+
+// a launch's work-items stay below 2^32
+bool plan_fits(const LinearPlan& p) { return p.tiles_m * p.tiles_n <= (int64_t(1) << 22); }
+
+KernelArgs linear_args(const LinearPlan& p, const void* A, int64_t lda, const void* B, int64_t ldb, void* C,
+                       int64_t M, int64_t N, int64_t K)
+{
+    KernelArgs a{};
+    a.A = static_cast<const unsigned char*>(A);
+    a.B = static_cast<const unsigned char*>(B);
+    a.C = static_cast<unsigned char*>(C);
+    a.M = int(M);
+    a.N = int(N);
+    a.K = int(K);
+    a.lda = int(lda);
+    a.ldb = int(ldb);
+    a.tiles_m = int(p.tiles_m);
+    a.tiles_n = int(p.tiles_n);
+    a.panel = int(std::min<int64_t>(8, p.tiles_m));
+    a.nxcd = 8;
+    return a;
+}
+
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+
+// dg and du of the backward pass in the workspace: row-major (rows of 2 hidden)
+// for dx, and transposed (rows of `rows`) for dweight, each row padded to 16
+// bytes.
+struct GradSpace {
+    int64_t ld, ld_t;
+    uint64_t dgu_t, bytes;      // offset of the transposed copy; total
+};
+GradSpace grad_space(int64_t rows, int64_t hidden)
+{
+    GradSpace s;
+    s.ld = round_up(2 * hidden, 8);
+    s.ld_t = round_up(rows, 8);
+    s.dgu_t = uint64_t(round_up(2 * rows * s.ld, 256));
+    s.bytes = s.dgu_t + uint64_t(2 * hidden) * uint64_t(s.ld_t) * 2;
+    return s;
+}
+
+}  // namespace
+
+// ------------------------------------------------------------- layer norm
+extern "C" int gemm_relu_layer_norm(const void* x, int64_t x_stride, const void* weight, const void* bias,
+                                    void* y, float* mean, float* rstd, int64_t rows, int64_t cols, int dtype,
+                                    int wdtype, float eps, void* stream)
+{
+    if (!size_ok(rows) || !size_ok(cols) || !is_float(dtype) || (wdtype != dtype && wdtype != GEMM_RELU_F32) ||
+        !(eps >= 0.0f) || (rows > 0 && cols < 1))
+        return GEMM_RELU_EINVAL;
+    if (rows == 0) return GEMM_RELU_OK;
+    const int e = elem_bytes(dtype), we = elem_bytes(wdtype);
+    const Mat m[] = {dense(y, rows, cols, e), dense(mean, mean ? rows : 0, 1, 4), dense(rstd, rstd ? rows : 0, 1, 4),
+                     {x, rows, cols, x_stride, e}, dense(weight, 1, cols, we), dense(bias, bias ? 1 : 0, cols, we)};
+    if (!mats_ok(m, 3)) return GEMM_RELU_EINVAL;
+    if (const int dev = check_device()) return dev;
+    NormArgs a{};
+    a.x = x;
+    a.w = weight;
+    a.b = bias;
+    a.y = y;
+    a.mean = mean;
+    a.rstd = rstd;
+    a.x_stride = x_stride;
+    a.rows = int(rows);
+    a.cols = int(cols);
+    a.eps = eps;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    return finish(launch_layer_norm(a, dtype, wdtype, st), st);
+}
+
+extern "C" int64_t gemm_relu_layer_norm_backward_workspace(int64_t rows, int64_t cols)
+{
+    if (!size_ok(rows) || !size_ok(cols)) return GEMM_RELU_EINVAL;
+    return int64_t(layer_norm_strips(rows)) * 2 * cols * 4;
+}
+
+extern "C" int gemm_relu_layer_norm_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
+                                             const void* weight, const float* mean, const float* rstd, void* dx,
+                                             void* dweight, void* dbias, int64_t rows, int64_t cols, int dtype,
+                                             int wdtype, void* workspace, uint64_t workspace_bytes, void* stream)
+{
+    if (!size_ok(rows) || !size_ok(cols) || !is_float(dtype) || (wdtype != dtype && wdtype != GEMM_RELU_F32) ||
+        (rows > 0 && cols < 1))
+        return GEMM_RELU_EINVAL;
+    if (cols == 0) return GEMM_RELU_OK;
+    const uint64_t need = uint64_t(gemm_relu_layer_norm_backward_workspace(rows, cols));
+    const int e = elem_bytes(dtype), we = elem_bytes(wdtype);
+    const Mat m[] = {dense(dx, rows, cols, e), dense(dweight, 1, cols, we), dense(dbias, dbias ? 1 : 0, cols, we),
+                     bytes_of(workspace, need), {dy, rows, cols, dy_stride, e}, {x, rows, cols, x_stride, e},
+                     dense(weight, 1, cols, we), dense(mean, rows, 1, 4), dense(rstd, rows, 1, 4)};
+    if (!mats_ok(m, 4) || !workspace_ok(workspace, workspace_bytes, need)) return GEMM_RELU_EINVAL;
+    if (const int dev = check_device()) return dev;
+    NormArgs a{};
+    a.x = x;
+    a.w = weight;
+    a.mean = const_cast<float*>(mean);
+    a.rstd = const_cast<float*>(rstd);
+    a.dy = dy;
+    a.dx = dx;
+    a.dw = dweight;
+    a.db = dbias;
+    a.partial = static_cast<float*>(workspace);
+    a.x_stride = x_stride;
+    a.dy_stride = dy_stride;
+    a.rows = int(rows);
+    a.cols = int(cols);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    return finish(launch_layer_norm_backward(a, dtype, wdtype, st), st);
+}
+
+// --------------------------------------------------------- gated projections
+static bool gated_sizes_ok(int64_t rows, int64_t hidden, int64_t cols, int dtype)
+{
+    return size_ok(rows) && size_ok(hidden) && 2 * hidden <= kLim && size_ok(cols) && is_16bit(dtype);
+}
+
+extern "C" int gemm_relu_gated(const void* x, int64_t x_stride, const void* weight, int64_t weight_stride, void* h,
+                               float* gu, int64_t rows, int64_t hidden, int64_t cols, int dtype, int act, void* stream)
+{
+    if (!gated_sizes_ok(rows, hidden, cols, dtype) || act < GEMM_RELU_ACT_SILU || act > GEMM_RELU_ACT_RELU)
+        return GEMM_RELU_EINVAL;
+    if (rows == 0 || hidden == 0) return GEMM_RELU_OK;
+    const Mat m[] = {dense(h, rows, hidden, 2), dense(gu, gu ? rows : 0, 2 * hidden, 4),
+                     {x, rows, cols, x_stride, 2}, {weight, 2 * hidden, cols, weight_stride, 2}};
+    if (!mats_ok(m, 2)) return GEMM_RELU_EINVAL;
+    const LinearPlan p = plan_linear(rows, 2 * hidden);
+    if (!plan_fits(p)) return GEMM_RELU_EUNSUPPORTED;
+    if (const int dev = check_device()) return dev;
+    KernelArgs a = linear_args(p, x, x_stride, weight, weight_stride, h, rows, 2 * hidden, cols);
+    a.hidden = int(hidden);
+    a.act = act;
+    a.GU = gu;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    return finish(launcher_gated(dtype, p.cfg)(a, int(p.tiles_m * p.tiles_n), st), st);
+}
+
+extern "C" const char* gemm_relu_gated_plan(int64_t rows, int64_t hidden, int64_t cols, int dtype)
+{
+    if (!gated_sizes_ok(rows, hidden, cols, dtype)) return nullptr;
+    if (rows == 0 || hidden == 0) return "none";
+    return linear_info(plan_linear(rows, 2 * hidden).cfg).name;
+}
+
+extern "C" int64_t gemm_relu_gated_backward_workspace(int64_t rows, int64_t hidden, int64_t cols)
+{
+    if (!gated_sizes_ok(rows, hidden, cols, GEMM_RELU_F16)) return GEMM_RELU_EINVAL;
+    if (cols == 0) return 0;
+    return int64_t(grad_space(rows, hidden).bytes);
+}
+
+extern "C" int gemm_relu_gated_backward(const void* dh, int64_t dh_stride, const float* gu, const void* x,
+                                        int64_t x_stride, const void* weight, int64_t weight_stride, void* dx,
+                                        void* dweight, int64_t rows, int64_t hidden, int64_t cols, int dtype,
+                                        int act, void* workspace, uint64_t workspace_bytes, void* stream)
+{
+    if (!gated_sizes_ok(rows, hidden, cols, dtype) || act < GEMM_RELU_ACT_SILU || act > GEMM_RELU_ACT_RELU)
+        return GEMM_RELU_EINVAL;
+    if (cols == 0 || (rows == 0 && hidden == 0)) return GEMM_RELU_OK;
+    const GradSpace s = grad_space(rows, hidden);
+    const Mat m[] = {dense(dx, rows, cols, 2), dense(dweight, 2 * hidden, cols, 2), bytes_of(workspace, s.bytes),
+                     {dh, rows, hidden, dh_stride, 2}, dense(gu, rows, 2 * hidden, 4), {x, rows, cols, x_stride, 2},
+                     {weight, 2 * hidden, cols, weight_stride, 2}};
+    if (!mats_ok(m, 3) || !workspace_ok(workspace, workspace_bytes, s.bytes)) return GEMM_RELU_EINVAL;
+    const LinearPlan px = plan_linear(rows, cols), pw = plan_linear(2 * hidden, cols);
+    if (!plan_fits(px) || !plan_fits(pw) || s.ld > kLim || s.ld_t > kLim ||
+        ceil_div(hidden, 64) * ceil_div(rows, 64) > (int64_t(1) << 23))
+        return GEMM_RELU_EUNSUPPORTED;
+    if (const int dev = check_device()) return dev;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    hipError_t e = hipSuccess;
+    if (rows > 0 && hidden > 0) {
+        GatedGradArgs g{};
+        g.gu = gu;
+        g.dh = dh;
+        g.dgu = ws;
+        g.dgu_t = ws + s.dgu_t;
+        g.dh_stride = dh_stride;
+        g.ld = int(s.ld);
+        g.ld_t = int(s.ld_t);
+        g.rows = int(rows);
+        g.hidden = int(hidden);
+        g.act = act;
+        e = launch_gated_grad(g, dtype, st);
+    }
+    if (e == hipSuccess && rows > 0)
+        e = launcher_cast(dtype, px.cfg)(linear_args(px, ws, s.ld, weight, weight_stride, dx, rows, cols, 2 * hidden),
+                                         int(px.tiles_m * px.tiles_n), st);
+    if (e == hipSuccess && hidden > 0)
+        e = launcher_cast(dtype, pw.cfg)(linear_args(pw, ws + s.dgu_t, s.ld_t, x, x_stride, dweight, 2 * hidden, cols,
+                                                     rows),
+                                         int(pw.tiles_m * pw.tiles_n), st);
+    return finish(e, st);
+}
+
+extern "C" const char* gemm_relu_gated_backward_plan(int64_t rows, int64_t hidden, int64_t cols, int dtype)
+{
+    if (!gated_sizes_ok(rows, hidden, cols, dtype)) return nullptr;
+    if (cols == 0 || (rows == 0 && hidden == 0)) return "none";
+    return "g64x64x64,g64x64x64";
+}
+
+// ------------------------------------------------------- 8-bit integers
+extern "C" int gemm_relu_quantize_rows(const void* x, int64_t x_stride, void* q, float* scale, int64_t rows,
+                                       int64_t cols, int dtype, void* stream)
+{
+    if (!size_ok(rows) || !size_ok(cols) || !is_float(dtype)) return GEMM_RELU_EINVAL;
+    if (rows == 0) return GEMM_RELU_OK;
+    const Mat m[] = {dense(q, rows, cols, 1), dense(scale, rows, 1, 4), {x, rows, cols, x_stride, elem_bytes(dtype)}};
+    if (!mats_ok(m, 2)) return GEMM_RELU_EINVAL;
+    if (const int dev = check_device()) return dev;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    return finish(launch_quantize_rows(x, x_stride, static_cast<signed char*>(q), scale, int(rows), int(cols), dtype, st),
+                  st);
+}
+
+constexpr int64_t kMaxK8 = 131071;      // 128 * 128 * k < 2^31
+
+extern "C" int gemm_relu_i8(const void* x, int64_t x_stride, const float* x_scale, const void* w, int64_t w_stride,
+                            const float* w_scale, void* y, int64_t rows, int64_t n, int64_t k, int out_dtype,
+                            void* stream)
+{
+    if (!size_ok(rows) || !size_ok(n) || !size_ok(k) || !is_float(out_dtype)) return GEMM_RELU_EINVAL;
+    if (rows == 0 || n == 0) return GEMM_RELU_OK;
+    const Mat m[] = {dense(y, rows, n, elem_bytes(out_dtype)), {x, rows, k, x_stride, 1}, {w, n, k, w_stride, 1},
+                     dense(x_scale, rows, 1, 4), dense(w_scale, n, 1, 4)};
+    if (!mats_ok(m, 1)) return GEMM_RELU_EINVAL;
+    const LinearPlan p = plan_linear(rows, n);
+    if (k > kMaxK8 || !plan_fits(p)) return GEMM_RELU_EUNSUPPORTED;
+    if (const int dev = check_device()) return dev;
+    KernelArgs a = linear_args(p, x, x_stride, w, w_stride, y, rows, n, k);
+    a.scale_a = x_scale;
+    a.scale_b = w_scale;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    return finish(launcher_i8(out_dtype, p.cfg)(a, int(p.tiles_m * p.tiles_n), st), st);
+}
+
+extern "C" const char* gemm_relu_i8_plan(int64_t rows, int64_t n, int64_t k, int out_dtype)
+{
+    if (!size_ok(rows) || !size_ok(n) || !size_ok(k) || !is_float(out_dtype)) return nullptr;
+    if (rows == 0 || n == 0) return "none";
+    if (k > kMaxK8) return "unsupported";
+    return linear_info(plan_linear(rows, n).cfg).name;
+}

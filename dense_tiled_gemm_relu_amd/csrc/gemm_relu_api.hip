@@ -15,6 +15,7 @@
 #include <string>
 #include <vector>
 
+#include "api_common.hpp"
 #include "configs.hpp"
 #include "gemm_relu.h"
 #include "gemm_sp_relu_kernel.hpp"
@@ -24,12 +25,34 @@ using namespace gemm_relu_hip;
 namespace gemm_relu_hip {
 typedef hipError_t (*SpLaunchFn)(const SpArgs& args, int grid, hipStream_t stream);
 SpLaunchFn launcher_sp(int in_dt, int out_dt, int transB, int variant);   // inst_sp.hip
+
+// Per-device "is this a gfx950" cache.
+namespace {
+struct DevState {
+    std::once_flag once;
+    bool ok = false;
+    hipError_t err = hipSuccess;
+};
+DevState g_dev[kMaxDevices];
+}  // namespace
+
+int check_device()
+{
+    int dev = -1;
+    if (hipGetDevice(&dev) != hipSuccess) return GEMM_RELU_EHIP;
+    if (dev < 0 || dev >= kMaxDevices) return GEMM_RELU_EUNSUPPORTED;
+    DevState& d = g_dev[dev];
+    std::call_once(d.once, [&] {
+        hipDeviceProp_t prop;
+        d.err = hipGetDeviceProperties(&prop, dev);
+        if (d.err == hipSuccess) d.ok = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0;
+    });
+    if (d.err != hipSuccess) return GEMM_RELU_EHIP;
+    return d.ok ? GEMM_RELU_OK : GEMM_RELU_EUNSUPPORTED;
 }
+}  // namespace gemm_relu_hip
 
 namespace {
-
-constexpr int kMaxDevices = 64;
-constexpr int kNumCUs = 256;   // MI355X: 8 XCDs x 32 CUs
 
 struct Env {
     bool sync = false;
@@ -72,41 +95,12 @@ Env env()
     return e;
 }
 
-// Per-device "is this a gfx950" cache.
-struct DevState {
-    std::once_flag once;
-    bool ok = false;
-    hipError_t err = hipSuccess;
-};
-DevState g_dev[kMaxDevices];
-
-int check_device()
-{
-    int dev = -1;
-    if (hipGetDevice(&dev) != hipSuccess) return GEMM_RELU_EHIP;
-    if (dev < 0 || dev >= kMaxDevices) return GEMM_RELU_EUNSUPPORTED;
-    DevState& d = g_dev[dev];
-    std::call_once(d.once, [&] {
-        hipDeviceProp_t prop;
-        d.err = hipGetDeviceProperties(&prop, dev);
-        if (d.err == hipSuccess) d.ok = std::strncmp(prop.gcnArchName, "gfx950", 6) == 0;
-    });
-    if (d.err != hipSuccess) return GEMM_RELU_EHIP;
-    return d.ok ? GEMM_RELU_OK : GEMM_RELU_EUNSUPPORTED;
-}
-
 int elem_bytes(int dt)
 {
     return dt == GEMM_RELU_F32 ? 4 : (dt == GEMM_RELU_F8_E4M3 || dt == GEMM_RELU_F8_E5M2) ? 1 : 2;
 }
 
 bool fp8_input(int dt) { return dt == GEMM_RELU_F8_E4M3 || dt == GEMM_RELU_F8_E5M2; }
-
-bool overlaps(uintptr_t a, uint64_t na, uintptr_t b, uint64_t nb)
-{
-    if (na == 0 || nb == 0) return false;
-    return a < b + nb && b < a + na;
-}
 
 struct Plan {
     int status = GEMM_RELU_OK;
@@ -217,8 +211,6 @@ bool direct_fits(int id, int64_t N, int64_t K, int transB)
     if (K > (int64_t(1) << 22) || N > (int64_t(1) << 24)) return false;
     return transB || N >= ci.bn;
 }
-
-int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 constexpr const char* kSplitName = "d256x256x32_s4_i16+d256x192x32_s4_i16";
 constexpr const char* kSplitName8 = "d256x256x32_s4_i16w8+d128x384x32_s4_i16w8";

@@ -47,6 +47,14 @@ enum : int { DT_F16 = 0, DT_BF16 = 1, DT_F32 = 2, DT_F8E4M3 = 3, DT_F8E5M2 = 4 }
 // two per byte (even k in the low nibble).  Their K geometry is in storage
 // bytes: an E2M1 row of K elements is K / 2 bytes.
 enum : int { DT_MX_E4M3 = 5, DT_MX_E5M2 = 6, DT_MX_E2M1 = 7 };
+enum : int { DT_I8 = 8 };   // signed 8-bit integers (EPI_I8 only), int32 accumulators
+
+// What a tile does with its finished sums.  EPI_RELU: the fused GEMM + ReLU.
+// The others serve the feed-forward operators and take row strides of A and B:
+// EPI_CAST stores the rounded sums; EPI_GATED holds the sums g and u of a gate
+// and an up projection side by side and stores act(g) u; EPI_I8 multiplies
+// integer sums by a scale per row of A and a scale per row of B.
+enum : int { EPI_RELU = 0, EPI_CAST = 1, EPI_GATED = 2, EPI_I8 = 3 };
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
@@ -57,6 +65,7 @@ typedef float f32x4_t __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
 typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
 typedef int i32x2_t __attribute__((ext_vector_type(2)));
+typedef int i32x4_t __attribute__((ext_vector_type(4)));
 typedef int i32x8_t __attribute__((ext_vector_type(8)));
 
 #define GR_LDS __attribute__((address_space(3)))
@@ -91,6 +100,16 @@ struct KernelArgs {
     // BN floats each); flags holds one arrival counter per tile, zero between
     // launches.
     int splits, split_steps;
+    // Feed-forward operators (every EPI but EPI_RELU): elements from one row of
+    // A, or of B as it is stored, to the next; C is dense.  EPI_GATED: B holds
+    // the `hidden` gate rows, then the `hidden` up rows; C is (M, hidden); GU,
+    // unless null, receives the fp32 sums, M rows of hidden g then hidden u.
+    // EPI_I8: one scale per row of A and per row of B.
+    int lda, ldb;
+    int hidden, act;
+    float* GU;
+    const float* scale_a;
+    const float* scale_b;
 };
 
 // The tiles one configuration covers inside a launch: a grid of tiles_m x
@@ -267,6 +286,25 @@ template <int FMT> struct InTraitsMX {
     __device__ static void set_tr(Op&, int, const GR_LDS unsigned char*) {}
     typedef int i32x4_raw __attribute__((ext_vector_type(4)));
 };
+// Signed 8-bit integers on v_mfma_i32_16x16x64_i8: the byte geometry of the
+// 16-bit 16x16x32 form (16 bytes per lane), twice the k, int32 sums.
+template <int MB> struct InTraits<DT_I8, MB> {
+    static_assert(MB == 16, "8-bit integers use the 16x16 block");
+    static constexpr int EB = 1, KMF = 64, OPB = 16, TRK = 8, NACC = 4;
+    static constexpr bool MX = false;
+    static constexpr int EPB = 1;
+    using Op = i32x4_t;
+    using Acc = i32x4_t;
+    __device__ static Acc mfma(Op a, Op b, Acc c)
+    {
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
+    }
+    template <int X> __device__ static void set_chunk(Op& v, u32x4_t c)
+    {
+        v = __builtin_bit_cast(Op, c);
+    }
+    __device__ static void set_tr(Op&, int, const GR_LDS unsigned char*) {}
+};
 template <int MB> struct InTraits<DT_MX_E4M3, MB> : InTraitsMX<0> {};
 template <int MB> struct InTraits<DT_MX_E5M2, MB> : InTraitsMX<1> {};
 template <int MB> struct InTraits<DT_MX_E2M1, MB> : InTraitsMX<4> {};
@@ -280,6 +318,64 @@ template <int MB> struct InTraits<DT_F8E5M2, MB> : InTraitsF8<1> {
 // Output conversion after the ReLU.  max(x, 0) is written as a select so that
 // a negative (or -0) sum becomes +0.
 __device__ __forceinline__ float relu(float x) { return x > 0.0f ? x : 0.0f; }
+
+// Activations of the gated projections, in fp32; __expf and the hardware
+// reciprocal are within a few fp32 ulps, far inside the 16-bit rounding of the
+// results.  The normal distribution function is taken from erfcf, which keeps
+// its relative accuracy in the lower tail where 1 + erf cancels.
+enum : int { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2, ACT_RELU = 3 };
+// 1 / (1 + e^-z), as t / (1 + t) with t = e^z for negative z; e^-|z| is the
+// square of e^(-|z| / 2), since the hardware exponential alone would return 0
+// where the result is below the normal range
+__device__ __forceinline__ float logistic(float z)
+{
+    const float e = __expf(-0.5f * fabsf(z)), t = e * e;
+    const float r = __builtin_amdgcn_rcpf(1.0f + t);
+    return z < 0.0f ? t * r : r;
+}
+__device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(z * -0.70710678118654752440f); }
+constexpr float kTwoGeluC = 1.5957691216057307f;     // 2 sqrt(2 / pi)
+__device__ __forceinline__ float activation(float g, int act)
+{
+    if (act == ACT_SILU) return g * logistic(g);
+    if (act == ACT_GELU) return g * normal_cdf(g);
+    // 0.5 (1 + tanh z) = 1 / (1 + e^-2z)
+    if (act == ACT_GELU_TANH) return g * logistic(kTwoGeluC * (g + 0.044715f * g * g * g));
+    return relu(g);
+}
+// value and slope of the activation at g
+__device__ __forceinline__ void activation_slope(float g, int act, float& value, float& slope)
+{
+    if (act == ACT_SILU) {
+        const float s = logistic(g);
+        value = g * s;
+        slope = s * (1.0f + g * (1.0f - s));
+    } else if (act == ACT_GELU) {
+        const float p = normal_cdf(g);
+        value = g * p;
+        slope = p + g * 0.39894228040143267794f * __expf(-0.5f * g * g);      // 1 / sqrt(2 pi)
+    } else if (act == ACT_GELU_TANH) {
+        const float s = logistic(kTwoGeluC * (g + 0.044715f * g * g * g));
+        value = g * s;
+        // s (1 - s) is 0 long before the square is capped
+        slope = s + g * s * (1.0f - s) * kTwoGeluC * (1.0f + 0.134145f * fminf(g * g, 1e30f));
+    } else {
+        value = relu(g);
+        slope = g > 0.0f ? 1.0f : 0.0f;
+    }
+}
+
+// Four consecutive fp32 values of a row whose columns n .. end at N.
+__device__ __forceinline__ void store_sums(float* dst, const f32x4_t& v, int n, int N)
+{
+    if (n + 4 <= N) {
+        __builtin_memcpy(dst, &v, 16);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (n + e < N) dst[e] = v[e];
+    }
+}
 
 template <int OUT_DT> struct OutTraits;
 template <> struct OutTraits<DT_F16> {
@@ -303,8 +399,11 @@ template <> struct OutTraits<DT_F32> {
 // ---------------------------------------------------------- configuration
 template <int IN_DT_, int OUT_DT_, bool TRANS_B_, int BM_, int BN_, int BK_, int WAVES_M_,
           int WAVES_N_, int STAGES_, bool DIRECT_, bool INTERLEAVE_ = false, int MB_ = 32,
-          bool PERSISTENT_ = false, bool STREAMK_ = false, bool SPLITK_ = false>
+          bool PERSISTENT_ = false, bool STREAMK_ = false, bool SPLITK_ = false,
+          int EPI_ = EPI_RELU>
 struct Cfg {
+    static constexpr int EPI = EPI_;
+    static constexpr bool GATED = EPI_ == EPI_GATED;
     static constexpr bool PERSISTENT = PERSISTENT_;   // tile loop over a grid of <= 1 per CU
     static constexpr bool STREAMK = STREAMK_;         // last round split along K
     static constexpr bool SPLITK = SPLITK_;           // every tile split along K into fp32 partials
@@ -372,6 +471,14 @@ struct Cfg {
                   "stream-K: the interleaved pipeline, unscaled inputs");
     static_assert(!SPLITK_ || (DIRECT_ && !INTERLEAVE_ && !MX && !PERSISTENT_ && !STREAMK_),
                   "K split: the plain direct pipeline, unscaled inputs");
+    static_assert(EPI_ == EPI_RELU || (!MX && !PERSISTENT_ && !STREAMK_),
+                  "feed-forward operators: one whole tile per workgroup, or a K split");
+    static_assert((EPI_ == EPI_I8) == (IN_DT_ == DT_I8) && (IN_DT_ != DT_I8 || (TRANS_B && !SPLITK_)),
+                  "8-bit integers: scaled sums, B stored (N,K), no fp32 partials");
+    // gate and up blocks alternate along the tile's columns, so one wave holds
+    // both sums of an output, and one 1 KiB copy lies inside one block
+    static_assert(EPI_ != EPI_GATED || (TRANS_B && !SPLITK_ && TN % 2 == 0 && MB % (64 / ROW_CH) == 0),
+                  "gated: B stored (N,K), an even number of column blocks per wave");
 
     // Interleaved direct pipeline: the LOADS_PER_STAGE copies of the stage
     // STAGES-1 ahead are spread over the KSUB k-steps of a BK step, one per
@@ -502,6 +609,9 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
     using Op = typename In::Op;
 
     const int M = args.M, N = args.N, K = args.K;
+    // elements from one stored row of A (of B) to the next
+    const int lda = C::EPI == EPI_RELU ? K : args.lda;
+    const int ldb = C::EPI == EPI_RELU ? (C::TRANS_B ? K : N) : args.ldb;
     const int tid = threadIdx.x;
     const int lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -540,7 +650,7 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
     };
     auto nrow_slot = [&](int q, int& k, int& c) {
         k = q / NROW_CH;
-        c = (q % NROW_CH) ^ swz_nrow<NROW_CH, In::TRK, C::MB>(k);
+        if constexpr (!C::TRANS_B) c = (q % NROW_CH) ^ swz_nrow<NROW_CH, In::TRK, C::MB>(k);
     };
     uint32_t a_src[APT];
 #pragma unroll
@@ -548,27 +658,45 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
         int r, c;
         krow_slot(i * C::NTHREADS + tid, r, c);
         const int row = min(m0 + r, M - 1) - m0;           // clamp: finite data, output discarded
-        a_src[i] = (uint32_t)row * (uint32_t)K * (uint32_t)EB + (uint32_t)c * 16u;
+        a_src[i] = (uint32_t)row * (uint32_t)lda * (uint32_t)EB + (uint32_t)c * 16u;
     }
+    // Gated: tile row r is row gated_index(r) of the gate rows (even blocks of MB
+    // rows) or of the up rows (odd blocks); the tile's first hidden index is
+    // n0 / 2.  All 64 lanes of a copy are in one block, so the step from gate to
+    // up rows (which may pass 32 bits) is added to its scalar base.
+    auto gated_index = [&](int r) { return (n0 >> 1) + (r / (2 * C::MB)) * C::MB + r % C::MB; };
+    auto gated_up = [&](int r) { return (r / C::MB) & 1; };
     uint32_t b_src[BPT];
 #pragma unroll
     for (int i = 0; i < BPT; ++i) {
         int r, c;
-        if constexpr (C::TRANS_B) {
+        if constexpr (C::GATED) {
+            krow_slot(i * C::NTHREADS + tid, r, c);
+            const int row = min(gated_index(r), args.hidden - 1) - (n0 >> 1);
+            b_src[i] = (uint32_t)row * (uint32_t)ldb * (uint32_t)EB + (uint32_t)c * 16u;
+        } else if constexpr (C::TRANS_B) {
             krow_slot(i * C::NTHREADS + tid, r, c);
             const int row = min(n0 + r, N - 1) - n0;
-            b_src[i] = (uint32_t)row * (uint32_t)K * (uint32_t)EB + (uint32_t)c * 16u;
+            b_src[i] = (uint32_t)row * (uint32_t)ldb * (uint32_t)EB + (uint32_t)c * 16u;
         } else {
             nrow_slot(i * C::NTHREADS + tid, r, c);
-            b_src[i] = (uint32_t)r * (uint32_t)N * (uint32_t)EB + (uint32_t)c * 16u;
+            b_src[i] = (uint32_t)r * (uint32_t)ldb * (uint32_t)EB + (uint32_t)c * 16u;
         }
     }
+    auto b_from = [&](const unsigned char* gb, int i) {
+        if constexpr (C::GATED)
+            return gb + (gated_up((i * C::NTHREADS + wave * 64) / ROW_CH)
+                             ? (size_t)args.hidden * (size_t)ldb * EB : 0);
+        else
+            return gb;
+    };
 
     // origins of the tile's A rows and B columns at the first K step
-    const unsigned char* a_tile = args.A + (size_t)m0 * (size_t)K * EB + (size_t)kt0 * BK * EB;
+    const unsigned char* a_tile = args.A + (size_t)m0 * (size_t)lda * EB + (size_t)kt0 * BK * EB;
     const unsigned char* b_tile = C::TRANS_B
-                                      ? args.B + (size_t)n0 * (size_t)K * EB + (size_t)kt0 * BK * EB
-                                      : args.B + (size_t)n0 * EB + (size_t)kt0 * BK * (size_t)N * EB;
+                                      ? args.B + (size_t)(C::GATED ? n0 >> 1 : n0) * (size_t)ldb * EB +
+                                            (size_t)kt0 * BK * EB
+                                      : args.B + (size_t)n0 * EB + (size_t)kt0 * BK * (size_t)ldb * EB;
 
     // ---- direct loader: global -> LDS without registers.
     const uint32_t smem_addr = lds_addr(smem);
@@ -578,12 +706,12 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
         const uint32_t sb = sa + C::A_BYTES;
         const unsigned char* ga = a_tile + (size_t)k0 * EB;
         const unsigned char* gb = C::TRANS_B ? b_tile + (size_t)k0 * EB
-                                             : b_tile + (size_t)k0 * (size_t)N * EB;
+                                             : b_tile + (size_t)k0 * (size_t)ldb * EB;
         // every pipelined step lies inside K and every chunk inside its row
 #pragma unroll
         for (int i = 0; i < APT; ++i) dma16(ga, a_src[i], sa + (i * C::NWAVES + wave) * 1024);
 #pragma unroll
-        for (int i = 0; i < BPT; ++i) dma16(gb, b_src[i], sb + (i * C::NWAVES + wave) * 1024);
+        for (int i = 0; i < BPT; ++i) dma16(b_from(gb, i), b_src[i], sb + (i * C::NWAVES + wave) * 1024);
     };
 
     // ---- register-staged loader: 16 B loads where a chunk lies inside its row
@@ -622,17 +750,22 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
     auto a_chunk = [&](int t, int q) -> u32x4_t {
         int r, c;
         krow_slot(q, r, c);
-        return load_chunk(args.A, (size_t)(m0 + r) * (size_t)K * EB, t * BK + EPC * c, K, m0 + r < M);
+        return load_chunk(args.A, (size_t)(m0 + r) * (size_t)lda * EB, t * BK + EPC * c, K, m0 + r < M);
     };
     auto b_chunk = [&](int t, int q) -> u32x4_t {
         int r, c;
-        if constexpr (C::TRANS_B) {
+        if constexpr (C::GATED) {
             krow_slot(q, r, c);
-            return load_chunk(args.B, (size_t)(n0 + r) * (size_t)K * EB, t * BK + EPC * c, K,
+            const int row = gated_index(r);
+            return load_chunk(args.B, ((size_t)row + (gated_up(r) ? args.hidden : 0)) * (size_t)ldb * EB,
+                              t * BK + EPC * c, K, row < args.hidden);
+        } else if constexpr (C::TRANS_B) {
+            krow_slot(q, r, c);
+            return load_chunk(args.B, (size_t)(n0 + r) * (size_t)ldb * EB, t * BK + EPC * c, K,
                               n0 + r < N);
         } else {
             nrow_slot(q, r, c);
-            return load_chunk(args.B, (size_t)(t * BK + r) * (size_t)N * EB, n0 + EPC * c, N,
+            return load_chunk(args.B, (size_t)(t * BK + r) * (size_t)ldb * EB, n0 + EPC * c, N,
                               t * BK + r < K);
         }
     };
@@ -861,11 +994,11 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
             const uint32_t sb = sa + C::A_BYTES;
             const unsigned char* ga = a_tile + (size_t)k0 * EB;
             const unsigned char* gb = C::TRANS_B ? b_tile + (size_t)k0 * EB
-                                                 : b_tile + (size_t)k0 * (size_t)N * EB;
+                                                 : b_tile + (size_t)k0 * (size_t)ldb * EB;
             if (l < APT)
                 dma16(ga, a_src[l], sa + (l * C::NWAVES + wave) * 1024);
             else
-                dma16(gb, b_src[l - APT], sb + ((l - APT) * C::NWAVES + wave) * 1024);
+                dma16(b_from(gb, l - APT), b_src[l - APT], sb + ((l - APT) * C::NWAVES + wave) * 1024);
         };
 
         // ---- block scales (block-scaled inputs), staged in LDS by groups of
@@ -1014,7 +1147,7 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
             const int ld_k0 = (t + S - 1) * BK;
             const unsigned char* ga = a_tile + (size_t)ld_k0 * EB;
             const unsigned char* gb = C::TRANS_B ? b_tile + (size_t)ld_k0 * EB
-                                                 : b_tile + (size_t)ld_k0 * (size_t)N * EB;
+                                                 : b_tile + (size_t)ld_k0 * (size_t)ldb * EB;
             const uint32_t lsa = smem_addr + ld_stage * C::STAGE_BYTES;
             const uint32_t lsb = lsa + C::A_BYTES;
             // a scale group's copies issued after stage t+1's, before this
@@ -1056,7 +1189,7 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
                         if (l < APT)
                             dma16(ga, a_src[l], lsa + (l * C::NWAVES + wave) * 1024);
                         else
-                            dma16(gb, b_src[l - APT], lsb + ((l - APT) * C::NWAVES + wave) * 1024);
+                            dma16(b_from(gb, l - APT), b_src[l - APT], lsb + ((l - APT) * C::NWAVES + wave) * 1024);
                     } else {
                         if (loads) issue_one(t + S - 1, ld_stage, l);
                     }
@@ -1126,7 +1259,7 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
                     const int ld_k0 = (t + S - 1) * BK;
                     const unsigned char* ga = a_tile + (size_t)ld_k0 * EB;
                     const unsigned char* gb = C::TRANS_B ? b_tile + (size_t)ld_k0 * EB
-                                                         : b_tile + (size_t)ld_k0 * (size_t)N * EB;
+                                                         : b_tile + (size_t)ld_k0 * (size_t)ldb * EB;
                     const uint32_t lsa = smem_addr + ld_stage * C::STAGE_BYTES;
                     const uint32_t lsb = lsa + C::A_BYTES;
                     const int rd_stage = (t + 1) % S;
@@ -1146,7 +1279,8 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
                         if constexpr (r < APT)
                             dma16(ga, a_src[r], lsa + (r * C::NWAVES + wave) * 1024);
                         else if constexpr (r < C::LOADS_PER_STAGE)
-                            dma16(gb, b_src[r - APT], lsb + ((r - APT) * C::NWAVES + wave) * 1024);
+                            dma16(b_from(gb, r - APT), b_src[r - APT],
+                                  lsb + ((r - APT) * C::NWAVES + wave) * 1024);
                         constexpr int half = r / 4, i0 = 2 * (r % 4);
                         constexpr int j0 = half ? HB0 : 0, hb = half ? HB1 : HB0;
 #pragma unroll
@@ -1415,19 +1549,24 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
     // larger than the ring): four values inside the row go out as one 8- or
     // 16-byte store (any element alignment: unaligned-access mode); a row's
     // last partial group element-wise.
+    // Gated: the tile's columns are BN / 2 hidden ones, of which block j holds
+    // the gate sums (even j) or the up sums (odd j) of MB columns.
     constexpr int OB = OutTraits<C::OUT_DT>::bytes;
-    constexpr bool STAGED = OB == 2 && BM * BN * 2 <= C::LDS_BYTES;
-    constexpr int RB = BN * 2, RCH = BN / 8;          // staged: bytes and chunks per tile row
+    constexpr int BNO = C::GATED ? BN / 2 : BN;       // columns of C in the tile
+    const int NC = C::GATED ? args.hidden : N;        // columns of C
+    const int c0 = C::GATED ? n0 >> 1 : n0, c_own = C::GATED ? c0 : n_own, wc0 = C::GATED ? wn0 >> 1 : wn0;
+    constexpr bool STAGED = OB == 2 && BM * BNO * 2 <= C::LDS_BYTES;
+    constexpr int RB = BNO * 2, RCH = BNO / 8;        // staged: bytes and chunks per tile row
     // chunk swizzle mask: the largest power of two <= 16 dividing RCH, less one
     // (a row of 24 chunks XORs inside aligned groups of 8)
     constexpr int XM = (RCH % 16 == 0 ? 16 : RCH % 8 == 0 ? 8 : RCH % 4 == 0 ? 4 : 1) - 1;
     auto put_group = [&](int i, int j, int q, const f32x4_t& x) {
         float v[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = relu(x[e]);
+        for (int e = 0; e < 4; ++e) v[e] = C::EPI == EPI_RELU ? relu(x[e]) : x[e];
         if constexpr (STAGED) {
             const int r = wm0 + MB * i + lr;
-            const int c = wn0 + MB * j + 4 * NG * q + 4 * g;
+            const int c = wc0 + MB * j + 4 * NG * q + 4 * g;
             unsigned short h[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) h[e] = OutTraits<C::OUT_DT>::cvt(v[e]);
@@ -1436,10 +1575,10 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
                                                (c & 7) * 2) = w;
         } else {
             const int m = m0 + wm0 + MB * i + lr;
-            const int n = n0 + wn0 + MB * j + 4 * NG * q + 4 * g;
-            if (m >= M || n >= N || n + 4 <= n_own) return;
-            unsigned char* crow = args.C + (size_t)m * (size_t)N * OB;
-            const bool whole = n >= n_own && n + 4 <= N;
+            const int n = c0 + wc0 + MB * j + 4 * NG * q + 4 * g;
+            if (m >= M || n >= NC || n + 4 <= c_own) return;
+            unsigned char* crow = args.C + (size_t)m * (size_t)NC * OB;
+            const bool whole = n >= c_own && n + 4 <= NC;
             if constexpr (C::OUT_DT == DT_F32) {
                 float* dst = reinterpret_cast<float*>(crow) + n;
                 if (whole) {
@@ -1452,7 +1591,7 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (n + e >= n_own && n + e < N) dst[e] = v[e];
+                        if (n + e >= c_own && n + e < NC) dst[e] = v[e];
                 }
             } else {
                 unsigned short h[4];
@@ -1465,7 +1604,7 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
                 } else {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (n + e >= n_own && n + e < N) dst[e] = h[e];
+                        if (n + e >= c_own && n + e < NC) dst[e] = h[e];
                 }
             }
         }
@@ -1475,14 +1614,57 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
         barrier_lds();
     }
     auto put_acc = [&] {
+        if constexpr (C::GATED) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN / 2; ++j)
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q) {
+                        f32x4_t gate, up, h;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            gate[e] = acc[i][2 * j][4 * q + e];
+                            up[e] = acc[i][2 * j + 1][4 * q + e];
+                            h[e] = activation(gate[e], args.act) * up[e];
+                        }
+                        put_group(i, j, q, h);
+                        const int m = m0 + wm0 + MB * i + lr;
+                        const int n = c0 + wc0 + MB * j + 4 * NG * q + 4 * g;
+                        if (args.GU && m < M && n < NC) {
+                            float* dst = args.GU + (size_t)m * (size_t)(2 * (int64_t)NC) + n;
+                            store_sums(dst, gate, n, NC);
+                            store_sums(dst + NC, up, n, NC);
+                        }
+                    }
+            return;
+        }
+        // scales of the lane's rows and columns (rows and columns past the edge
+        // take the last one's; their results are not stored)
+        float sa[C::EPI == EPI_I8 ? TM : 1], sb[C::EPI == EPI_I8 ? TN * NQ : 1][4];
+        if constexpr (C::EPI == EPI_I8) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i) sa[i] = args.scale_a[min(m0 + wm0 + MB * i + lr, M - 1)];
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int q = 0; q < NQ; ++q)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        sb[j * NQ + q][e] = args.scale_b[min(n0 + wn0 + MB * j + 4 * NG * q + 4 * g + e, N - 1)];
+        }
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
                 for (int q = 0; q < NQ; ++q) {
-                    const f32x4_t x = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                                       acc[i][j][4 * q + 3]};
+                    f32x4_t x = {(float)acc[i][j][4 * q], (float)acc[i][j][4 * q + 1],
+                                 (float)acc[i][j][4 * q + 2], (float)acc[i][j][4 * q + 3]};
+                    if constexpr (C::EPI == EPI_I8) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[e] = x[e] * sa[i] * sb[j * NQ + q][e];
+                    }
                     put_group(i, j, q, x);
                 }
     };
@@ -1526,19 +1708,19 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
     if constexpr (STAGED) {
         barrier_lds();
         auto store_chunk = [&](int r, int cc) {
-            const int m = m0 + r, n = n0 + 8 * cc;
-            if (m >= M || n >= N || n + 8 <= n_own) return;
+            const int m = m0 + r, n = c0 + 8 * cc;
+            if (m >= M || n >= NC || n + 8 <= c_own) return;
             const u32x4_t v = *reinterpret_cast<const GR_LDS u32x4_t*>(
                 smem + r * RB + ((cc ^ (r & XM)) << 4));
-            unsigned short* dst = reinterpret_cast<unsigned short*>(args.C) + (size_t)m * N + n;
-            if (n >= n_own && n + 8 <= N) {
+            unsigned short* dst = reinterpret_cast<unsigned short*>(args.C) + (size_t)m * NC + n;
+            if (n >= c_own && n + 8 <= NC) {
                 // streaming store: C is not read again, so its lines should not
                 // push the next tiles' operand panels out of L2
                 __builtin_nontemporal_store(v, reinterpret_cast<u32x4_t*>(dst));
             } else {
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    if (n + e >= n_own && n + e < N)
+                    if (n + e >= c_own && n + e < NC)
                         dst[e] = (unsigned short)(v[e >> 1] >> (16 * (e & 1)));
             }
         };
