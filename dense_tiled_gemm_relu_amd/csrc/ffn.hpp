@@ -11,7 +11,10 @@
 namespace gemm_relu_hip {
 
 // ---- matrix products (inst_ffn.hip)
-enum LinearConfig : int { LIN_G64 = 0, LIN_COUNT };
+// The tiles of the GEMM + ReLU, with the epilogues of the feed-forward operators;
+// BK in a name counts 16-bit elements, as there.  LIN_32x64, LIN_64x32 and
+// LIN_SPLITK serve only products with B stored (K,N).
+enum LinearConfig : int { LIN_256 = 0, LIN_128, LIN_64, LIN_32x64, LIN_64x32, LIN_SPLITK, LIN_G64, LIN_COUNT };
 
 struct LinearInfo {
     const char* name;
@@ -21,10 +24,14 @@ struct LinearInfo {
 inline const LinearInfo& linear_info(int cfg)
 {
     static const LinearInfo table[LIN_COUNT] = {
+        {"d256x256x32_s4_i16w8", 256, 256}, {"d128x128x64_s3", 128, 128}, {"d64x64x64_s4", 64, 64},
+        {"d32x64x128_s4", 32, 64},          {"d64x32x128_s4", 64, 32},    {"d64x128x64_s4_splitk", 64, 128},
         {"g64x64x64", 64, 64},
     };
     return table[cfg];
 }
+constexpr int kSplitkBK = 64;          // K elements per step of LIN_SPLITK
+constexpr int kSplitkFlagWords = 1024; // arrival counters at the start of its workspace
 
 typedef hipError_t (*LinearLaunchFn)(const KernelArgs& args, int grid, hipStream_t stream);
 LinearLaunchFn launcher_gated(int dt, int cfg);                // B stored (N,K)
@@ -61,6 +68,7 @@ struct GatedGradArgs {
     int64_t dh_stride;
     int ld, ld_t;
     int rows, hidden, act;
+    unsigned* flags;        // kSplitkFlagWords words to clear, or null
 };
 hipError_t launch_gated_grad(const GatedGradArgs& a, int dt, hipStream_t stream);
 

@@ -4,8 +4,8 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <cstdio>
 #include <cstdlib>
-#include <cstring>
 
 #include "api_common.hpp"
 #include "ffn.hpp"
@@ -66,61 +66,112 @@ int finish(hipError_t e, hipStream_t st)
     return GEMM_RELU_OK;
 }
 
-// ---- matrix products
+// ---- matrix products: C (M x N) = A op(B) over K, element rows lda and ldb apart
+struct Linear {
+    int64_t M, N, K, lda, ldb;
+    bool trans;             // B stored (N,K); else (K,N)
+    bool split_ok = false;  // a workspace for a K split can be had
+};
 struct LinearPlan {
     int cfg;
     int64_t tiles_m, tiles_n;
+    int64_t splits = 1, split_steps = 0;
+    uint64_t split_bytes() const
+    {
+        return splits < 2 ? 0 : 4 * kSplitkFlagWords + uint64_t(splits * tiles_m * tiles_n) * 64 * 128 * 4;
+    }
 };
 
-// N counts columns of the tile's own width (gated: both projections).
-LinearPlan plan_linear(int64_t M, int64_t N)
+// K split of a skinny product with B stored (K,N), as gemm_relu_ws takes it:
+// 64 x 128 tiles that fill at most half the CUs, each tile's K steps cut into
+// equal parts of at least 8 steps, enough to give every CU a part.
+bool plan_split(LinearPlan& p, const Linear& l)
+{
+    const int64_t tiles = ceil_div(l.M, 64) * ceil_div(l.N, 128), steps = ceil_div(l.K, kSplitkBK);
+    if (!l.split_ok || l.trans || l.M > 64 || l.N < 128 || tiles * 2 > kNumCUs) return false;
+    const int64_t parts = std::min<int64_t>({16, kNumCUs / tiles, steps / 8});
+    if (parts < 2) return false;
+    p.cfg = LIN_SPLITK;
+    p.split_steps = ceil_div(steps, parts);
+    p.splits = ceil_div(steps, p.split_steps);
+    return p.splits >= 2;
+}
+
+LinearPlan plan_linear(const Linear& l)
 {
     LinearPlan p;
+    auto tiles = [&](int cfg) { return ceil_div(l.M, linear_info(cfg).bm) * ceil_div(l.N, linear_info(cfg).bn); };
+    // 32-bit copy offsets: a tile spans 256 rows of A (of B stored (N,K)), or a
+    // K step's rows of B stored (K,N), whose last tile column ends at N
+    const bool direct = l.lda <= (int64_t(1) << 22) && l.ldb <= (int64_t(1) << (l.trans ? 22 : 24));
+    auto usable = [&](int cfg) { return direct && (l.trans || l.N >= linear_info(cfg).bn); };
+    // rounds of workgroups over the CUs, each the longer of the tile's matrix
+    // time and the time to stream its operands, as for the GEMM + ReLU
+    auto cost = [&](int cfg) {
+        const LinearInfo& t = linear_info(cfg);
+        const double eff = t.bm >= 256 ? 1.0 : t.bm >= 128 ? 0.57 : t.bn >= 64 ? 0.5 : 0.25;
+        return double(ceil_div(tiles(cfg), kNumCUs)) * std::max(t.bm * t.bn / eff, 98.0 * (t.bm + t.bn));
+    };
+    const bool skinny = l.M <= 64 && tiles(LIN_64) * 2 <= kNumCUs;
     p.cfg = LIN_G64;
-    p.tiles_m = ceil_div(M, linear_info(p.cfg).bm);
-    p.tiles_n = ceil_div(N, linear_info(p.cfg).bn);
+    double best = 0.0;
+    for (int cfg : {LIN_256, LIN_128, LIN_64, LIN_32x64, LIN_64x32}) {
+        if (!usable(cfg) || (l.trans && cfg > LIN_64) || (cfg == LIN_32x64 && !skinny)) continue;
+        if (p.cfg == LIN_G64 || cost(cfg) < best) {
+            p.cfg = cfg;
+            best = cost(cfg);
+        }
+    }
+    if (direct) plan_split(p, l);
+    p.tiles_m = ceil_div(l.M, linear_info(p.cfg).bm);
+    p.tiles_n = ceil_div(l.N, linear_info(p.cfg).bn);
     return p;
 }
 
 // a launch's work-items stay below 2^32
-bool plan_fits(const LinearPlan& p) { return p.tiles_m * p.tiles_n <= (int64_t(1) << 22); }
+bool plan_fits(const LinearPlan& p) { return p.tiles_m * p.tiles_n * p.splits <= (int64_t(1) << 22); }
 
-KernelArgs linear_args(const LinearPlan& p, const void* A, int64_t lda, const void* B, int64_t ldb, void* C,
-                       int64_t M, int64_t N, int64_t K)
+KernelArgs linear_args(const LinearPlan& p, const Linear& l, const void* A, const void* B, void* C)
 {
     KernelArgs a{};
     a.A = static_cast<const unsigned char*>(A);
     a.B = static_cast<const unsigned char*>(B);
     a.C = static_cast<unsigned char*>(C);
-    a.M = int(M);
-    a.N = int(N);
-    a.K = int(K);
-    a.lda = int(lda);
-    a.ldb = int(ldb);
+    a.M = int(l.M);
+    a.N = int(l.N);
+    a.K = int(l.K);
+    a.lda = int(l.lda);
+    a.ldb = int(l.ldb);
     a.tiles_m = int(p.tiles_m);
     a.tiles_n = int(p.tiles_n);
     a.panel = int(std::min<int64_t>(8, p.tiles_m));
     a.nxcd = 8;
     return a;
 }
+int linear_grid(const LinearPlan& p) { return int(p.tiles_m * p.tiles_n * p.splits); }
 
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
-// dg and du of the backward pass in the workspace: row-major (rows of 2 hidden)
-// for dx, and transposed (rows of `rows`) for dweight, each row padded to 16
-// bytes.
-struct GradSpace {
-    int64_t ld, ld_t;
-    uint64_t dgu_t, bytes;      // offset of the transposed copy; total
+// The backward pass of the gated projections: dg and du go to the workspace
+// row-major (rows of 2 hidden) for dx, and transposed (rows of `rows`) for
+// dweight, each row padded to 16 bytes; a K split of dx follows.
+struct GradPlan {
+    Linear lx, lw;
+    LinearPlan x, w;            // of dx = dgu weight and of dweight = dgu^T x
+    uint64_t dgu_t, split, bytes;
 };
-GradSpace grad_space(int64_t rows, int64_t hidden)
+GradPlan plan_grad(int64_t rows, int64_t hidden, int64_t cols, int64_t x_stride, int64_t weight_stride)
 {
-    GradSpace s;
-    s.ld = round_up(2 * hidden, 8);
-    s.ld_t = round_up(rows, 8);
-    s.dgu_t = uint64_t(round_up(2 * rows * s.ld, 256));
-    s.bytes = s.dgu_t + uint64_t(2 * hidden) * uint64_t(s.ld_t) * 2;
-    return s;
+    GradPlan g;
+    const int64_t ld = round_up(2 * hidden, 8), ld_t = round_up(rows, 8);
+    g.lx = Linear{rows, cols, 2 * hidden, ld, weight_stride, false, rows > 0 && hidden > 0};
+    g.lw = Linear{2 * hidden, cols, rows, ld_t, x_stride, false};
+    g.x = plan_linear(g.lx);
+    g.w = plan_linear(g.lw);
+    g.dgu_t = uint64_t(round_up(2 * rows * ld, 256));
+    g.split = uint64_t(round_up(int64_t(g.dgu_t + uint64_t(2 * hidden) * uint64_t(ld_t) * 2), 256));
+    g.bytes = g.split + g.x.split_bytes();
+    return g;
 }
 
 }  // namespace
@@ -200,6 +251,12 @@ static bool gated_sizes_ok(int64_t rows, int64_t hidden, int64_t cols, int dtype
     return size_ok(rows) && size_ok(hidden) && 2 * hidden <= kLim && size_ok(cols) && is_16bit(dtype);
 }
 
+// both projections' columns, dense rows unless told otherwise
+static Linear gated_linear(int64_t rows, int64_t hidden, int64_t cols, int64_t lda, int64_t ldb)
+{
+    return Linear{rows, 2 * hidden, cols, lda, ldb, true};
+}
+
 extern "C" int gemm_relu_gated(const void* x, int64_t x_stride, const void* weight, int64_t weight_stride, void* h,
                                float* gu, int64_t rows, int64_t hidden, int64_t cols, int dtype, int act, void* stream)
 {
@@ -209,29 +266,30 @@ extern "C" int gemm_relu_gated(const void* x, int64_t x_stride, const void* weig
     const Mat m[] = {dense(h, rows, hidden, 2), dense(gu, gu ? rows : 0, 2 * hidden, 4),
                      {x, rows, cols, x_stride, 2}, {weight, 2 * hidden, cols, weight_stride, 2}};
     if (!mats_ok(m, 2)) return GEMM_RELU_EINVAL;
-    const LinearPlan p = plan_linear(rows, 2 * hidden);
+    const Linear l = gated_linear(rows, hidden, cols, x_stride, weight_stride);
+    const LinearPlan p = plan_linear(l);
     if (!plan_fits(p)) return GEMM_RELU_EUNSUPPORTED;
     if (const int dev = check_device()) return dev;
-    KernelArgs a = linear_args(p, x, x_stride, weight, weight_stride, h, rows, 2 * hidden, cols);
+    KernelArgs a = linear_args(p, l, x, weight, h);
     a.hidden = int(hidden);
     a.act = act;
     a.GU = gu;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    return finish(launcher_gated(dtype, p.cfg)(a, int(p.tiles_m * p.tiles_n), st), st);
+    return finish(launcher_gated(dtype, p.cfg)(a, linear_grid(p), st), st);
 }
 
 extern "C" const char* gemm_relu_gated_plan(int64_t rows, int64_t hidden, int64_t cols, int dtype)
 {
     if (!gated_sizes_ok(rows, hidden, cols, dtype)) return nullptr;
     if (rows == 0 || hidden == 0) return "none";
-    return linear_info(plan_linear(rows, 2 * hidden).cfg).name;
+    return linear_info(plan_linear(gated_linear(rows, hidden, cols, cols, cols)).cfg).name;
 }
 
 extern "C" int64_t gemm_relu_gated_backward_workspace(int64_t rows, int64_t hidden, int64_t cols)
 {
     if (!gated_sizes_ok(rows, hidden, cols, GEMM_RELU_F16)) return GEMM_RELU_EINVAL;
     if (cols == 0) return 0;
-    return int64_t(grad_space(rows, hidden).bytes);
+    return int64_t(plan_grad(rows, hidden, cols, cols, cols).bytes);
 }
 
 extern "C" int gemm_relu_gated_backward(const void* dh, int64_t dh_stride, const float* gu, const void* x,
@@ -242,40 +300,44 @@ extern "C" int gemm_relu_gated_backward(const void* dh, int64_t dh_stride, const
     if (!gated_sizes_ok(rows, hidden, cols, dtype) || act < GEMM_RELU_ACT_SILU || act > GEMM_RELU_ACT_RELU)
         return GEMM_RELU_EINVAL;
     if (cols == 0 || (rows == 0 && hidden == 0)) return GEMM_RELU_OK;
-    const GradSpace s = grad_space(rows, hidden);
-    const Mat m[] = {dense(dx, rows, cols, 2), dense(dweight, 2 * hidden, cols, 2), bytes_of(workspace, s.bytes),
+    const GradPlan p = plan_grad(rows, hidden, cols, x_stride, weight_stride);
+    const Mat m[] = {dense(dx, rows, cols, 2), dense(dweight, 2 * hidden, cols, 2), bytes_of(workspace, p.bytes),
                      {dh, rows, hidden, dh_stride, 2}, dense(gu, rows, 2 * hidden, 4), {x, rows, cols, x_stride, 2},
                      {weight, 2 * hidden, cols, weight_stride, 2}};
-    if (!mats_ok(m, 3) || !workspace_ok(workspace, workspace_bytes, s.bytes)) return GEMM_RELU_EINVAL;
-    const LinearPlan px = plan_linear(rows, cols), pw = plan_linear(2 * hidden, cols);
-    if (!plan_fits(px) || !plan_fits(pw) || s.ld > kLim || s.ld_t > kLim ||
+    if (!mats_ok(m, 3) || !workspace_ok(workspace, workspace_bytes, p.bytes)) return GEMM_RELU_EINVAL;
+    if (!plan_fits(p.x) || !plan_fits(p.w) || p.lx.lda > kLim || p.lw.lda > kLim ||
         ceil_div(hidden, 64) * ceil_div(rows, 64) > (int64_t(1) << 23))
         return GEMM_RELU_EUNSUPPORTED;
     if (const int dev = check_device()) return dev;
     hipStream_t st = static_cast<hipStream_t>(stream);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
+    unsigned* flags = p.x.splits > 1 ? reinterpret_cast<unsigned*>(ws + p.split) : nullptr;
     hipError_t e = hipSuccess;
     if (rows > 0 && hidden > 0) {
         GatedGradArgs g{};
         g.gu = gu;
         g.dh = dh;
         g.dgu = ws;
-        g.dgu_t = ws + s.dgu_t;
+        g.dgu_t = ws + p.dgu_t;
         g.dh_stride = dh_stride;
-        g.ld = int(s.ld);
-        g.ld_t = int(s.ld_t);
+        g.ld = int(p.lx.lda);
+        g.ld_t = int(p.lw.lda);
         g.rows = int(rows);
         g.hidden = int(hidden);
         g.act = act;
+        g.flags = flags;
         e = launch_gated_grad(g, dtype, st);
     }
-    if (e == hipSuccess && rows > 0)
-        e = launcher_cast(dtype, px.cfg)(linear_args(px, ws, s.ld, weight, weight_stride, dx, rows, cols, 2 * hidden),
-                                         int(px.tiles_m * px.tiles_n), st);
+    if (e == hipSuccess && rows > 0) {
+        KernelArgs a = linear_args(p.x, p.lx, ws, weight, dx);
+        a.flags = flags;
+        a.ws = flags ? reinterpret_cast<float*>(flags + kSplitkFlagWords) : nullptr;
+        a.splits = int(p.x.splits);
+        a.split_steps = int(p.x.split_steps);
+        e = launcher_cast(dtype, p.x.cfg)(a, linear_grid(p.x), st);
+    }
     if (e == hipSuccess && hidden > 0)
-        e = launcher_cast(dtype, pw.cfg)(linear_args(pw, ws + s.dgu_t, s.ld_t, x, x_stride, dweight, 2 * hidden, cols,
-                                                     rows),
-                                         int(pw.tiles_m * pw.tiles_n), st);
+        e = launcher_cast(dtype, p.w.cfg)(linear_args(p.w, p.lw, ws + p.dgu_t, x, dweight), linear_grid(p.w), st);
     return finish(e, st);
 }
 
@@ -283,7 +345,10 @@ extern "C" const char* gemm_relu_gated_backward_plan(int64_t rows, int64_t hidde
 {
     if (!gated_sizes_ok(rows, hidden, cols, dtype)) return nullptr;
     if (cols == 0 || (rows == 0 && hidden == 0)) return "none";
-    return "g64x64x64,g64x64x64";
+    const GradPlan p = plan_grad(rows, hidden, cols, cols, cols);
+    static thread_local char names[64];
+    std::snprintf(names, sizeof names, "%s,%s", linear_info(p.x.cfg).name, linear_info(p.w.cfg).name);
+    return names;
 }
 
 // ------------------------------------------------------- 8-bit integers
@@ -311,14 +376,15 @@ extern "C" int gemm_relu_i8(const void* x, int64_t x_stride, const float* x_scal
     const Mat m[] = {dense(y, rows, n, elem_bytes(out_dtype)), {x, rows, k, x_stride, 1}, {w, n, k, w_stride, 1},
                      dense(x_scale, rows, 1, 4), dense(w_scale, n, 1, 4)};
     if (!mats_ok(m, 1)) return GEMM_RELU_EINVAL;
-    const LinearPlan p = plan_linear(rows, n);
+    const Linear l{rows, n, k, x_stride, w_stride, true};
+    const LinearPlan p = plan_linear(l);
     if (k > kMaxK8 || !plan_fits(p)) return GEMM_RELU_EUNSUPPORTED;
     if (const int dev = check_device()) return dev;
-    KernelArgs a = linear_args(p, x, x_stride, w, w_stride, y, rows, n, k);
+    KernelArgs a = linear_args(p, l, x, w, y);
     a.scale_a = x_scale;
     a.scale_b = w_scale;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    return finish(launcher_i8(out_dtype, p.cfg)(a, int(p.tiles_m * p.tiles_n), st), st);
+    return finish(launcher_i8(out_dtype, p.cfg)(a, linear_grid(p), st), st);
 }
 
 extern "C" const char* gemm_relu_i8_plan(int64_t rows, int64_t n, int64_t k, int out_dtype)
@@ -326,5 +392,5 @@ extern "C" const char* gemm_relu_i8_plan(int64_t rows, int64_t n, int64_t k, int
     if (!size_ok(rows) || !size_ok(n) || !size_ok(k) || !is_float(out_dtype)) return nullptr;
     if (rows == 0 || n == 0) return "none";
     if (k > kMaxK8) return "unsupported";
-    return linear_info(plan_linear(rows, n).cfg).name;
+    return linear_info(plan_linear(Linear{rows, n, k, k, k, true}).cfg).name;
 }

@@ -141,6 +141,8 @@ template <int DT> __global__ void __launch_bounds__(kThreads) gated_grad_kernel(
     const int htiles = (a.hidden + 63) / 64;
     const int h0 = (int)(blockIdx.x % htiles) * 64, r0 = (int)(blockIdx.x / htiles) * 64;
     const int c = threadIdx.x & 63, q = threadIdx.x >> 6;
+    if (a.flags && blockIdx.x == 0)
+        for (int k = threadIdx.x; k < kSplitkFlagWords; k += kThreads) a.flags[k] = 0u;
     for (int k = q; k < 64; k += 4) {
         const int r = r0 + k, h = h0 + c;
         T dg = (T)0.0f, du = (T)0.0f;

@@ -9,7 +9,8 @@ namespace {
 template <class C> __global__ void __launch_bounds__(C::NTHREADS, 1) linear_kernel(KernelArgs args)
 {
     __shared__ __attribute__((aligned(1024))) unsigned char smem_raw[C::LDS_BYTES];
-    gemm_relu_tile<C>(args, blockIdx.x, (GR_LDS unsigned char*)(smem_raw), nullptr,
+    // a K split's workgroups take part blockIdx / tiles of tile blockIdx % tiles
+    gemm_relu_tile<C>(args, C::SPLITK ? (int)blockIdx.x % (args.tiles_m * args.tiles_n) : (int)blockIdx.x, (GR_LDS unsigned char*)(smem_raw), nullptr,
                       Region{args.tiles_m, args.tiles_n, args.panel, 0});
 }
 
@@ -20,19 +21,54 @@ template <class C> hipError_t launch(const KernelArgs& args, int grid, hipStream
                            params, 0, stream);
 }
 
-// EPI over inputs IN: gated and integer products take B stored (N,K)
+// EPI over inputs IN.  Gated and integer products take B stored (N,K) and
+// 16x16 blocks everywhere: the two blocks a gated wave needs side by side fit
+// the small tiles, and the integer instruction has no other form here.
 template <int IN, int OUT, int EPI, int cfg> struct LinearCfg;
+template <int IN, int BK16> constexpr int bk = IN == DT_I8 ? 2 * BK16 : BK16;
+template <int EPI> constexpr bool nt = EPI != EPI_CAST;
+template <int EPI> constexpr int mb = EPI == EPI_CAST ? 32 : 16;
+
+template <int IN, int OUT, int EPI> struct LinearCfg<IN, OUT, EPI, LIN_256> {
+    using type = Cfg<IN, OUT, nt<EPI>, 256, 256, bk<IN, 32>, 2, 4, 4, true, true, 16, false, false, false, EPI>;
+};
+template <int IN, int OUT, int EPI> struct LinearCfg<IN, OUT, EPI, LIN_128> {
+    using type = Cfg<IN, OUT, nt<EPI>, 128, 128, bk<IN, 64>, 2, 2, 3, true, false, mb<EPI>, false, false, false, EPI>;
+};
+template <int IN, int OUT, int EPI> struct LinearCfg<IN, OUT, EPI, LIN_64> {
+    using type = Cfg<IN, OUT, nt<EPI>, 64, 64, bk<IN, 64>, 2, 2, 4, true, false, mb<EPI>, false, false, false, EPI>;
+};
 template <int IN, int OUT, int EPI> struct LinearCfg<IN, OUT, EPI, LIN_G64> {
-    static constexpr int BK = IN == DT_I8 ? 128 : 64, MB = EPI == EPI_CAST ? 32 : 16;
-    using type = Cfg<IN, OUT, EPI != EPI_CAST, 64, 64, BK, 2, 2, 2, false, false, MB, false, false, false, EPI>;
+    using type = Cfg<IN, OUT, nt<EPI>, 64, 64, bk<IN, 64>, 2, 2, 2, false, false, mb<EPI>, false, false, false, EPI>;
+};
+template <int IN, int OUT> struct LinearCfg<IN, OUT, EPI_CAST, LIN_32x64> {
+    using type = Cfg<IN, OUT, false, 32, 64, 128, 1, 2, 4, true, false, 32, false, false, false, EPI_CAST>;
+};
+template <int IN, int OUT> struct LinearCfg<IN, OUT, EPI_CAST, LIN_64x32> {
+    using type = Cfg<IN, OUT, false, 64, 32, 128, 2, 1, 4, true, false, 32, false, false, false, EPI_CAST>;
+};
+template <int IN, int OUT> struct LinearCfg<IN, OUT, EPI_CAST, LIN_SPLITK> {
+    using type = Cfg<IN, OUT, false, 64, 128, kSplitkBK, 2, 2, 4, true, false, 32, false, false, true, EPI_CAST>;
 };
 
 template <int IN, int OUT, int EPI> LinearLaunchFn pick(int cfg)
 {
     switch (cfg) {
+    case LIN_256: return &launch<typename LinearCfg<IN, OUT, EPI, LIN_256>::type>;
+    case LIN_128: return &launch<typename LinearCfg<IN, OUT, EPI, LIN_128>::type>;
+    case LIN_64: return &launch<typename LinearCfg<IN, OUT, EPI, LIN_64>::type>;
     case LIN_G64: return &launch<typename LinearCfg<IN, OUT, EPI, LIN_G64>::type>;
-    default: return nullptr;
+    default: break;
     }
+    if constexpr (EPI == EPI_CAST) {
+        switch (cfg) {
+        case LIN_32x64: return &launch<typename LinearCfg<IN, OUT, EPI, LIN_32x64>::type>;
+        case LIN_64x32: return &launch<typename LinearCfg<IN, OUT, EPI, LIN_64x32>::type>;
+        case LIN_SPLITK: return &launch<typename LinearCfg<IN, OUT, EPI, LIN_SPLITK>::type>;
+        default: break;
+        }
+    }
+    return nullptr;
 }
 
 }  // namespace
