@@ -57,7 +57,7 @@ struct NormArgs {
 };
 hipError_t launch_layer_norm(const NormArgs& a, int dt, int wdt, hipStream_t stream);
 // strips of rows the backward pass sums on their own before joining them
-int layer_norm_strips(int64_t rows);
+int layer_norm_strips(int64_t rows, int64_t cols);
 hipError_t launch_layer_norm_backward(const NormArgs& a, int dt, int wdt, hipStream_t stream);
 
 struct GatedGradArgs {

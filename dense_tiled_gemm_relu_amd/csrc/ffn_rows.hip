@@ -1,6 +1,10 @@
 // Row-wise and element-wise kernels of the feed-forward operators: layer norm
 // forward and backward, the gated projections' element-wise gradient, and the
 // quantisation of rows to 8 bits.
+#include <algorithm>
+#include <type_traits>
+
+#include "api_common.hpp"
 #include "ffn.hpp"
 
 namespace gemm_relu_hip {
@@ -8,6 +12,7 @@ namespace gemm_relu_hip {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kForwardGroups = 256 * 2048;   // threads of a row kernel at most: a full device
 
 template <int DT> struct Elem;
 template <> struct Elem<DT_F16> {
@@ -20,92 +25,383 @@ template <> struct Elem<DT_F32> {
     using T = float;
 };
 
-// Sum over the workgroup, the same value in every thread.
-__device__ __forceinline__ float block_sum(float v, float* lds)
+// ---- sums and maxima over a wave, the same value in every lane: register
+// exchanges inside rows of 16 lanes, then between them (a shuffle through LDS
+// costs about a hundred cycles a step)
+template <int CTRL> __device__ __forceinline__ unsigned dpp(unsigned v)
 {
-#pragma unroll
-    for (int s = 32; s > 0; s >>= 1) v += __shfl_xor(v, s);
-    __syncthreads();                      // earlier reads of lds are done
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    return (lds[0] + lds[1]) + (lds[2] + lds[3]);
+    return (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
 }
-__device__ __forceinline__ float block_max(float v, float* lds)
+struct Sum {
+    static __device__ __forceinline__ float of(float a, float b) { return a + b; }
+};
+struct Max {
+    static __device__ __forceinline__ unsigned of(unsigned a, unsigned b) { return a > b ? a : b; }
+};
+template <class F, class T> __device__ __forceinline__ T wave_all(T v)
 {
+    auto bits = [](T x) { return __builtin_bit_cast(unsigned, x); };
+    auto val = [](unsigned x) { return __builtin_bit_cast(T, x); };
+    v = F::of(v, val(dpp<0xB1>(bits(v))));        // lane ^ 1
+    v = F::of(v, val(dpp<0x4E>(bits(v))));        // lane ^ 2
+    v = F::of(v, val(dpp<0x141>(bits(v))));       // the other four of 8
+    v = F::of(v, val(dpp<0x140>(bits(v))));       // the other eight of 16
+    const auto p = __builtin_amdgcn_permlane16_swap(bits(v), bits(v), false, false);
+    v = F::of(val(p[0]), val(p[1]));
+    const auto q = __builtin_amdgcn_permlane32_swap(bits(v), bits(v), false, false);
+    return F::of(val(q[0]), val(q[1]));
+}
+// ... over the G threads that share a row.  lds holds G / 64 values; the caller
+// alternates between two of them, so one barrier a sum is enough: whoever writes
+// a buffer again has passed the barrier of the other one, behind every read.
+template <int G, class F, class T> __device__ __forceinline__ T group_all(T v, T* lds)
+{
+    v = wave_all<F>(v);
+    if constexpr (G > 64) {
+        const int wave = (int)(threadIdx.x >> 6);
+        if ((threadIdx.x & 63) == 0) lds[wave] = v;
+        __syncthreads();
+        v = lds[0];
 #pragma unroll
-    for (int s = 32; s > 0; s >>= 1) v = fmaxf(v, __shfl_xor(v, s));
-    __syncthreads();
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    return fmaxf(fmaxf(lds[0], lds[1]), fmaxf(lds[2], lds[3]));
+        for (int k = 1; k < G / 64; ++k) v = F::of(v, lds[k]);
+    }
+    return v;
 }
 
-// ------------------------------------------------------------- layer norm
-// One workgroup per row: the mean, then the squares around it (so a large
-// common offset costs no digits), then the output.
-template <int DT, int WDT> __global__ void __launch_bounds__(kThreads) layer_norm_kernel(NormArgs a)
+// ---- a row held in registers by G threads, V chunks of 16 bytes each
+// Rows need only the alignment of an element (16-byte loads at any address).  A
+// row whose length is no multiple of a chunk ends in a chunk moved back inside
+// it; the elements it shares with its neighbour are left out of sums, and are
+// written twice with the same value.  Only the last of a thread's chunks can be
+// moved or missing: rows have more than (V - 1) G chunks.
+template <class T> struct Chunk {
+    static constexpr int N = 16 / sizeof(T);
+    typedef T Vec __attribute__((ext_vector_type(N)));
+};
+template <class T, int N> struct VecN {
+    typedef T Vec __attribute__((ext_vector_type(N)));
+};
+template <class V, class T> __device__ __forceinline__ V load_vec(const T* p)
 {
-    using T = typename Elem<DT>::T;
-    using W = typename Elem<WDT>::T;
-    __shared__ float lds[4];
+    V v;
+    __builtin_memcpy(&v, p, sizeof v);
+    return v;
+}
+
+// Keeps a vector packed across this point: without it the compiler holds the fp32
+// values it has unpacked, two registers for one, and spills.
+template <class V> __device__ __forceinline__ void stay_packed(V& v)
+{
+    u32x4_t* words = reinterpret_cast<u32x4_t*>(&v);
+#pragma unroll
+    for (unsigned k = 0; k < sizeof(V) / 16; ++k) asm volatile("" : "+v"(words[k]));
+}
+
+template <class T, int G, int V> struct RowMap {
+    static constexpr int N = Chunk<T>::N;
+    int start[V], skip;      // first column of each chunk; elements of the last one that the neighbour owns
+    bool last;               // whether the last chunk exists
+    __device__ __forceinline__ RowMap(int cols)
+    {
+        const int t = (int)threadIdx.x % G;
+#pragma unroll
+        for (int v = 0; v < V; ++v) start[v] = (v * G + t) * N;
+        const int j = start[V - 1];
+        last = j < cols;
+        start[V - 1] = min(j, cols - N);
+        skip = j - start[V - 1];
+    }
+    __device__ __forceinline__ bool has(int v) const { return v < V - 1 || last; }
+    // whether element e of chunk v belongs to this thread
+    __device__ __forceinline__ bool owns(int v, int e) const { return v < V - 1 || e >= skip; }
+};
+
+// Rows r, r + step, ... of a group; G = 64: four groups a workgroup.
+template <int G> __device__ __forceinline__ int group_index()
+{
+    return G == 64 ? (int)(blockIdx.x * (kThreads / 64) + (threadIdx.x >> 6)) : (int)blockIdx.x;
+}
+template <int G> constexpr int kGroupThreads = G == 64 ? kThreads : G;
+template <int G> constexpr int kGroups = kGroupThreads<G> / G;
+
+// ------------------------------------------------------------- layer norm
+// One read and one write of the row: it stays in registers between the mean,
+// the squares around it (so a large common offset costs no digits) and the
+// output; the next row of the group is loaded meanwhile, and the weight and the
+// bias stay in registers over all of its rows.
+template <class T, class W, int G, int V> __global__ void __launch_bounds__(kGroupThreads<G>) layer_norm_kernel(NormArgs a)
+{
+    constexpr int N = Chunk<T>::N;
+    using X = typename Chunk<T>::Vec;
+    using WV = typename VecN<W, N>::Vec;
+    __shared__ float lds[2][G / 64];
+    const RowMap<T, G, V> map(a.cols);
+    WV w[V], b[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        w[v] = b[v] = WV{};
+        if (map.has(v)) {
+            w[v] = load_vec<WV>(static_cast<const W*>(a.w) + map.start[v]);
+            if (a.b) b[v] = load_vec<WV>(static_cast<const W*>(a.b) + map.start[v]);
+        }
+    }
+    const int step = (int)gridDim.x * kGroups<G>;
+    int64_t row = group_index<G>();          // 64 bits: the last row's successor may pass 2^31
+    X next[V];
+    auto fetch = [&](int64_t r) {
+        const T* x = static_cast<const T*>(a.x) + (size_t)r * (size_t)a.x_stride;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (map.has(v)) next[v] = load_vec<X>(x + map.start[v]);
+    };
+#pragma unroll
+    for (int v = 0; v < V; ++v) next[v] = X{};
+    if (row < a.rows) fetch(row);
+    const float n = (float)a.cols;
+    for (; row < a.rows; row += step) {
+        X x[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[v] = next[v];
+        if (row < a.rows - step) fetch(row + step);
+        float s = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int e = 0; e < N; ++e) s += map.owns(v, e) ? (float)x[v][e] : 0.0f;
+        const float mean = group_all<G, Sum>(s, lds[0]) / n;
+        s = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float d = map.owns(v, e) ? (float)x[v][e] - mean : 0.0f;
+                s += d * d;
+            }
+        const float rstd = 1.0f / sqrtf(group_all<G, Sum>(s, lds[1]) / n + a.eps);
+        T* y = static_cast<T*>(a.y) + (size_t)row * (size_t)a.cols;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (map.has(v)) {
+                X out;
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    out[e] = (T)(((float)x[v][e] - mean) * rstd * (float)w[v][e] + (float)b[v][e]);
+                __builtin_memcpy(y + map.start[v], &out, sizeof out);
+            }
+        if (threadIdx.x % G == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
+    }
+}
+
+// The backward pass in one read of dy and x: the row's two sums and dx, and the
+// thread's columns of dweight and dbias, summed in registers over the rows of
+// the group.  A workgroup leaves one strip of partial sums; a second kernel
+// joins the strips in order.
+template <class T, class W, int G, int V>
+__global__ void __launch_bounds__(kGroupThreads<G>) __attribute__((amdgpu_waves_per_eu(4)))
+layer_norm_backward_kernel(NormArgs a)
+{
+    constexpr int N = Chunk<T>::N;
+    using X = typename Chunk<T>::Vec;
+    using WV = typename VecN<W, N>::Vec;
+    __shared__ float lds[2][2][G / 64];
+    __shared__ __attribute__((aligned(16))) float part[G == 64 ? 3 * 64 * N * V : 1];
+    const RowMap<T, G, V> map(a.cols);
+    WV w[V];
+    float dw[V][N], db[V][N];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        w[v] = WV{};
+        if (map.has(v)) w[v] = load_vec<WV>(static_cast<const W*>(a.w) + map.start[v]);
+#pragma unroll
+        for (int e = 0; e < N; ++e) dw[v][e] = db[v][e] = 0.0f;
+    }
+    const int step = (int)gridDim.x * kGroups<G>;
+    int64_t row = group_index<G>();          // 64 bits: the last row's successor may pass 2^31
+    X nx[V], nd[V];
+    float nmean = 0.0f, nrstd = 0.0f;
+    auto fetch = [&](int64_t r) {
+        const T* x = static_cast<const T*>(a.x) + (size_t)r * (size_t)a.x_stride;
+        const T* d = static_cast<const T*>(a.dy) + (size_t)r * (size_t)a.dy_stride;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (map.has(v)) {
+                nx[v] = load_vec<X>(x + map.start[v]);
+                nd[v] = load_vec<X>(d + map.start[v]);
+            }
+        nmean = a.mean[r];
+        nrstd = a.rstd[r];
+    };
+#pragma unroll
+    for (int v = 0; v < V; ++v) nx[v] = nd[v] = X{};
+    if (row < a.rows) fetch(row);
+    const float n = (float)a.cols;
+    for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
+        X x[V], d[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            x[v] = nx[v];
+            d[v] = nd[v];
+        }
+        const float mean = nmean, rstd = nrstd;
+#pragma unroll
+        for (int v = 0; v < V; ++v) stay_packed(w[v]);
+        if (row < a.rows - step) fetch(row + step);
+        float s0 = 0.0f, s1 = 0.0f;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float xhat = ((float)x[v][e] - mean) * rstd;
+                // a missing chunk's x counts as 0 too, so that 0 times it stays 0
+                const float g = map.owns(v, e) ? (float)d[v][e] : 0.0f, gx = map.owns(v, e) ? g * xhat : 0.0f;
+                db[v][e] += g;
+                dw[v][e] += gx;
+                s0 += g * (float)w[v][e];
+                s1 += gx * (float)w[v][e];
+            }
+        if constexpr (G == 64) {
+            s0 = wave_all<Sum>(s0);
+            s1 = wave_all<Sum>(s1);
+        } else {
+            s0 = wave_all<Sum>(s0);
+            s1 = wave_all<Sum>(s1);
+            float(*l)[G / 64] = lds[turn];
+            if ((threadIdx.x & 63) == 0) {
+                l[0][threadIdx.x >> 6] = s0;
+                l[1][threadIdx.x >> 6] = s1;
+            }
+            __syncthreads();
+            s0 = l[0][0];
+            s1 = l[1][0];
+#pragma unroll
+            for (int k = 1; k < G / 64; ++k) {
+                s0 += l[0][k];
+                s1 += l[1][k];
+            }
+        }
+        s0 /= n;
+        s1 /= n;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            stay_packed(x[v]);
+            stay_packed(d[v]);
+            stay_packed(w[v]);
+        }
+        T* dx = static_cast<T*>(a.dx) + (size_t)row * (size_t)a.cols;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (map.has(v)) {
+                X out;
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    out[e] = (T)(rstd * ((float)d[v][e] * (float)w[v][e] - s0 - ((float)x[v][e] - mean) * rstd * s1));
+                __builtin_memcpy(dx + map.start[v], &out, sizeof out);
+            }
+    }
+    // one wave a row: the four waves' sums join first
+    float* p = a.partial + (size_t)blockIdx.x * 2 * (size_t)a.cols;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        float(&own)[V][N] = half ? db : dw;
+        if constexpr (G == 64) {
+            const int wave = (int)(threadIdx.x >> 6), lane = (int)(threadIdx.x & 63);
+            __syncthreads();
+            if (wave) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+#pragma unroll
+                    for (int e = 0; e < N; ++e) part[(((wave - 1) * V + v) * N + e) * 64 + lane] = own[v][e];
+            }
+            __syncthreads();
+            if (wave) continue;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+#pragma unroll
+                    for (int k = 0; k < 3; ++k) own[v][e] += part[((k * V + v) * N + e) * 64 + lane];
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (map.has(v)) {
+                float* q = p + (size_t)half * a.cols + map.start[v];
+                if (v < V - 1 || map.skip == 0) {
+#pragma unroll
+                    for (int e = 0; e < N; e += 4) {
+                        const f32x4_t four = {own[v][e], own[v][e + 1], own[v][e + 2], own[v][e + 3]};
+                        __builtin_memcpy(q + e, &four, 16);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < N; ++e)
+                        if (e >= map.skip) q[e] = own[v][e];
+                }
+            }
+    }
+}
+
+// ---- rows shorter than a chunk, or longer than 512 threads hold: one workgroup
+// a row, read once per use (a long row's second and third reads come from L2)
+template <class T, class W> __global__ void __launch_bounds__(kThreads) layer_norm_any_kernel(NormArgs a)
+{
+    __shared__ float lds[2][4];
     const W* w = static_cast<const W*>(a.w);
     const W* b = static_cast<const W*>(a.b);
     for (size_t row = blockIdx.x; row < (size_t)a.rows; row += gridDim.x) {
-    const T* x = static_cast<const T*>(a.x) + row * (size_t)a.x_stride;
-    T* y = static_cast<T*>(a.y) + row * (size_t)a.cols;
-    float s = 0.0f;
-    for (int j = threadIdx.x; j < a.cols; j += kThreads) s += (float)x[j];
-    const float mean = block_sum(s, lds) / (float)a.cols;
-    float v = 0.0f;
-    for (int j = threadIdx.x; j < a.cols; j += kThreads) {
-        const float d = (float)x[j] - mean;
-        v += d * d;
-    }
-    const float rstd = 1.0f / sqrtf(block_sum(v, lds) / (float)a.cols + a.eps);
-    for (int j = threadIdx.x; j < a.cols; j += kThreads)
-        y[j] = (T)(((float)x[j] - mean) * rstd * (float)w[j] + (b ? (float)b[j] : 0.0f));
-    if (threadIdx.x == 0) {
-        if (a.mean) a.mean[row] = mean;
-        if (a.rstd) a.rstd[row] = rstd;
-    }
+        const T* x = static_cast<const T*>(a.x) + row * (size_t)a.x_stride;
+        T* y = static_cast<T*>(a.y) + row * (size_t)a.cols;
+        float s = 0.0f;
+        for (int j = threadIdx.x; j < a.cols; j += kThreads) s += (float)x[j];
+        const float mean = group_all<kThreads, Sum>(s, lds[0]) / (float)a.cols;
+        float v = 0.0f;
+        for (int j = threadIdx.x; j < a.cols; j += kThreads) {
+            const float d = (float)x[j] - mean;
+            v += d * d;
+        }
+        const float rstd = 1.0f / sqrtf(group_all<kThreads, Sum>(v, lds[1]) / (float)a.cols + a.eps);
+        for (int j = threadIdx.x; j < a.cols; j += kThreads)
+            y[j] = (T)(((float)x[j] - mean) * rstd * (float)w[j] + (b ? (float)b[j] : 0.0f));
+        if (threadIdx.x == 0) {
+            if (a.mean) a.mean[row] = mean;
+            if (a.rstd) a.rstd[row] = rstd;
+        }
     }
 }
-
-template <int DT, int WDT> __global__ void __launch_bounds__(kThreads) layer_norm_dx_kernel(NormArgs a)
+template <class T, class W> __global__ void __launch_bounds__(kThreads) layer_norm_dx_any_kernel(NormArgs a)
 {
-    using T = typename Elem<DT>::T;
-    using W = typename Elem<WDT>::T;
-    __shared__ float lds[4];
+    __shared__ float lds[2][4];
     const W* w = static_cast<const W*>(a.w);
     for (size_t row = blockIdx.x; row < (size_t)a.rows; row += gridDim.x) {
-    const T* x = static_cast<const T*>(a.x) + row * (size_t)a.x_stride;
-    const T* dy = static_cast<const T*>(a.dy) + row * (size_t)a.dy_stride;
-    T* dx = static_cast<T*>(a.dx) + row * (size_t)a.cols;
-    const float mean = a.mean[row], rstd = a.rstd[row];
-    float s0 = 0.0f, s1 = 0.0f;
-    for (int j = threadIdx.x; j < a.cols; j += kThreads) {
-        const float c = (float)dy[j] * (float)w[j];
-        s0 += c;
-        s1 += c * (((float)x[j] - mean) * rstd);
-    }
-    s0 = block_sum(s0, lds) / (float)a.cols;
-    s1 = block_sum(s1, lds) / (float)a.cols;
-    for (int j = threadIdx.x; j < a.cols; j += kThreads) {
-        const float c = (float)dy[j] * (float)w[j];
-        dx[j] = (T)(rstd * (c - s0 - ((float)x[j] - mean) * rstd * s1));
-    }
+        const T* x = static_cast<const T*>(a.x) + row * (size_t)a.x_stride;
+        const T* dy = static_cast<const T*>(a.dy) + row * (size_t)a.dy_stride;
+        T* dx = static_cast<T*>(a.dx) + row * (size_t)a.cols;
+        const float mean = a.mean[row], rstd = a.rstd[row];
+        float s0 = 0.0f, s1 = 0.0f;
+        for (int j = threadIdx.x; j < a.cols; j += kThreads) {
+            const float c = (float)dy[j] * (float)w[j];
+            s0 += c;
+            s1 += c * (((float)x[j] - mean) * rstd);
+        }
+        s0 = group_all<kThreads, Sum>(s0, lds[0]) / (float)a.cols;
+        s1 = group_all<kThreads, Sum>(s1, lds[1]) / (float)a.cols;
+        for (int j = threadIdx.x; j < a.cols; j += kThreads) {
+            const float c = (float)dy[j] * (float)w[j];
+            dx[j] = (T)(rstd * (c - s0 - ((float)x[j] - mean) * rstd * s1));
+        }
     }
 }
-
 // Column sums of one strip of rows: thread per column.
-template <int DT> __global__ void __launch_bounds__(kThreads) layer_norm_strip_kernel(NormArgs a, int strip_rows)
+template <class T, class W>
+__global__ void __launch_bounds__(kThreads) layer_norm_strip_any_kernel(NormArgs a, int strip_rows)
 {
-    using T = typename Elem<DT>::T;
     const int j = blockIdx.x * kThreads + threadIdx.x;
     if (j >= a.cols) return;
-    const int r0 = blockIdx.y * strip_rows, r1 = min(a.rows, r0 + strip_rows);
+    const int64_t r0 = (int64_t)blockIdx.y * strip_rows, r1 = min((int64_t)a.rows, r0 + strip_rows);
     float dw = 0.0f, db = 0.0f;
-    for (int r = r0; r < r1; ++r) {
+    for (int64_t r = r0; r < r1; ++r) {
         const float g = (float)static_cast<const T*>(a.dy)[(size_t)r * (size_t)a.dy_stride + j];
         const float v = (float)static_cast<const T*>(a.x)[(size_t)r * (size_t)a.x_stride + j];
         dw += g * ((v - a.mean[r]) * a.rstd[r]);
@@ -116,19 +412,32 @@ template <int DT> __global__ void __launch_bounds__(kThreads) layer_norm_strip_k
     p[a.cols + j] = db;
 }
 
-template <int WDT> __global__ void __launch_bounds__(kThreads) layer_norm_join_kernel(NormArgs a, int strips)
+// The strips' sums, in order: 64 columns a workgroup, each of 16 waves takes every
+// 16th strip.
+template <class W> __global__ void __launch_bounds__(1024) layer_norm_join_kernel(NormArgs a, int strips)
 {
-    using W = typename Elem<WDT>::T;
-    const int j = blockIdx.x * kThreads + threadIdx.x;
-    if (j >= a.cols) return;
-    float dw = 0.0f, db = 0.0f;
-    for (int s = 0; s < strips; ++s) {
-        const float* p = a.partial + (size_t)s * 2 * (size_t)a.cols;
-        dw += p[j];
-        db += p[a.cols + j];
+    __shared__ float part[16][64];
+    const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
+    const int64_t all = 2 * (int64_t)a.cols;
+    for (int64_t j0 = (int64_t)blockIdx.x * 64; j0 < all; j0 += (int64_t)gridDim.x * 64) {
+        const int64_t j = j0 + lane;
+        float s = 0.0f;
+        if (j < all) {
+#pragma unroll 8
+            for (int k = wave; k < strips; k += 16) s += a.partial[(size_t)k * (size_t)all + j];
+        }
+        part[wave][lane] = s;
+        __syncthreads();
+        if (!wave && j < all) {
+#pragma unroll
+            for (int k = 1; k < 16; ++k) s += part[k][lane];
+            if (j < a.cols)
+                static_cast<W*>(a.dw)[j] = (W)s;
+            else if (a.db)
+                static_cast<W*>(a.db)[j - a.cols] = (W)s;
+        }
+        __syncthreads();
     }
-    static_cast<W*>(a.dw)[j] = (W)dw;
-    if (a.db) static_cast<W*>(a.db)[j] = (W)db;
 }
 
 // --------------------------------------------- gradient of act(g) u
@@ -172,107 +481,243 @@ template <int DT> __global__ void __launch_bounds__(kThreads) gated_grad_kernel(
 }
 
 // ------------------------------------------------------- quantisation
+// The largest magnitude is taken over the values' bits without the sign, whose
+// order as whole numbers is that of the values with infinities and NaN on top.
 // 127 x / max is formed as one fp32 division of the product 127 x.  For 16-bit x
 // the product is exact and the quotient's distance from a rounding border is
 // either zero or more than half an fp32 step, so the result is that of exact
 // arithmetic.  A row whose largest value is near the top of the fp32 range is
 // scaled down by a power of two first, so that 127 x stays finite.
-template <int DT>
-__global__ void __launch_bounds__(kThreads) quantize_rows_kernel(const void* xs, int64_t x_stride,
-                                                                 signed char* qs, float* scale, int rows, int cols)
-{
-    using T = typename Elem<DT>::T;
-    __shared__ float lds[4];
-    for (size_t row = blockIdx.x; row < (size_t)rows; row += gridDim.x) {
-    const T* x = static_cast<const T*>(xs) + row * (size_t)x_stride;
-    signed char* q = qs + row * (size_t)cols;
-    float top = 0.0f, bad = 0.0f;
-    for (int j = threadIdx.x; j < cols; j += kThreads) {
-        const float v = fabsf((float)x[j]);
-        top = fmaxf(top, v);
-        bad = v < INFINITY ? bad : 1.0f;
+struct Quantiser {
+    float mul, by;
+    __device__ __forceinline__ Quantiser(float top)
+    {
+        const float down = top > 0x1p120f ? 0x1p-8f : 1.0f;
+        mul = down;
+        by = top * down;
     }
-    top = block_max(top, lds);
-    bad = block_max(bad, lds);
-    const bool empty = bad > 0.0f || top == 0.0f;
-    const float down = top > 0x1p120f ? 0x1p-8f : 1.0f;
-    for (int j = threadIdx.x; j < cols; j += kThreads)
-        q[j] = empty ? (signed char)0 : (signed char)(int)rintf(127.0f * ((float)x[j] * down) / (top * down));
-    if (threadIdx.x == 0) scale[row] = bad > 0.0f ? NAN : top / 127.0f;
+    __device__ __forceinline__ signed char operator()(float x) const
+    {
+        return (signed char)(int)rintf(127.0f * (x * mul) / by);
+    }
+};
+template <class T> __device__ __forceinline__ unsigned magnitude(T x)
+{
+    if constexpr (sizeof(T) == 2)
+        return __builtin_bit_cast(unsigned short, x) & 0x7fffu;
+    else
+        return __builtin_bit_cast(unsigned, x) & 0x7fffffffu;
+}
+template <class T> __device__ __forceinline__ float from_magnitude(unsigned m)
+{
+    if constexpr (sizeof(T) == 2)
+        return (float)__builtin_bit_cast(T, (unsigned short)m);
+    else
+        return __builtin_bit_cast(float, m);
+}
+struct QuantArgs {
+    const void* x;
+    signed char* q;
+    float* scale;
+    int64_t x_stride;
+    int rows, cols;
+};
+
+// The row stays in registers between its largest value and its quotients.
+template <class T, int G, int V> __global__ void __launch_bounds__(kGroupThreads<G>) quantize_rows_kernel(QuantArgs a)
+{
+    constexpr int N = Chunk<T>::N;
+    using X = typename Chunk<T>::Vec;
+    using Q = typename VecN<signed char, N>::Vec;
+    __shared__ unsigned lds[2][G / 64];
+    const RowMap<T, G, V> map(a.cols);
+    const int step = (int)gridDim.x * kGroups<G>;
+    int64_t row = group_index<G>();          // 64 bits: the last row's successor may pass 2^31
+    X next[V];
+    auto fetch = [&](int64_t r) {
+        const T* x = static_cast<const T*>(a.x) + (size_t)r * (size_t)a.x_stride;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (map.has(v)) next[v] = load_vec<X>(x + map.start[v]);
+    };
+#pragma unroll
+    for (int v = 0; v < V; ++v) next[v] = X{};
+    if (row < a.rows) fetch(row);
+    for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
+        X x[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) x[v] = next[v];
+        if (row < a.rows - step) fetch(row + step);
+        unsigned most = 0;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int e = 0; e < N; ++e) most = Max::of(most, magnitude<T>(x[v][e]));
+        const float top = from_magnitude<T>(group_all<G, Max>(most, lds[turn]));
+        const bool bad = !(top < INFINITY), empty = bad || top == 0.0f;
+        const Quantiser quantise(top);
+        signed char* q = a.q + (size_t)row * (size_t)a.cols;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (map.has(v)) {
+                Q out = Q{};
+                if (!empty) {
+#pragma unroll
+                    for (int e = 0; e < N; ++e) out[e] = quantise((float)x[v][e]);
+                }
+                __builtin_memcpy(q + map.start[v], &out, sizeof out);
+            }
+        if (threadIdx.x % G == 0) a.scale[row] = bad ? NAN : top / 127.0f;
+    }
+}
+template <class T> __global__ void __launch_bounds__(kThreads) quantize_rows_any_kernel(QuantArgs a)
+{
+    __shared__ unsigned lds[2][4];
+    int turn = 0;
+    for (size_t row = blockIdx.x; row < (size_t)a.rows; row += gridDim.x, turn ^= 1) {
+        const T* x = static_cast<const T*>(a.x) + row * (size_t)a.x_stride;
+        signed char* q = a.q + row * (size_t)a.cols;
+        unsigned most = 0;
+        for (int j = threadIdx.x; j < a.cols; j += kThreads) most = Max::of(most, magnitude<T>(x[j]));
+        const float top = from_magnitude<T>(group_all<kThreads, Max>(most, lds[turn]));
+        const bool bad = !(top < INFINITY), empty = bad || top == 0.0f;
+        const Quantiser quantise(top);
+        for (int j = threadIdx.x; j < a.cols; j += kThreads) q[j] = empty ? (signed char)0 : quantise((float)x[j]);
+        if (threadIdx.x == 0) a.scale[row] = bad ? NAN : top / 127.0f;
     }
 }
 
-template <class... A> hipError_t start(void (*kernel)(A...), dim3 grid, hipStream_t stream, A... args)
+template <class... A> hipError_t start(void (*kernel)(A...), dim3 grid, int threads, hipStream_t stream, A... args)
 {
     void* params[] = {&args...};
-    return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(kThreads), params, 0, stream);
+    return hipLaunchKernel(reinterpret_cast<const void*>(kernel), grid, dim3(threads), params, 0, stream);
 }
 
-constexpr int kStripRows = 64, kMaxStrips = 1024;
-constexpr int kMaxRowGrid = 1 << 20;     // workgroups of a row kernel; each takes rows that far apart
-int row_grid(int rows) { return rows < kMaxRowGrid ? rows : kMaxRowGrid; }
+constexpr int kMaxRowGrid = 1 << 20;     // workgroups of a kernel that takes rows that far apart
+int any_grid(int rows) { return rows < kMaxRowGrid ? rows : kMaxRowGrid; }
+
+// Threads that share a row (0: the kernels for any length) and 16-byte chunks of
+// it each.  Forward: up to four chunks a thread, one wave where that holds the
+// row, so that short rows need no barrier.  Backward: one chunk a thread as long
+// as 1024 threads hold the row, since a thread keeps two fp32 sums a column
+// beside two rows and the weight.
+struct RowShape {
+    int g, v;
+};
+template <bool BACK> RowShape row_shape(int cols, int bytes)
+{
+    const int n = 16 / bytes;
+    if (cols < n) return {0, 0};
+    const int chunks = (int)(((int64_t)cols + n - 1) / n);
+    for (int g = 64; g <= 1024; g *= 2) {
+        const int v = (int)ceil_div(chunks, g);
+        if (v <= (!BACK ? 4 : g == 1024 ? 2 : 1)) return {g, v};
+    }
+    return {0, 0};
+}
+// Calls f<G, V> for a shape row_shape can give.
+template <bool BACK, class F> hipError_t with_shape(RowShape s, F&& f)
+{
+#define GR_SHAPE(G, V) \
+    if (s.g == G && s.v == V) return f(std::integral_constant<int, G>{}, std::integral_constant<int, V>{});
+    if constexpr (BACK) {
+        GR_SHAPE(64, 1) GR_SHAPE(128, 1) GR_SHAPE(256, 1) GR_SHAPE(512, 1) GR_SHAPE(1024, 1) GR_SHAPE(1024, 2)
+    } else {
+        GR_SHAPE(64, 1) GR_SHAPE(64, 2) GR_SHAPE(64, 3) GR_SHAPE(64, 4) GR_SHAPE(128, 3) GR_SHAPE(128, 4)
+        GR_SHAPE(256, 3) GR_SHAPE(256, 4) GR_SHAPE(512, 3) GR_SHAPE(512, 4) GR_SHAPE(1024, 3) GR_SHAPE(1024, 4)
+    }
+#undef GR_SHAPE
+    return hipErrorInvalidValue;
+}
+template <class F> hipError_t with_types(int dt, int wdt, F&& f)
+{
+    if (dt == DT_F32) return f(float{}, float{});
+    if (dt == DT_F16) return wdt == DT_F32 ? f(_Float16{}, float{}) : f(_Float16{}, _Float16{});
+    return wdt == DT_F32 ? f(__bf16{}, float{}) : f(__bf16{}, __bf16{});
+}
+int elem_size(int dt) { return dt == DT_F32 ? 4 : 2; }
+
+// Workgroups that take rows in turns: at most `most`, and as many rows each as
+// the busiest has anyway, so that they end together.
+int even_grid(int64_t rows, int rows_each_turn, int most)
+{
+    const int64_t turns = ceil_div(rows, (int64_t)rows_each_turn * most);
+    return (int)ceil_div(rows, rows_each_turn * turns);
+}
 
 }  // namespace
 
 hipError_t launch_layer_norm(const NormArgs& a, int dt, int wdt, hipStream_t stream)
 {
-    const dim3 grid(row_grid(a.rows));
-    if (dt == DT_F32) return start(&layer_norm_kernel<DT_F32, DT_F32>, grid, stream, a);
-    if (dt == DT_F16)
-        return wdt == DT_F32 ? start(&layer_norm_kernel<DT_F16, DT_F32>, grid, stream, a)
-                             : start(&layer_norm_kernel<DT_F16, DT_F16>, grid, stream, a);
-    return wdt == DT_F32 ? start(&layer_norm_kernel<DT_BF16, DT_F32>, grid, stream, a)
-                         : start(&layer_norm_kernel<DT_BF16, DT_BF16>, grid, stream, a);
+    const RowShape s = row_shape<false>(a.cols, elem_size(dt));
+    return with_types(dt, wdt, [&](auto x, auto w) {
+        using T = decltype(x);
+        using W = decltype(w);
+        if (!s.g) return start(&layer_norm_any_kernel<T, W>, dim3(any_grid(a.rows)), kThreads, stream, a);
+        return with_shape<false>(s, [&](auto g, auto v) {
+            constexpr int G = decltype(g)::value;
+            const int grid = even_grid(a.rows, kGroups<G>, kForwardGroups / kGroupThreads<G>);
+            return start(&layer_norm_kernel<T, W, G, decltype(v)::value>, dim3(grid), kGroupThreads<G>, stream, a);
+        });
+    });
 }
 
-// strips of at least kStripRows rows, at most kMaxStrips of them
-int layer_norm_strips(int64_t rows)
+// workgroups of the backward pass, each of which leaves one strip of sums
+int layer_norm_strips(int64_t rows, int64_t cols)
 {
-    const int64_t n = (rows + kStripRows - 1) / kStripRows;
-    return (int)(n < kMaxStrips ? n : kMaxStrips);
+    return rows == 0 ? 0 : even_grid(rows, cols <= 512 ? 4 : 2, cols <= 2048 ? 1024 : cols <= 4096 ? 512 : 256);
 }
 
 hipError_t launch_layer_norm_backward(const NormArgs& a, int dt, int wdt, hipStream_t stream)
 {
-    const int strips = layer_norm_strips(a.rows), colblocks = (a.cols + kThreads - 1) / kThreads;
-    hipError_t e = hipSuccess;
-    if (a.rows > 0) {
-        const dim3 grid(row_grid(a.rows)), sgrid(colblocks, strips);
-        const int strip_rows = (a.rows + strips - 1) / strips;
-        if (dt == DT_F32) {
-            e = start(&layer_norm_dx_kernel<DT_F32, DT_F32>, grid, stream, a);
-            if (e == hipSuccess) e = start(&layer_norm_strip_kernel<DT_F32>, sgrid, stream, a, strip_rows);
-        } else if (dt == DT_F16) {
-            e = wdt == DT_F32 ? start(&layer_norm_dx_kernel<DT_F16, DT_F32>, grid, stream, a)
-                              : start(&layer_norm_dx_kernel<DT_F16, DT_F16>, grid, stream, a);
-            if (e == hipSuccess) e = start(&layer_norm_strip_kernel<DT_F16>, sgrid, stream, a, strip_rows);
-        } else {
-            e = wdt == DT_F32 ? start(&layer_norm_dx_kernel<DT_BF16, DT_F32>, grid, stream, a)
-                              : start(&layer_norm_dx_kernel<DT_BF16, DT_BF16>, grid, stream, a);
-            if (e == hipSuccess) e = start(&layer_norm_strip_kernel<DT_BF16>, sgrid, stream, a, strip_rows);
+    const int strips = layer_norm_strips(a.rows, a.cols);
+    const RowShape s = row_shape<true>(a.cols, elem_size(dt));
+    return with_types(dt, wdt, [&](auto x, auto w) {
+        using T = decltype(x);
+        using W = decltype(w);
+        hipError_t e = hipSuccess;
+        if (a.rows > 0 && s.g) {
+            e = with_shape<true>(s, [&](auto g, auto v) {
+                constexpr int G = decltype(g)::value;
+                return start(&layer_norm_backward_kernel<T, W, G, decltype(v)::value>, dim3(strips), kGroupThreads<G>,
+                             stream, a);
+            });
+        } else if (a.rows > 0) {
+            const int strip_rows = (int)ceil_div(a.rows, strips);
+            e = start(&layer_norm_dx_any_kernel<T, W>, dim3(any_grid(a.rows)), kThreads, stream, a);
+            if (e == hipSuccess)
+                e = start(&layer_norm_strip_any_kernel<T, W>, dim3((unsigned)ceil_div(a.cols, kThreads), strips), kThreads,
+                          stream, a, strip_rows);
         }
         if (e != hipSuccess) return e;
-    }
-    const dim3 jgrid(colblocks);
-    if (wdt == DT_F32) return start(&layer_norm_join_kernel<DT_F32>, jgrid, stream, a, strips);
-    if (wdt == DT_F16) return start(&layer_norm_join_kernel<DT_F16>, jgrid, stream, a, strips);
-    return start(&layer_norm_join_kernel<DT_BF16>, jgrid, stream, a, strips);
+        return start(&layer_norm_join_kernel<W>, dim3((unsigned)std::min<int64_t>(ceil_div(2 * (int64_t)a.cols, 64), kMaxRowGrid)), 1024, stream, a, strips);
+    });
 }
 
 hipError_t launch_gated_grad(const GatedGradArgs& a, int dt, hipStream_t stream)
 {
     const dim3 grid((unsigned)((a.hidden + 63) / 64) * (unsigned)((a.rows + 63) / 64));
-    return dt == DT_F16 ? start(&gated_grad_kernel<DT_F16>, grid, stream, a)
-                        : start(&gated_grad_kernel<DT_BF16>, grid, stream, a);
+    return dt == DT_F16 ? start(&gated_grad_kernel<DT_F16>, grid, kThreads, stream, a)
+                        : start(&gated_grad_kernel<DT_BF16>, grid, kThreads, stream, a);
 }
 
 hipError_t launch_quantize_rows(const void* x, int64_t x_stride, signed char* q, float* scale, int rows,
                                 int cols, int dt, hipStream_t stream)
 {
-    const dim3 grid(row_grid(rows));
-    if (dt == DT_F32) return start(&quantize_rows_kernel<DT_F32>, grid, stream, x, x_stride, q, scale, rows, cols);
-    if (dt == DT_F16) return start(&quantize_rows_kernel<DT_F16>, grid, stream, x, x_stride, q, scale, rows, cols);
-    return start(&quantize_rows_kernel<DT_BF16>, grid, stream, x, x_stride, q, scale, rows, cols);
+    const QuantArgs a{x, q, scale, x_stride, rows, cols};
+    const RowShape s = row_shape<false>(cols, elem_size(dt));
+    return with_types(dt, dt, [&](auto x0, auto w) {
+        using T = decltype(x0);
+        if constexpr (std::is_same_v<T, decltype(w)>) {
+            if (!s.g) return start(&quantize_rows_any_kernel<T>, dim3(any_grid(rows)), kThreads, stream, a);
+            return with_shape<false>(s, [&](auto g, auto v) {
+                constexpr int G = decltype(g)::value;
+                const int grid = even_grid(rows, kGroups<G>, kForwardGroups / kGroupThreads<G>);
+                return start(&quantize_rows_kernel<T, G, decltype(v)::value>, dim3(grid), kGroupThreads<G>, stream, a);
+            });
+        }
+        return hipErrorInvalidValue;
+    });
 }
 
 }  // namespace gemm_relu_hip

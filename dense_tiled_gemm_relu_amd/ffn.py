@@ -12,7 +12,6 @@ hipStream_t, or None for torch's current stream); results and workspaces are
 allocated for that stream.  A tensor made on another stream has to be ready
 before the call, as with any torch operation.
 """
-import contextlib
 import ctypes
 
 ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2, "relu": 3}
@@ -43,14 +42,28 @@ def declare(lib):
         fn.argtypes, fn.restype = args, res
 
 
-def _library():
-    from . import library
-    return library()
+class _Env:
+    """What every call needs of torch and the library, looked up once: a call's
+    own cost on the host is that of a short kernel."""
+
+    def __init__(self):
+        import torch
+        from . import library
+        self.codes = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+        self.torch, self.lib = torch, library()
+        self.empty, self.f32 = torch.empty, torch.float32
+        self.current_device = torch._C._cuda_getDevice
+        self.raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _codes():
-    import torch
-    return {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
+_env = None
+
+
+def _get_env():
+    global _env
+    if _env is None:
+        _env = _Env()
+    return _env
 
 
 def _check(status):
@@ -61,16 +74,22 @@ def _check(status):
 
 def _rows(t, name):
     """(rows, columns, elements from row to row) of an activation tensor."""
-    if t.dim() < 1:
+    shape = t.shape
+    if len(shape) == 2:
+        rows, cols = shape
+        if t.is_contiguous():
+            return rows, cols, cols
+        ld, one = t.stride()
+        if one == 1 and ld >= cols:
+            return rows, cols, ld
+    elif len(shape) == 0:
         raise ValueError("%s must have at least one dimension" % name)
-    cols = t.shape[-1]
-    if t.is_contiguous():
+    elif t.is_contiguous():
+        cols = shape[-1]
         rows = 1
-        for n in t.shape[:-1]:
+        for n in shape[:-1]:
             rows *= n
         return rows, cols, cols
-    if t.dim() == 2 and t.stride(1) == 1 and t.stride(0) >= cols:
-        return t.shape[0], cols, t.stride(0)
     raise ValueError("%s must be contiguous, or 2-D with contiguous rows" % name)
 
 
@@ -87,29 +106,33 @@ def _vector(t, name, n, dtypes):
         raise ValueError("%s must be contiguous with %d elements" % (name, n))
 
 
-def _one_gpu(first, *others):
-    if not first.is_cuda or any(t is not None and t.device != first.device for t in others):
-        raise ValueError("all tensors must be on the same GPU")
+def _one_gpu(*tensors):
+    """The index of the GPU that holds all of the tensors."""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t.get_device() != index or index < 0:
+            raise ValueError("all tensors must be on the same GPU")
+    return index
 
 
-@contextlib.contextmanager
-def _on(device, stream):
-    """Makes `device` and `stream` current for the allocations and the launch
-    inside; gives the raw stream."""
-    import torch
-    with torch.cuda.device(device):
+def _launch(index, stream, inputs, call):
+    """call(raw stream) with GPU `index` and the stream current for its
+    allocations and its launch."""
+    env = _get_env()
+    if stream is None and env.current_device() == index:
+        return call(env.raw_stream(index))
+    cuda = env.torch.cuda
+    with cuda.device(index):
         if stream is None:
-            yield torch.cuda.current_stream().cuda_stream
-            return
+            return call(env.raw_stream(index))
         if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=device)
-        with torch.cuda.stream(stream):
-            yield stream.cuda_stream
-
-
-def _workspace(nbytes, device):
-    import torch
-    return torch.empty(nbytes, dtype=torch.uint8, device=device)
+            stream = cuda.ExternalStream(stream, device=index)
+        with cuda.stream(stream):
+            out = call(stream.cuda_stream)
+        # the caller may drop an input while the stream still reads it
+        for t in inputs:
+            t.record_stream(stream)
+        return out
 
 
 def layer_norm(x, weight, bias=None, eps=1e-5, stats=False, stream=None):
@@ -119,67 +142,81 @@ def layer_norm(x, weight, bias=None, eps=1e-5, stats=False, stream=None):
     float32.  Returns y, or with ``stats`` (y, mean, rstd), the fp32 statistics
     of each row that the backward pass takes.
     """
-    import torch
-    codes = _codes()
-    if x.dtype not in codes:
-        raise TypeError("x must be float16, bfloat16 or float32, not %s" % x.dtype)
+    env = _get_env()
+    codes, dt = env.codes, x.dtype
+    if dt not in codes:
+        raise TypeError("x must be float16, bfloat16 or float32, not %s" % dt)
     rows, cols, ld = _rows(x, "x")
-    _vector(weight, "weight", cols, (x.dtype, torch.float32))
-    if bias is not None:
-        _vector(bias, "bias", cols, (weight.dtype,))
-    _one_gpu(x, weight, bias)
-    with _on(x.device, stream) as st:
-        y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    wdt = weight.dtype
+    _vector(weight, "weight", cols, (dt, env.f32))
+    if bias is None:
+        inputs = (x, weight)
+    else:
+        _vector(bias, "bias", cols, (wdt,))
+        inputs = (x, weight, bias)
+    index = _one_gpu(*inputs)
+
+    def call(st):
+        device = x.device
+        y = env.empty(x.shape, dtype=dt, device=device)
         mean = rstd = None
         if stats:
-            mean, rstd = (torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device) for _ in range(2))
-        _check(_library().gemm_relu_layer_norm(
+            mean, rstd = (env.empty(x.shape[:-1], dtype=env.f32, device=device) for _ in range(2))
+        _check(env.lib.gemm_relu_layer_norm(
             x.data_ptr(), ld, weight.data_ptr(), None if bias is None else bias.data_ptr(), y.data_ptr(),
             mean.data_ptr() if stats else None, rstd.data_ptr() if stats else None, rows, cols,
-            codes[x.dtype], codes[weight.dtype], eps, st))
-    return (y, mean, rstd) if stats else y
+            codes[dt], codes[wdt], eps, st))
+        return (y, mean, rstd) if stats else y
+
+    return _launch(index, stream, inputs, call)
 
 
 def layer_norm_backward(dy, x, weight, mean, rstd, stream=None):
     """Gradients (dx, dweight, dbias) of layer_norm, given dy and the statistics
     of the forward call.  dx has x's type, dweight and dbias weight's."""
-    import torch
-    codes = _codes()
-    if x.dtype not in codes:
-        raise TypeError("x must be float16, bfloat16 or float32, not %s" % x.dtype)
-    if dy.dtype != x.dtype:
+    env = _get_env()
+    codes, dt, f32 = env.codes, x.dtype, env.f32
+    if dt not in codes:
+        raise TypeError("x must be float16, bfloat16 or float32, not %s" % dt)
+    if dy.dtype != dt:
         raise TypeError("dy must have x's type")
     if dy.shape != x.shape:
         raise ValueError("dy and x must have the same shape")
     rows, cols, ld = _rows(x, "x")
     dy_ld = _rows(dy, "dy")[2]
-    _vector(weight, "weight", cols, (x.dtype, torch.float32))
-    _vector(mean, "mean", rows, (torch.float32,))
-    _vector(rstd, "rstd", rows, (torch.float32,))
-    _one_gpu(x, dy, weight, mean, rstd)
-    lib = _library()
-    with _on(x.device, stream) as st:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dw, db = torch.empty_like(weight), torch.empty_like(weight)
-        ws = _workspace(lib.gemm_relu_layer_norm_backward_workspace(rows, cols), x.device)
+    _vector(weight, "weight", cols, (dt, f32))
+    _vector(mean, "mean", rows, (f32,))
+    _vector(rstd, "rstd", rows, (f32,))
+    inputs = (x, dy, weight, mean, rstd)
+    index = _one_gpu(*inputs)
+
+    def call(st):
+        lib, device, wdt = env.lib, x.device, weight.dtype
+        dx = env.empty(x.shape, dtype=dt, device=device)
+        dw, db = (env.empty(weight.shape, dtype=wdt, device=device) for _ in range(2))
+        nbytes = lib.gemm_relu_layer_norm_backward_workspace(rows, cols)
+        ws = env.empty(nbytes, dtype=env.torch.uint8, device=device)
         _check(lib.gemm_relu_layer_norm_backward(
             dy.data_ptr(), dy_ld, x.data_ptr(), ld, weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
-            dx.data_ptr(), dw.data_ptr(), db.data_ptr(), rows, cols, codes[x.dtype], codes[weight.dtype],
-            ws.data_ptr(), ws.numel(), st))
-    return dx, dw, db
+            dx.data_ptr(), dw.data_ptr(), db.data_ptr(), rows, cols, codes[dt], codes[wdt],
+            ws.data_ptr(), nbytes, st))
+        return dx, dw, db
+
+    return _launch(index, stream, inputs, call)
 
 
-def _gated_args(x, weight, act):
-    import torch
-    if act not in ACTIVATIONS:
+def _gated_args(env, x, weight, act):
+    code = ACTIVATIONS.get(act)
+    if code is None:
         raise ValueError("act must be one of %s" % ", ".join(sorted(ACTIVATIONS)))
-    if x.dtype not in (torch.float16, torch.bfloat16) or weight.dtype != x.dtype:
+    dt = x.dtype
+    if dt == env.f32 or dt not in env.codes or weight.dtype != dt:
         raise TypeError("x and weight must share dtype float16 or bfloat16")
     rows, cols, ld = _rows(x, "x")
     wrows, wcols, wld = _weight(weight, "weight")
     if wcols != cols or wrows % 2:
         raise ValueError("weight must be (2 * hidden, %d), gate rows first" % cols)
-    return rows, cols, ld, wrows // 2, wld
+    return rows, cols, ld, wrows // 2, wld, code
 
 
 def matmul_gated(x, weight, act="silu", save=False, stream=None):
@@ -191,58 +228,70 @@ def matmul_gated(x, weight, act="silu", save=False, stream=None):
     fp32 sums x Wg^T and x Wu^T for matmul_gated_backward (in 16 bits their
     rounding would be as large as that of the gradients themselves).
     """
-    import torch
-    rows, cols, ld, hidden, wld = _gated_args(x, weight, act)
-    _one_gpu(x, weight)
-    with _on(x.device, stream) as st:
-        h = torch.empty(x.shape[:-1] + (hidden,), dtype=x.dtype, device=x.device)
-        gu = torch.empty(x.shape[:-1] + (2 * hidden,), dtype=torch.float32, device=x.device) if save else None
-        _check(_library().gemm_relu_gated(x.data_ptr(), ld, weight.data_ptr(), wld, h.data_ptr(),
-                                          gu.data_ptr() if save else None, rows, hidden, cols,
-                                          _codes()[x.dtype], ACTIVATIONS[act], st))
-    return (h, gu) if save else h
+    env = _get_env()
+    rows, cols, ld, hidden, wld, code = _gated_args(env, x, weight, act)
+    index = _one_gpu(x, weight)
+
+    def call(st):
+        device, lead = x.device, x.shape[:-1]
+        h = env.empty(lead + (hidden,), dtype=x.dtype, device=device)
+        gu = env.empty(lead + (2 * hidden,), dtype=env.f32, device=device) if save else None
+        _check(env.lib.gemm_relu_gated(x.data_ptr(), ld, weight.data_ptr(), wld, h.data_ptr(),
+                                       gu.data_ptr() if save else None, rows, hidden, cols,
+                                       env.codes[x.dtype], code, st))
+        return (h, gu) if save else h
+
+    return _launch(index, stream, (x, weight), call)
 
 
 def matmul_gated_backward(dh, gu, x, weight, act="silu", stream=None):
     """Gradients (dx, dweight) of matmul_gated, given dh and the forward call's
     gu.  Both have x's type."""
-    import torch
-    rows, cols, ld, hidden, wld = _gated_args(x, weight, act)
+    env = _get_env()
+    rows, cols, ld, hidden, wld, code = _gated_args(env, x, weight, act)
     if dh.dtype != x.dtype:
         raise TypeError("dh must have x's type")
     if dh.shape != x.shape[:-1] + (hidden,):
         raise ValueError("dh must have matmul_gated's shape %s" % (tuple(x.shape[:-1]) + (hidden,),))
     dh_ld = _rows(dh, "dh")[2]
-    _vector(gu, "gu", rows * 2 * hidden, (torch.float32,))
-    _one_gpu(x, weight, dh, gu)
-    lib = _library()
-    with _on(x.device, stream) as st:
-        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device)
-        dw = torch.empty(weight.shape, dtype=x.dtype, device=x.device)
-        ws = _workspace(lib.gemm_relu_gated_backward_workspace(rows, hidden, cols), x.device)
+    _vector(gu, "gu", rows * 2 * hidden, (env.f32,))
+    inputs = (x, weight, dh, gu)
+    index = _one_gpu(*inputs)
+
+    def call(st):
+        lib, device, dt = env.lib, x.device, x.dtype
+        dx = env.empty(x.shape, dtype=dt, device=device)
+        dw = env.empty(weight.shape, dtype=dt, device=device)
+        nbytes = lib.gemm_relu_gated_backward_workspace(rows, hidden, cols)
+        ws = env.empty(nbytes, dtype=env.torch.uint8, device=device)
         _check(lib.gemm_relu_gated_backward(
             dh.data_ptr(), dh_ld, gu.data_ptr(), x.data_ptr(), ld, weight.data_ptr(), wld, dx.data_ptr(),
-            dw.data_ptr(), rows, hidden, cols, _codes()[x.dtype], ACTIVATIONS[act], ws.data_ptr(),
-            ws.numel(), st))
-    return dx, dw
+            dw.data_ptr(), rows, hidden, cols, env.codes[dt], code, ws.data_ptr(), nbytes, st))
+        return dx, dw
+
+    return _launch(index, stream, inputs, call)
 
 
 def quantize_rows(x, stream=None):
     """Each row (last dimension) of x in 8 bits: returns (q, scale), int8 q of x's
     shape and fp32 scale = max|row| / 127, with row ~ q * scale.  A row that holds
     an infinity or NaN has scale NaN."""
-    import torch
-    codes = _codes()
-    if x.dtype not in codes:
+    env = _get_env()
+    code = env.codes.get(x.dtype)
+    if code is None:
         raise TypeError("x must be float16, bfloat16 or float32, not %s" % x.dtype)
     rows, cols, ld = _rows(x, "x")
-    _one_gpu(x)
-    with _on(x.device, stream) as st:
-        q = torch.empty(x.shape, dtype=torch.int8, device=x.device)
-        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-        _check(_library().gemm_relu_quantize_rows(x.data_ptr(), ld, q.data_ptr(), scale.data_ptr(), rows, cols,
-                                                  codes[x.dtype], st))
-    return q, scale
+    index = _one_gpu(x)
+
+    def call(st):
+        device = x.device
+        q = env.empty(x.shape, dtype=env.torch.int8, device=device)
+        scale = env.empty(x.shape[:-1], dtype=env.f32, device=device)
+        _check(env.lib.gemm_relu_quantize_rows(x.data_ptr(), ld, q.data_ptr(), scale.data_ptr(), rows, cols,
+                                               code, st))
+        return q, scale
+
+    return _launch(index, stream, (x,), call)
 
 
 def matmul_i8(x, x_scale, weight, weight_scale, out_dtype=None, stream=None):
@@ -252,22 +301,27 @@ def matmul_i8(x, x_scale, weight, weight_scale, out_dtype=None, stream=None):
     fp32 scale per row (output channel).  Sums are exact (k <= 131071).  Returns
     y (..., n) of out_dtype (float16, bfloat16 or float32; default bfloat16).
     """
-    import torch
-    codes = _codes()
+    env = _get_env()
+    torch = env.torch
     out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
     if x.dtype != torch.int8 or weight.dtype != torch.int8:
         raise TypeError("x and weight must be int8")
-    if out_dtype not in codes:
+    code = env.codes.get(out_dtype)
+    if code is None:
         raise TypeError("out_dtype must be float16, bfloat16 or float32, not %s" % out_dtype)
     rows, k, ld = _rows(x, "x")
     n, wk, wld = _weight(weight, "weight")
     if wk != k:
         raise ValueError("inner dimensions differ: %d vs %d" % (k, wk))
-    _vector(x_scale, "x_scale", rows, (torch.float32,))
-    _vector(weight_scale, "weight_scale", n, (torch.float32,))
-    _one_gpu(x, x_scale, weight, weight_scale)
-    with _on(x.device, stream) as st:
-        y = torch.empty(x.shape[:-1] + (n,), dtype=out_dtype, device=x.device)
-        _check(_library().gemm_relu_i8(x.data_ptr(), ld, x_scale.data_ptr(), weight.data_ptr(), wld,
-                                       weight_scale.data_ptr(), y.data_ptr(), rows, n, k, codes[out_dtype], st))
-    return y
+    _vector(x_scale, "x_scale", rows, (env.f32,))
+    _vector(weight_scale, "weight_scale", n, (env.f32,))
+    inputs = (x, x_scale, weight, weight_scale)
+    index = _one_gpu(*inputs)
+
+    def call(st):
+        y = env.empty(x.shape[:-1] + (n,), dtype=out_dtype, device=x.device)
+        _check(env.lib.gemm_relu_i8(x.data_ptr(), ld, x_scale.data_ptr(), weight.data_ptr(), wld,
+                                    weight_scale.data_ptr(), y.data_ptr(), rows, n, k, code, st))
+        return y
+
+    return _launch(index, stream, inputs, call)
