@@ -12,9 +12,12 @@ namespace gemm_relu_hip {
 
 // ---- matrix products (inst_ffn.hip)
 // The tiles of the GEMM + ReLU, with the epilogues of the feed-forward operators;
-// BK in a name counts 16-bit elements, as there.  LIN_32x64, LIN_64x32 and
-// LIN_SPLITK serve only products with B stored (K,N).
-enum LinearConfig : int { LIN_256 = 0, LIN_128, LIN_64, LIN_32x64, LIN_64x32, LIN_SPLITK, LIN_G64, LIN_COUNT };
+// The tiles of the GEMM + ReLU, with the epilogues of the feed-forward operators;
+// BK in a name counts 16-bit elements, as there.  LIN_128 has eight waves and a
+// CU to itself, LIN_128X2 four and half a CU, LIN_64 half a CU.  LIN_K16 and
+// LIN_K32 (ffn_skinny.hip: K cut between a workgroup's waves) serve only products
+// with B stored (N,K).
+enum LinearConfig : int { LIN_256 = 0, LIN_128, LIN_128X2, LIN_64, LIN_G64, LIN_K16, LIN_K32, LIN_COUNT };
 
 struct LinearInfo {
     const char* name;
@@ -24,19 +27,25 @@ struct LinearInfo {
 inline const LinearInfo& linear_info(int cfg)
 {
     static const LinearInfo table[LIN_COUNT] = {
-        {"d256x256x32_s4_i16w8", 256, 256}, {"d128x128x64_s3", 128, 128}, {"d64x64x64_s4", 64, 64},
-        {"d32x64x128_s4", 32, 64},          {"d64x32x128_s4", 64, 32},    {"d64x128x64_s4_splitk", 64, 128},
-        {"g64x64x64", 64, 64},
+        {"d256x256x32_s4_i16w8", 256, 256}, {"d128x128x64_s4_i16w8", 128, 128}, {"d128x128x64_s2", 128, 128},
+        {"d64x64x64_s4", 64, 64},           {"g64x64x64", 64, 64},              {"k16x16x64_s4", 16, 16},
+        {"k32x32x64_s4", 32, 32},
     };
     return table[cfg];
 }
-constexpr int kSplitkBK = 64;          // K elements per step of LIN_SPLITK
-constexpr int kSplitkFlagWords = 1024; // arrival counters at the start of its workspace
 
 typedef hipError_t (*LinearLaunchFn)(const KernelArgs& args, int grid, hipStream_t stream);
+// two products (either may be empty), B stored (K,N), of one configuration in one launch: `first` workgroups of a, then b's
+struct LinearPair {
+    KernelArgs a, b;
+    int first;
+};
+typedef hipError_t (*PairLaunchFn)(const LinearPair& pair, int grid, hipStream_t stream);
+PairLaunchFn launcher_cast_pair(int dt, int cfg);
 LinearLaunchFn launcher_gated(int dt, int cfg);                // B stored (N,K)
-LinearLaunchFn launcher_cast(int dt, int cfg);                 // B stored (K,N), C of type dt
 LinearLaunchFn launcher_i8(int out_dt, int cfg);               // B stored (N,K)
+LinearLaunchFn launcher_skinny_gated(int dt, int cfg);         // the LIN_K* forms of both
+LinearLaunchFn launcher_skinny_i8(int out_dt, int cfg);
 
 // ---- rows and element-wise work (ffn_rows.hip)
 struct NormArgs {
@@ -68,7 +77,6 @@ struct GatedGradArgs {
     int64_t dh_stride;
     int ld, ld_t;
     int rows, hidden, act;
-    unsigned* flags;        // kSplitkFlagWords words to clear, or null
 };
 hipError_t launch_gated_grad(const GatedGradArgs& a, int dt, hipStream_t stream);
 

@@ -70,66 +70,80 @@ int finish(hipError_t e, hipStream_t st)
 struct Linear {
     int64_t M, N, K, lda, ldb;
     bool trans;             // B stored (N,K); else (K,N)
-    bool split_ok = false;  // a workspace for a K split can be had
+    int bytes = 2;          // of an element of A and B
 };
 struct LinearPlan {
-    int cfg;
-    int64_t tiles_m, tiles_n;
-    int64_t splits = 1, split_steps = 0;
-    uint64_t split_bytes() const
-    {
-        return splits < 2 ? 0 : 4 * kSplitkFlagWords + uint64_t(splits * tiles_m * tiles_n) * 64 * 128 * 4;
-    }
+    int cfg = LIN_G64;
+    int64_t tiles_m = 0, tiles_n = 0;
 };
 
-// K split of a skinny product with B stored (K,N), as gemm_relu_ws takes it:
-// 64 x 128 tiles that fill at most half the CUs, each tile's K steps cut into
-// equal parts of at least 8 steps, enough to give every CU a part.
-bool plan_split(LinearPlan& p, const Linear& l)
+// Estimated times, in ns, from measurements of each configuration between 1 and
+// 14 rounds of workgroups, K from 250 to 16384 and 16-bit and 8-bit inputs (the
+// bytes of K count: what bounds the small tiles is the rate at which the L2 feeds
+// the copies, 11-12 TB/s, and the largest tile's matrix rate scales alike).
+struct TileTime {
+    double per_byte, fixed;   // of a tile, per byte of K and for its start and end
+    int slots;                // tiles in flight on the device
+    double alone;             // share of that time where a CU holds one of two possible tiles
+};
+TileTime tile_time(int cfg)
 {
-    const int64_t tiles = ceil_div(l.M, 64) * ceil_div(l.N, 128), steps = ceil_div(l.K, kSplitkBK);
-    if (!l.split_ok || l.trans || l.M > 64 || l.N < 128 || tiles * 2 > kNumCUs) return false;
-    const int64_t parts = std::min<int64_t>({16, kNumCUs / tiles, steps / 8});
-    if (parts < 2) return false;
-    p.cfg = LIN_SPLITK;
-    p.split_steps = ceil_div(steps, parts);
-    p.splits = ceil_div(steps, p.split_steps);
-    return p.splits >= 2;
+    switch (cfg) {
+    case LIN_256: return {12.0, 4000, kNumCUs, 1.0};
+    case LIN_128: return {4.6, 2500, kNumCUs, 1.0};
+    case LIN_128X2: return {9.0, 3500, 2 * kNumCUs, 0.72};
+    case LIN_64: return {5.2, 2000, 2 * kNumCUs, 0.55};
+    case LIN_K16: return {1.2, 1000, 2 * kNumCUs, 0.6};
+    case LIN_K32: return {1.4, 800, kNumCUs, 1.0};
+    default: return {15.0, 4000, 2 * kNumCUs, 0.6};      // LIN_G64
+    }
+}
+int64_t tiles_of(int cfg, const Linear& l)
+{
+    return ceil_div(l.M, linear_info(cfg).bm) * ceil_div(l.N, linear_info(cfg).bn);
+}
+double linear_time(int cfg, const Linear& l)
+{
+    const TileTime t = tile_time(cfg);
+    const double one = t.per_byte * double(l.K) * l.bytes + t.fixed;
+    const int64_t tiles = tiles_of(cfg, l), rest = tiles % t.slots;
+    return one * double(tiles / t.slots) + (rest == 0 ? 0.0 : rest <= kNumCUs ? t.alone * one : one);
 }
 
-LinearPlan plan_linear(const Linear& l)
+// Whether a configuration can take a product: the tiles' copies have 32-bit
+// offsets (256 rows of A, or of B stored (N,K), or a K step's rows of B stored
+// (K,N), whose last tile column ends at N); the LIN_K* forms have no such limit.
+bool usable(int cfg, const Linear& l)
+{
+    if (cfg == LIN_G64) return true;
+    if (cfg >= LIN_K16) return l.trans && l.K * l.bytes >= 16 && l.K * l.bytes <= (int64_t(1) << 30);
+    return l.lda <= (int64_t(1) << 22) && l.ldb <= (int64_t(1) << (l.trans ? 22 : 24)) &&
+           (l.trans || l.N >= linear_info(cfg).bn);
+}
+
+LinearPlan plan_as(int cfg, const Linear& l)
 {
     LinearPlan p;
-    auto tiles = [&](int cfg) { return ceil_div(l.M, linear_info(cfg).bm) * ceil_div(l.N, linear_info(cfg).bn); };
-    // 32-bit copy offsets: a tile spans 256 rows of A (of B stored (N,K)), or a
-    // K step's rows of B stored (K,N), whose last tile column ends at N
-    const bool direct = l.lda <= (int64_t(1) << 22) && l.ldb <= (int64_t(1) << (l.trans ? 22 : 24));
-    auto usable = [&](int cfg) { return direct && (l.trans || l.N >= linear_info(cfg).bn); };
-    // rounds of workgroups over the CUs, each the longer of the tile's matrix
-    // time and the time to stream its operands, as for the GEMM + ReLU
-    auto cost = [&](int cfg) {
-        const LinearInfo& t = linear_info(cfg);
-        const double eff = t.bm >= 256 ? 1.0 : t.bm >= 128 ? 0.57 : t.bn >= 64 ? 0.5 : 0.25;
-        return double(ceil_div(tiles(cfg), kNumCUs)) * std::max(t.bm * t.bn / eff, 98.0 * (t.bm + t.bn));
-    };
-    const bool skinny = l.M <= 64 && tiles(LIN_64) * 2 <= kNumCUs;
-    p.cfg = LIN_G64;
-    double best = 0.0;
-    for (int cfg : {LIN_256, LIN_128, LIN_64, LIN_32x64, LIN_64x32}) {
-        if (!usable(cfg) || (l.trans && cfg > LIN_64) || (cfg == LIN_32x64 && !skinny)) continue;
-        if (p.cfg == LIN_G64 || cost(cfg) < best) {
-            p.cfg = cfg;
-            best = cost(cfg);
-        }
-    }
-    if (direct) plan_split(p, l);
-    p.tiles_m = ceil_div(l.M, linear_info(p.cfg).bm);
-    p.tiles_n = ceil_div(l.N, linear_info(p.cfg).bn);
+    p.cfg = cfg;
+    p.tiles_m = ceil_div(l.M, linear_info(cfg).bm);
+    p.tiles_n = ceil_div(l.N, linear_info(cfg).bn);
     return p;
 }
 
+// The configuration of least estimated time; equal ones go to the smaller tile.
+LinearPlan plan_linear(const Linear& l)
+{
+    int best = LIN_G64;
+    for (int cfg : {LIN_K16, LIN_K32, LIN_64, LIN_128, LIN_128X2, LIN_256})
+        if (usable(cfg, l) && (best == LIN_G64 || linear_time(cfg, l) < linear_time(best, l))) best = cfg;
+    return plan_as(best, l);
+}
+
 // a launch's work-items stay below 2^32
-bool plan_fits(const LinearPlan& p) { return p.tiles_m * p.tiles_n * p.splits <= (int64_t(1) << 22); }
+bool plan_fits(const LinearPlan& p, const LinearPlan& q = {})
+{
+    return p.tiles_m * p.tiles_n + q.tiles_m * q.tiles_n <= (int64_t(1) << 22);
+}
 
 KernelArgs linear_args(const LinearPlan& p, const Linear& l, const void* A, const void* B, void* C)
 {
@@ -148,29 +162,48 @@ KernelArgs linear_args(const LinearPlan& p, const Linear& l, const void* A, cons
     a.nxcd = 8;
     return a;
 }
-int linear_grid(const LinearPlan& p) { return int(p.tiles_m * p.tiles_n * p.splits); }
+int linear_grid(const LinearPlan& p) { return int(p.tiles_m * p.tiles_n); }
 
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
 // The backward pass of the gated projections: dg and du go to the workspace
 // row-major (rows of 2 hidden) for dx, and transposed (rows of `rows`) for
-// dweight, each row padded to 16 bytes; a K split of dx follows.
+// dweight, each row padded to 16 bytes.  Both products share one launch, and so
+// one configuration: dx alone seldom fills the device.
 struct GradPlan {
     Linear lx, lw;
     LinearPlan x, w;            // of dx = dgu weight and of dweight = dgu^T x
-    uint64_t dgu_t, split, bytes;
+    uint64_t dgu_t, bytes;
 };
+double pair_time(int cfg, const Linear& a, const Linear& b)
+{
+    const TileTime t = tile_time(cfg);
+    const double one_a = t.per_byte * double(a.K) * a.bytes + t.fixed, one_b = t.per_byte * double(b.K) * b.bytes + t.fixed;
+    const int64_t na = tiles_of(cfg, a), nb = tiles_of(cfg, b);
+    const double alone = na + nb <= kNumCUs ? t.alone : 1.0;
+    return std::max((one_a * double(na) + one_b * double(nb)) / t.slots + 0.5 * std::min(one_a, one_b),
+                    alone * std::max(one_a, one_b));
+}
 GradPlan plan_grad(int64_t rows, int64_t hidden, int64_t cols, int64_t x_stride, int64_t weight_stride)
 {
     GradPlan g;
     const int64_t ld = round_up(2 * hidden, 8), ld_t = round_up(rows, 8);
-    g.lx = Linear{rows, cols, 2 * hidden, ld, weight_stride, false, rows > 0 && hidden > 0};
+    g.lx = Linear{rows, cols, 2 * hidden, ld, weight_stride, false};
     g.lw = Linear{2 * hidden, cols, rows, ld_t, x_stride, false};
-    g.x = plan_linear(g.lx);
-    g.w = plan_linear(g.lw);
+    int both = LIN_G64;
+    double best = 0.0;
+    for (int cfg : {LIN_64, LIN_128, LIN_128X2, LIN_256}) {
+        if (!usable(cfg, g.lx) || !usable(cfg, g.lw)) continue;
+        const double t = pair_time(cfg, g.lx, g.lw);
+        if (both == LIN_G64 || t < best) {
+            both = cfg;
+            best = t;
+        }
+    }
+    g.x = plan_as(both, g.lx);
+    g.w = plan_as(both, g.lw);
     g.dgu_t = uint64_t(round_up(2 * rows * ld, 256));
-    g.split = uint64_t(round_up(int64_t(g.dgu_t + uint64_t(2 * hidden) * uint64_t(ld_t) * 2), 256));
-    g.bytes = g.split + g.x.split_bytes();
+    g.bytes = g.dgu_t + uint64_t(2 * hidden) * uint64_t(ld_t) * 2;
     return g;
 }
 
@@ -305,13 +338,12 @@ extern "C" int gemm_relu_gated_backward(const void* dh, int64_t dh_stride, const
                      {dh, rows, hidden, dh_stride, 2}, dense(gu, rows, 2 * hidden, 4), {x, rows, cols, x_stride, 2},
                      {weight, 2 * hidden, cols, weight_stride, 2}};
     if (!mats_ok(m, 3) || !workspace_ok(workspace, workspace_bytes, p.bytes)) return GEMM_RELU_EINVAL;
-    if (!plan_fits(p.x) || !plan_fits(p.w) || p.lx.lda > kLim || p.lw.lda > kLim ||
+    if (!plan_fits(p.x, p.w) || p.lx.lda > kLim || p.lw.lda > kLim ||
         ceil_div(hidden, 64) * ceil_div(rows, 64) > (int64_t(1) << 23))
         return GEMM_RELU_EUNSUPPORTED;
     if (const int dev = check_device()) return dev;
     hipStream_t st = static_cast<hipStream_t>(stream);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
-    unsigned* flags = p.x.splits > 1 ? reinterpret_cast<unsigned*>(ws + p.split) : nullptr;
     hipError_t e = hipSuccess;
     if (rows > 0 && hidden > 0) {
         GatedGradArgs g{};
@@ -325,19 +357,15 @@ extern "C" int gemm_relu_gated_backward(const void* dh, int64_t dh_stride, const
         g.rows = int(rows);
         g.hidden = int(hidden);
         g.act = act;
-        g.flags = flags;
         e = launch_gated_grad(g, dtype, st);
     }
-    if (e == hipSuccess && rows > 0) {
-        KernelArgs a = linear_args(p.x, p.lx, ws, weight, dx);
-        a.flags = flags;
-        a.ws = flags ? reinterpret_cast<float*>(flags + kSplitkFlagWords) : nullptr;
-        a.splits = int(p.x.splits);
-        a.split_steps = int(p.x.split_steps);
-        e = launcher_cast(dtype, p.x.cfg)(a, linear_grid(p.x), st);
+    const KernelArgs gx = linear_args(p.x, p.lx, ws, weight, dx), gw = linear_args(p.w, p.lw, ws + p.dgu_t, x, dweight);
+    const int nx = rows > 0 ? linear_grid(p.x) : 0, nw = hidden > 0 ? linear_grid(p.w) : 0;
+    if (e == hipSuccess) {
+        // the product with the longer K first: its tiles take longest
+        const bool x_first = p.lx.K >= p.lw.K;
+        e = launcher_cast_pair(dtype, p.x.cfg)(x_first ? LinearPair{gx, gw, nx} : LinearPair{gw, gx, nw}, nx + nw, st);
     }
-    if (e == hipSuccess && hidden > 0)
-        e = launcher_cast(dtype, p.w.cfg)(linear_args(p.w, p.lw, ws + p.dgu_t, x, dweight), linear_grid(p.w), st);
     return finish(e, st);
 }
 
@@ -376,7 +404,7 @@ extern "C" int gemm_relu_i8(const void* x, int64_t x_stride, const float* x_scal
     const Mat m[] = {dense(y, rows, n, elem_bytes(out_dtype)), {x, rows, k, x_stride, 1}, {w, n, k, w_stride, 1},
                      dense(x_scale, rows, 1, 4), dense(w_scale, n, 1, 4)};
     if (!mats_ok(m, 1)) return GEMM_RELU_EINVAL;
-    const Linear l{rows, n, k, x_stride, w_stride, true};
+    const Linear l{rows, n, k, x_stride, w_stride, true, 1};
     const LinearPlan p = plan_linear(l);
     if (k > kMaxK8 || !plan_fits(p)) return GEMM_RELU_EUNSUPPORTED;
     if (const int dev = check_device()) return dev;
@@ -392,5 +420,5 @@ extern "C" const char* gemm_relu_i8_plan(int64_t rows, int64_t n, int64_t k, int
     if (!size_ok(rows) || !size_ok(n) || !size_ok(k) || !is_float(out_dtype)) return nullptr;
     if (rows == 0 || n == 0) return "none";
     if (k > kMaxK8) return "unsupported";
-    return linear_info(plan_linear(Linear{rows, n, k, k, k, true}).cfg).name;
+    return linear_info(plan_linear(Linear{rows, n, k, k, k, true, 1}).cfg).name;
 }

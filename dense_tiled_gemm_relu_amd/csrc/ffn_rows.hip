@@ -441,42 +441,89 @@ template <class W> __global__ void __launch_bounds__(1024) layer_norm_join_kerne
 }
 
 // --------------------------------------------- gradient of act(g) u
-// A 64 x 64 tile of (rows, hidden): dg and du go out row-major, and transposed
-// through LDS.
+// A 64 x 64 tile of (rows, hidden), 4 x 4 elements a thread with all loads issued
+// before the first is used: dg and du go out row-major, and transposed through
+// LDS.  Both outputs' rows are padded to 16 bytes with zeros, so that the
+// products may read them in whole pieces.
 template <int DT> __global__ void __launch_bounds__(kThreads) gated_grad_kernel(GatedGradArgs a)
 {
     using T = typename Elem<DT>::T;
-    __shared__ T tile[2][64][66];
+    typedef T T4 __attribute__((ext_vector_type(4)));
+    constexpr int PITCH = 68;                      // elements of a transposed row: 8-byte pieces on spread banks
+    __shared__ __attribute__((aligned(16))) T tile[2][64][PITCH];
     const int htiles = (a.hidden + 63) / 64;
     const int h0 = (int)(blockIdx.x % htiles) * 64, r0 = (int)(blockIdx.x / htiles) * 64;
-    const int c = threadIdx.x & 63, q = threadIdx.x >> 6;
-    if (a.flags && blockIdx.x == 0)
-        for (int k = threadIdx.x; k < kSplitkFlagWords; k += kThreads) a.flags[k] = 0u;
-    for (int k = q; k < 64; k += 4) {
-        const int r = r0 + k, h = h0 + c;
-        T dg = (T)0.0f, du = (T)0.0f;
-        if (r < a.rows && h < a.hidden) {
-            const float* gu = a.gu + (size_t)r * 2 * (size_t)a.hidden;
-            const float d = (float)static_cast<const T*>(a.dh)[(size_t)r * (size_t)a.dh_stride + h];
-            float value, slope;
-            activation_slope(gu[h], a.act, value, slope);
-            dg = (T)(d * gu[a.hidden + h] * slope);
-            du = (T)(d * value);
-            T* out = static_cast<T*>(a.dgu) + (size_t)r * (size_t)a.ld;
-            out[h] = dg;
-            out[a.hidden + h] = du;
+    const int c = (int)(threadIdx.x & 15) * 4, h = h0 + c, q = (int)(threadIdx.x >> 4) * 4;
+    const bool whole = h + 4 <= a.hidden;
+    f32x4_t g[4], u[4];
+    T4 d[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        g[k] = u[k] = f32x4_t{};
+        d[k] = T4{};
+        const int r = r0 + q + k;
+        if (r >= a.rows) continue;
+        const float* gu = a.gu + (size_t)r * 2 * (size_t)a.hidden + h;
+        const T* dh = static_cast<const T*>(a.dh) + (size_t)r * (size_t)a.dh_stride + h;
+        if (whole) {
+            g[k] = load_vec<f32x4_t>(gu);
+            u[k] = load_vec<f32x4_t>(gu + a.hidden);
+            d[k] = load_vec<T4>(dh);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (h + e < a.hidden) {
+                    g[k][e] = gu[e];
+                    u[k][e] = gu[a.hidden + e];
+                    d[k][e] = dh[e];
+                }
         }
-        tile[0][c][k] = dg;
-        tile[1][c][k] = du;
+    }
+    T4 dg[4], du[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float value, slope;
+            activation_slope(g[k][e], a.act, value, slope);
+            dg[k][e] = (T)((float)d[k][e] * u[k][e] * slope);
+            du[k][e] = (T)((float)d[k][e] * value);
+        }
+        const int r = r0 + q + k;
+        if (r >= a.rows) continue;
+        T* out = static_cast<T*>(a.dgu) + (size_t)r * (size_t)a.ld + h;
+        if (whole) {
+            __builtin_memcpy(out, &dg[k], 8);
+            __builtin_memcpy(out + a.hidden, &du[k], 8);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (h + e < a.hidden) {
+                    out[e] = dg[k][e];
+                    out[a.hidden + e] = du[k][e];
+                }
+        }
+        // the row's padding, by the thread behind its last tile column
+        if (h0 + 64 >= a.hidden && c == 60)
+            for (int j = 2 * a.hidden; j < a.ld; ++j) static_cast<T*>(a.dgu)[(size_t)r * (size_t)a.ld + j] = (T)0.0f;
+    }
+    // rows past the edge hold d = 0: their dg and du are the transposed padding
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const T4 x = {dg[0][e], dg[1][e], dg[2][e], dg[3][e]}, y = {du[0][e], du[1][e], du[2][e], du[3][e]};
+        *reinterpret_cast<T4*>(&tile[0][c + e][q]) = x;
+        *reinterpret_cast<T4*>(&tile[1][c + e][q]) = y;
     }
     __syncthreads();
-    for (int k = q; k < 64; k += 4) {
-        const int h = h0 + k, r = r0 + c;
-        if (r < a.rows && h < a.hidden) {
-            T* out = static_cast<T*>(a.dgu_t);
-            out[(size_t)h * (size_t)a.ld_t + r] = tile[0][k][c];
-            out[(size_t)(a.hidden + h) * (size_t)a.ld_t + r] = tile[1][k][c];
-        }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int p = k * kThreads + (int)threadIdx.x, half = p >> 9, hh = (p >> 3) & 63, rr = (p & 7) * 8;
+        if (h0 + hh >= a.hidden || r0 + rr >= a.rows) continue;
+        const T4* from = reinterpret_cast<const T4*>(&tile[half][hh][rr]);
+        T* out = static_cast<T*>(a.dgu_t) + ((size_t)(h0 + hh) + (half ? (size_t)a.hidden : 0)) * (size_t)a.ld_t + r0 + rr;
+        const T4 lo = from[0], hi = from[1];
+        __builtin_memcpy(out, &lo, 8);
+        __builtin_memcpy(out + 4, &hi, 8);
     }
 }
 

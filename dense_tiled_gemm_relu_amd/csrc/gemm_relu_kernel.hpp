@@ -51,7 +51,8 @@ enum : int { DT_I8 = 8 };   // signed 8-bit integers (EPI_I8 only), int32 accumu
 
 // What a tile does with its finished sums.  EPI_RELU: the fused GEMM + ReLU.
 // The others serve the feed-forward operators and take row strides of A and B:
-// EPI_CAST stores the rounded sums; EPI_GATED holds the sums g and u of a gate
+// EPI_CAST stores the rounded sums (A's rows are padded to lda, a multiple of 16
+// bytes, with zeros); EPI_GATED holds the sums g and u of a gate
 // and an up projection side by side and stores act(g) u; EPI_I8 multiplies
 // integer sums by a scale per row of A and a scale per row of B.
 enum : int { EPI_RELU = 0, EPI_CAST = 1, EPI_GATED = 2, EPI_I8 = 3 };
@@ -363,6 +364,17 @@ __device__ __forceinline__ void activation_slope(float g, int act, float& value,
         value = relu(g);
         slope = g > 0.0f ? 1.0f : 0.0f;
     }
+}
+
+// The first `zeros` bytes of a 16-byte chunk cleared.
+__device__ __forceinline__ u32x4_t clear_front(u32x4_t v, int zeros)
+{
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        const int n = zeros - 4 * d;
+        v[d] &= n >= 4 ? 0u : n > 0 ? ~0u << (8 * n) : ~0u;
+    }
+    return v;
 }
 
 // Four consecutive fp32 values of a row whose columns n .. end at N.
@@ -719,12 +731,21 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
     // loads with zero fill where it crosses the end of the row or the matrix,
     // then one 16 B LDS write per chunk.  The whole step of the register-staged
     // configurations; the K tail step of the direct ones.
+    constexpr bool MOVED_TAIL = C::EPI == EPI_GATED || C::EPI == EPI_I8;
     u32x4_t ra[APT], rb[BPT];
     auto load_chunk = [&](const unsigned char* base, size_t row_off, int e0, int e_lim,
                           bool row_ok) -> u32x4_t {
         // EPC consecutive elements e0 .. e0+EPC-1 of one row; valid if e < e_lim.
         u32x4_t v = {0u, 0u, 0u, 0u};
         if (!row_ok) return v;
+        // gated and integer products: a chunk across the end of K is read from 16
+        // bytes before the end, with what the previous chunk holds cleared, in
+        // both operands alike
+        if (MOVED_TAIL && e_lim >= EPC) {
+            const int from = min(e0, e_lim - EPC);
+            __builtin_memcpy(&v, base + row_off + (size_t)from * EB, 16);
+            return clear_front(v, min(e0 - from, EPC) * EB);
+        }
         if (e0 + EPC <= e_lim) {
             __builtin_memcpy(&v, base + row_off + (size_t)e0 * EB, 16);
         } else if constexpr (EB == 2) {
@@ -750,7 +771,8 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
     auto a_chunk = [&](int t, int q) -> u32x4_t {
         int r, c;
         krow_slot(q, r, c);
-        return load_chunk(args.A, (size_t)(m0 + r) * (size_t)lda * EB, t * BK + EPC * c, K, m0 + r < M);
+        return load_chunk(args.A, (size_t)(m0 + r) * (size_t)lda * EB, t * BK + EPC * c,
+                          C::EPI == EPI_CAST ? lda : K, m0 + r < M);
     };
     auto b_chunk = [&](int t, int q) -> u32x4_t {
         int r, c;
@@ -785,6 +807,13 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
         for (int i = 0; i < BPT; ++i)
             *reinterpret_cast<GR_LDS u32x4_t*>(sb + (i * C::NTHREADS + tid) * 16) = rb[i];
     };
+
+    // Feed-forward operators: the K tail of a direct configuration is loaded
+    // before the main loop where registers allow (all but the largest tile), all
+    // chunks at once otherwise, since at their sizes the loop is often short.
+    constexpr bool TAIL_EARLY = C::DIRECT && C::EPI != EPI_RELU && BM * BN < 256 * 256;
+    if constexpr (TAIL_EARLY)
+        if (K % BK != 0 && kt1 > K / BK) load_staged(kt0 + nk);
 
     // one chunk at a time (load, then LDS write): few live registers, for the
     // single K-tail step of the direct configurations
@@ -1372,7 +1401,12 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
             __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
             barrier_lds();
             if constexpr (C::MX) load_scales_tail(nk, sc_cur);
-            fill_staged(kt0 + nk, 0);
+            if constexpr (C::EPI == EPI_RELU) {
+                fill_staged(kt0 + nk, 0);
+            } else {
+                if (!TAIL_EARLY) load_staged(kt0 + nk);
+                store_staged(0);
+            }
             barrier_lds();
             read_frags(0, 0, fr[0]);
 #pragma unroll

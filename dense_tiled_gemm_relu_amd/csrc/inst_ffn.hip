@@ -9,8 +9,7 @@ namespace {
 template <class C> __global__ void __launch_bounds__(C::NTHREADS, 1) linear_kernel(KernelArgs args)
 {
     __shared__ __attribute__((aligned(1024))) unsigned char smem_raw[C::LDS_BYTES];
-    // a K split's workgroups take part blockIdx / tiles of tile blockIdx % tiles
-    gemm_relu_tile<C>(args, C::SPLITK ? (int)blockIdx.x % (args.tiles_m * args.tiles_n) : (int)blockIdx.x, (GR_LDS unsigned char*)(smem_raw), nullptr,
+    gemm_relu_tile<C>(args, (int)blockIdx.x, (GR_LDS unsigned char*)(smem_raw), nullptr,
                       Region{args.tiles_m, args.tiles_n, args.panel, 0});
 }
 
@@ -18,6 +17,22 @@ template <class C> hipError_t launch(const KernelArgs& args, int grid, hipStream
 {
     void* params[] = {const_cast<KernelArgs*>(&args)};
     return hipLaunchKernel(reinterpret_cast<const void*>(&linear_kernel<C>), dim3(grid), dim3(C::NTHREADS),
+                           params, 0, stream);
+}
+
+template <class C> __global__ void __launch_bounds__(C::NTHREADS, 1) linear_pair_kernel(LinearPair pair)
+{
+    __shared__ __attribute__((aligned(1024))) unsigned char smem_raw[C::LDS_BYTES];
+    const bool second = (int)blockIdx.x >= pair.first;
+    const KernelArgs& args = second ? pair.b : pair.a;
+    gemm_relu_tile<C>(args, (int)blockIdx.x - (second ? pair.first : 0), (GR_LDS unsigned char*)(smem_raw), nullptr,
+                      Region{args.tiles_m, args.tiles_n, args.panel, 0});
+}
+
+template <class C> hipError_t launch_pair(const LinearPair& pair, int grid, hipStream_t stream)
+{
+    void* params[] = {const_cast<LinearPair*>(&pair)};
+    return hipLaunchKernel(reinterpret_cast<const void*>(&linear_pair_kernel<C>), dim3(grid), dim3(C::NTHREADS),
                            params, 0, stream);
 }
 
@@ -33,7 +48,10 @@ template <int IN, int OUT, int EPI> struct LinearCfg<IN, OUT, EPI, LIN_256> {
     using type = Cfg<IN, OUT, nt<EPI>, 256, 256, bk<IN, 32>, 2, 4, 4, true, true, 16, false, false, false, EPI>;
 };
 template <int IN, int OUT, int EPI> struct LinearCfg<IN, OUT, EPI, LIN_128> {
-    using type = Cfg<IN, OUT, nt<EPI>, 128, 128, bk<IN, 64>, 2, 2, 3, true, false, mb<EPI>, false, false, false, EPI>;
+    using type = Cfg<IN, OUT, nt<EPI>, 128, 128, bk<IN, 64>, 2, 4, 4, true, true, 16, false, false, false, EPI>;
+};
+template <int IN, int OUT, int EPI> struct LinearCfg<IN, OUT, EPI, LIN_128X2> {
+    using type = Cfg<IN, OUT, nt<EPI>, 128, 128, bk<IN, 64>, 2, 2, 2, true, false, mb<EPI>, false, false, false, EPI>;
 };
 template <int IN, int OUT, int EPI> struct LinearCfg<IN, OUT, EPI, LIN_64> {
     using type = Cfg<IN, OUT, nt<EPI>, 64, 64, bk<IN, 64>, 2, 2, 4, true, false, mb<EPI>, false, false, false, EPI>;
@@ -41,54 +59,50 @@ template <int IN, int OUT, int EPI> struct LinearCfg<IN, OUT, EPI, LIN_64> {
 template <int IN, int OUT, int EPI> struct LinearCfg<IN, OUT, EPI, LIN_G64> {
     using type = Cfg<IN, OUT, nt<EPI>, 64, 64, bk<IN, 64>, 2, 2, 2, false, false, mb<EPI>, false, false, false, EPI>;
 };
-template <int IN, int OUT> struct LinearCfg<IN, OUT, EPI_CAST, LIN_32x64> {
-    using type = Cfg<IN, OUT, false, 32, 64, 128, 1, 2, 4, true, false, 32, false, false, false, EPI_CAST>;
-};
-template <int IN, int OUT> struct LinearCfg<IN, OUT, EPI_CAST, LIN_64x32> {
-    using type = Cfg<IN, OUT, false, 64, 32, 128, 2, 1, 4, true, false, 32, false, false, false, EPI_CAST>;
-};
-template <int IN, int OUT> struct LinearCfg<IN, OUT, EPI_CAST, LIN_SPLITK> {
-    using type = Cfg<IN, OUT, false, 64, 128, kSplitkBK, 2, 2, 4, true, false, 32, false, false, true, EPI_CAST>;
-};
-
 template <int IN, int OUT, int EPI> LinearLaunchFn pick(int cfg)
 {
     switch (cfg) {
     case LIN_256: return &launch<typename LinearCfg<IN, OUT, EPI, LIN_256>::type>;
     case LIN_128: return &launch<typename LinearCfg<IN, OUT, EPI, LIN_128>::type>;
+    case LIN_128X2: return &launch<typename LinearCfg<IN, OUT, EPI, LIN_128X2>::type>;
     case LIN_64: return &launch<typename LinearCfg<IN, OUT, EPI, LIN_64>::type>;
     case LIN_G64: return &launch<typename LinearCfg<IN, OUT, EPI, LIN_G64>::type>;
-    default: break;
+    default: return nullptr;
     }
-    if constexpr (EPI == EPI_CAST) {
-        switch (cfg) {
-        case LIN_32x64: return &launch<typename LinearCfg<IN, OUT, EPI, LIN_32x64>::type>;
-        case LIN_64x32: return &launch<typename LinearCfg<IN, OUT, EPI, LIN_64x32>::type>;
-        case LIN_SPLITK: return &launch<typename LinearCfg<IN, OUT, EPI, LIN_SPLITK>::type>;
-        default: break;
-        }
+}
+
+template <int DT> PairLaunchFn pick_pair(int cfg)
+{
+    switch (cfg) {
+    case LIN_256: return &launch_pair<typename LinearCfg<DT, DT, EPI_CAST, LIN_256>::type>;
+    case LIN_128: return &launch_pair<typename LinearCfg<DT, DT, EPI_CAST, LIN_128>::type>;
+    case LIN_128X2: return &launch_pair<typename LinearCfg<DT, DT, EPI_CAST, LIN_128X2>::type>;
+    case LIN_64: return &launch_pair<typename LinearCfg<DT, DT, EPI_CAST, LIN_64>::type>;
+    case LIN_G64: return &launch_pair<typename LinearCfg<DT, DT, EPI_CAST, LIN_G64>::type>;
+    default: return nullptr;
     }
-    return nullptr;
 }
 
 }  // namespace
 
 LinearLaunchFn launcher_gated(int dt, int cfg)
 {
+    if (cfg >= LIN_K16) return launcher_skinny_gated(dt, cfg);
     if (dt == DT_F16) return pick<DT_F16, DT_F16, EPI_GATED>(cfg);
     if (dt == DT_BF16) return pick<DT_BF16, DT_BF16, EPI_GATED>(cfg);
     return nullptr;
 }
 
-LinearLaunchFn launcher_cast(int dt, int cfg)
+PairLaunchFn launcher_cast_pair(int dt, int cfg)
 {
-    if (dt == DT_F16) return pick<DT_F16, DT_F16, EPI_CAST>(cfg);
-    if (dt == DT_BF16) return pick<DT_BF16, DT_BF16, EPI_CAST>(cfg);
+    if (dt == DT_F16) return pick_pair<DT_F16>(cfg);
+    if (dt == DT_BF16) return pick_pair<DT_BF16>(cfg);
     return nullptr;
 }
 
 LinearLaunchFn launcher_i8(int out_dt, int cfg)
 {
+    if (cfg >= LIN_K16) return launcher_skinny_i8(out_dt, cfg);
     if (out_dt == DT_F16) return pick<DT_I8, DT_F16, EPI_I8>(cfg);
     if (out_dt == DT_BF16) return pick<DT_I8, DT_BF16, EPI_I8>(cfg);
     if (out_dt == DT_F32) return pick<DT_I8, DT_F32, EPI_I8>(cfg);

@@ -51,7 +51,7 @@ class _Env:
         from . import library
         self.codes = {torch.float16: 0, torch.bfloat16: 1, torch.float32: 2}
         self.torch, self.lib = torch, library()
-        self.empty, self.f32 = torch.empty, torch.float32
+        self.empty_like, self.f32, self.i8, self.u8 = torch.empty_like, torch.float32, torch.int8, torch.uint8
         self.current_device = torch._C._cuda_getDevice
         self.raw_stream = torch._C._cuda_getCurrentRawStream
 
@@ -115,20 +115,17 @@ def _one_gpu(*tensors):
     return index
 
 
-def _launch(index, stream, inputs, call):
-    """call(raw stream) with GPU `index` and the stream current for its
-    allocations and its launch."""
-    env = _get_env()
-    if stream is None and env.current_device() == index:
-        return call(env.raw_stream(index))
-    cuda = env.torch.cuda
+def _elsewhere(index, stream, inputs, fn, *args):
+    """fn(*args) with GPU `index` and `stream` current, for its allocations and
+    its launches."""
+    cuda = _get_env().torch.cuda
     with cuda.device(index):
         if stream is None:
-            return call(env.raw_stream(index))
+            return fn(*args)
         if isinstance(stream, int):
             stream = cuda.ExternalStream(stream, device=index)
         with cuda.stream(stream):
-            out = call(stream.cuda_stream)
+            out = fn(*args)
         # the caller may drop an input while the stream still reads it
         for t in inputs:
             t.record_stream(stream)
@@ -155,20 +152,17 @@ def layer_norm(x, weight, bias=None, eps=1e-5, stats=False, stream=None):
         _vector(bias, "bias", cols, (wdt,))
         inputs = (x, weight, bias)
     index = _one_gpu(*inputs)
-
-    def call(st):
-        device = x.device
-        y = env.empty(x.shape, dtype=dt, device=device)
-        mean = rstd = None
-        if stats:
-            mean, rstd = (env.empty(x.shape[:-1], dtype=env.f32, device=device) for _ in range(2))
-        _check(env.lib.gemm_relu_layer_norm(
-            x.data_ptr(), ld, weight.data_ptr(), None if bias is None else bias.data_ptr(), y.data_ptr(),
-            mean.data_ptr() if stats else None, rstd.data_ptr() if stats else None, rows, cols,
-            codes[dt], codes[wdt], eps, st))
-        return (y, mean, rstd) if stats else y
-
-    return _launch(index, stream, inputs, call)
+    if stream is not None or env.current_device() != index:
+        return _elsewhere(index, stream, inputs, layer_norm, x, weight, bias, eps, stats)
+    y = env.empty_like(x) if ld == cols else x.new_empty(x.shape)
+    mean = rstd = None
+    if stats:
+        mean, rstd = x.new_empty((2,) + x.shape[:-1], dtype=env.f32).unbind(0)
+    _check(env.lib.gemm_relu_layer_norm(
+        x.data_ptr(), ld, weight.data_ptr(), None if bias is None else bias.data_ptr(), y.data_ptr(),
+        mean.data_ptr() if stats else None, rstd.data_ptr() if stats else None, rows, cols,
+        codes[dt], codes[wdt], eps, env.raw_stream(index)))
+    return (y, mean, rstd) if stats else y
 
 
 def layer_norm_backward(dy, x, weight, mean, rstd, stream=None):
@@ -189,20 +183,18 @@ def layer_norm_backward(dy, x, weight, mean, rstd, stream=None):
     _vector(rstd, "rstd", rows, (f32,))
     inputs = (x, dy, weight, mean, rstd)
     index = _one_gpu(*inputs)
-
-    def call(st):
-        lib, device, wdt = env.lib, x.device, weight.dtype
-        dx = env.empty(x.shape, dtype=dt, device=device)
-        dw, db = (env.empty(weight.shape, dtype=wdt, device=device) for _ in range(2))
-        nbytes = lib.gemm_relu_layer_norm_backward_workspace(rows, cols)
-        ws = env.empty(nbytes, dtype=env.torch.uint8, device=device)
-        _check(lib.gemm_relu_layer_norm_backward(
-            dy.data_ptr(), dy_ld, x.data_ptr(), ld, weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
-            dx.data_ptr(), dw.data_ptr(), db.data_ptr(), rows, cols, codes[dt], codes[wdt],
-            ws.data_ptr(), nbytes, st))
-        return dx, dw, db
-
-    return _launch(index, stream, inputs, call)
+    if stream is not None or env.current_device() != index:
+        return _elsewhere(index, stream, inputs, layer_norm_backward, dy, x, weight, mean, rstd)
+    lib = env.lib
+    dx = env.empty_like(x) if ld == cols else x.new_empty(x.shape)
+    dw, db = weight.new_empty((2,) + weight.shape).unbind(0)
+    nbytes = lib.gemm_relu_layer_norm_backward_workspace(rows, cols)
+    ws = x.new_empty(nbytes, dtype=env.u8)
+    _check(lib.gemm_relu_layer_norm_backward(
+        dy.data_ptr(), dy_ld, x.data_ptr(), ld, weight.data_ptr(), mean.data_ptr(), rstd.data_ptr(),
+        dx.data_ptr(), dw.data_ptr(), db.data_ptr(), rows, cols, codes[dt], codes[weight.dtype],
+        ws.data_ptr(), nbytes, env.raw_stream(index)))
+    return dx, dw, db
 
 
 def _gated_args(env, x, weight, act):
@@ -231,17 +223,15 @@ def matmul_gated(x, weight, act="silu", save=False, stream=None):
     env = _get_env()
     rows, cols, ld, hidden, wld, code = _gated_args(env, x, weight, act)
     index = _one_gpu(x, weight)
-
-    def call(st):
-        device, lead = x.device, x.shape[:-1]
-        h = env.empty(lead + (hidden,), dtype=x.dtype, device=device)
-        gu = env.empty(lead + (2 * hidden,), dtype=env.f32, device=device) if save else None
-        _check(env.lib.gemm_relu_gated(x.data_ptr(), ld, weight.data_ptr(), wld, h.data_ptr(),
-                                       gu.data_ptr() if save else None, rows, hidden, cols,
-                                       env.codes[x.dtype], code, st))
-        return (h, gu) if save else h
-
-    return _launch(index, stream, (x, weight), call)
+    if stream is not None or env.current_device() != index:
+        return _elsewhere(index, stream, (x, weight), matmul_gated, x, weight, act, save)
+    lead = x.shape[:-1]
+    h = x.new_empty(lead + (hidden,))
+    gu = x.new_empty(lead + (2 * hidden,), dtype=env.f32) if save else None
+    _check(env.lib.gemm_relu_gated(x.data_ptr(), ld, weight.data_ptr(), wld, h.data_ptr(),
+                                   gu.data_ptr() if save else None, rows, hidden, cols, env.codes[x.dtype],
+                                   code, env.raw_stream(index)))
+    return (h, gu) if save else h
 
 
 def matmul_gated_backward(dh, gu, x, weight, act="silu", stream=None):
@@ -257,19 +247,18 @@ def matmul_gated_backward(dh, gu, x, weight, act="silu", stream=None):
     _vector(gu, "gu", rows * 2 * hidden, (env.f32,))
     inputs = (x, weight, dh, gu)
     index = _one_gpu(*inputs)
-
-    def call(st):
-        lib, device, dt = env.lib, x.device, x.dtype
-        dx = env.empty(x.shape, dtype=dt, device=device)
-        dw = env.empty(weight.shape, dtype=dt, device=device)
-        nbytes = lib.gemm_relu_gated_backward_workspace(rows, hidden, cols)
-        ws = env.empty(nbytes, dtype=env.torch.uint8, device=device)
-        _check(lib.gemm_relu_gated_backward(
-            dh.data_ptr(), dh_ld, gu.data_ptr(), x.data_ptr(), ld, weight.data_ptr(), wld, dx.data_ptr(),
-            dw.data_ptr(), rows, hidden, cols, env.codes[dt], code, ws.data_ptr(), nbytes, st))
-        return dx, dw
-
-    return _launch(index, stream, inputs, call)
+    if stream is not None or env.current_device() != index:
+        return _elsewhere(index, stream, inputs, matmul_gated_backward, dh, gu, x, weight, act)
+    lib = env.lib
+    dx = env.empty_like(x) if ld == cols else x.new_empty(x.shape)
+    dw = env.empty_like(weight) if wld == cols else weight.new_empty(weight.shape)
+    nbytes = lib.gemm_relu_gated_backward_workspace(rows, hidden, cols)
+    ws = x.new_empty(nbytes, dtype=env.u8)
+    _check(lib.gemm_relu_gated_backward(
+        dh.data_ptr(), dh_ld, gu.data_ptr(), x.data_ptr(), ld, weight.data_ptr(), wld, dx.data_ptr(),
+        dw.data_ptr(), rows, hidden, cols, env.codes[x.dtype], code, ws.data_ptr(), nbytes,
+        env.raw_stream(index)))
+    return dx, dw
 
 
 def quantize_rows(x, stream=None):
@@ -282,16 +271,13 @@ def quantize_rows(x, stream=None):
         raise TypeError("x must be float16, bfloat16 or float32, not %s" % x.dtype)
     rows, cols, ld = _rows(x, "x")
     index = _one_gpu(x)
-
-    def call(st):
-        device = x.device
-        q = env.empty(x.shape, dtype=env.torch.int8, device=device)
-        scale = env.empty(x.shape[:-1], dtype=env.f32, device=device)
-        _check(env.lib.gemm_relu_quantize_rows(x.data_ptr(), ld, q.data_ptr(), scale.data_ptr(), rows, cols,
-                                               code, st))
-        return q, scale
-
-    return _launch(index, stream, (x,), call)
+    if stream is not None or env.current_device() != index:
+        return _elsewhere(index, stream, (x,), quantize_rows, x)
+    q = x.new_empty(x.shape, dtype=env.i8)
+    scale = x.new_empty(x.shape[:-1], dtype=env.f32)
+    _check(env.lib.gemm_relu_quantize_rows(x.data_ptr(), ld, q.data_ptr(), scale.data_ptr(), rows, cols, code,
+                                           env.raw_stream(index)))
+    return q, scale
 
 
 def matmul_i8(x, x_scale, weight, weight_scale, out_dtype=None, stream=None):
@@ -302,9 +288,8 @@ def matmul_i8(x, x_scale, weight, weight_scale, out_dtype=None, stream=None):
     y (..., n) of out_dtype (float16, bfloat16 or float32; default bfloat16).
     """
     env = _get_env()
-    torch = env.torch
-    out_dtype = torch.bfloat16 if out_dtype is None else out_dtype
-    if x.dtype != torch.int8 or weight.dtype != torch.int8:
+    out_dtype = env.torch.bfloat16 if out_dtype is None else out_dtype
+    if x.dtype != env.i8 or weight.dtype != env.i8:
         raise TypeError("x and weight must be int8")
     code = env.codes.get(out_dtype)
     if code is None:
@@ -317,11 +302,9 @@ def matmul_i8(x, x_scale, weight, weight_scale, out_dtype=None, stream=None):
     _vector(weight_scale, "weight_scale", n, (env.f32,))
     inputs = (x, x_scale, weight, weight_scale)
     index = _one_gpu(*inputs)
-
-    def call(st):
-        y = env.empty(x.shape[:-1] + (n,), dtype=out_dtype, device=x.device)
-        _check(env.lib.gemm_relu_i8(x.data_ptr(), ld, x_scale.data_ptr(), weight.data_ptr(), wld,
-                                    weight_scale.data_ptr(), y.data_ptr(), rows, n, k, code, st))
-        return y
-
-    return _launch(index, stream, inputs, call)
+    if stream is not None or env.current_device() != index:
+        return _elsewhere(index, stream, inputs, matmul_i8, x, x_scale, weight, weight_scale, out_dtype)
+    y = x.new_empty(x.shape[:-1] + (n,), dtype=out_dtype)
+    _check(env.lib.gemm_relu_i8(x.data_ptr(), ld, x_scale.data_ptr(), weight.data_ptr(), wld,
+                                weight_scale.data_ptr(), y.data_ptr(), rows, n, k, code, env.raw_stream(index)))
+    return y
