@@ -2,15 +2,19 @@
 
 * ``libgemm_relu.so``       — the product: the C-ABI of include/gemm_relu.h and of
                               include/gemm_relu_ffn.h;
+* ``_ffn.so``              — the tensor front end of include/gemm_relu_ffn.h, a
+                              CPython module (host code) on torch's tensors;
 * ``libgemm_relu_probe.so`` — test-only lane-layout probes and the MFMA-rate
   diagnostic (MFMA-only throughput on random operands).
 
 Objects go to ``_build/`` at the repository root; the libraries are written
 next to this file, where the Python binding loads them.
 """
+import importlib.util
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -22,6 +26,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 LIB = os.path.join(PKG, "libgemm_relu.so")
 PROBE_LIB = os.path.join(PKG, "libgemm_relu_probe.so")
+FFN_MODULE = os.path.join(PKG, "_ffn.so")
 
 LIB_SOURCES = ["gemm_relu_api.hip", "inst_f16_nn.hip", "inst_f16_nt.hip",
                "inst_bf16_nn.hip", "inst_bf16_nt.hip", "inst_f8e4m3_nn.hip",
@@ -92,13 +97,35 @@ def _link(objs, out, verbose):
     os.replace(tmp, out)
 
 
+def _front_end(force, verbose):
+    """The CPython module: host code only, so the host compiler builds it."""
+    src = os.path.join(CSRC, "ffn_torch.cpp")
+    if not force and not _newer(FFN_MODULE, [src, os.path.join(INCLUDE, "gemm_relu_ffn.h")]):
+        return
+    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
+    inc, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
+    tmp = FFN_MODULE + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden", "-I", INCLUDE,
+           "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], src, "-o", tmp, "-L", lib, "-lc10", "-ltorch_cpu",
+           "-ltorch_python"]
+    if verbose:
+        print(" ".join(cmd), flush=True)
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("g++ failed for %s:\n%s" % (src, r.stderr[-4000:]))
+    os.replace(tmp, FFN_MODULE)
+
+
 def build(force=True, verbose=False, jobs=None):
-    """Compile and link both libraries.  force=False skips up-to-date objects."""
+    """Compile and link the libraries and the front end.  force=False skips up-to-date objects."""
     os.makedirs(BUILD, exist_ok=True)
     jobs = jobs or min(8, os.cpu_count() or 1)
     srcs = LIB_SOURCES + PROBE_SOURCES
     with ThreadPoolExecutor(max_workers=jobs) as ex:
+        front = ex.submit(_front_end, force, verbose)
         objs = dict(zip(srcs, ex.map(lambda s: _compile(s, force, verbose), srcs)))
+        front.result()
     _link([objs[s] for s in LIB_SOURCES], LIB, verbose)
     _link([objs[s] for s in PROBE_SOURCES], PROBE_LIB, verbose)
     return LIB, PROBE_LIB
