@@ -10,6 +10,18 @@
 
 namespace gemm_relu_hip {
 
+// 1 KiB, 16 bytes a lane from any address, to LDS bytes lds .. lds + 1023 in lane
+// order; no register holds it on the way, so it is waited for with vmcnt.
+__device__ __forceinline__ void copy_to_lds(const unsigned char* from, uint32_t lds)
+{
+    asm volatile("s_mov_b32 m0, %1\n\t"
+                 "s_nop 0\n\t"
+                 "global_load_lds_dwordx4 %0, off"
+                 :
+                 : "v"(from), "s"(lds)
+                 : "memory", "m0");
+}
+
 // ---- matrix products (inst_ffn.hip)
 // The tiles of the GEMM + ReLU, with the epilogues of the feed-forward operators;
 // The tiles of the GEMM + ReLU, with the epilogues of the feed-forward operators;

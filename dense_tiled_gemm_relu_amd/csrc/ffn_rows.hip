@@ -12,7 +12,6 @@ namespace gemm_relu_hip {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kForwardGroups = 256 * 2048;   // threads of a row kernel at most: a full device
 
 template <int DT> struct Elem;
 template <> struct Elem<DT_F16> {
@@ -38,6 +37,14 @@ struct Sum {
 struct Max {
     static __device__ __forceinline__ unsigned of(unsigned a, unsigned b) { return a > b ? a : b; }
 };
+// ... over the 16 lanes of a row
+__device__ __forceinline__ float row16_sum(float v)
+{
+    v += __builtin_bit_cast(float, dpp<0xB1>(__builtin_bit_cast(unsigned, v)));
+    v += __builtin_bit_cast(float, dpp<0x4E>(__builtin_bit_cast(unsigned, v)));
+    v += __builtin_bit_cast(float, dpp<0x141>(__builtin_bit_cast(unsigned, v)));
+    return v + __builtin_bit_cast(float, dpp<0x140>(__builtin_bit_cast(unsigned, v)));
+}
 template <class F, class T> __device__ __forceinline__ T wave_all(T v)
 {
     auto bits = [](T x) { return __builtin_bit_cast(unsigned, x); };
@@ -97,15 +104,15 @@ template <class V> __device__ __forceinline__ void stay_packed(V& v)
     for (unsigned k = 0; k < sizeof(V) / 16; ++k) asm volatile("" : "+v"(words[k]));
 }
 
-template <class T, int G, int V> struct RowMap {
+template <class T, int V> struct RowMap {
     static constexpr int N = Chunk<T>::N;
     int start[V], skip;      // first column of each chunk; elements of the last one that the neighbour owns
     bool last;               // whether the last chunk exists
-    __device__ __forceinline__ RowMap(int cols)
+    // thread t of the g that share the row
+    __device__ __forceinline__ RowMap(int cols, int t, int g)
     {
-        const int t = (int)threadIdx.x % G;
 #pragma unroll
-        for (int v = 0; v < V; ++v) start[v] = (v * G + t) * N;
+        for (int v = 0; v < V; ++v) start[v] = (v * g + t) * N;
         const int j = start[V - 1];
         last = j < cols;
         start[V - 1] = min(j, cols - N);
@@ -135,7 +142,7 @@ template <class T, class W, int G, int V> __global__ void __launch_bounds__(kGro
     using X = typename Chunk<T>::Vec;
     using WV = typename VecN<W, N>::Vec;
     __shared__ float lds[2][G / 64];
-    const RowMap<T, G, V> map(a.cols);
+    const RowMap<T, V> map(a.cols, (int)threadIdx.x % G, G);
     WV w[V], b[V];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -196,118 +203,139 @@ template <class T, class W, int G, int V> __global__ void __launch_bounds__(kGro
 }
 
 // The backward pass in one read of dy and x: the row's two sums and dx, and the
-// thread's columns of dweight and dbias, summed in registers over the rows of
-// the group.  A workgroup leaves one strip of partial sums; a second kernel
-// joins the strips in order.
-template <class T, class W, int G, int V>
-__global__ void __launch_bounds__(kGroupThreads<G>) __attribute__((amdgpu_waves_per_eu(4)))
+// thread's columns of dweight and dbias, summed in registers over its rows.  A
+// workgroup leaves one strip of partial sums; a second kernel joins the strips in
+// order.  WAVES = 1: four rows a workgroup, one wave each; else the workgroup, of
+// as many waves as the row has chunks for, at most WAVES, takes one row at a time.
+//
+// A row takes a trip to memory, two sums over the group and a store, and a CU
+// holds few rows at a time (the sums fill its registers), so the rows to come are
+// copied ahead into LDS, RING of them: each lane's own 16 bytes, which no other
+// lane reads, so the only wait is the wave's own.  What is left is the vector
+// instructions: about 13 an element.
+template <class T, class W, int WAVES, int V>
+__global__ void __launch_bounds__(WAVES == 1 ? kThreads : 64 * WAVES) __attribute__((amdgpu_waves_per_eu(4)))
 layer_norm_backward_kernel(NormArgs a)
 {
     constexpr int N = Chunk<T>::N;
+    constexpr bool ONE = WAVES == 1;
     using X = typename Chunk<T>::Vec;
     using WV = typename VecN<W, N>::Vec;
-    __shared__ float lds[2][2][G / 64];
-    __shared__ __attribute__((aligned(16))) float part[G == 64 ? 3 * 64 * N * V : 1];
-    const RowMap<T, G, V> map(a.cols);
+    constexpr int RING = V == 1 ? 4 : 2, ROW_BYTES = 2 * V * 1024;       // of a wave
+    constexpr int RINGS = ONE ? kThreads / 64 : WAVES;
+    __shared__ __attribute__((aligned(1024))) unsigned char rows_raw[RINGS * RING * ROW_BYTES];
+    __shared__ float lds[2][2][16];
+    static_assert(!ONE || 3 * 64 * N * V * 4 <= RINGS * RING * ROW_BYTES, "the waves' sums fit the rings");
+    const int lane = (int)(threadIdx.x & 63), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const RowMap<T, V> map(a.cols, ONE ? lane : (int)threadIdx.x, ONE ? 64 : (int)blockDim.x);
     WV w[V];
     float dw[V][N], db[V][N];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        w[v] = WV{};
-        if (map.has(v)) w[v] = load_vec<WV>(static_cast<const W*>(a.w) + map.start[v]);
+        w[v] = load_vec<WV>(static_cast<const W*>(a.w) + map.start[v]);
 #pragma unroll
         for (int e = 0; e < N; ++e) dw[v][e] = db[v][e] = 0.0f;
     }
-    const int step = (int)gridDim.x * kGroups<G>;
-    int64_t row = group_index<G>();          // 64 bits: the last row's successor may pass 2^31
-    X nx[V], nd[V];
-    float nmean = 0.0f, nrstd = 0.0f;
-    auto fetch = [&](int64_t r) {
-        const T* x = static_cast<const T*>(a.x) + (size_t)r * (size_t)a.x_stride;
-        const T* d = static_cast<const T*>(a.dy) + (size_t)r * (size_t)a.dy_stride;
+    // sums of waves that are not there
+    if (!ONE && threadIdx.x < 64) lds[threadIdx.x >> 5][(threadIdx.x >> 4) & 1][threadIdx.x & 15] = 0.0f;
+    const int64_t step = (int64_t)gridDim.x * (ONE ? RINGS : 1);
+    int64_t row = ONE ? (int64_t)blockIdx.x * RINGS + wave : (int64_t)blockIdx.x;
+    GR_LDS unsigned char* const ring = (GR_LDS unsigned char*)rows_raw + wave * RING * ROW_BYTES;
+    // row r (the last one in place of those past it) to a slot; a missing chunk is
+    // the row's last
+    auto fetch = [&](int64_t r, int slot) {
+        const size_t at = (size_t)min(r, (int64_t)a.rows - 1);
+        const T* x = static_cast<const T*>(a.x) + at * (size_t)a.x_stride;
+        const T* d = static_cast<const T*>(a.dy) + at * (size_t)a.dy_stride;
+        const uint32_t to = lds_addr(ring) + slot * ROW_BYTES;
 #pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (map.has(v)) {
-                nx[v] = load_vec<X>(x + map.start[v]);
-                nd[v] = load_vec<X>(d + map.start[v]);
-            }
-        nmean = a.mean[r];
-        nrstd = a.rstd[r];
+        for (int v = 0; v < V; ++v) {
+            copy_to_lds(reinterpret_cast<const unsigned char*>(x + map.start[v]), to + 2 * v * 1024);
+            copy_to_lds(reinterpret_cast<const unsigned char*>(d + map.start[v]), to + (2 * v + 1) * 1024);
+        }
     };
 #pragma unroll
-    for (int v = 0; v < V; ++v) nx[v] = nd[v] = X{};
-    if (row < a.rows) fetch(row);
-    const float n = (float)a.cols;
+    for (int k = 0; k < RING; ++k) fetch(row + k * step, k);
+    // the weight has arrived here, so that no load but the copies is waited for below
+#pragma unroll
+    for (int v = 0; v < V; ++v) stay_packed(w[v]);
+    if (!ONE) __syncthreads();
+    const float inv_n = 1.0f / (float)a.cols;
+    // one value for the whole wave: read through the scalar cache
+    typedef const __attribute__((address_space(4))) float* Scalars;
+    const Scalars means = (Scalars)(uintptr_t)a.mean, rstds = (Scalars)(uintptr_t)a.rstd;
+    int slot = 0;
     for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
+        const float mean = means[row], rstd = rstds[row];
+        // behind this row's copies are those of RING - 1 rows; the stores between
+        // them only make the wait stricter
+        __builtin_amdgcn_s_waitcnt(waitcnt_vm((RING - 1) * 2 * V));
+        asm volatile("" ::: "memory");
         X x[V], d[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            x[v] = nx[v];
-            d[v] = nd[v];
+            const GR_LDS unsigned char* from = ring + slot * ROW_BYTES + 2 * v * 1024 + lane * 16;
+            x[v] = __builtin_bit_cast(X, lds_read_b128(from));
+            d[v] = __builtin_bit_cast(X, lds_read_b128(from + 1024));
+            stay_packed(x[v]);
+            stay_packed(d[v]);
+            if (V > 1) stay_packed(w[v]);
         }
-        const float mean = nmean, rstd = nrstd;
-#pragma unroll
-        for (int v = 0; v < V; ++v) stay_packed(w[v]);
-        if (row < a.rows - step) fetch(row + step);
-        float s0 = 0.0f, s1 = 0.0f;
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");      // read, so the slot is free
+        fetch(row + RING * step, slot);
+        slot = slot == RING - 1 ? 0 : slot + 1;
+        // c = dy weight: s0 = sum c, s1 = sum c xhat.  Elements that the neighbour
+        // owns count in its sums only (and its columns: these are not stored).
+        float s0 = 0.0f, s1 = 0.0f, xhat[V][N], c[V][N];
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                const float xhat = ((float)x[v][e] - mean) * rstd;
-                // a missing chunk's x counts as 0 too, so that 0 times it stays 0
-                const float g = map.owns(v, e) ? (float)d[v][e] : 0.0f, gx = map.owns(v, e) ? g * xhat : 0.0f;
+                const float g = (float)d[v][e];
+                xhat[v][e] = ((float)x[v][e] - mean) * rstd;
+                c[v][e] = g * (float)w[v][e];
+                dw[v][e] = fmaf(g, xhat[v][e], dw[v][e]);
                 db[v][e] += g;
-                dw[v][e] += gx;
-                s0 += g * (float)w[v][e];
-                s1 += gx * (float)w[v][e];
+                const float own = map.owns(v, e) ? c[v][e] : 0.0f;
+                s0 += own;
+                s1 = fmaf(own, map.owns(v, e) ? xhat[v][e] : 0.0f, s1);
             }
-        if constexpr (G == 64) {
-            s0 = wave_all<Sum>(s0);
-            s1 = wave_all<Sum>(s1);
-        } else {
-            s0 = wave_all<Sum>(s0);
-            s1 = wave_all<Sum>(s1);
-            float(*l)[G / 64] = lds[turn];
-            if ((threadIdx.x & 63) == 0) {
-                l[0][threadIdx.x >> 6] = s0;
-                l[1][threadIdx.x >> 6] = s1;
-            }
+        // both sums at once: s0 in the lower half of the wave, s1 in the upper
+        const auto p = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, s0), __builtin_bit_cast(unsigned, s1),
+                                                        false, false);
+        float s = __builtin_bit_cast(float, (unsigned)p[0]) + __builtin_bit_cast(float, (unsigned)p[1]);
+        const auto q = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, s), __builtin_bit_cast(unsigned, s),
+                                                        false, false);
+        s = row16_sum(__builtin_bit_cast(float, (unsigned)q[0]) + __builtin_bit_cast(float, (unsigned)q[1]));
+        if constexpr (!ONE) {
+            // lane 0 and lane 32 hold the wave's; 16 lanes each add the waves'
+            if ((lane & 31) == 0) lds[turn][lane >> 5][wave] = s;
             __syncthreads();
-            s0 = l[0][0];
-            s1 = l[1][0];
-#pragma unroll
-            for (int k = 1; k < G / 64; ++k) {
-                s0 += l[0][k];
-                s1 += l[1][k];
-            }
+            s = row16_sum(lds[turn][lane >> 5][lane & 15]);
         }
-        s0 /= n;
-        s1 /= n;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            stay_packed(x[v]);
-            stay_packed(d[v]);
-            stay_packed(w[v]);
-        }
+        s0 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, s), 0)) * inv_n * rstd;
+        s1 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, s), 32)) * inv_n * rstd;
         T* dx = static_cast<T*>(a.dx) + (size_t)row * (size_t)a.cols;
 #pragma unroll
         for (int v = 0; v < V; ++v)
             if (map.has(v)) {
                 X out;
 #pragma unroll
-                for (int e = 0; e < N; ++e)
-                    out[e] = (T)(rstd * ((float)d[v][e] * (float)w[v][e] - s0 - ((float)x[v][e] - mean) * rstd * s1));
+                for (int e = 0; e < N; ++e) out[e] = (T)fmaf(-xhat[v][e], s1, fmaf(c[v][e], rstd, -s0));
                 __builtin_memcpy(dx + map.start[v], &out, sizeof out);
             }
     }
+    // the ring's last copies, of rows past the end, land before its memory is used
+    // again or given back
+    __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
+    asm volatile("" ::: "memory");
     // one wave a row: the four waves' sums join first
-    float* p = a.partial + (size_t)blockIdx.x * 2 * (size_t)a.cols;
+    GR_LDS float* const part = (GR_LDS float*)rows_raw;
+    float* strip = a.partial + (size_t)blockIdx.x * 2 * (size_t)a.cols;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         float(&own)[V][N] = half ? db : dw;
-        if constexpr (G == 64) {
-            const int wave = (int)(threadIdx.x >> 6), lane = (int)(threadIdx.x & 63);
+        if constexpr (ONE) {
             __syncthreads();
             if (wave) {
 #pragma unroll
@@ -327,17 +355,17 @@ layer_norm_backward_kernel(NormArgs a)
 #pragma unroll
         for (int v = 0; v < V; ++v)
             if (map.has(v)) {
-                float* q = p + (size_t)half * a.cols + map.start[v];
+                float* to = strip + (size_t)half * a.cols + map.start[v];
                 if (v < V - 1 || map.skip == 0) {
 #pragma unroll
                     for (int e = 0; e < N; e += 4) {
                         const f32x4_t four = {own[v][e], own[v][e + 1], own[v][e + 2], own[v][e + 3]};
-                        __builtin_memcpy(q + e, &four, 16);
+                        __builtin_memcpy(to + e, &four, 16);
                     }
                 } else {
 #pragma unroll
                     for (int e = 0; e < N; ++e)
-                        if (e >= map.skip) q[e] = own[v][e];
+                        if (e >= map.skip) to[e] = own[v][e];
                 }
             }
     }
@@ -577,7 +605,7 @@ template <class T, int G, int V> __global__ void __launch_bounds__(kGroupThreads
     using X = typename Chunk<T>::Vec;
     using Q = typename VecN<signed char, N>::Vec;
     __shared__ unsigned lds[2][G / 64];
-    const RowMap<T, G, V> map(a.cols);
+    const RowMap<T, V> map(a.cols, (int)threadIdx.x % G, G);
     const int step = (int)gridDim.x * kGroups<G>;
     int64_t row = group_index<G>();          // 64 bits: the last row's successor may pass 2^31
     X next[V];
@@ -644,35 +672,32 @@ constexpr int kMaxRowGrid = 1 << 20;     // workgroups of a kernel that takes ro
 int any_grid(int rows) { return rows < kMaxRowGrid ? rows : kMaxRowGrid; }
 
 // Threads that share a row (0: the kernels for any length) and 16-byte chunks of
-// it each.  Forward: up to four chunks a thread, one wave where that holds the
-// row, so that short rows need no barrier.  Backward: one chunk a thread as long
-// as 1024 threads hold the row, since a thread keeps two fp32 sums a column
-// beside two rows and the weight.
+// it each: up to four chunks a thread, one wave where that holds the row, so that
+// short rows need no barrier.
 struct RowShape {
     int g, v;
 };
-template <bool BACK> RowShape row_shape(int cols, int bytes)
+int row_chunks(int cols, int bytes)
 {
     const int n = 16 / bytes;
-    if (cols < n) return {0, 0};
-    const int chunks = (int)(((int64_t)cols + n - 1) / n);
-    for (int g = 64; g <= 1024; g *= 2) {
+    return cols < n ? 0 : (int)(((int64_t)cols + n - 1) / n);
+}
+RowShape row_shape(int cols, int bytes)
+{
+    const int chunks = row_chunks(cols, bytes);
+    for (int g = 64; chunks > 0 && g <= 1024; g *= 2) {
         const int v = (int)ceil_div(chunks, g);
-        if (v <= (!BACK ? 4 : g == 1024 ? 2 : 1)) return {g, v};
+        if (v <= 4) return {g, v};
     }
     return {0, 0};
 }
 // Calls f<G, V> for a shape row_shape can give.
-template <bool BACK, class F> hipError_t with_shape(RowShape s, F&& f)
+template <class F> hipError_t with_shape(RowShape s, F&& f)
 {
 #define GR_SHAPE(G, V) \
     if (s.g == G && s.v == V) return f(std::integral_constant<int, G>{}, std::integral_constant<int, V>{});
-    if constexpr (BACK) {
-        GR_SHAPE(64, 1) GR_SHAPE(128, 1) GR_SHAPE(256, 1) GR_SHAPE(512, 1) GR_SHAPE(1024, 1) GR_SHAPE(1024, 2)
-    } else {
-        GR_SHAPE(64, 1) GR_SHAPE(64, 2) GR_SHAPE(64, 3) GR_SHAPE(64, 4) GR_SHAPE(128, 3) GR_SHAPE(128, 4)
-        GR_SHAPE(256, 3) GR_SHAPE(256, 4) GR_SHAPE(512, 3) GR_SHAPE(512, 4) GR_SHAPE(1024, 3) GR_SHAPE(1024, 4)
-    }
+    GR_SHAPE(64, 1) GR_SHAPE(64, 2) GR_SHAPE(64, 3) GR_SHAPE(64, 4) GR_SHAPE(128, 3) GR_SHAPE(128, 4)
+    GR_SHAPE(256, 3) GR_SHAPE(256, 4) GR_SHAPE(512, 3) GR_SHAPE(512, 4) GR_SHAPE(1024, 3) GR_SHAPE(1024, 4)
 #undef GR_SHAPE
     return hipErrorInvalidValue;
 }
@@ -686,6 +711,14 @@ int elem_size(int dt) { return dt == DT_F32 ? 4 : 2; }
 
 // Workgroups that take rows in turns: at most `most`, and as many rows each as
 // the busiest has anyway, so that they end together.
+// A forward kernel's limit is a full device (256 CUs of 2048 threads), so that the
+// weight is read once a group; four times that where the rows come from HBM
+// (above 64 MiB), whose waits more short workgroups cover better: 16384 x 8192
+// bf16 93 us against 98, but 4097 x 3001 fp16 12.8 against 10.9.
+int row_groups(int64_t rows, int64_t cols, int bytes, int threads)
+{
+    return kNumCUs * 2048 / threads * (rows * cols * bytes > (int64_t(64) << 20) ? 4 : 1);
+}
 int even_grid(int64_t rows, int rows_each_turn, int most)
 {
     const int64_t turns = ceil_div(rows, (int64_t)rows_each_turn * most);
@@ -696,14 +729,14 @@ int even_grid(int64_t rows, int rows_each_turn, int most)
 
 hipError_t launch_layer_norm(const NormArgs& a, int dt, int wdt, hipStream_t stream)
 {
-    const RowShape s = row_shape<false>(a.cols, elem_size(dt));
+    const RowShape s = row_shape(a.cols, elem_size(dt));
     return with_types(dt, wdt, [&](auto x, auto w) {
         using T = decltype(x);
         using W = decltype(w);
         if (!s.g) return start(&layer_norm_any_kernel<T, W>, dim3(any_grid(a.rows)), kThreads, stream, a);
-        return with_shape<false>(s, [&](auto g, auto v) {
+        return with_shape(s, [&](auto g, auto v) {
             constexpr int G = decltype(g)::value;
-            const int grid = even_grid(a.rows, kGroups<G>, kForwardGroups / kGroupThreads<G>);
+            const int grid = even_grid(a.rows, kGroups<G>, row_groups(a.rows, a.cols, sizeof(T), kGroupThreads<G>));
             return start(&layer_norm_kernel<T, W, G, decltype(v)::value>, dim3(grid), kGroupThreads<G>, stream, a);
         });
     });
@@ -712,23 +745,26 @@ hipError_t launch_layer_norm(const NormArgs& a, int dt, int wdt, hipStream_t str
 // workgroups of the backward pass, each of which leaves one strip of sums
 int layer_norm_strips(int64_t rows, int64_t cols)
 {
-    return rows == 0 ? 0 : even_grid(rows, cols <= 512 ? 4 : 2, cols <= 2048 ? 1024 : cols <= 4096 ? 512 : 256);
+    return rows == 0 ? 0 : even_grid(rows, cols <= 512 ? 4 : 2, cols <= 512 ? 512 : 256);
 }
 
 hipError_t launch_layer_norm_backward(const NormArgs& a, int dt, int wdt, hipStream_t stream)
 {
     const int strips = layer_norm_strips(a.rows, a.cols);
-    const RowShape s = row_shape<true>(a.cols, elem_size(dt));
     return with_types(dt, wdt, [&](auto x, auto w) {
         using T = decltype(x);
         using W = decltype(w);
         hipError_t e = hipSuccess;
-        if (a.rows > 0 && s.g) {
-            e = with_shape<true>(s, [&](auto g, auto v) {
-                constexpr int G = decltype(g)::value;
-                return start(&layer_norm_backward_kernel<T, W, G, decltype(v)::value>, dim3(strips), kGroupThreads<G>,
-                             stream, a);
-            });
+        // one chunk a thread as long as 1024 threads hold the row: a thread keeps
+        // two fp32 sums a column beside the row and the weight
+        const int chunks = row_chunks(a.cols, sizeof(T)), waves = (int)ceil_div(chunks, 64);
+        if (a.rows > 0 && chunks > 0 && waves <= 32) {
+            const auto go = [&](auto kernel, int threads) { return start(kernel, dim3(strips), threads, stream, a); };
+            e = waves == 1   ? go(&layer_norm_backward_kernel<T, W, 1, 1>, kThreads)
+                : waves <= 4  ? go(&layer_norm_backward_kernel<T, W, 4, 1>, 64 * waves)
+                : waves <= 8  ? go(&layer_norm_backward_kernel<T, W, 8, 1>, 64 * waves)
+                : waves <= 16 ? go(&layer_norm_backward_kernel<T, W, 16, 1>, 64 * waves)
+                              : go(&layer_norm_backward_kernel<T, W, 16, 2>, 32 * (waves + (waves & 1)));
         } else if (a.rows > 0) {
             const int strip_rows = (int)ceil_div(a.rows, strips);
             e = start(&layer_norm_dx_any_kernel<T, W>, dim3(any_grid(a.rows)), kThreads, stream, a);
@@ -752,14 +788,14 @@ hipError_t launch_quantize_rows(const void* x, int64_t x_stride, signed char* q,
                                 int cols, int dt, hipStream_t stream)
 {
     const QuantArgs a{x, q, scale, x_stride, rows, cols};
-    const RowShape s = row_shape<false>(cols, elem_size(dt));
+    const RowShape s = row_shape(cols, elem_size(dt));
     return with_types(dt, dt, [&](auto x0, auto w) {
         using T = decltype(x0);
         if constexpr (std::is_same_v<T, decltype(w)>) {
             if (!s.g) return start(&quantize_rows_any_kernel<T>, dim3(any_grid(rows)), kThreads, stream, a);
-            return with_shape<false>(s, [&](auto g, auto v) {
+            return with_shape(s, [&](auto g, auto v) {
                 constexpr int G = decltype(g)::value;
-                const int grid = even_grid(rows, kGroups<G>, kForwardGroups / kGroupThreads<G>);
+                const int grid = even_grid(rows, kGroups<G>, row_groups(rows, cols, sizeof(T), kGroupThreads<G>));
                 return start(&quantize_rows_kernel<T, G, decltype(v)::value>, dim3(grid), kGroupThreads<G>, stream, a);
             });
         }

@@ -24,18 +24,6 @@ namespace {
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kStepBytes = 64;                 // of K per matrix instruction: 32 16-bit or 64 8-bit elements
 
-// 1 KiB, 16 bytes a lane from any address, to LDS bytes lds .. lds + 1023 in lane
-// order; no register holds it on the way, so it is waited for with vmcnt.
-__device__ __forceinline__ void copy_to_lds(const unsigned char* from, uint32_t lds)
-{
-    asm volatile("s_mov_b32 m0, %1\n\t"
-                 "s_nop 0\n\t"
-                 "global_load_lds_dwordx4 %0, off"
-                 :
-                 : "v"(from), "s"(lds)
-                 : "memory", "m0");
-}
-
 template <int IN, int OUT, int EPI, int MT, int NT, int CB, int STAGES>
 __global__ void __launch_bounds__(kThreads) skinny_kernel(KernelArgs a)
 {
