@@ -26,7 +26,8 @@ __device__ __forceinline__ void copy_to_lds(const unsigned char* from, uint32_t 
 // The tiles of the GEMM + ReLU, with the epilogues of the feed-forward operators;
 // The tiles of the GEMM + ReLU, with the epilogues of the feed-forward operators;
 // BK in a name counts 16-bit elements, as there.  LIN_128 has eight waves and a
-// CU to itself, LIN_128X2 four and half a CU, LIN_64 half a CU.  LIN_K16 and
+// CU to itself, LIN_128X2 four and half a CU, LIN_64 half a CU; with B stored
+// (K,N) LIN_64 can cut a tile's K into parts.  LIN_K16 and
 // LIN_K32 (ffn_skinny.hip: K cut between a workgroup's waves) serve only products
 // with B stored (N,K).
 enum LinearConfig : int { LIN_256 = 0, LIN_128, LIN_128X2, LIN_64, LIN_G64, LIN_K16, LIN_K32, LIN_COUNT };
@@ -89,6 +90,8 @@ struct GatedGradArgs {
     int64_t dh_stride;
     int ld, ld_t;
     int rows, hidden, act;
+    unsigned* flags;        // `nflags` arrival counters to clear for a K split that follows
+    int nflags;
 };
 hipError_t launch_gated_grad(const GatedGradArgs& a, int dt, hipStream_t stream);
 

@@ -75,6 +75,9 @@ struct Linear {
 struct LinearPlan {
     int cfg = LIN_G64;
     int64_t tiles_m = 0, tiles_n = 0;
+    int64_t splits = 1, split_steps = 0;   // LIN_64 with B stored (K,N): parts of K, steps each
+    int64_t tiles() const { return tiles_m * tiles_n; }
+    int64_t grid() const { return tiles() * splits; }
 };
 
 // Estimated times, in ns, from measurements of each configuration between 1 and
@@ -142,7 +145,7 @@ LinearPlan plan_linear(const Linear& l)
 // a launch's work-items stay below 2^32
 bool plan_fits(const LinearPlan& p, const LinearPlan& q = {})
 {
-    return p.tiles_m * p.tiles_n + q.tiles_m * q.tiles_n <= (int64_t(1) << 22);
+    return p.grid() + q.grid() <= (int64_t(1) << 22);
 }
 
 KernelArgs linear_args(const LinearPlan& p, const Linear& l, const void* A, const void* B, void* C)
@@ -158,30 +161,48 @@ KernelArgs linear_args(const LinearPlan& p, const Linear& l, const void* A, cons
     a.ldb = int(l.ldb);
     a.tiles_m = int(p.tiles_m);
     a.tiles_n = int(p.tiles_n);
+    a.splits = int(p.splits);
+    a.split_steps = int(p.split_steps);
     a.panel = int(std::min<int64_t>(8, p.tiles_m));
     a.nxcd = 8;
     return a;
 }
-int linear_grid(const LinearPlan& p) { return int(p.tiles_m * p.tiles_n); }
 
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
 // The backward pass of the gated projections: dg and du go to the workspace
 // row-major (rows of 2 hidden) for dx, and transposed (rows of `rows`) for
 // dweight, each row padded to 16 bytes.  Both products share one launch, and so
-// one configuration: dx alone seldom fills the device.
+// one configuration: dx alone seldom fills the device.  Where one of them has few
+// tiles and a long K, its K is cut into parts, whose fp32 sums and arrival
+// counters are the workspace's last pieces.
 struct GradPlan {
     Linear lx, lw;
     LinearPlan x, w;            // of dx = dgu weight and of dweight = dgu^T x
-    uint64_t dgu_t, bytes;
+    uint64_t dgu_t, flags, sums_x, sums_w, bytes;
+    int nflags() const { return int((x.splits > 1 ? x.tiles() : 0) + (w.splits > 1 ? w.tiles() : 0)); }
 };
-double pair_time(int cfg, const Linear& a, const Linear& b)
+constexpr int64_t kSplitStep = 64;         // K elements per step of LIN_64
+
+// p cut into `parts` of whole steps; false where that leaves a part under 4 steps
+bool split(LinearPlan& p, const Linear& l, int64_t parts)
 {
-    const TileTime t = tile_time(cfg);
-    const double one_a = t.per_byte * double(a.K) * a.bytes + t.fixed, one_b = t.per_byte * double(b.K) * b.bytes + t.fixed;
-    const int64_t na = tiles_of(cfg, a), nb = tiles_of(cfg, b);
-    const double alone = na + nb <= kNumCUs ? t.alone : 1.0;
-    return std::max((one_a * double(na) + one_b * double(nb)) / t.slots + 0.5 * std::min(one_a, one_b),
+    const int64_t steps = ceil_div(l.K, kSplitStep);
+    if (parts > 1 && (steps < 4 * parts || p.tiles() > kNumCUs)) return false;
+    p.split_steps = steps == 0 ? 1 : ceil_div(steps, parts);
+    p.splits = steps == 0 ? 1 : ceil_div(steps, p.split_steps);
+    return true;
+}
+double pair_time(const LinearPlan& p, const Linear& a, const LinearPlan& q, const Linear& b)
+{
+    const TileTime t = tile_time(p.cfg);
+    // a part exchanges its sums through memory, about 3 us
+    auto one = [&](const LinearPlan& p, const Linear& l) {
+        return t.per_byte * double(l.K) * l.bytes / double(p.splits) + t.fixed + (p.splits > 1 ? 3000.0 : 0.0);
+    };
+    const double one_a = one(p, a), one_b = one(q, b);
+    const double alone = p.grid() + q.grid() <= kNumCUs ? t.alone : 1.0;
+    return std::max((one_a * double(p.grid()) + one_b * double(q.grid())) / t.slots + 0.5 * std::min(one_a, one_b),
                     alone * std::max(one_a, one_b));
 }
 GradPlan plan_grad(int64_t rows, int64_t hidden, int64_t cols, int64_t x_stride, int64_t weight_stride)
@@ -190,20 +211,31 @@ GradPlan plan_grad(int64_t rows, int64_t hidden, int64_t cols, int64_t x_stride,
     const int64_t ld = round_up(2 * hidden, 8), ld_t = round_up(rows, 8);
     g.lx = Linear{rows, cols, 2 * hidden, ld, weight_stride, false};
     g.lw = Linear{2 * hidden, cols, rows, ld_t, x_stride, false};
-    int both = LIN_G64;
+    g.x = plan_as(LIN_G64, g.lx);
+    g.w = plan_as(LIN_G64, g.lw);
     double best = 0.0;
-    for (int cfg : {LIN_64, LIN_128, LIN_128X2, LIN_256}) {
-        if (!usable(cfg, g.lx) || !usable(cfg, g.lw)) continue;
-        const double t = pair_time(cfg, g.lx, g.lw);
-        if (both == LIN_G64 || t < best) {
-            both = cfg;
-            best = t;
+    auto consider = [&](int cfg, int64_t parts_x, int64_t parts_w) {
+        LinearPlan x = plan_as(cfg, g.lx), w = plan_as(cfg, g.lw);
+        if (cfg == LIN_64 && !(split(x, g.lx, parts_x) && split(w, g.lw, parts_w))) return;
+        const double t = pair_time(x, g.lx, w, g.lw);
+        if (g.x.cfg != LIN_G64 && t >= best) return;
+        g.x = x;
+        g.w = w;
+        best = t;
+    };
+    for (int cfg : {LIN_64, LIN_128, LIN_128X2, LIN_256})
+        if (usable(cfg, g.lx) && usable(cfg, g.lw)) consider(cfg, 1, 1);
+    if (usable(LIN_64, g.lx) && usable(LIN_64, g.lw) && rows > 0 && hidden > 0)
+        for (int64_t parts : {2, 4, 8, 16}) {
+            consider(LIN_64, parts, 1);
+            consider(LIN_64, 1, parts);
         }
-    }
-    g.x = plan_as(both, g.lx);
-    g.w = plan_as(both, g.lw);
+    auto sums = [](const LinearPlan& p) { return p.splits > 1 ? uint64_t(p.grid()) * 64 * 64 * 4 : 0; };
     g.dgu_t = uint64_t(round_up(2 * rows * ld, 256));
-    g.bytes = g.dgu_t + uint64_t(2 * hidden) * uint64_t(ld_t) * 2;
+    g.flags = uint64_t(round_up(int64_t(g.dgu_t + uint64_t(2 * hidden) * uint64_t(ld_t) * 2), 256));
+    g.sums_x = g.flags + uint64_t(round_up(4 * int64_t(g.nflags()), 256));
+    g.sums_w = g.sums_x + sums(g.x);
+    g.bytes = g.sums_w + sums(g.w);
     return g;
 }
 
@@ -308,7 +340,7 @@ extern "C" int gemm_relu_gated(const void* x, int64_t x_stride, const void* weig
     a.act = act;
     a.GU = gu;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    return finish(launcher_gated(dtype, p.cfg)(a, linear_grid(p), st), st);
+    return finish(launcher_gated(dtype, p.cfg)(a, int(p.grid()), st), st);
 }
 
 extern "C" const char* gemm_relu_gated_plan(int64_t rows, int64_t hidden, int64_t cols, int dtype)
@@ -344,6 +376,7 @@ extern "C" int gemm_relu_gated_backward(const void* dh, int64_t dh_stride, const
     if (const int dev = check_device()) return dev;
     hipStream_t st = static_cast<hipStream_t>(stream);
     unsigned char* ws = static_cast<unsigned char*>(workspace);
+    unsigned* flags = reinterpret_cast<unsigned*>(ws + p.flags);
     hipError_t e = hipSuccess;
     if (rows > 0 && hidden > 0) {
         GatedGradArgs g{};
@@ -357,13 +390,19 @@ extern "C" int gemm_relu_gated_backward(const void* dh, int64_t dh_stride, const
         g.rows = int(rows);
         g.hidden = int(hidden);
         g.act = act;
+        g.flags = flags;
+        g.nflags = p.nflags();
         e = launch_gated_grad(g, dtype, st);
     }
-    const KernelArgs gx = linear_args(p.x, p.lx, ws, weight, dx), gw = linear_args(p.w, p.lw, ws + p.dgu_t, x, dweight);
-    const int nx = rows > 0 ? linear_grid(p.x) : 0, nw = hidden > 0 ? linear_grid(p.w) : 0;
+    KernelArgs gx = linear_args(p.x, p.lx, ws, weight, dx), gw = linear_args(p.w, p.lw, ws + p.dgu_t, x, dweight);
+    gx.flags = flags;
+    gx.ws = reinterpret_cast<float*>(ws + p.sums_x);
+    gw.flags = flags + (p.x.splits > 1 ? p.x.tiles() : 0);
+    gw.ws = reinterpret_cast<float*>(ws + p.sums_w);
+    const int nx = rows > 0 ? int(p.x.grid()) : 0, nw = hidden > 0 ? int(p.w.grid()) : 0;
     if (e == hipSuccess) {
-        // the product with the longer K first: its tiles take longest
-        const bool x_first = p.lx.K >= p.lw.K;
+        // the product whose tiles take longest first
+        const bool x_first = p.lx.K * p.w.splits >= p.lw.K * p.x.splits;
         e = launcher_cast_pair(dtype, p.x.cfg)(x_first ? LinearPair{gx, gw, nx} : LinearPair{gw, gx, nw}, nx + nw, st);
     }
     return finish(e, st);
@@ -412,7 +451,7 @@ extern "C" int gemm_relu_i8(const void* x, int64_t x_stride, const float* x_scal
     a.scale_a = x_scale;
     a.scale_b = w_scale;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    return finish(launcher_i8(out_dtype, p.cfg)(a, linear_grid(p), st), st);
+    return finish(launcher_i8(out_dtype, p.cfg)(a, int(p.grid()), st), st);
 }
 
 extern "C" const char* gemm_relu_i8_plan(int64_t rows, int64_t n, int64_t k, int out_dtype)

@@ -481,6 +481,8 @@ template <int DT> __global__ void __launch_bounds__(kThreads) gated_grad_kernel(
     __shared__ __attribute__((aligned(16))) T tile[2][64][PITCH];
     const int htiles = (a.hidden + 63) / 64;
     const int h0 = (int)(blockIdx.x % htiles) * 64, r0 = (int)(blockIdx.x / htiles) * 64;
+    if (blockIdx.x == 0)
+        for (int k = threadIdx.x; k < a.nflags; k += kThreads) a.flags[k] = 0u;
     const int c = (int)(threadIdx.x & 15) * 4, h = h0 + c, q = (int)(threadIdx.x >> 4) * 4;
     const bool whole = h + 4 <= a.hidden;
     f32x4_t g[4], u[4];

@@ -99,7 +99,8 @@ struct KernelArgs {
     // w mod T (T = tiles_m tiles_n): the K steps [s split_steps, (s + 1)
     // split_steps).  Its fp32 partial tile goes to slot s T + tile of ws (BM x
     // BN floats each); flags holds one arrival counter per tile, zero between
-    // launches.
+    // launches.  The feed-forward products may have one part only, which needs
+    // neither.
     int splits, split_steps;
     // Feed-forward operators (every EPI but EPI_RELU): elements from one row of
     // A, or of B as it is stored, to the next; C is dense.  EPI_GATED: B holds
@@ -117,6 +118,7 @@ struct KernelArgs {
 // tiles_n tiles whose first column starts at n_org.
 struct Region {
     int tiles_m, tiles_n, panel, n_org;
+    int part = 0;      // K-split configurations: which part of the tile's K
 };
 
 // ------------------------------------------------------------------ helpers
@@ -644,7 +646,7 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
     // A stream-K piece or a K-split part covers the steps [kt0, kt1) of
     // ceil(K / BK): its full steps, and the tail step if it ends the K range.
     const int ksteps = (K + BK - 1) / BK;
-    const int split = C::SPLITK ? (int)blockIdx.x / (reg.tiles_m * reg.tiles_n) : 0;
+    const int split = C::SPLITK ? reg.part : 0;
     const int kt0 = C::STREAMK ? sk->pc.kt0 : C::SPLITK ? split * args.split_steps : 0;
     const int kt1 = C::STREAMK ? sk->pc.kt1 : C::SPLITK ? min(ksteps, kt0 + args.split_steps) : ksteps;
     const int nk = C::DIRECT ? max(0, min(kt1, K / BK) - kt0) : ksteps;
@@ -1495,10 +1497,10 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
     // e of group v = (i TN + j) NQ + q of thread tid at float (4 v + e)
     // NTHREADS + tid of the slot (each dword store of a wave is 256
     // consecutive bytes).
-    if constexpr (C::SPLITK) {
+    if constexpr (C::SPLITK) if (C::EPI == EPI_RELU || args.splits > 1) {
         constexpr int NQS = NACC / 4, NV = TM * TN * NQS;
         const int tiles = reg.tiles_m * reg.tiles_n;
-        const int tile = (int)blockIdx.x - split * tiles;
+        const int tile = wg;
         auto slot = [&](int p) { return args.ws + ((size_t)(p * tiles + tile) * (BM * BN) + tid); };
         float* own = slot(split);
 #pragma unroll
@@ -2184,8 +2186,9 @@ __global__ void __launch_bounds__(C::NTHREADS, 1) gemm_relu_kernel(KernelArgs ar
             barrier_lds();
         }
     } else if constexpr (C::SPLITK) {
-        gemm_relu_tile<C>(args, (int)blockIdx.x % (args.tiles_m * args.tiles_n), smem, nullptr,
-                          Region{args.tiles_m, args.tiles_n, args.panel, 0});
+        const int tiles = args.tiles_m * args.tiles_n;
+        gemm_relu_tile<C>(args, (int)blockIdx.x % tiles, smem, nullptr,
+                          Region{args.tiles_m, args.tiles_n, args.panel, 0, (int)blockIdx.x / tiles});
     } else {
         gemm_relu_tile<C>(args, blockIdx.x, smem, nullptr,
                           Region{args.tiles_m, args.tiles_n, args.panel, 0});

@@ -25,8 +25,10 @@ template <class C> __global__ void __launch_bounds__(C::NTHREADS, 1) linear_pair
     __shared__ __attribute__((aligned(1024))) unsigned char smem_raw[C::LDS_BYTES];
     const bool second = (int)blockIdx.x >= pair.first;
     const KernelArgs& args = second ? pair.b : pair.a;
-    gemm_relu_tile<C>(args, (int)blockIdx.x - (second ? pair.first : 0), (GR_LDS unsigned char*)(smem_raw), nullptr,
-                      Region{args.tiles_m, args.tiles_n, args.panel, 0});
+    const int wg = (int)blockIdx.x - (second ? pair.first : 0), tiles = args.tiles_m * args.tiles_n;
+    // a K split's workgroups take part wg / tiles of tile wg % tiles
+    gemm_relu_tile<C>(args, C::SPLITK ? wg % tiles : wg, (GR_LDS unsigned char*)(smem_raw), nullptr,
+                      Region{args.tiles_m, args.tiles_n, args.panel, 0, C::SPLITK ? wg / tiles : 0});
 }
 
 template <class C> hipError_t launch_pair(const LinearPair& pair, int grid, hipStream_t stream)
@@ -54,7 +56,7 @@ template <int IN, int OUT, int EPI> struct LinearCfg<IN, OUT, EPI, LIN_128X2> {
     using type = Cfg<IN, OUT, nt<EPI>, 128, 128, bk<IN, 64>, 2, 2, 2, true, false, mb<EPI>, false, false, false, EPI>;
 };
 template <int IN, int OUT, int EPI> struct LinearCfg<IN, OUT, EPI, LIN_64> {
-    using type = Cfg<IN, OUT, nt<EPI>, 64, 64, bk<IN, 64>, 2, 2, 4, true, false, mb<EPI>, false, false, false, EPI>;
+    using type = Cfg<IN, OUT, nt<EPI>, 64, 64, bk<IN, 64>, 2, 2, 4, true, false, mb<EPI>, false, false, EPI == EPI_CAST, EPI>;
 };
 template <int IN, int OUT, int EPI> struct LinearCfg<IN, OUT, EPI, LIN_G64> {
     using type = Cfg<IN, OUT, nt<EPI>, 64, 64, bk<IN, 64>, 2, 2, 2, false, false, mb<EPI>, false, false, false, EPI>;
