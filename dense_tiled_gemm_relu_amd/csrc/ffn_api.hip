@@ -94,7 +94,7 @@ TileTime tile_time(int cfg)
     switch (cfg) {
     case LIN_256: return {12.0, 4000, kNumCUs, 1.0};
     case LIN_128: return {4.6, 2500, kNumCUs, 1.0};
-    case LIN_128X2: return {9.0, 3500, 2 * kNumCUs, 0.72};
+    case LIN_128X2: return {8.5, 3200, 2 * kNumCUs, 0.75};
     case LIN_64: return {5.2, 2000, 2 * kNumCUs, 0.55};
     case LIN_K16: return {1.2, 1000, 2 * kNumCUs, 0.6};
     case LIN_K32: return {1.4, 800, kNumCUs, 1.0};

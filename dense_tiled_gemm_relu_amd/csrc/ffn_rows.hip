@@ -560,22 +560,25 @@ template <int DT> __global__ void __launch_bounds__(kThreads) gated_grad_kernel(
 // ------------------------------------------------------- quantisation
 // The largest magnitude is taken over the values' bits without the sign, whose
 // order as whole numbers is that of the values with infinities and NaN on top.
-// 127 x / max is formed as one fp32 division of the product 127 x.  For 16-bit x
-// the product is exact and the quotient's distance from a rounding border is
-// either zero or more than half an fp32 step, so the result is that of exact
-// arithmetic.  A row whose largest value is near the top of the fp32 range is
-// scaled down by a power of two first, so that 127 x stays finite.
+// The row is scaled by a power of two (exactly) so that its largest value m is in
+// [1/2, 1); then 127 x / m is a product with the reciprocal and one step that adds
+// the exact remainder's share, which costs half of a division.  For 16-bit x the
+// products and the remainder are exact, the quotient's distance from a rounding
+// border is either zero or more than 2^-20 of it, and a quotient on a border,
+// being a short number, comes out exactly: the result is that of exact arithmetic.
 struct Quantiser {
-    float mul, by;
+    int down;
+    float m, r;
     __device__ __forceinline__ Quantiser(float top)
     {
-        const float down = top > 0x1p120f ? 0x1p-8f : 1.0f;
-        mul = down;
-        by = top * down;
+        down = -__builtin_amdgcn_frexp_expf(top);
+        m = ldexpf(top, down);
+        r = __builtin_amdgcn_rcpf(m);
     }
     __device__ __forceinline__ signed char operator()(float x) const
     {
-        return (signed char)(int)rintf(127.0f * (x * mul) / by);
+        const float v = 127.0f * ldexpf(x, down), p = v * r;
+        return (signed char)(int)rintf(fmaf(fmaf(-p, m, v), r, p));
     }
 };
 template <class T> __device__ __forceinline__ unsigned magnitude(T x)

@@ -53,7 +53,7 @@ template <int IN, int OUT, int EPI> struct LinearCfg<IN, OUT, EPI, LIN_128> {
     using type = Cfg<IN, OUT, nt<EPI>, 128, 128, bk<IN, 64>, 2, 4, 4, true, true, 16, false, false, false, EPI>;
 };
 template <int IN, int OUT, int EPI> struct LinearCfg<IN, OUT, EPI, LIN_128X2> {
-    using type = Cfg<IN, OUT, nt<EPI>, 128, 128, bk<IN, 64>, 2, 2, 2, true, false, mb<EPI>, false, false, false, EPI>;
+    using type = Cfg<IN, OUT, nt<EPI>, 128, 128, bk<IN, 64>, 2, 4, 2, true, false, 16, false, false, false, EPI>;
 };
 template <int IN, int OUT, int EPI> struct LinearCfg<IN, OUT, EPI, LIN_64> {
     using type = Cfg<IN, OUT, nt<EPI>, 64, 64, bk<IN, 64>, 2, 2, 4, true, false, mb<EPI>, false, false, EPI == EPI_CAST, EPI>;
