@@ -142,6 +142,42 @@ LinearPlan plan_linear(const Linear& l)
     return plan_as(best, l);
 }
 
+// A product with B stored (N,K) whose last tile row holds a few rows only: these
+// go to a launch of their own with small tiles where the estimate says so, since
+// the row of mostly empty tiles can cost a whole round (gated 1027 x 2003 x 1501:
+// 38 us in one launch).
+struct RowsPlan {
+    Linear top, rest;
+    LinearPlan p, q;            // q: of the rest, if it has rows
+};
+constexpr int64_t kRestRows = 32;
+RowsPlan plan_rows(const Linear& l)
+{
+    RowsPlan r{l, l, plan_linear(l), {}};
+    r.rest.M = 0;
+    double best = linear_time(r.p.cfg, l);
+    for (int cfg : {LIN_128, LIN_128X2, LIN_256}) {
+        Linear top = l, rest = l;
+        rest.M = l.M % linear_info(cfg).bm;
+        top.M = l.M - rest.M;
+        if (top.M == 0 || rest.M == 0 || rest.M > kRestRows || !usable(cfg, l)) continue;
+        const LinearPlan q = plan_linear(rest);
+        const double t = linear_time(cfg, top) + linear_time(q.cfg, rest) + 3000.0;    // a second launch
+        if (t < best) {
+            r = RowsPlan{top, rest, plan_as(cfg, top), q};
+            best = t;
+        }
+    }
+    return r;
+}
+const char* rows_plan_name(const RowsPlan& r)
+{
+    if (r.rest.M == 0) return linear_info(r.p.cfg).name;
+    static thread_local char names[64];
+    std::snprintf(names, sizeof names, "%s+%s", linear_info(r.p.cfg).name, linear_info(r.q.cfg).name);
+    return names;
+}
+
 // a launch's work-items stay below 2^32
 bool plan_fits(const LinearPlan& p, const LinearPlan& q = {})
 {
@@ -331,23 +367,28 @@ extern "C" int gemm_relu_gated(const void* x, int64_t x_stride, const void* weig
     const Mat m[] = {dense(h, rows, hidden, 2), dense(gu, gu ? rows : 0, 2 * hidden, 4),
                      {x, rows, cols, x_stride, 2}, {weight, 2 * hidden, cols, weight_stride, 2}};
     if (!mats_ok(m, 2)) return GEMM_RELU_EINVAL;
-    const Linear l = gated_linear(rows, hidden, cols, x_stride, weight_stride);
-    const LinearPlan p = plan_linear(l);
-    if (!plan_fits(p)) return GEMM_RELU_EUNSUPPORTED;
+    const RowsPlan r = plan_rows(gated_linear(rows, hidden, cols, x_stride, weight_stride));
+    if (!plan_fits(r.p)) return GEMM_RELU_EUNSUPPORTED;
     if (const int dev = check_device()) return dev;
-    KernelArgs a = linear_args(p, l, x, weight, h);
-    a.hidden = int(hidden);
-    a.act = act;
-    a.GU = gu;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    return finish(launcher_gated(dtype, p.cfg)(a, int(p.grid()), st), st);
+    auto go = [&](const LinearPlan& p, const Linear& l, int64_t first) {
+        KernelArgs a = linear_args(p, l, static_cast<const char*>(x) + 2 * first * x_stride, weight,
+                                   static_cast<char*>(h) + 2 * first * hidden);
+        a.hidden = int(hidden);
+        a.act = act;
+        a.GU = gu ? gu + first * 2 * hidden : nullptr;
+        return launcher_gated(dtype, p.cfg)(a, int(p.grid()), st);
+    };
+    hipError_t e = go(r.p, r.top, 0);
+    if (e == hipSuccess && r.rest.M > 0) e = go(r.q, r.rest, r.top.M);
+    return finish(e, st);
 }
 
 extern "C" const char* gemm_relu_gated_plan(int64_t rows, int64_t hidden, int64_t cols, int dtype)
 {
     if (!gated_sizes_ok(rows, hidden, cols, dtype)) return nullptr;
     if (rows == 0 || hidden == 0) return "none";
-    return linear_info(plan_linear(gated_linear(rows, hidden, cols, cols, cols)).cfg).name;
+    return rows_plan_name(plan_rows(gated_linear(rows, hidden, cols, cols, cols)));
 }
 
 extern "C" int64_t gemm_relu_gated_backward_workspace(int64_t rows, int64_t hidden, int64_t cols)
@@ -443,15 +484,20 @@ extern "C" int gemm_relu_i8(const void* x, int64_t x_stride, const float* x_scal
     const Mat m[] = {dense(y, rows, n, elem_bytes(out_dtype)), {x, rows, k, x_stride, 1}, {w, n, k, w_stride, 1},
                      dense(x_scale, rows, 1, 4), dense(w_scale, n, 1, 4)};
     if (!mats_ok(m, 1)) return GEMM_RELU_EINVAL;
-    const Linear l{rows, n, k, x_stride, w_stride, true, 1};
-    const LinearPlan p = plan_linear(l);
-    if (k > kMaxK8 || !plan_fits(p)) return GEMM_RELU_EUNSUPPORTED;
+    const RowsPlan r = plan_rows(Linear{rows, n, k, x_stride, w_stride, true, 1});
+    if (k > kMaxK8 || !plan_fits(r.p)) return GEMM_RELU_EUNSUPPORTED;
     if (const int dev = check_device()) return dev;
-    KernelArgs a = linear_args(p, l, x, w, y);
-    a.scale_a = x_scale;
-    a.scale_b = w_scale;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    return finish(launcher_i8(out_dtype, p.cfg)(a, int(p.grid()), st), st);
+    auto go = [&](const LinearPlan& p, const Linear& l, int64_t first) {
+        KernelArgs a = linear_args(p, l, static_cast<const char*>(x) + first * x_stride, w,
+                                   static_cast<char*>(y) + first * n * elem_bytes(out_dtype));
+        a.scale_a = x_scale + first;
+        a.scale_b = w_scale;
+        return launcher_i8(out_dtype, p.cfg)(a, int(p.grid()), st);
+    };
+    hipError_t e = go(r.p, r.top, 0);
+    if (e == hipSuccess && r.rest.M > 0) e = go(r.q, r.rest, r.top.M);
+    return finish(e, st);
 }
 
 extern "C" const char* gemm_relu_i8_plan(int64_t rows, int64_t n, int64_t k, int out_dtype)
@@ -459,5 +505,5 @@ extern "C" const char* gemm_relu_i8_plan(int64_t rows, int64_t n, int64_t k, int
     if (!size_ok(rows) || !size_ok(n) || !size_ok(k) || !is_float(out_dtype)) return nullptr;
     if (rows == 0 || n == 0) return "none";
     if (k > kMaxK8) return "unsupported";
-    return linear_info(plan_linear(Linear{rows, n, k, k, k, true, 1}).cfg).name;
+    return rows_plan_name(plan_rows(Linear{rows, n, k, k, k, true, 1}));
 }

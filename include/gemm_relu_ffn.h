@@ -81,8 +81,9 @@ int gemm_relu_gated(const void* x, int64_t x_stride, const void* weight, int64_t
                     void* h, float* gu, int64_t rows, int64_t hidden, int64_t cols, int dtype,
                     int act, void* stream);
 
-/* Name of the kernel configuration gemm_relu_gated would launch ("none" for an
- * empty call, NULL for invalid sizes or codes).  Host-only. */
+/* Name of the kernel configuration gemm_relu_gated would launch ("a+b" where the
+ * last rows take a second launch; "none" for an empty call, NULL for invalid
+ * sizes or codes).  Host-only. */
 const char* gemm_relu_gated_plan(int64_t rows, int64_t hidden, int64_t cols, int dtype);
 
 /*

@@ -35,3 +35,12 @@ def test_workspace_covers_every_plan():
     for m, n, k in itertools.product((1, 34, 320, 4096), (1, 64, 2816), (64, 119, 4096)):
         both = 2 * (m * 2 * n) * 2
         assert lib.gemm_relu_gated_backward_workspace(m, n, k) >= both
+
+
+def test_a_few_rows_past_a_tile_take_a_launch_of_their_own():
+    lib = gr.library()
+    assert lib.gemm_relu_gated_plan(1027, 2003, 1501, gr.F16) == b"d128x128x64_s4_i16w8+k16x16x64_s4"
+    assert lib.gemm_relu_gated_plan(1024, 2003, 1501, gr.F16) == b"d128x128x64_s4_i16w8"
+    assert lib.gemm_relu_i8_plan(1027, 4006, 1501, gr.F16) == b"d128x128x64_s4_i16w8+k16x16x64_s4"
+    # no round is saved: 17 x 24 tiles are two rounds, and so are 16 x 24
+    assert lib.gemm_relu_gated_plan(4097, 3000, 2000, gr.BF16) == b"d256x256x32_s4_i16w8"

@@ -132,6 +132,22 @@ def test_i8_edges(rows, n, k):
     assert torch.equal(gr.matmul_i8(shifted(x), sx, strided(w, 3), sw, BF16), y)
 
 
+# a last tile row of a few rows goes to a second launch
+@pytest.mark.parametrize("rows,n,k", [(1027, 4006, 1501), (2051, 2000, 2000), (4100, 2002, 1000)])
+def test_rows_in_two_launches(rows, n, k):
+    assert b"+" in gr.library().gemm_relu_gated_plan(rows, n // 2, k, gr.F16)
+    x, w = gated_inputs(rows, n // 2, k, F16, 31)
+    h, gu = gr.matmul_gated(x, w, "silu", save=True)
+    gated_check(x, w, "silu", h, gu)
+    xs, ws = strided(x, 5), strided(w, 3)
+    h2, gu2 = gr.matmul_gated(xs, ws, "silu", save=True)
+    assert torch.equal(h2, h) and torch.equal(gu2, gu) and torch.equal(gr.matmul_gated(x, w, "silu"), h)
+    x, sx, w, sw = i8_inputs(rows, n, k, 33)
+    y = gr.matmul_i8(x, sx, w, sw, F32)
+    i8_check(x, sx, w, sw, y)
+    assert torch.equal(gr.matmul_i8(strided(x, 5), sx, strided(w, 3), sw, F32), y)
+
+
 def test_inputs_dropped_after_a_call_on_another_stream():
     # the caching allocator may give an input's memory away as soon as it is dropped;
     # the kernel on the other stream must still read what was there
