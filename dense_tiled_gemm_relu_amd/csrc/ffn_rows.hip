@@ -473,7 +473,7 @@ template <class W> __global__ void __launch_bounds__(1024) layer_norm_join_kerne
 // before the first is used: dg and du go out row-major, and transposed through
 // LDS.  Both outputs' rows are padded to 16 bytes with zeros, so that the
 // products may read them in whole pieces.
-template <int DT> __global__ void __launch_bounds__(kThreads) gated_grad_kernel(GatedGradArgs a)
+template <int DT, int ACT> __global__ void __launch_bounds__(kThreads) gated_grad_kernel(GatedGradArgs a)
 {
     using T = typename Elem<DT>::T;
     typedef T T4 __attribute__((ext_vector_type(4)));
@@ -515,7 +515,7 @@ template <int DT> __global__ void __launch_bounds__(kThreads) gated_grad_kernel(
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float value, slope;
-            activation_slope(g[k][e], a.act, value, slope);
+            activation_slope<ACT>(g[k][e], value, slope);
             dg[k][e] = (T)((float)d[k][e] * u[k][e] * slope);
             du[k][e] = (T)((float)d[k][e] * value);
         }
@@ -785,8 +785,18 @@ hipError_t launch_layer_norm_backward(const NormArgs& a, int dt, int wdt, hipStr
 hipError_t launch_gated_grad(const GatedGradArgs& a, int dt, hipStream_t stream)
 {
     const dim3 grid((unsigned)((a.hidden + 63) / 64) * (unsigned)((a.rows + 63) / 64));
-    return dt == DT_F16 ? start(&gated_grad_kernel<DT_F16>, grid, kThreads, stream, a)
-                        : start(&gated_grad_kernel<DT_BF16>, grid, kThreads, stream, a);
+    const auto go = [&](auto dtype, auto act) {
+        return start(&gated_grad_kernel<decltype(dtype)::value, decltype(act)::value>, grid, kThreads, stream, a);
+    };
+    const auto with = [&](auto dtype) {
+        switch (a.act) {
+        case ACT_SILU: return go(dtype, std::integral_constant<int, ACT_SILU>{});
+        case ACT_GELU: return go(dtype, std::integral_constant<int, ACT_GELU>{});
+        case ACT_GELU_TANH: return go(dtype, std::integral_constant<int, ACT_GELU_TANH>{});
+        default: return go(dtype, std::integral_constant<int, ACT_RELU>{});
+        }
+    };
+    return dt == DT_F16 ? with(std::integral_constant<int, DT_F16>{}) : with(std::integral_constant<int, DT_BF16>{});
 }
 
 hipError_t launch_quantize_rows(const void* x, int64_t x_stride, signed char* q, float* scale, int rows,

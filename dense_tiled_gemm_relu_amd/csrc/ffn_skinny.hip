@@ -162,11 +162,13 @@ __global__ void __launch_bounds__(kThreads) skinny_kernel(KernelArgs a)
             c = c0 + 8 * j + 4 * (g4 & 1);
             if (a.GU && mine && c < cols)
                 store_sums(a.GU + (size_t)m * (size_t)(2 * (int64_t)cols) + (g4 < 2 ? 0 : cols) + c, s, c, cols);
+            with_activation(a.act, [&](auto kind) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float up = __shfl_xor(s[e], 32);
-                v[e] = activation(s[e], a.act) * up;
-            }
+                for (int e = 0; e < 4; ++e) {
+                    const float up = __shfl_xor(s[e], 32);
+                    v[e] = activation<decltype(kind)::value>(s[e]) * up;
+                }
+            });
             mine = mine && g4 < 2;
         } else {
             c = c0 + 16 * j + 4 * g4;

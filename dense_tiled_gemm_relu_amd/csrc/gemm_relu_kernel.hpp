@@ -338,26 +338,38 @@ __device__ __forceinline__ float logistic(float z)
 }
 __device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(z * -0.70710678118654752440f); }
 constexpr float kTwoGeluC = 1.5957691216057307f;     // 2 sqrt(2 / pi)
-__device__ __forceinline__ float activation(float g, int act)
+template <int ACT> __device__ __forceinline__ float activation(float g)
 {
-    if (act == ACT_SILU) return g * logistic(g);
-    if (act == ACT_GELU) return g * normal_cdf(g);
+    if constexpr (ACT == ACT_SILU) return g * logistic(g);
+    if constexpr (ACT == ACT_GELU) return g * normal_cdf(g);
     // 0.5 (1 + tanh z) = 1 / (1 + e^-2z)
-    if (act == ACT_GELU_TANH) return g * logistic(kTwoGeluC * (g + 0.044715f * g * g * g));
+    if constexpr (ACT == ACT_GELU_TANH) return g * logistic(kTwoGeluC * (g + 0.044715f * g * g * g));
     return relu(g);
 }
-// value and slope of the activation at g
-__device__ __forceinline__ void activation_slope(float g, int act, float& value, float& slope)
+// f(the activation as a constant): one choice for a whole loop of elements, so that
+// a wave runs through one activation's code and not past the others' at every
+// element
+template <class F> __device__ __forceinline__ void with_activation(int act, F&& f)
 {
-    if (act == ACT_SILU) {
+    switch (act) {
+    case ACT_SILU: f(std::integral_constant<int, ACT_SILU>{}); break;
+    case ACT_GELU: f(std::integral_constant<int, ACT_GELU>{}); break;
+    case ACT_GELU_TANH: f(std::integral_constant<int, ACT_GELU_TANH>{}); break;
+    default: f(std::integral_constant<int, ACT_RELU>{}); break;
+    }
+}
+// value and slope of the activation at g
+template <int ACT> __device__ __forceinline__ void activation_slope(float g, float& value, float& slope)
+{
+    if constexpr (ACT == ACT_SILU) {
         const float s = logistic(g);
         value = g * s;
         slope = s * (1.0f + g * (1.0f - s));
-    } else if (act == ACT_GELU) {
+    } else if constexpr (ACT == ACT_GELU) {
         const float p = normal_cdf(g);
         value = g * p;
         slope = p + g * 0.39894228040143267794f * __expf(-0.5f * g * g);      // 1 / sqrt(2 pi)
-    } else if (act == ACT_GELU_TANH) {
+    } else if constexpr (ACT == ACT_GELU_TANH) {
         const float s = logistic(kTwoGeluC * (g + 0.044715f * g * g * g));
         value = g * s;
         // s (1 - s) is 0 long before the square is capped
@@ -1651,28 +1663,30 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
     }
     auto put_acc = [&] {
         if constexpr (C::GATED) {
+            with_activation(args.act, [&](auto kind) {
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
+                for (int i = 0; i < TM; ++i)
 #pragma unroll
-                for (int j = 0; j < TN / 2; ++j)
+                    for (int j = 0; j < TN / 2; ++j)
 #pragma unroll
-                    for (int q = 0; q < NQ; ++q) {
-                        f32x4_t gate, up, h;
+                        for (int q = 0; q < NQ; ++q) {
+                            f32x4_t gate, up, h;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            gate[e] = acc[i][2 * j][4 * q + e];
-                            up[e] = acc[i][2 * j + 1][4 * q + e];
-                            h[e] = activation(gate[e], args.act) * up[e];
+                            for (int e = 0; e < 4; ++e) {
+                                gate[e] = acc[i][2 * j][4 * q + e];
+                                up[e] = acc[i][2 * j + 1][4 * q + e];
+                                h[e] = activation<decltype(kind)::value>(gate[e]) * up[e];
+                            }
+                            put_group(i, j, q, h);
+                            const int m = m0 + wm0 + MB * i + lr;
+                            const int n = c0 + wc0 + MB * j + 4 * NG * q + 4 * g;
+                            if (args.GU && m < M && n < NC) {
+                                float* dst = args.GU + (size_t)m * (size_t)(2 * (int64_t)NC) + n;
+                                store_sums(dst, gate, n, NC);
+                                store_sums(dst + NC, up, n, NC);
+                            }
                         }
-                        put_group(i, j, q, h);
-                        const int m = m0 + wm0 + MB * i + lr;
-                        const int n = c0 + wc0 + MB * j + 4 * NG * q + 4 * g;
-                        if (args.GU && m < M && n < NC) {
-                            float* dst = args.GU + (size_t)m * (size_t)(2 * (int64_t)NC) + n;
-                            store_sums(dst, gate, n, NC);
-                            store_sums(dst + NC, up, n, NC);
-                        }
-                    }
+            });
             return;
         }
         // scales of the lane's rows and columns (rows and columns past the edge
