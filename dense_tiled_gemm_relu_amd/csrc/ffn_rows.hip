@@ -469,26 +469,30 @@ template <class W> __global__ void __launch_bounds__(1024) layer_norm_join_kerne
 }
 
 // --------------------------------------------- gradient of act(g) u
-// A 64 x 64 tile of (rows, hidden), 4 x 4 elements a thread with all loads issued
+// A 64 x 64 tile of (rows, hidden), 2 x 4 elements a thread (more would only make
+// its code longer, and a short call waits for code too) with all loads issued
 // before the first is used: dg and du go out row-major, and transposed through
 // LDS.  Both outputs' rows are padded to 16 bytes with zeros, so that the
 // products may read them in whole pieces.
-template <int DT, int ACT> __global__ void __launch_bounds__(kThreads) gated_grad_kernel(GatedGradArgs a)
+constexpr int kGradThreads = 512;
+template <int DT, int ACT> __global__ void __launch_bounds__(kGradThreads) gated_grad_kernel(GatedGradArgs a)
 {
     using T = typename Elem<DT>::T;
     typedef T T4 __attribute__((ext_vector_type(4)));
+    typedef T T2 __attribute__((ext_vector_type(2)));
+    constexpr int ROWS = 64 * 16 / kGradThreads;
     constexpr int PITCH = 68;                      // elements of a transposed row: 8-byte pieces on spread banks
     __shared__ __attribute__((aligned(16))) T tile[2][64][PITCH];
     const int htiles = (a.hidden + 63) / 64;
     const int h0 = (int)(blockIdx.x % htiles) * 64, r0 = (int)(blockIdx.x / htiles) * 64;
     if (blockIdx.x == 0)
-        for (int k = threadIdx.x; k < a.nflags; k += kThreads) a.flags[k] = 0u;
-    const int c = (int)(threadIdx.x & 15) * 4, h = h0 + c, q = (int)(threadIdx.x >> 4) * 4;
+        for (int k = threadIdx.x; k < a.nflags; k += kGradThreads) a.flags[k] = 0u;
+    const int c = (int)(threadIdx.x & 15) * 4, h = h0 + c, q = (int)(threadIdx.x >> 4) * ROWS;
     const bool whole = h + 4 <= a.hidden;
-    f32x4_t g[4], u[4];
-    T4 d[4];
+    f32x4_t g[ROWS], u[ROWS];
+    T4 d[ROWS];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < ROWS; ++k) {
         g[k] = u[k] = f32x4_t{};
         d[k] = T4{};
         const int r = r0 + q + k;
@@ -509,9 +513,9 @@ template <int DT, int ACT> __global__ void __launch_bounds__(kThreads) gated_gra
                 }
         }
     }
-    T4 dg[4], du[4];
+    T4 dg[ROWS], du[ROWS];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < ROWS; ++k) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float value, slope;
@@ -540,14 +544,14 @@ template <int DT, int ACT> __global__ void __launch_bounds__(kThreads) gated_gra
     // rows past the edge hold d = 0: their dg and du are the transposed padding
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-        const T4 x = {dg[0][e], dg[1][e], dg[2][e], dg[3][e]}, y = {du[0][e], du[1][e], du[2][e], du[3][e]};
-        *reinterpret_cast<T4*>(&tile[0][c + e][q]) = x;
-        *reinterpret_cast<T4*>(&tile[1][c + e][q]) = y;
+        const T2 x = {dg[0][e], dg[1][e]}, y = {du[0][e], du[1][e]};
+        *reinterpret_cast<T2*>(&tile[0][c + e][q]) = x;
+        *reinterpret_cast<T2*>(&tile[1][c + e][q]) = y;
     }
     __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const int p = k * kThreads + (int)threadIdx.x, half = p >> 9, hh = (p >> 3) & 63, rr = (p & 7) * 8;
+    for (int k = 0; k < 1024 / kGradThreads; ++k) {
+        const int p = k * kGradThreads + (int)threadIdx.x, half = p >> 9, hh = (p >> 3) & 63, rr = (p & 7) * 8;
         if (h0 + hh >= a.hidden || r0 + rr >= a.rows) continue;
         const T4* from = reinterpret_cast<const T4*>(&tile[half][hh][rr]);
         T* out = static_cast<T*>(a.dgu_t) + ((size_t)(h0 + hh) + (half ? (size_t)a.hidden : 0)) * (size_t)a.ld_t + r0 + rr;
@@ -786,7 +790,7 @@ hipError_t launch_gated_grad(const GatedGradArgs& a, int dt, hipStream_t stream)
 {
     const dim3 grid((unsigned)((a.hidden + 63) / 64) * (unsigned)((a.rows + 63) / 64));
     const auto go = [&](auto dtype, auto act) {
-        return start(&gated_grad_kernel<decltype(dtype)::value, decltype(act)::value>, grid, kThreads, stream, a);
+        return start(&gated_grad_kernel<decltype(dtype)::value, decltype(act)::value>, grid, kGradThreads, stream, a);
     };
     const auto with = [&](auto dtype) {
         switch (a.act) {
