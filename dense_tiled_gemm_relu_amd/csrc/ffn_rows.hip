@@ -371,6 +371,92 @@ layer_norm_backward_kernel(NormArgs a)
     }
 }
 
+// Few rows: the whole backward pass in one launch, since a second one would take
+// longer than the work (256 x 4096 bf16 4.1 us against 8.7 in two launches; 512 x
+// 1001 5.4 against 8.0; 1024 x 256 8.1 against 6.3).  The first workgroups take rows (as many waves a row as it
+// has chunks for, rounded up to a power of two) and write dx; the others take 64
+// columns each over all rows, which they read a second time from the L2, and write
+// dweight and dbias.
+constexpr int kFewRows = 512;
+template <class T, class W, int V>
+__global__ void __launch_bounds__(1024) layer_norm_backward_few_kernel(NormArgs a, int row_blocks, int waves)
+{
+    constexpr int N = Chunk<T>::N;
+    using X = typename Chunk<T>::Vec;
+    using WV = typename VecN<W, N>::Vec;
+    __shared__ float lds[2][16][64];
+    const int lane = (int)(threadIdx.x & 63), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    typedef const __attribute__((address_space(4))) float* Scalars;
+    const Scalars means = (Scalars)(uintptr_t)a.mean, rstds = (Scalars)(uintptr_t)a.rstd;
+    if ((int)blockIdx.x < row_blocks) {
+        const int rows_here = 16 / waves, first = wave & ~(waves - 1);
+        const int wanted = (int)blockIdx.x * rows_here + wave / waves, row = min(wanted, a.rows - 1);
+        const RowMap<T, V> map(a.cols, (wave - first) * 64 + lane, 64 * waves);
+        const T* x = static_cast<const T*>(a.x) + (size_t)row * (size_t)a.x_stride;
+        const T* d = static_cast<const T*>(a.dy) + (size_t)row * (size_t)a.dy_stride;
+        float xhat[V][N], c[V][N], s0 = 0.0f, s1 = 0.0f;
+        const float mean = means[row], rstd = rstds[row];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            const X xv = load_vec<X>(x + map.start[v]), dv = load_vec<X>(d + map.start[v]);
+            const WV w = load_vec<WV>(static_cast<const W*>(a.w) + map.start[v]);
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                xhat[v][e] = ((float)xv[e] - mean) * rstd;
+                c[v][e] = (float)dv[e] * (float)w[e];
+                const float own = map.owns(v, e) ? c[v][e] : 0.0f;
+                s0 += own;
+                s1 = fmaf(own, map.owns(v, e) ? xhat[v][e] : 0.0f, s1);
+            }
+        }
+        s0 = wave_all<Sum>(s0);
+        s1 = wave_all<Sum>(s1);
+        if (lane == 0) {
+            lds[0][wave][0] = s0;
+            lds[1][wave][0] = s1;
+        }
+        __syncthreads();
+        s0 = s1 = 0.0f;
+        for (int k = 0; k < waves; ++k) {
+            s0 += lds[0][first + k][0];
+            s1 += lds[1][first + k][0];
+        }
+        const float inv_n = 1.0f / (float)a.cols;
+        s0 *= inv_n * rstd;
+        s1 *= inv_n * rstd;
+        T* dx = static_cast<T*>(a.dx) + (size_t)row * (size_t)a.cols;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (map.has(v) && wanted < a.rows) {
+                X out;
+#pragma unroll
+                for (int e = 0; e < N; ++e) out[e] = (T)fmaf(-xhat[v][e], s1, fmaf(c[v][e], rstd, -s0));
+                __builtin_memcpy(dx + map.start[v], &out, sizeof out);
+            }
+        return;
+    }
+    const int j = ((int)blockIdx.x - row_blocks) * 64 + lane, col = min(j, a.cols - 1);
+    float dw = 0.0f, db = 0.0f;
+#pragma unroll 4
+    for (int r = wave; r < a.rows; r += 16) {
+        const float g = (float)static_cast<const T*>(a.dy)[(size_t)r * (size_t)a.dy_stride + col];
+        const float v = (float)static_cast<const T*>(a.x)[(size_t)r * (size_t)a.x_stride + col];
+        dw = fmaf(g, (v - means[r]) * rstds[r], dw);
+        db += g;
+    }
+    lds[0][wave][lane] = dw;
+    lds[1][wave][lane] = db;
+    __syncthreads();
+    if (wave > 1 || j >= a.cols) return;
+    float s = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) s += lds[wave][k][lane];
+    if (wave == 0)
+        static_cast<W*>(a.dw)[j] = (W)s;
+    else if (a.db)
+        static_cast<W*>(a.db)[j] = (W)s;
+}
+
 // ---- rows shorter than a chunk, or longer than 512 threads hold: one workgroup
 // a row, read once per use (a long row's second and third reads come from L2)
 template <class T, class W> __global__ void __launch_bounds__(kThreads) layer_norm_any_kernel(NormArgs a)
@@ -767,6 +853,14 @@ hipError_t launch_layer_norm_backward(const NormArgs& a, int dt, int wdt, hipStr
         // one chunk a thread as long as 1024 threads hold the row: a thread keeps
         // two fp32 sums a column beside the row and the weight
         const int chunks = row_chunks(a.cols, sizeof(T)), waves = (int)ceil_div(chunks, 64);
+        if (a.rows > 0 && a.rows <= kFewRows && chunks > 0 && waves <= 32) {
+            int per_row = 1;
+            while (per_row < waves && per_row < 16) per_row *= 2;
+            const int row_blocks = (int)ceil_div(a.rows, 16 / per_row);
+            const dim3 grid((unsigned)(row_blocks + ceil_div(a.cols, 64)));
+            return waves <= 16 ? start(&layer_norm_backward_few_kernel<T, W, 1>, grid, 1024, stream, a, row_blocks, per_row)
+                               : start(&layer_norm_backward_few_kernel<T, W, 2>, grid, 1024, stream, a, row_blocks, per_row);
+        }
         if (a.rows > 0 && chunks > 0 && waves <= 32) {
             const auto go = [&](auto kernel, int threads) { return start(kernel, dim3(strips), threads, stream, a); };
             e = waves == 1   ? go(&layer_norm_backward_kernel<T, W, 1, 1>, kThreads)
