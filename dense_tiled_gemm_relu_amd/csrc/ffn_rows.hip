@@ -205,29 +205,30 @@ template <class T, class W, int G, int V> __global__ void __launch_bounds__(kGro
 // The backward pass in one read of dy and x: the row's two sums and dx, and the
 // thread's columns of dweight and dbias, summed in registers over its rows.  A
 // workgroup leaves one strip of partial sums; a second kernel joins the strips in
-// order.  WAVES = 1: four rows a workgroup, one wave each; else the workgroup, of
-// as many waves as the row has chunks for, at most WAVES, takes one row at a time.
+// order.  ONE: four rows a workgroup, one wave each; else `waves` waves a row, as
+// many as it has chunks for, and as many rows at a time as 16 waves hold.
 //
 // A row takes a trip to memory, two sums over the group and a store, and a CU
 // holds few rows at a time (the sums fill its registers), so the rows to come are
 // copied ahead into LDS, RING of them: each lane's own 16 bytes, which no other
 // lane reads, so the only wait is the wave's own.  What is left is the vector
 // instructions: about 13 an element.
-template <class T, class W, int WAVES, int V>
-__global__ void __launch_bounds__(WAVES == 1 ? kThreads : 64 * WAVES) __attribute__((amdgpu_waves_per_eu(4)))
-layer_norm_backward_kernel(NormArgs a)
+template <class T, class W, bool ONE, int V>
+__global__ void __launch_bounds__(ONE ? kThreads : 1024) __attribute__((amdgpu_waves_per_eu(4)))
+layer_norm_backward_kernel(NormArgs a, int waves)
 {
     constexpr int N = Chunk<T>::N;
-    constexpr bool ONE = WAVES == 1;
     using X = typename Chunk<T>::Vec;
     using WV = typename VecN<W, N>::Vec;
     constexpr int RING = V == 1 ? 4 : 2, ROW_BYTES = 2 * V * 1024;       // of a wave
-    constexpr int RINGS = ONE ? kThreads / 64 : WAVES;
+    constexpr int RINGS = ONE ? kThreads / 64 : 16;
     __shared__ __attribute__((aligned(1024))) unsigned char rows_raw[RINGS * RING * ROW_BYTES];
     __shared__ float lds[2][2][16];
-    static_assert(!ONE || 3 * 64 * N * V * 4 <= RINGS * RING * ROW_BYTES, "the waves' sums fit the rings");
+    static_assert(RINGS * 64 * N * V * 4 <= RINGS * RING * ROW_BYTES, "the waves' sums fit the rings");
     const int lane = (int)(threadIdx.x & 63), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const RowMap<T, V> map(a.cols, ONE ? lane : (int)threadIdx.x, ONE ? 64 : (int)blockDim.x);
+    const int groups = ONE ? RINGS : (int)(blockDim.x >> 6) / waves, group = ONE ? wave : wave / waves;
+    const int in_row = ONE ? 0 : wave - group * waves;                    // the wave's place in its row
+    const RowMap<T, V> map(a.cols, in_row * 64 + lane, ONE ? 64 : 64 * waves);
     WV w[V];
     float dw[V][N], db[V][N];
 #pragma unroll
@@ -236,10 +237,9 @@ layer_norm_backward_kernel(NormArgs a)
 #pragma unroll
         for (int e = 0; e < N; ++e) dw[v][e] = db[v][e] = 0.0f;
     }
-    // sums of waves that are not there
-    if (!ONE && threadIdx.x < 64) lds[threadIdx.x >> 5][(threadIdx.x >> 4) & 1][threadIdx.x & 15] = 0.0f;
-    const int64_t step = (int64_t)gridDim.x * (ONE ? RINGS : 1);
-    int64_t row = ONE ? (int64_t)blockIdx.x * RINGS + wave : (int64_t)blockIdx.x;
+    const int64_t step = (int64_t)gridDim.x * groups;
+    int64_t row = (int64_t)blockIdx.x * groups + group;
+    const int64_t first_row = row - group;
     GR_LDS unsigned char* const ring = (GR_LDS unsigned char*)rows_raw + wave * RING * ROW_BYTES;
     // row r (the last one in place of those past it) to a slot; a missing chunk is
     // the row's last
@@ -259,14 +259,18 @@ layer_norm_backward_kernel(NormArgs a)
     // the weight has arrived here, so that no load but the copies is waited for below
 #pragma unroll
     for (int v = 0; v < V; ++v) stay_packed(w[v]);
-    if (!ONE) __syncthreads();
     const float inv_n = 1.0f / (float)a.cols;
     // one value for the whole wave: read through the scalar cache
     typedef const __attribute__((address_space(4))) float* Scalars;
     const Scalars means = (Scalars)(uintptr_t)a.mean, rstds = (Scalars)(uintptr_t)a.rstd;
     int slot = 0;
-    for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
-        const float mean = means[row], rstd = rstds[row];
+    // all rows of a workgroup meet at one barrier, so a row past the end runs along
+    // with nothing to add and nothing to store
+    const int64_t behind = ONE ? 0 : row - first_row;
+    for (int turn = 0; row - behind < a.rows; row += step, turn ^= 1) {
+        const bool live = ONE || row < a.rows;
+        const int64_t at = min(row, (int64_t)a.rows - 1);
+        const float mean = means[at], rstd = rstds[at];
         // behind this row's copies are those of RING - 1 rows; the stores between
         // them only make the wait stricter
         __builtin_amdgcn_s_waitcnt(waitcnt_vm((RING - 1) * 2 * V));
@@ -294,8 +298,10 @@ layer_norm_backward_kernel(NormArgs a)
                 const float g = (float)d[v][e];
                 xhat[v][e] = ((float)x[v][e] - mean) * rstd;
                 c[v][e] = g * (float)w[v][e];
-                dw[v][e] = fmaf(g, xhat[v][e], dw[v][e]);
-                db[v][e] += g;
+                if (live) {
+                    dw[v][e] = fmaf(g, xhat[v][e], dw[v][e]);
+                    db[v][e] += g;
+                }
                 const float own = map.owns(v, e) ? c[v][e] : 0.0f;
                 s0 += own;
                 s1 = fmaf(own, map.owns(v, e) ? xhat[v][e] : 0.0f, s1);
@@ -311,14 +317,15 @@ layer_norm_backward_kernel(NormArgs a)
             // lane 0 and lane 32 hold the wave's; 16 lanes each add the waves'
             if ((lane & 31) == 0) lds[turn][lane >> 5][wave] = s;
             __syncthreads();
-            s = row16_sum(lds[turn][lane >> 5][lane & 15]);
+            const int k = lane & 15;
+            s = row16_sum(k < waves ? lds[turn][lane >> 5][group * waves + k] : 0.0f);
         }
         s0 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, s), 0)) * inv_n * rstd;
         s1 = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, s), 32)) * inv_n * rstd;
         T* dx = static_cast<T*>(a.dx) + (size_t)row * (size_t)a.cols;
 #pragma unroll
         for (int v = 0; v < V; ++v)
-            if (map.has(v)) {
+            if (map.has(v) && live) {
                 X out;
 #pragma unroll
                 for (int e = 0; e < N; ++e) out[e] = (T)fmaf(-xhat[v][e], s1, fmaf(c[v][e], rstd, -s0));
@@ -329,29 +336,27 @@ layer_norm_backward_kernel(NormArgs a)
     // again or given back
     __builtin_amdgcn_s_waitcnt(waitcnt_vm(0));
     asm volatile("" ::: "memory");
-    // one wave a row: the four waves' sums join first
+    // the groups' sums join first, in order
     GR_LDS float* const part = (GR_LDS float*)rows_raw;
+    const int per_row = ONE ? 1 : waves;
     float* strip = a.partial + (size_t)blockIdx.x * 2 * (size_t)a.cols;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
         float(&own)[V][N] = half ? db : dw;
-        if constexpr (ONE) {
-            __syncthreads();
-            if (wave) {
-#pragma unroll
-                for (int v = 0; v < V; ++v)
-#pragma unroll
-                    for (int e = 0; e < N; ++e) part[(((wave - 1) * V + v) * N + e) * 64 + lane] = own[v][e];
-            }
-            __syncthreads();
-            if (wave) continue;
+        __syncthreads();
+        if (group) {
 #pragma unroll
             for (int v = 0; v < V; ++v)
 #pragma unroll
-                for (int e = 0; e < N; ++e)
-#pragma unroll
-                    for (int k = 0; k < 3; ++k) own[v][e] += part[((k * V + v) * N + e) * 64 + lane];
+                for (int e = 0; e < N; ++e) part[((wave * V + v) * N + e) * 64 + lane] = own[v][e];
         }
+        __syncthreads();
+        if (group) continue;
+        for (int k = 1; k < groups; ++k)
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int e = 0; e < N; ++e) own[v][e] += part[(((k * per_row + in_row) * V + v) * N + e) * 64 + lane];
 #pragma unroll
         for (int v = 0; v < V; ++v)
             if (map.has(v)) {
@@ -537,8 +542,16 @@ template <class W> __global__ void __launch_bounds__(1024) layer_norm_join_kerne
         const int64_t j = j0 + lane;
         float s = 0.0f;
         if (j < all) {
-#pragma unroll 8
-            for (int k = wave; k < strips; k += 16) s += a.partial[(size_t)k * (size_t)all + j];
+            // a wave's strips in batches of 8, all loads of one in flight together
+            // (strips past the end are the last one's, and count for nothing)
+            for (int k = wave; k < strips; k += 16 * 8) {
+                float v[8];
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    v[u] = a.partial[(size_t)min(k + 16 * u, strips - 1) * (size_t)all + j];
+#pragma unroll
+                for (int u = 0; u < 8; ++u) s += k + 16 * u < strips ? v[u] : 0.0f;
+            }
         }
         part[wave][lane] = s;
         __syncthreads();
@@ -837,10 +850,12 @@ hipError_t launch_layer_norm(const NormArgs& a, int dt, int wdt, hipStream_t str
     });
 }
 
-// workgroups of the backward pass, each of which leaves one strip of sums
+// Workgroups of the backward pass, each of which leaves one strip of sums: one a
+// CU (4097 x 3001 25 us, 32 with two), and two where a wave holds a row (12000 x 300
+// 14.6 us, 15.5 with one).
 int layer_norm_strips(int64_t rows, int64_t cols)
 {
-    return rows == 0 ? 0 : even_grid(rows, cols <= 512 ? 4 : 2, cols <= 512 ? 512 : 256);
+    return rows == 0 ? 0 : even_grid(rows, cols <= 256 ? 4 : 2, cols <= 256 ? 512 : 256);
 }
 
 hipError_t launch_layer_norm_backward(const NormArgs& a, int dt, int wdt, hipStream_t stream)
@@ -862,12 +877,11 @@ hipError_t launch_layer_norm_backward(const NormArgs& a, int dt, int wdt, hipStr
                                : start(&layer_norm_backward_few_kernel<T, W, 2>, grid, 1024, stream, a, row_blocks, per_row);
         }
         if (a.rows > 0 && chunks > 0 && waves <= 32) {
-            const auto go = [&](auto kernel, int threads) { return start(kernel, dim3(strips), threads, stream, a); };
-            e = waves == 1   ? go(&layer_norm_backward_kernel<T, W, 1, 1>, kThreads)
-                : waves <= 4  ? go(&layer_norm_backward_kernel<T, W, 4, 1>, 64 * waves)
-                : waves <= 8  ? go(&layer_norm_backward_kernel<T, W, 8, 1>, 64 * waves)
-                : waves <= 16 ? go(&layer_norm_backward_kernel<T, W, 16, 1>, 64 * waves)
-                              : go(&layer_norm_backward_kernel<T, W, 16, 2>, 32 * (waves + (waves & 1)));
+            const int per_row = waves <= 16 ? waves : (waves + 1) / 2;
+            const auto go = [&](auto kernel, int threads) { return start(kernel, dim3(strips), threads, stream, a, per_row); };
+            e = waves == 1   ? go(&layer_norm_backward_kernel<T, W, true, 1>, kThreads)
+                : waves <= 16 ? go(&layer_norm_backward_kernel<T, W, false, 1>, 64 * waves * (16 / waves))
+                              : go(&layer_norm_backward_kernel<T, W, false, 2>, 64 * per_row);
         } else if (a.rows > 0) {
             const int strip_rows = (int)ceil_div(a.rows, strips);
             e = start(&layer_norm_dx_any_kernel<T, W>, dim3(any_grid(a.rows)), kThreads, stream, a);
