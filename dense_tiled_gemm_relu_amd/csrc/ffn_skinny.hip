@@ -14,6 +14,11 @@
 // The operand's order (16 rows, 16 bytes each) reads the L2 at 9-16 TB/s, and at
 // 2.4 TB/s where rows do not start at a multiple of 4 bytes; whole row pieces
 // come at 22 TB/s, and at 12-15 TB/s from any address.
+//
+// Measured: one token on 7168 x 4096 gated bf16 weights 22 us (5.3 TB/s; 26 on 64 x
+// 64 tiles), on 8192 x 8192 8-bit weights 11.3 (5.9 TB/s; 17); 64 x 1000 x 4096 gated
+// 8.9 (18.1), 128 x 1000 x 1000 8-bit 3.4 (9.3).  Above about 64 rows of a wide
+// weight the tiles' fewer bytes from the L2 win: 64 x 8192 x 8192 gated 89 against 60.
 #include "api_common.hpp"
 #include "ffn.hpp"
 

@@ -11,7 +11,8 @@ contiguous, or 2-D with contiguous rows any distance apart.  Results are new
 contiguous tensors.  The kernels run on ``stream`` (a torch.cuda.Stream, a raw
 hipStream_t, or None for torch's current stream); results and workspaces are
 allocated for that stream.  A tensor made on another stream has to be ready
-before the call, as with any torch operation.
+before the call, as with any torch operation.  Results carry no autograd graph: a
+backward function is a call of its own.
 """
 import ctypes
 import importlib.machinery
