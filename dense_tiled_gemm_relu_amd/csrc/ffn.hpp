@@ -26,10 +26,10 @@ __device__ __forceinline__ void copy_to_lds(const unsigned char* from, uint32_t 
 // The tiles of the GEMM + ReLU, with the epilogues of the feed-forward operators;
 // BK in a name counts 16-bit elements, as there.  LIN_128 has four stages and a
 // CU to itself, LIN_128X2 two and half a CU, LIN_64 four and half a CU; with B
-// stored (K,N), LIN_64 can cut a tile's K into parts.  LIN_K16 and LIN_K32
-// (ffn_skinny.hip: K cut between a workgroup's waves) serve only products with B
+// stored (K,N), LIN_64 can cut a tile's K into parts.  LIN_K16 and the others of
+// ffn_skinny.hip (K cut between a workgroup's waves) serve only products with B
 // stored (N,K).
-enum LinearConfig : int { LIN_256 = 0, LIN_128, LIN_128X2, LIN_64, LIN_G64, LIN_K16, LIN_K32, LIN_COUNT };
+enum LinearConfig : int { LIN_256 = 0, LIN_128, LIN_128X2, LIN_64, LIN_G64, LIN_K16, LIN_K32, LIN_K32X48, LIN_K48X32, LIN_COUNT };
 
 struct LinearInfo {
     const char* name;
@@ -41,7 +41,7 @@ inline const LinearInfo& linear_info(int cfg)
     static const LinearInfo table[LIN_COUNT] = {
         {"d256x256x32_s4_i16w8", 256, 256}, {"d128x128x64_s4_i16w8", 128, 128}, {"d128x128x64_s2w8", 128, 128},
         {"d64x64x64_s4", 64, 64},           {"g64x64x64", 64, 64},              {"k16x16x64_s4", 16, 16},
-        {"k32x32x64_s4", 32, 32},
+        {"k32x32x64_s4", 32, 32},           {"k32x48x64_s3", 32, 48},       {"k48x32x64_s3", 48, 32},
     };
     return table[cfg];
 }

@@ -98,6 +98,8 @@ TileTime tile_time(int cfg)
     case LIN_64: return {5.2, 2000, 2 * kNumCUs, 0.55};
     case LIN_K16: return {1.2, 1000, 2 * kNumCUs, 0.6};
     case LIN_K32: return {1.4, 800, kNumCUs, 1.0};
+    case LIN_K32X48:
+    case LIN_K48X32: return {1.75, 900, kNumCUs, 1.0};
     default: return {15.0, 4000, 2 * kNumCUs, 0.6};      // LIN_G64
     }
 }
@@ -137,7 +139,7 @@ LinearPlan plan_as(int cfg, const Linear& l)
 LinearPlan plan_linear(const Linear& l)
 {
     int best = LIN_G64;
-    for (int cfg : {LIN_K16, LIN_K32, LIN_64, LIN_128, LIN_128X2, LIN_256})
+    for (int cfg : {LIN_K16, LIN_K32, LIN_K32X48, LIN_K48X32, LIN_64, LIN_128, LIN_128X2, LIN_256})
         if (usable(cfg, l) && (best == LIN_G64 || linear_time(cfg, l) < linear_time(best, l))) best = cfg;
     return plan_as(best, l);
 }

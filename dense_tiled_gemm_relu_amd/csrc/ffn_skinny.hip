@@ -19,6 +19,9 @@
 // 64 tiles), on 8192 x 8192 8-bit weights 11.3 (5.9 TB/s; 17); 64 x 1000 x 4096 gated
 // 8.9 (18.1), 128 x 1000 x 1000 8-bit 3.4 (9.3).  Above about 64 rows of a wide
 // weight the tiles' fewer bytes from the L2 win: 64 x 8192 x 8192 gated 89 against 60.
+// 32 x 48 and 48 x 32 are for what just misses one round of smaller ones: 77 x 3001 x
+// 5003 8-bit 13.3 against 19, 100 x 3000 x 3000 7.2 against 10; elsewhere they are
+// slower (64 x 4096 x 8192 10.4 against 9.2).
 #include "api_common.hpp"
 #include "ffn.hpp"
 
@@ -213,6 +216,8 @@ template <int IN, int OUT, int EPI> LinearLaunchFn pick(int cfg)
     switch (cfg) {
     case LIN_K16: return &launch<IN, OUT, EPI, 1, 1, 128, 4>;
     case LIN_K32: return &launch<IN, OUT, EPI, 2, 2, 128, 4>;
+    case LIN_K32X48: return &launch<IN, OUT, EPI, 2, 3, 128, 3>;
+    case LIN_K48X32: return &launch<IN, OUT, EPI, 3, 2, 128, 3>;
     default: return nullptr;
     }
 }

@@ -10,8 +10,11 @@ def test_every_configuration_is_reached():
     lib = gr.library()
     gated = {lib.gemm_relu_gated_plan(m, n, k, gr.F16) for m, n, k in itertools.product(SIZES, SIZES, SIZES)}
     i8 = {lib.gemm_relu_i8_plan(m, n, k, gr.F16) for m, n, k in itertools.product(SIZES, SIZES, SIZES)}
+    for sizes in ((100, 3000, 3000), (40, 7000, 3000)):           # just over a round of 32 x 32 tiles
+        i8.add(lib.gemm_relu_i8_plan(*sizes, gr.F16))
+        gated.add(lib.gemm_relu_gated_plan(sizes[0], sizes[1] // 2, sizes[2], gr.F16))
     tiles = {b"d256x256x32_s4_i16w8", b"d128x128x64_s4_i16w8", b"d128x128x64_s2w8", b"d64x64x64_s4"}
-    assert gated == i8 == tiles | {b"k16x16x64_s4", b"k32x32x64_s4"}
+    assert gated == i8 == tiles | {b"k16x16x64_s4", b"k32x32x64_s4", b"k32x48x64_s3", b"k48x32x64_s3"}
     back = set()
     for m, n, k in itertools.product(SIZES, SIZES, SIZES):
         back.update(lib.gemm_relu_gated_backward_plan(m, n, k, gr.BF16).split(b","))
