@@ -80,6 +80,16 @@ def _load():
     return ops
 
 
+def _as_torch_stream(stream, index):
+    """`stream` as a torch stream of GPU `index`.  0 is the handle of the default
+    stream; ExternalStream would take it for "none given" and hand out a stream of
+    torch's pool, which waits for nothing."""
+    import torch
+    if not isinstance(stream, int):
+        return stream
+    return torch.cuda.ExternalStream(stream, device=index) if stream else torch.cuda.default_stream(index)
+
+
 def _call(name, stream, *args):
     """One call of the front end: on the tensors' GPU and `stream`, both made
     current for the allocations and the launches."""
@@ -92,8 +102,7 @@ def _call(name, stream, *args):
     with torch.cuda.device(index):
         if stream is None:
             return getattr(ops, name)(*args, _raw_stream(index))
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=index)
+        stream = _as_torch_stream(stream, index)
         with torch.cuda.stream(stream):
             out = getattr(ops, name)(*args, stream.cuda_stream)
         # the caller may drop an input while the stream still reads it
