@@ -466,54 +466,126 @@ __global__ void __launch_bounds__(1024) layer_norm_backward_few_kernel(NormArgs 
         static_cast<W*>(a.db)[j] = (W)s;
 }
 
-// ---- rows shorter than a chunk, or longer than 512 threads hold: one workgroup
+// ---- rows shorter than a chunk, or longer than 1024 threads hold: one workgroup
 // a row, read once per use (a long row's second and third reads come from L2)
-template <class T, class W> __global__ void __launch_bounds__(kThreads) layer_norm_any_kernel(NormArgs a)
+
+// use(j, load(j)) for every column j of a thread, the loads of a batch in flight
+// together.  64-bit columns: the last one's successors may pass 2^31.  SHORT: at most
+// one column a thread (the same kernels without their loops, whose registers would
+// cost such rows a third: 100000 x 5 bf16 85 us against 66).
+constexpr int kBatch = 16;
+template <bool SHORT, class L, class U, class E>
+__device__ __forceinline__ void each_column(int cols, L&& load, U&& use, E&& end_of_batch)
 {
-    __shared__ float lds[2][4];
+    if constexpr (SHORT) {
+        if ((int)threadIdx.x < cols) use((int64_t)threadIdx.x, load((int64_t)threadIdx.x));
+        end_of_batch();
+        return;
+    }
+    int64_t j = threadIdx.x;
+    for (; j + (kBatch - 1) * kThreads < cols; j += kBatch * kThreads) {
+        decltype(load(j)) v[kBatch];
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) v[u] = load(j + u * kThreads);
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) use(j + u * kThreads, v[u]);
+        end_of_batch();
+    }
+    for (; j < cols; j += kThreads) use(j, load(j));
+    end_of_batch();
+}
+template <bool SHORT, class L, class U> __device__ __forceinline__ void each_column(int cols, L&& load, U&& use)
+{
+    each_column<SHORT>(cols, load, use, [] {});
+}
+// Means over a row of load(j)'s SUMS values: a batch in fp32, the batches in
+// binary64 (a row may have 2^31 elements, millions a thread, and an fp32 sum of so
+// many stops growing).  lds holds one of two buffers, as in group_all.
+template <int SUMS> struct Values {
+    float v[SUMS];
+};
+template <int SUMS> struct RowSums {
+    double v[SUMS];
+};
+template <bool SHORT, int SUMS, class L> __device__ __forceinline__ Values<SUMS> row_means(int cols, L&& load, RowSums<SUMS>* lds)
+{
+    if constexpr (SHORT) {
+        Values<SUMS> one{};
+        if ((int)threadIdx.x < cols) one = load((int64_t)threadIdx.x);
+#pragma unroll
+        for (int k = 0; k < SUMS; ++k)
+            one.v[k] = group_all<kThreads, Sum>(one.v[k], reinterpret_cast<float*>(lds) + k * (kThreads / 64)) / (float)cols;
+        return one;
+    }
+    RowSums<SUMS> all{};
+    Values<SUMS> part{};
+    each_column<SHORT>(
+        cols, load,
+        [&](int64_t, Values<SUMS> v) {
+#pragma unroll
+            for (int k = 0; k < SUMS; ++k) part.v[k] += v.v[k];
+        },
+        [&] {
+#pragma unroll
+            for (int k = 0; k < SUMS; ++k) all.v[k] += (double)part.v[k];
+            part = Values<SUMS>{};
+        });
+#pragma unroll
+    for (int k = 0; k < SUMS; ++k)
+#pragma unroll
+        for (int step = 1; step < 64; step *= 2) all.v[k] += __shfl_xor(all.v[k], step);
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = all;
+    __syncthreads();
+    all = lds[0];
+#pragma unroll
+    for (int w = 1; w < kThreads / 64; ++w)
+#pragma unroll
+        for (int k = 0; k < SUMS; ++k) all.v[k] += lds[w].v[k];
+#pragma unroll
+    for (int k = 0; k < SUMS; ++k) part.v[k] = (float)(all.v[k] / cols);
+    return part;
+}
+template <class T, class W, bool SHORT> __global__ void __launch_bounds__(kThreads) layer_norm_any_kernel(NormArgs a)
+{
+    __shared__ RowSums<1> lds[2][kThreads / 64];
     const W* w = static_cast<const W*>(a.w);
     const W* b = static_cast<const W*>(a.b);
     for (size_t row = blockIdx.x; row < (size_t)a.rows; row += gridDim.x) {
         const T* x = static_cast<const T*>(a.x) + row * (size_t)a.x_stride;
         T* y = static_cast<T*>(a.y) + row * (size_t)a.cols;
-        float s = 0.0f;
-        for (int j = threadIdx.x; j < a.cols; j += kThreads) s += (float)x[j];
-        const float mean = group_all<kThreads, Sum>(s, lds[0]) / (float)a.cols;
-        float v = 0.0f;
-        for (int j = threadIdx.x; j < a.cols; j += kThreads) {
+        const float mean = row_means<SHORT, 1>(a.cols, [&](int64_t j) { return Values<1>{(float)x[j]}; }, lds[0]).v[0];
+        const auto square = [&](int64_t j) {
             const float d = (float)x[j] - mean;
-            v += d * d;
-        }
-        const float rstd = 1.0f / sqrtf(group_all<kThreads, Sum>(v, lds[1]) / (float)a.cols + a.eps);
-        for (int j = threadIdx.x; j < a.cols; j += kThreads)
-            y[j] = (T)(((float)x[j] - mean) * rstd * (float)w[j] + (b ? (float)b[j] : 0.0f));
+            return Values<1>{d * d};
+        };
+        const float rstd = 1.0f / sqrtf(row_means<SHORT, 1>(a.cols, square, lds[1]).v[0] + a.eps);
+        each_column<SHORT>(
+            a.cols, [&](int64_t j) { return (T)(((float)x[j] - mean) * rstd * (float)w[j] + (b ? (float)b[j] : 0.0f)); },
+            [&](int64_t j, T v) { y[j] = v; });
         if (threadIdx.x == 0) {
             if (a.mean) a.mean[row] = mean;
             if (a.rstd) a.rstd[row] = rstd;
         }
     }
 }
-template <class T, class W> __global__ void __launch_bounds__(kThreads) layer_norm_dx_any_kernel(NormArgs a)
+template <class T, class W, bool SHORT> __global__ void __launch_bounds__(kThreads) layer_norm_dx_any_kernel(NormArgs a)
 {
-    __shared__ float lds[2][4];
+    __shared__ RowSums<2> lds[2][kThreads / 64];
     const W* w = static_cast<const W*>(a.w);
-    for (size_t row = blockIdx.x; row < (size_t)a.rows; row += gridDim.x) {
+    int turn = 0;
+    for (size_t row = blockIdx.x; row < (size_t)a.rows; row += gridDim.x, turn ^= 1) {
         const T* x = static_cast<const T*>(a.x) + row * (size_t)a.x_stride;
         const T* dy = static_cast<const T*>(a.dy) + row * (size_t)a.dy_stride;
         T* dx = static_cast<T*>(a.dx) + row * (size_t)a.cols;
         const float mean = a.mean[row], rstd = a.rstd[row];
-        float s0 = 0.0f, s1 = 0.0f;
-        for (int j = threadIdx.x; j < a.cols; j += kThreads) {
-            const float c = (float)dy[j] * (float)w[j];
-            s0 += c;
-            s1 += c * (((float)x[j] - mean) * rstd);
-        }
-        s0 = group_all<kThreads, Sum>(s0, lds[0]) / (float)a.cols;
-        s1 = group_all<kThreads, Sum>(s1, lds[1]) / (float)a.cols;
-        for (int j = threadIdx.x; j < a.cols; j += kThreads) {
-            const float c = (float)dy[j] * (float)w[j];
-            dx[j] = (T)(rstd * (c - s0 - ((float)x[j] - mean) * rstd * s1));
-        }
+        const auto c_xhat = [&](int64_t j) { return Values<2>{(float)dy[j] * (float)w[j], ((float)x[j] - mean) * rstd}; };
+        const auto terms = [&](int64_t j) {
+            const Values<2> v = c_xhat(j);
+            return Values<2>{v.v[0], v.v[0] * v.v[1]};
+        };
+        const Values<2> s = row_means<SHORT, 2>(a.cols, terms, lds[turn]);
+        const float s0 = s.v[0], s1 = s.v[1];
+        each_column<SHORT>(a.cols, c_xhat, [&](int64_t j, Values<2> v) { dx[j] = (T)(rstd * (v.v[0] - s0 - v.v[1] * s1)); });
     }
 }
 // Column sums of one strip of rows: thread per column.
@@ -532,7 +604,7 @@ __global__ void __launch_bounds__(kThreads) layer_norm_strip_any_kernel(NormArgs
     }
     float* p = a.partial + (size_t)blockIdx.y * 2 * (size_t)a.cols;
     p[j] = dw;
-    p[a.cols + j] = db;
+    p[(size_t)a.cols + j] = db;
 }
 
 // The strips' sums, in order: 64 columns a workgroup, each of 16 waves takes every
@@ -759,7 +831,7 @@ template <class T, int G, int V> __global__ void __launch_bounds__(kGroupThreads
         if (threadIdx.x % G == 0) a.scale[row] = bad ? NAN : top / 127.0f;
     }
 }
-template <class T> __global__ void __launch_bounds__(kThreads) quantize_rows_any_kernel(QuantArgs a)
+template <class T, bool SHORT> __global__ void __launch_bounds__(kThreads) quantize_rows_any_kernel(QuantArgs a)
 {
     __shared__ unsigned lds[2][4];
     int turn = 0;
@@ -767,11 +839,14 @@ template <class T> __global__ void __launch_bounds__(kThreads) quantize_rows_any
         const T* x = static_cast<const T*>(a.x) + row * (size_t)a.x_stride;
         signed char* q = a.q + row * (size_t)a.cols;
         unsigned most = 0;
-        for (int j = threadIdx.x; j < a.cols; j += kThreads) most = Max::of(most, magnitude<T>(x[j]));
+        each_column<SHORT>(
+            a.cols, [&](int64_t j) { return x[j]; }, [&](int64_t, T v) { most = Max::of(most, magnitude<T>(v)); });
         const float top = from_magnitude<T>(group_all<kThreads, Max>(most, lds[turn]));
         const bool bad = !(top < INFINITY), empty = bad || top == 0.0f;
         const Quantiser quantise(top);
-        for (int j = threadIdx.x; j < a.cols; j += kThreads) q[j] = empty ? (signed char)0 : quantise((float)x[j]);
+        each_column<SHORT>(
+            a.cols, [&](int64_t j) { return x[j]; },
+            [&](int64_t j, T v) { q[j] = empty ? (signed char)0 : quantise((float)v); });
         if (threadIdx.x == 0) a.scale[row] = bad ? NAN : top / 127.0f;
     }
 }
@@ -847,7 +922,9 @@ hipError_t launch_layer_norm(const NormArgs& a, int dt, int wdt, hipStream_t str
     return with_types(dt, wdt, [&](auto x, auto w) {
         using T = decltype(x);
         using W = decltype(w);
-        if (!s.g) return start(&layer_norm_any_kernel<T, W>, dim3(any_grid(a.rows)), kThreads, stream, a);
+        if (!s.g)
+            return start(a.cols <= kThreads ? &layer_norm_any_kernel<T, W, true> : &layer_norm_any_kernel<T, W, false>,
+                         dim3(any_grid(a.rows)), kThreads, stream, a);
         return with_shape(s, [&](auto g, auto v) {
             constexpr int G = decltype(g)::value;
             const int grid = even_grid(a.rows, kGroups<G>, row_groups(a.rows, a.cols, sizeof(T), kGroupThreads<G>));
@@ -890,7 +967,8 @@ hipError_t launch_layer_norm_backward(const NormArgs& a, int dt, int wdt, hipStr
                               : go(&layer_norm_backward_kernel<T, W, false, 2>, 64 * per_row);
         } else if (a.rows > 0) {
             const int strip_rows = (int)ceil_div(a.rows, strips);
-            e = start(&layer_norm_dx_any_kernel<T, W>, dim3(any_grid(a.rows)), kThreads, stream, a);
+            e = start(a.cols <= kThreads ? &layer_norm_dx_any_kernel<T, W, true> : &layer_norm_dx_any_kernel<T, W, false>,
+                      dim3(any_grid(a.rows)), kThreads, stream, a);
             if (e == hipSuccess)
                 e = start(&layer_norm_strip_any_kernel<T, W>, dim3((unsigned)ceil_div(a.cols, kThreads), strips), kThreads,
                           stream, a, strip_rows);
@@ -925,7 +1003,9 @@ hipError_t launch_quantize_rows(const void* x, int64_t x_stride, signed char* q,
     return with_types(dt, dt, [&](auto x0, auto w) {
         using T = decltype(x0);
         if constexpr (std::is_same_v<T, decltype(w)>) {
-            if (!s.g) return start(&quantize_rows_any_kernel<T>, dim3(any_grid(rows)), kThreads, stream, a);
+            if (!s.g)
+                return start(cols <= kThreads ? &quantize_rows_any_kernel<T, true> : &quantize_rows_any_kernel<T, false>,
+                             dim3(any_grid(rows)), kThreads, stream, a);
             return with_shape(s, [&](auto g, auto v) {
                 constexpr int G = decltype(g)::value;
                 const int grid = even_grid(rows, kGroups<G>, row_groups(rows, cols, sizeof(T), kGroupThreads<G>));
