@@ -7,6 +7,8 @@ namespace gemm_relu_hip {
 
 constexpr int kMaxDevices = 64;
 constexpr int kNumCUs = 256;   // MI355X: 8 XCDs x 32 CUs
+// The tiles count K in 32 bits and round it up to a step, of at most 128 elements.
+constexpr int64_t kMaxK = INT32_MAX - 127;
 
 // GEMM_RELU_OK where the current device is a gfx950 (cached per device).
 int check_device();

@@ -370,7 +370,7 @@ extern "C" int gemm_relu_gated(const void* x, int64_t x_stride, const void* weig
                      {x, rows, cols, x_stride, 2}, {weight, 2 * hidden, cols, weight_stride, 2}};
     if (!mats_ok(m, 2)) return GEMM_RELU_EINVAL;
     const RowsPlan r = plan_rows(gated_linear(rows, hidden, cols, x_stride, weight_stride));
-    if (!plan_fits(r.p)) return GEMM_RELU_EUNSUPPORTED;
+    if (cols > kMaxK || !plan_fits(r.p)) return GEMM_RELU_EUNSUPPORTED;
     if (const int dev = check_device()) return dev;
     hipStream_t st = static_cast<hipStream_t>(stream);
     auto go = [&](const LinearPlan& p, const Linear& l, int64_t first) {
@@ -390,6 +390,7 @@ extern "C" const char* gemm_relu_gated_plan(int64_t rows, int64_t hidden, int64_
 {
     if (!gated_sizes_ok(rows, hidden, cols, dtype)) return nullptr;
     if (rows == 0 || hidden == 0) return "none";
+    if (cols > kMaxK) return "unsupported";
     return rows_plan_name(plan_rows(gated_linear(rows, hidden, cols, cols, cols)));
 }
 

@@ -302,6 +302,10 @@ Plan make_plan(const void* A, const void* B, const void* C, int64_t M, int64_t N
         p.status = GEMM_RELU_EINVAL;
         return p;
     }
+    if (K > kMaxK) {
+        p.status = GEMM_RELU_EUNSUPPORTED;
+        return p;
+    }
 
     auto tiles = [&](int id) { return ceil_div(M, config_info(id).bm) * ceil_div(N, config_info(id).bn); };
     // K steps of the 256x256x32 tile (64 elements a step for 8-bit inputs);

@@ -57,7 +57,8 @@ extern "C" {
  *              element is overwritten; nothing is read from C.
  *   M, N, K    sizes, >= 0 and <= INT32_MAX.  M == 0 or N == 0: nothing to do,
  *              returns GEMM_RELU_OK without touching the device.  K == 0: every
- *              element of C becomes +0 (an empty sum).
+ *              element of C becomes +0 (an empty sum).  K <= INT32_MAX - 127, else
+ *              GEMM_RELU_EUNSUPPORTED.
  *   in_dtype   GEMM_RELU_F16, GEMM_RELU_BF16, GEMM_RELU_F8_E4M3 or
  *              GEMM_RELU_F8_E5M2 (A and B share it).
  *   out_dtype  GEMM_RELU_F16, GEMM_RELU_BF16 or GEMM_RELU_F32.
@@ -91,8 +92,9 @@ extern "C" {
  * Errors: GEMM_RELU_EINVAL for negative or too-large sizes, a NULL pointer for
  * an operand that has elements, a misaligned pointer, an unknown dtype code or
  * combination, transB not in {0, 1}, or C overlapping A or B (checked before
- * any HIP call); GEMM_RELU_EUNSUPPORTED when the current device is not gfx950;
- * GEMM_RELU_EHIP when a HIP call fails.  On error nothing is launched.
+ * any HIP call); GEMM_RELU_EUNSUPPORTED when the current device is not gfx950 or
+ * K is above its limit; GEMM_RELU_EHIP when a HIP call fails.  On error nothing is
+ * launched.
  */
 int gemm_relu(const void* A, const void* B, void* C, int64_t M, int64_t N, int64_t K,
               int in_dtype, int out_dtype, int transB, void* stream);

@@ -75,7 +75,8 @@ int gemm_relu_layer_norm_backward(const void* dy, int64_t dy_stride, const void*
  *   g = x Wg^T,  u = x Wu^T,  h = act(g) u      (rows x hidden).
  * dtype (x, weight, h): F16 or BF16.  gu, unless NULL, receives the fp32 sums
  * for the backward pass: rows x 2 hidden, g then u in each row.  2 hidden and
- * every stride <= INT32_MAX.  cols == 0 gives zeros.
+ * every stride <= INT32_MAX; cols <= INT32_MAX - 127, else
+ * GEMM_RELU_EUNSUPPORTED.  cols == 0 gives zeros.
  */
 int gemm_relu_gated(const void* x, int64_t x_stride, const void* weight, int64_t weight_stride,
                     void* h, float* gu, int64_t rows, int64_t hidden, int64_t cols, int dtype,
