@@ -81,6 +81,7 @@ hipError_t launch_layer_norm(const NormArgs& a, int dt, int wdt, hipStream_t str
 int layer_norm_strips(int64_t rows, int64_t cols);
 hipError_t launch_layer_norm_backward(const NormArgs& a, int dt, int wdt, hipStream_t stream);
 
+constexpr int kGradThreads = 512;          // of a workgroup, which takes a 64 x 64 tile
 struct GatedGradArgs {
     const float* gu;        // (rows, 2 hidden)
     const void* dh;

@@ -144,6 +144,10 @@ LinearPlan plan_linear(const Linear& l)
     return plan_as(best, l);
 }
 
+// Workgroups a product's launch may have: a launch's work-items have to stay below
+// 2^32, and a workgroup has up to 512.
+constexpr int64_t kMaxGrid = int64_t(1) << 22;
+
 // A product with B stored (N,K) whose last tile row holds a few rows only: these
 // go to a launch of their own with small tiles where the estimate says so, since
 // the row of mostly empty tiles can cost a whole round (gated 1027 x 2003 x 1501:
@@ -164,6 +168,7 @@ RowsPlan plan_rows(const Linear& l)
         top.M = l.M - rest.M;
         if (top.M == 0 || rest.M == 0 || rest.M > kRestRows || !usable(cfg, l)) continue;
         const LinearPlan q = plan_linear(rest);
+        if (q.grid() > kMaxGrid) continue;
         const double t = linear_time(cfg, top) + linear_time(q.cfg, rest) + 3000.0;    // a second launch
         if (t < best) {
             r = RowsPlan{top, rest, plan_as(cfg, top), q};
@@ -178,12 +183,6 @@ const char* rows_plan_name(const RowsPlan& r)
     static thread_local char names[64];
     std::snprintf(names, sizeof names, "%s+%s", linear_info(r.p.cfg).name, linear_info(r.q.cfg).name);
     return names;
-}
-
-// a launch's work-items stay below 2^32
-bool plan_fits(const LinearPlan& p, const LinearPlan& q = {})
-{
-    return p.grid() + q.grid() <= (int64_t(1) << 22);
 }
 
 KernelArgs linear_args(const LinearPlan& p, const Linear& l, const void* A, const void* B, void* C)
@@ -220,6 +219,9 @@ struct GradPlan {
     uint64_t dgu_t, flags, sums_x, sums_w, bytes;
     int nflags() const { return int((x.splits > 1 ? x.tiles() : 0) + (w.splits > 1 ? w.tiles() : 0)); }
 };
+// of dx and of dweight: a launch of the largest tiles has no room for more (and the
+// workspace's size stays below 2^63)
+constexpr int64_t kMaxGradRows = kMaxGrid * 256;
 constexpr int64_t kSplitStep = 64;         // K elements per step of LIN_64
 
 // p cut into `parts` of whole steps; false where that leaves a part under 4 steps
@@ -370,7 +372,7 @@ extern "C" int gemm_relu_gated(const void* x, int64_t x_stride, const void* weig
                      {x, rows, cols, x_stride, 2}, {weight, 2 * hidden, cols, weight_stride, 2}};
     if (!mats_ok(m, 2)) return GEMM_RELU_EINVAL;
     const RowsPlan r = plan_rows(gated_linear(rows, hidden, cols, x_stride, weight_stride));
-    if (cols > kMaxK || !plan_fits(r.p)) return GEMM_RELU_EUNSUPPORTED;
+    if (cols > kMaxK || r.p.grid() > kMaxGrid) return GEMM_RELU_EUNSUPPORTED;
     if (const int dev = check_device()) return dev;
     hipStream_t st = static_cast<hipStream_t>(stream);
     auto go = [&](const LinearPlan& p, const Linear& l, int64_t first) {
@@ -398,6 +400,7 @@ extern "C" int64_t gemm_relu_gated_backward_workspace(int64_t rows, int64_t hidd
 {
     if (!gated_sizes_ok(rows, hidden, cols, GEMM_RELU_F16)) return GEMM_RELU_EINVAL;
     if (cols == 0) return 0;
+    if (rows > kMaxGradRows || 2 * hidden > kMaxGradRows) return GEMM_RELU_EUNSUPPORTED;
     return int64_t(plan_grad(rows, hidden, cols, cols, cols).bytes);
 }
 
@@ -409,13 +412,13 @@ extern "C" int gemm_relu_gated_backward(const void* dh, int64_t dh_stride, const
     if (!gated_sizes_ok(rows, hidden, cols, dtype) || act < GEMM_RELU_ACT_SILU || act > GEMM_RELU_ACT_RELU)
         return GEMM_RELU_EINVAL;
     if (cols == 0 || (rows == 0 && hidden == 0)) return GEMM_RELU_OK;
+    if (rows > kMaxGradRows || 2 * hidden > kMaxGradRows) return GEMM_RELU_EUNSUPPORTED;
     const GradPlan p = plan_grad(rows, hidden, cols, x_stride, weight_stride);
     const Mat m[] = {dense(dx, rows, cols, 2), dense(dweight, 2 * hidden, cols, 2), bytes_of(workspace, p.bytes),
                      {dh, rows, hidden, dh_stride, 2}, dense(gu, rows, 2 * hidden, 4), {x, rows, cols, x_stride, 2},
                      {weight, 2 * hidden, cols, weight_stride, 2}};
     if (!mats_ok(m, 3) || !workspace_ok(workspace, workspace_bytes, p.bytes)) return GEMM_RELU_EINVAL;
-    if (!plan_fits(p.x, p.w) || p.lx.lda > kLim || p.lw.lda > kLim ||
-        ceil_div(hidden, 64) * ceil_div(rows, 64) > (int64_t(1) << 23))
+    if (p.x.grid() + p.w.grid() > kMaxGrid || ceil_div(hidden, 64) * ceil_div(rows, 64) * kGradThreads >= (int64_t(1) << 32))
         return GEMM_RELU_EUNSUPPORTED;
     if (const int dev = check_device()) return dev;
     hipStream_t st = static_cast<hipStream_t>(stream);
@@ -488,7 +491,7 @@ extern "C" int gemm_relu_i8(const void* x, int64_t x_stride, const float* x_scal
                      dense(x_scale, rows, 1, 4), dense(w_scale, n, 1, 4)};
     if (!mats_ok(m, 1)) return GEMM_RELU_EINVAL;
     const RowsPlan r = plan_rows(Linear{rows, n, k, x_stride, w_stride, true, 1});
-    if (k > kMaxK8 || !plan_fits(r.p)) return GEMM_RELU_EUNSUPPORTED;
+    if (k > kMaxK8 || r.p.grid() > kMaxGrid) return GEMM_RELU_EUNSUPPORTED;
     if (const int dev = check_device()) return dev;
     hipStream_t st = static_cast<hipStream_t>(stream);
     auto go = [&](const LinearPlan& p, const Linear& l, int64_t first) {

@@ -650,7 +650,6 @@ template <class W> __global__ void __launch_bounds__(1024) layer_norm_join_kerne
 // LDS.  Both outputs' rows are padded to 16 bytes with zeros, so that the
 // products may read them in whole pieces.  Bound by HBM: 4096 x 7168 bf16 reads and
 // writes 0.53 GB in 89 us, 5.9 TB/s.
-constexpr int kGradThreads = 512;
 template <int DT, int ACT> __global__ void __launch_bounds__(kGradThreads) gated_grad_kernel(GatedGradArgs a)
 {
     using T = typename Elem<DT>::T;

@@ -22,8 +22,10 @@
  *   - Errors: GEMM_RELU_EINVAL for a bad size, stride, code or alignment, a NULL
  *     pointer to a tensor with elements, a workspace that is too small, or an
  *     output that overlaps an input or another output (checked before any HIP
- *     call); GEMM_RELU_EUNSUPPORTED where the device is no gfx950 or a stated
- *     limit is passed; GEMM_RELU_EHIP when a HIP call fails.
+ *     call); GEMM_RELU_EUNSUPPORTED where the device is no gfx950, a stated limit
+ *     is passed, or a product would take more than 2^22 workgroups (tiles of the
+ *     configuration that its *_plan function names); GEMM_RELU_EHIP when a HIP call
+ *     fails.  Both of the former launch nothing.
  */
 #ifndef GEMM_RELU_FFN_H
 #define GEMM_RELU_FFN_H
@@ -92,7 +94,8 @@ const char* gemm_relu_gated_plan(int64_t rows, int64_t hidden, int64_t cols, int
  *   dg = dh u act'(g),  du = dh act(g),  dx = dg Wg + du Wu,
  *   dweight = [dg^T x; du^T x]                  (2 hidden x cols).
  * dg and du are rounded to dtype before the two products, whose matrix
- * instructions take 16-bit inputs.  max(g, 0) has slope 0 at 0.
+ * instructions take 16-bit inputs.  max(g, 0) has slope 0 at 0.  rows and 2 hidden
+ * <= 2^30, else GEMM_RELU_EUNSUPPORTED (from the workspace function too).
  */
 int64_t gemm_relu_gated_backward_workspace(int64_t rows, int64_t hidden, int64_t cols);
 int gemm_relu_gated_backward(const void* dh, int64_t dh_stride, const float* gu, const void* x,
