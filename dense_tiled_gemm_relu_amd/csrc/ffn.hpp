@@ -82,6 +82,11 @@ int layer_norm_strips(int64_t rows, int64_t cols);
 hipError_t launch_layer_norm_backward(const NormArgs& a, int dt, int wdt, hipStream_t stream);
 
 constexpr int kGradThreads = 512;          // of a workgroup, which takes a 64 x 64 tile
+// What a tile of dg and du holds past float16's largest value: its rows, its units of
+// dg and its units of du, a bit each.
+struct GradOver {
+    unsigned long long rows, gate, up;
+};
 struct GatedGradArgs {
     const float* gu;        // (rows, 2 hidden)
     const void* dh;
@@ -92,8 +97,18 @@ struct GatedGradArgs {
     int rows, hidden, act;
     unsigned* flags;        // `nflags` arrival counters to clear for a K split that follows
     int nflags;
+    GradOver* over;         // F16: one a tile, hidden fastest
+    // launch_gated_repair
+    const void* x;
+    const void* w;
+    void* dx;
+    void* dw;
+    int64_t x_stride, w_stride;
+    int cols;
 };
 hipError_t launch_gated_grad(const GatedGradArgs& a, int dt, hipStream_t stream);
+// F16, behind the products: the rows of dx and dweight that `over` names once more
+hipError_t launch_gated_repair(const GatedGradArgs& a, hipStream_t stream);
 
 hipError_t launch_quantize_rows(const void* x, int64_t x_stride, signed char* q, float* scale, int rows,
                                 int cols, int dt, hipStream_t stream);

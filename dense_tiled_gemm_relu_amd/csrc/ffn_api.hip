@@ -212,11 +212,12 @@ int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 // dweight, each row padded to 16 bytes.  Both products share one launch, and so
 // one configuration: dx alone seldom fills the device.  Where one of them has few
 // tiles and a long K, its K is cut into parts, whose fp32 sums and arrival
-// counters are the workspace's last pieces.
+// counters follow in the workspace, and last what the element-wise pass notes of
+// values past float16.
 struct GradPlan {
     Linear lx, lw;
     LinearPlan x, w;            // of dx = dgu weight and of dweight = dgu^T x
-    uint64_t dgu_t, flags, sums_x, sums_w, bytes;
+    uint64_t dgu_t, flags, sums_x, sums_w, over, bytes;
     int nflags() const { return int((x.splits > 1 ? x.tiles() : 0) + (w.splits > 1 ? w.tiles() : 0)); }
 };
 // of dx and of dweight: a launch of the largest tiles has no room for more (and the
@@ -275,7 +276,8 @@ GradPlan plan_grad(int64_t rows, int64_t hidden, int64_t cols, int64_t x_stride,
     g.flags = uint64_t(round_up(int64_t(g.dgu_t + uint64_t(2 * hidden) * uint64_t(ld_t) * 2), 256));
     g.sums_x = g.flags + uint64_t(round_up(4 * int64_t(g.nflags()), 256));
     g.sums_w = g.sums_x + sums(g.x);
-    g.bytes = g.sums_w + sums(g.w);
+    g.over = g.sums_w + sums(g.w);
+    g.bytes = g.over + uint64_t(ceil_div(rows, 64) * ceil_div(hidden, 64)) * sizeof(GradOver);
     return g;
 }
 
@@ -425,8 +427,9 @@ extern "C" int gemm_relu_gated_backward(const void* dh, int64_t dh_stride, const
     unsigned char* ws = static_cast<unsigned char*>(workspace);
     unsigned* flags = reinterpret_cast<unsigned*>(ws + p.flags);
     hipError_t e = hipSuccess;
-    if (rows > 0 && hidden > 0) {
-        GatedGradArgs g{};
+    GatedGradArgs g{};
+    const bool grad = rows > 0 && hidden > 0;
+    if (grad) {
         g.gu = gu;
         g.dh = dh;
         g.dgu = ws;
@@ -439,6 +442,14 @@ extern "C" int gemm_relu_gated_backward(const void* dh, int64_t dh_stride, const
         g.act = act;
         g.flags = flags;
         g.nflags = p.nflags();
+        g.over = reinterpret_cast<GradOver*>(ws + p.over);
+        g.x = x;
+        g.w = weight;
+        g.dx = dx;
+        g.dw = dweight;
+        g.x_stride = x_stride;
+        g.w_stride = weight_stride;
+        g.cols = int(cols);
         e = launch_gated_grad(g, dtype, st);
     }
     KernelArgs gx = linear_args(p.x, p.lx, ws, weight, dx), gw = linear_args(p.w, p.lw, ws + p.dgu_t, x, dweight);
@@ -452,6 +463,7 @@ extern "C" int gemm_relu_gated_backward(const void* dh, int64_t dh_stride, const
         const bool x_first = p.lx.K * p.w.splits >= p.lw.K * p.x.splits;
         e = launcher_cast_pair(dtype, p.x.cfg)(x_first ? LinearPair{gx, gw, nx} : LinearPair{gw, gx, nw}, nx + nw, st);
     }
+    if (e == hipSuccess && grad && dtype == GEMM_RELU_F16) e = launch_gated_repair(g, st);
     return finish(e, st);
 }
 

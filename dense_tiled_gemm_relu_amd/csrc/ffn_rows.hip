@@ -650,6 +650,18 @@ template <class W> __global__ void __launch_bounds__(1024) layer_norm_join_kerne
 // LDS.  Both outputs' rows are padded to 16 bytes with zeros, so that the
 // products may read them in whole pieces.  Bound by HBM: 4096 x 7168 bf16 reads and
 // writes 0.53 GB in 89 us, 5.9 TB/s.
+//
+// A finite value whose rounding to float16 is an infinity is noted, for
+// gated_repair_kernel.
+constexpr float kHalfOver = 65520.0f;              // half a step above the largest float16, the first that rounds up
+__device__ __forceinline__ bool passes_half(float v) { return fabsf(v) >= kHalfOver && fabsf(v) < INFINITY; }
+template <int ACT> __device__ __forceinline__ void gated_slopes(float d, float g, float u, float& dg, float& du)
+{
+    float value, slope;
+    activation_slope<ACT>(g, value, slope);
+    dg = d * u * slope;
+    du = d * value;
+}
 template <int DT, int ACT> __global__ void __launch_bounds__(kGradThreads) gated_grad_kernel(GatedGradArgs a)
 {
     using T = typename Elem<DT>::T;
@@ -658,6 +670,11 @@ template <int DT, int ACT> __global__ void __launch_bounds__(kGradThreads) gated
     constexpr int ROWS = 64 * 16 / kGradThreads;
     constexpr int PITCH = 68;                      // elements of a transposed row: 8-byte pieces on spread banks
     __shared__ __attribute__((aligned(16))) T tile[2][64][PITCH];
+    __shared__ GradOver over;
+    if constexpr (DT == DT_F16) {
+        if (threadIdx.x == 0) over = GradOver{};
+        __syncthreads();
+    }
     const int htiles = (a.hidden + 63) / 64;
     const int h0 = (int)(blockIdx.x % htiles) * 64, r0 = (int)(blockIdx.x / htiles) * 64;
     if (blockIdx.x == 0)
@@ -691,12 +708,22 @@ template <int DT, int ACT> __global__ void __launch_bounds__(kGradThreads) gated
     T4 dg[ROWS], du[ROWS];
 #pragma unroll
     for (int k = 0; k < ROWS; ++k) {
+        float gate[4], up[4], top = 0.0f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-            float value, slope;
-            activation_slope<ACT>(g[k][e], value, slope);
-            dg[k][e] = (T)((float)d[k][e] * u[k][e] * slope);
-            du[k][e] = (T)((float)d[k][e] * value);
+            gated_slopes<ACT>((float)d[k][e], g[k][e], u[k][e], gate[e], up[e]);
+            dg[k][e] = (T)gate[e];
+            du[k][e] = (T)up[e];
+            top = fmaxf(top, fmaxf(fabsf(gate[e]), fabsf(up[e])));
+        }
+        if (DT == DT_F16 && top >= kHalfOver) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool in_gate = passes_half(gate[e]), in_up = passes_half(up[e]);
+                if (in_gate) atomicOr(&over.gate, 1ull << (c + e));
+                if (in_up) atomicOr(&over.up, 1ull << (c + e));
+                if (in_gate || in_up) atomicOr(&over.rows, 1ull << (q + k));
+            }
         }
         const int r = r0 + q + k;
         if (r >= a.rows) continue;
@@ -724,6 +751,8 @@ template <int DT, int ACT> __global__ void __launch_bounds__(kGradThreads) gated
         *reinterpret_cast<T2*>(&tile[1][c + e][q]) = y;
     }
     __syncthreads();
+    if constexpr (DT == DT_F16)
+        if (threadIdx.x == 0) a.over[blockIdx.x] = over;
 #pragma unroll
     for (int k = 0; k < 1024 / kGradThreads; ++k) {
         const int p = k * kGradThreads + (int)threadIdx.x, half = p >> 9, hh = (p >> 3) & 63, rr = (p & 7) * 8;
@@ -733,6 +762,121 @@ template <int DT, int ACT> __global__ void __launch_bounds__(kGradThreads) gated
         const T4 lo = from[0], hi = from[1];
         __builtin_memcpy(out, &lo, 8);
         __builtin_memcpy(out + 4, &hi, 8);
+    }
+}
+
+// ---- where float16 cannot hold dg or du
+// The products' operands are 16-bit, so a finite dg or du above 65504 has become an
+// infinity, and with it its row of dx and its row of dweight, whose own values may
+// be far inside the range (weights are small).  These rows are summed here once more,
+// in fp32 from dg and du as they are.  A row counts if any of its elements passes the
+// range; the others keep the products' results, whatever shares their tile.
+//
+// One launch more for float16, which finds nothing to do but for gradients that large:
+// 2-3 us of a small call, 10 of 835 at 4096 x 7168 x 4096.  Otherwise it takes 0.8 ms at
+// 1027 x 2003 x 1501, 6.6 (one element) to 26 (all rows) at 4096 x 7168 x 4096, bound by
+// its steps' latency: 64 x 64 outputs a workgroup, 4 x 4 a thread, 16 K elements of
+// both operands a step in LDS, for a case that a loss scale meets once in a while.
+constexpr int kRepairK = 16;
+__device__ __forceinline__ unsigned long long group_or(unsigned long long v, unsigned long long* lds)
+{
+#pragma unroll
+    for (int step = 1; step < 64; step *= 2) v |= __shfl_xor(v, step);
+    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
+    __syncthreads();
+    return lds[0] | lds[1] | lds[2] | lds[3];
+}
+template <int ACT> __global__ void __launch_bounds__(kThreads) gated_repair_kernel(GatedGradArgs a, int parts)
+{
+    using T = _Float16;
+    __shared__ unsigned long long masks[2][kThreads / 64];
+    __shared__ float left[2][kRepairK][64], right[2][kRepairK][64];
+    const int tid = (int)threadIdx.x, block = (int)blockIdx.x / parts, part = (int)blockIdx.x % parts;
+    const int htiles = (a.hidden + 63) / 64, rtiles = (a.rows + 63) / 64;
+    const bool of_dx = block < rtiles;
+    const int m0 = 64 * (of_dx ? block : block - rtiles);       // its first row of dx, or unit
+    // what the tiles along the other side found
+    unsigned long long gate = 0, up = 0;
+    if (of_dx) {
+        for (int t = tid; t < htiles; t += kThreads) gate |= a.over[(size_t)block * htiles + t].rows;
+    } else {
+        for (int t = tid; t < rtiles; t += kThreads) {
+            const GradOver& o = a.over[(size_t)t * htiles + (block - rtiles)];
+            gate |= o.gate;
+            up |= o.up;
+        }
+    }
+    gate = group_or(gate, masks[0]);
+    up = group_or(up, masks[1]);
+    if (!(gate | up)) return;
+
+    const int K = of_dx ? a.hidden : a.rows, mi = (tid >> 4) * 4, ni = (tid & 15) * 4;
+    constexpr int NL = 64 * kRepairK / kThreads, NR = 2 * NL;
+    for (int64_t n0 = (int64_t)part * 64; n0 < a.cols; n0 += (int64_t)parts * 64) {
+        float sums[2][4][4] = {};           // dx: the first only
+        for (int k0 = 0; k0 < K; k0 += kRepairK) {
+            __syncthreads();                // the last step's reads are done
+            // all loads in flight together: what lies past an edge is the last one's, and
+            // counts as zero
+            float g[NL], u[NL], d[NL], other[NR];
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const int e = i * kThreads + tid;
+                // units are the fastest in memory
+                const int m = of_dx ? e / kRepairK : e % 64, k = of_dx ? e % kRepairK : e / 64;
+                const size_t row = (size_t)min(of_dx ? m0 + m : k0 + k, a.rows - 1);
+                const size_t unit = (size_t)min(of_dx ? k0 + k : m0 + m, a.hidden - 1);
+                g[i] = a.gu[row * 2 * (size_t)a.hidden + unit];
+                u[i] = a.gu[row * 2 * (size_t)a.hidden + (size_t)a.hidden + unit];
+                d[i] = (float)static_cast<const T*>(a.dh)[row * (size_t)a.dh_stride + unit];
+            }
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                const int e = i * kThreads + tid, k = (e / 64) % kRepairK, half = e / (64 * kRepairK);
+                const size_t row = (size_t)min(k0 + k, K - 1) + (of_dx && half ? (size_t)a.hidden : 0);
+                other[i] = (float)static_cast<const T*>(of_dx ? a.w : a.x)[row * (size_t)(of_dx ? a.w_stride : a.x_stride) +
+                                                                          (size_t)min(n0 + e % 64, (int64_t)a.cols - 1)];
+            }
+#pragma unroll
+            for (int i = 0; i < NL; ++i) {
+                const int e = i * kThreads + tid;
+                const int m = of_dx ? e / kRepairK : e % 64, k = of_dx ? e % kRepairK : e / 64;
+                float dg, du;
+                gated_slopes<ACT>(d[i], g[i], u[i], dg, du);
+                left[0][k][m] = k0 + k < K ? dg : 0.0f;
+                left[1][k][m] = k0 + k < K ? du : 0.0f;
+            }
+#pragma unroll
+            for (int i = 0; i < NR; ++i) {
+                const int e = i * kThreads + tid, k = (e / 64) % kRepairK;
+                right[e / (64 * kRepairK)][k][e % 64] = k0 + k < K ? other[i] : 0.0f;
+            }
+            __syncthreads();
+            auto add = [&](int k, int half, float(&s)[4][4]) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[i][j] = fmaf(left[half][k][mi + i], right[half][k][ni + j], s[i][j]);
+            };
+            for (int k = 0; k < kRepairK; ++k) {
+                add(k, 0, sums[0]);
+                if (of_dx)
+                    add(k, 1, sums[0]);
+                else
+                    add(k, 1, sums[1]);
+            }
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (!((half ? up : gate) >> (mi + i) & 1)) continue;      // of dx: no up
+                T* out = static_cast<T*>(of_dx ? a.dx : a.dw) +
+                         ((size_t)(m0 + mi + i) + (half ? (size_t)a.hidden : 0)) * (size_t)a.cols + n0 + ni;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (n0 + ni + j < a.cols) out[j] = (T)sums[half][i][j];
+            }
     }
 }
 
@@ -977,21 +1121,36 @@ hipError_t launch_layer_norm_backward(const NormArgs& a, int dt, int wdt, hipStr
     });
 }
 
+// f(the activation as a constant)
+template <class F> hipError_t with_act(int act, F&& f)
+{
+    switch (act) {
+    case ACT_SILU: return f(std::integral_constant<int, ACT_SILU>{});
+    case ACT_GELU: return f(std::integral_constant<int, ACT_GELU>{});
+    case ACT_GELU_TANH: return f(std::integral_constant<int, ACT_GELU_TANH>{});
+    default: return f(std::integral_constant<int, ACT_RELU>{});
+    }
+}
+
 hipError_t launch_gated_grad(const GatedGradArgs& a, int dt, hipStream_t stream)
 {
     const dim3 grid((unsigned)((a.hidden + 63) / 64) * (unsigned)((a.rows + 63) / 64));
-    const auto go = [&](auto dtype, auto act) {
-        return start(&gated_grad_kernel<decltype(dtype)::value, decltype(act)::value>, grid, kGradThreads, stream, a);
-    };
-    const auto with = [&](auto dtype) {
-        switch (a.act) {
-        case ACT_SILU: return go(dtype, std::integral_constant<int, ACT_SILU>{});
-        case ACT_GELU: return go(dtype, std::integral_constant<int, ACT_GELU>{});
-        case ACT_GELU_TANH: return go(dtype, std::integral_constant<int, ACT_GELU_TANH>{});
-        default: return go(dtype, std::integral_constant<int, ACT_RELU>{});
-        }
-    };
-    return dt == DT_F16 ? with(std::integral_constant<int, DT_F16>{}) : with(std::integral_constant<int, DT_BF16>{});
+    return with_act(a.act, [&](auto act) {
+        constexpr int ACT = decltype(act)::value;
+        return start(dt == DT_F16 ? &gated_grad_kernel<DT_F16, ACT> : &gated_grad_kernel<DT_BF16, ACT>, grid, kGradThreads,
+                     stream, a);
+    });
+}
+
+hipError_t launch_gated_repair(const GatedGradArgs& a, hipStream_t stream)
+{
+    // every 64 rows of dx and every 64 units of dweight, 64 of their columns a workgroup
+    // up to 2^13 workgroups: a single large element is spread over the device
+    const int64_t blocks = ceil_div(a.hidden, 64) + ceil_div(a.rows, 64);
+    const int parts = (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(a.cols, 64), (1 << 13) / blocks));
+    return with_act(a.act, [&](auto act) {
+        return start(&gated_repair_kernel<decltype(act)::value>, dim3((unsigned)(blocks * parts)), kThreads, stream, a, parts);
+    });
 }
 
 hipError_t launch_quantize_rows(const void* x, int64_t x_stride, signed char* q, float* scale, int rows,

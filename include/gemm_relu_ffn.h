@@ -94,7 +94,9 @@ const char* gemm_relu_gated_plan(int64_t rows, int64_t hidden, int64_t cols, int
  *   dg = dh u act'(g),  du = dh act(g),  dx = dg Wg + du Wu,
  *   dweight = [dg^T x; du^T x]                  (2 hidden x cols).
  * dg and du are rounded to dtype before the two products, whose matrix
- * instructions take 16-bit inputs.  max(g, 0) has slope 0 at 0.  rows and 2 hidden
+ * instructions take 16-bit inputs (F16 values below its normal range to a multiple
+ * of 2^-24).  Where a finite dg or du would become an F16 infinity, its row of dx
+ * and its row of dweight are summed in fp32 without that rounding.  max(g, 0) has slope 0 at 0.  rows and 2 hidden
  * <= 2^30, else GEMM_RELU_EUNSUPPORTED (from the workspace function too).
  */
 int64_t gemm_relu_gated_backward_workspace(int64_t rows, int64_t hidden, int64_t cols);
