@@ -12,6 +12,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/ops/empty.h>
 #include <c10/util/StringUtil.h>
 #include <torch/csrc/Dtype.h>
@@ -111,6 +112,20 @@ void expect_one_gpu(std::initializer_list<const at::Tensor*> all)
         if (t && (!t->is_cuda() || t->get_device() != first.get_device()))
             refuse(PyExc_ValueError, "all tensors must be on the same GPU");
 }
+// Results carry no autograd graph.  A caller who counts on one is told so: a result
+// that needs no gradient would stop training without a word.  (Where the caller has
+// switched gradients off, as torch.autograd.Function does, nothing is lost.)
+void warn_of_lost_gradients(const char* name, std::initializer_list<const at::Tensor*> all)
+{
+    const bool recording = at::GradMode::is_enabled();
+    for (const at::Tensor* t : all)
+        if (t && ((recording && t->requires_grad()) || t->_fw_grad(/*level=*/0).defined())) {
+            const std::string text = c10::str(name, ": an input requires a gradient, but the result carries no autograd graph; "
+                                              "take the gradients from the *_backward functions, or call under torch.no_grad()");
+            if (PyErr_WarnEx(PyExc_UserWarning, text.c_str(), 2) != 0) throw python_error();
+            return;
+        }
+}
 int float_code(const at::Tensor& x)
 {
     const int c = code_of(x.scalar_type());
@@ -168,6 +183,7 @@ PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n)
     const Rows r = rows_of(x, "x");
     expect_vector(w, "weight", r.cols, x.scalar_type(), at::kFloat);
     if (b) expect_vector(*b, "bias", r.cols, w.scalar_type(), w.scalar_type());
+    warn_of_lost_gradients("layer_norm", {&x, &w, b});
     expect_one_gpu({&x, &w, b});
     at::Tensor y = make(x, x.sizes(), x.scalar_type()), mean, rstd;
     if (stats) {
@@ -196,6 +212,7 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
     expect_vector(w, "weight", r.cols, x.scalar_type(), at::kFloat);
     expect_vector(mean, "mean", r.rows, at::kFloat, at::kFloat);
     expect_vector(rstd, "rstd", r.rows, at::kFloat, at::kFloat);
+    warn_of_lost_gradients("layer_norm_backward", {&x, &dy, &w, &mean, &rstd});
     expect_one_gpu({&x, &dy, &w, &mean, &rstd});
     at::Tensor dx = make(x, x.sizes(), x.scalar_type()), dw = make(w, w.sizes(), w.scalar_type()),
                db = make(w, w.sizes(), w.scalar_type());
@@ -242,6 +259,7 @@ PyObject* matmul_gated(PyObject*, PyObject* const* a, Py_ssize_t n)
     const int act = activation_code(a[2]);
     const bool save = truth(a[3]);
     const Gated g = gated_args(x, w);
+    warn_of_lost_gradients("matmul_gated", {&x, &w});
     expect_one_gpu({&x, &w});
     at::Tensor h = make(x, with_last(x, g.hidden), x.scalar_type()), gu;
     if (save) gu = make(x, with_last(x, 2 * g.hidden), at::kFloat);
@@ -264,6 +282,7 @@ PyObject* matmul_gated_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
         refuse(PyExc_ValueError, "dh must have matmul_gated's shape: x's, with ", g.hidden, " for the last dimension");
     const int64_t dh_ld = rows_of(dh, "dh").ld;
     expect_vector(gu, "gu", g.x.rows * 2 * g.hidden, at::kFloat, at::kFloat);
+    warn_of_lost_gradients("matmul_gated_backward", {&x, &w, &dh, &gu});
     expect_one_gpu({&x, &w, &dh, &gu});
     at::Tensor dx = make(x, x.sizes(), x.scalar_type()), dw = make(w, w.sizes(), w.scalar_type());
     const int64_t bytes = api.gated_backward_workspace(g.x.rows, g.hidden, g.x.cols);
@@ -283,6 +302,7 @@ PyObject* quantize_rows(PyObject*, PyObject* const* a, Py_ssize_t n)
     const at::Tensor& x = tensor(a[0], "x");
     const int code = float_code(x);
     const Rows r = rows_of(x, "x");
+    warn_of_lost_gradients("quantize_rows", {&x});
     expect_one_gpu({&x});
     at::Tensor q = make(x, x.sizes(), at::kChar), scale = make(x, leading(x), at::kFloat);
     check(api.quantize_rows(x.data_ptr(), r.ld, q.data_ptr(), floats(scale), r.rows, r.cols, code, pointer(a[1])));
@@ -311,6 +331,7 @@ PyObject* matmul_i8(PyObject*, PyObject* const* a, Py_ssize_t n)
         refuse(PyExc_ValueError, "inner dimensions differ: ", rx.cols, " vs ", rw.cols);
     expect_vector(xs, "x_scale", rx.rows, at::kFloat, at::kFloat);
     expect_vector(ws, "weight_scale", rw.rows, at::kFloat, at::kFloat);
+    warn_of_lost_gradients("matmul_i8", {&x, &xs, &w, &ws});
     expect_one_gpu({&x, &xs, &w, &ws});
     at::Tensor y = make(x, with_last(x, rw.rows), out);
     check(api.i8(x.data_ptr(), rx.ld, floats(xs), w.data_ptr(), rw.ld, floats(ws), y.data_ptr(), rx.rows, rw.rows, rx.cols,

@@ -12,7 +12,8 @@ contiguous tensors.  The kernels run on ``stream`` (a torch.cuda.Stream, a raw
 hipStream_t, or None for torch's current stream); results and workspaces are
 allocated for that stream.  A tensor made on another stream has to be ready
 before the call, as with any torch operation.  Results carry no autograd graph: a
-backward function is a call of its own.
+backward function is a call of its own.  An input that requires a gradient, where
+gradients are recorded, gives a UserWarning.
 """
 import ctypes
 import importlib.machinery
