@@ -60,13 +60,13 @@ def _status_error(status):
     return GemmReluError(status, gemm_relu_strerror(status))
 
 
-_ops = _current_device = _raw_stream = None
+_ops = _current_device = _raw_stream = _tensor = None
 
 
 def _load():
     """The front end module, bound to the loaded library; raises if either has
     not been built."""
-    global _ops, _current_device, _raw_stream
+    global _ops, _current_device, _raw_stream, _tensor
     from . import library
     lib = library()
     if not os.path.exists(MODULE_PATH):
@@ -77,6 +77,7 @@ def _load():
     loader.exec_module(ops)
     ops.bind(_status_error, *(ctypes.cast(getattr(lib, name), _vp).value for name in _BOUND))
     _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    _tensor = torch.Tensor
     _ops = ops
     return ops
 
@@ -120,7 +121,7 @@ def layer_norm(x, weight, bias=None, eps=1e-5, stats=False, stream=None):
     float32.  Returns y, or with ``stats`` (y, mean, rstd), the fp32 statistics
     of each row that the backward pass takes.
     """
-    if stream is None and _ops is not None:
+    if stream is None and _ops is not None and isinstance(x, _tensor):
         index = x.get_device()
         if index >= 0 and _current_device() == index:
             return _ops.layer_norm(x, weight, bias, eps, stats, _raw_stream(index))
@@ -130,7 +131,7 @@ def layer_norm(x, weight, bias=None, eps=1e-5, stats=False, stream=None):
 def layer_norm_backward(dy, x, weight, mean, rstd, stream=None):
     """Gradients (dx, dweight, dbias) of layer_norm, given dy and the statistics
     of the forward call.  dx has x's type, dweight and dbias weight's."""
-    if stream is None and _ops is not None:
+    if stream is None and _ops is not None and isinstance(x, _tensor):
         index = x.get_device()
         if index >= 0 and _current_device() == index:
             return _ops.layer_norm_backward(dy, x, weight, mean, rstd, _raw_stream(index))
@@ -154,7 +155,7 @@ def matmul_gated(x, weight, act="silu", save=False, stream=None):
     rounding would be as large as that of the gradients themselves).
     """
     code = _activation(act)
-    if stream is None and _ops is not None:
+    if stream is None and _ops is not None and isinstance(x, _tensor):
         index = x.get_device()
         if index >= 0 and _current_device() == index:
             return _ops.matmul_gated(x, weight, code, save, _raw_stream(index))
@@ -165,7 +166,7 @@ def matmul_gated_backward(dh, gu, x, weight, act="silu", stream=None):
     """Gradients (dx, dweight) of matmul_gated, given dh and the forward call's
     gu.  Both have x's type."""
     code = _activation(act)
-    if stream is None and _ops is not None:
+    if stream is None and _ops is not None and isinstance(x, _tensor):
         index = x.get_device()
         if index >= 0 and _current_device() == index:
             return _ops.matmul_gated_backward(dh, gu, x, weight, code, _raw_stream(index))
@@ -176,7 +177,7 @@ def quantize_rows(x, stream=None):
     """Each row (last dimension) of x in 8 bits: returns (q, scale), int8 q of x's
     shape and fp32 scale = max|row| / 127, with row ~ q * scale.  A row that holds
     an infinity or NaN has scale NaN."""
-    if stream is None and _ops is not None:
+    if stream is None and _ops is not None and isinstance(x, _tensor):
         index = x.get_device()
         if index >= 0 and _current_device() == index:
             return _ops.quantize_rows(x, _raw_stream(index))
@@ -190,7 +191,7 @@ def matmul_i8(x, x_scale, weight, weight_scale, out_dtype=None, stream=None):
     fp32 scale per row (output channel).  Sums are exact (k <= 131071).  Returns
     y (..., n) of out_dtype (float16, bfloat16 or float32; default bfloat16).
     """
-    if stream is None and _ops is not None:
+    if stream is None and _ops is not None and isinstance(x, _tensor):
         index = x.get_device()
         if index >= 0 and _current_device() == index:
             return _ops.matmul_i8(x, x_scale, weight, weight_scale, out_dtype, _raw_stream(index))
