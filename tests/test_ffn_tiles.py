@@ -151,3 +151,17 @@ def test_i8_rows_past_32_bits_of_the_first():
     x, sx, w, sw = i8_inputs(rows, n, k, 27)
     far = far_apart(w, 2 ** 22)                       # 4.6 GB
     assert torch.equal(gr.matmul_i8(x, sx, far, sw), gr.matmul_i8(x, sx, w, sw))
+
+
+@pytest.mark.parametrize("rows,hidden,cols", [(1024, 512, 32), (1000, 500, 121), (900, 450, 515)])
+def test_far_rows_of_many_tiles(rows, hidden, cols):
+    # short rows take the register-staged tile, the last the 32 x 32 one: whole numbers, so
+    # both have the dense rows' bits
+    x, w = ints(31, -2, 2, rows, cols), ints(32, -2, 2, 2 * hidden, cols)
+    for dtype in (F16, BF16):
+        h, gu = gr.matmul_gated(x.to(dtype), w.to(dtype), "silu", save=True)
+        h2, gu2 = gr.matmul_gated(far_apart(x.to(dtype), FAR), far_apart(w.to(dtype), FAR), "silu", save=True)
+        assert torch.equal(gu2.to(F64), x.to(F64) @ w.to(F64).t()) and torch.equal(gu, gu2) and torch.equal(h, h2)
+    sx, sw = torch.rand(rows, device="cuda"), torch.rand(2 * hidden, device="cuda")
+    xi, wi = x.to(torch.int8), w.to(torch.int8)
+    assert torch.equal(gr.matmul_i8(far_apart(xi, FAR), sx, far_apart(wi, FAR), sw), gr.matmul_i8(xi, sx, wi, sw))
