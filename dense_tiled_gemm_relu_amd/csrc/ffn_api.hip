@@ -180,12 +180,20 @@ RowsPlan plan_rows(const Linear& l)
     }
     return r;
 }
+// Names of two configurations with `between` between them, kept for good.
+struct PairNames {
+    char text[LIN_COUNT][LIN_COUNT][64];
+    explicit PairNames(char between)
+    {
+        for (int a = 0; a < LIN_COUNT; ++a)
+            for (int b = 0; b < LIN_COUNT; ++b)
+                std::snprintf(text[a][b], sizeof text[a][b], "%s%c%s", linear_info(a).name, between, linear_info(b).name);
+    }
+};
 const char* rows_plan_name(const RowsPlan& r)
 {
-    if (r.rest.M == 0) return linear_info(r.p.cfg).name;
-    static thread_local char names[64];
-    std::snprintf(names, sizeof names, "%s+%s", linear_info(r.p.cfg).name, linear_info(r.q.cfg).name);
-    return names;
+    static const PairNames names('+');
+    return r.rest.M == 0 ? linear_info(r.p.cfg).name : names.text[r.p.cfg][r.q.cfg];
 }
 
 KernelArgs linear_args(const LinearPlan& p, const Linear& l, const void* A, const void* B, void* C)
@@ -475,9 +483,8 @@ extern "C" const char* gemm_relu_gated_backward_plan(int64_t rows, int64_t hidde
     if (!gated_sizes_ok(rows, hidden, cols, dtype)) return nullptr;
     if (cols == 0 || (rows == 0 && hidden == 0)) return "none";
     const GradPlan p = plan_grad(rows, hidden, cols, cols, cols);
-    static thread_local char names[64];
-    std::snprintf(names, sizeof names, "%s,%s", linear_info(p.x.cfg).name, linear_info(p.w.cfg).name);
-    return names;
+    static const PairNames names(',');
+    return names.text[p.x.cfg][p.w.cfg];
 }
 
 // ------------------------------------------------------- 8-bit integers

@@ -84,9 +84,10 @@ int gemm_relu_gated(const void* x, int64_t x_stride, const void* weight, int64_t
                     void* h, float* gu, int64_t rows, int64_t hidden, int64_t cols, int dtype,
                     int act, void* stream);
 
-/* Name of the kernel configuration gemm_relu_gated would launch ("a+b" where the
- * last rows take a second launch; "none" for an empty call, NULL for invalid
- * sizes or codes).  Host-only. */
+/* Name of the kernel configuration gemm_relu_gated would launch for dense rows
+ * ("a+b" where the last rows take a second launch; "none" for an empty call,
+ * "unsupported" above a stated limit, NULL for invalid sizes or codes).  Rows more
+ * than 2^22 elements apart can take another.  The text stays valid.  Host-only. */
 const char* gemm_relu_gated_plan(int64_t rows, int64_t hidden, int64_t cols, int dtype);
 
 /*
@@ -106,7 +107,8 @@ int gemm_relu_gated_backward(const void* dh, int64_t dh_stride, const float* gu,
                              int dtype, int act, void* workspace, uint64_t workspace_bytes,
                              void* stream);
 
-/* Configuration names of its two products, "dx,dweight" (as above). */
+/* Configuration names of its two products, "dx,dweight" (as above; other ones for rows
+ * of x or weight more than 2^24 elements apart). */
 const char* gemm_relu_gated_backward_plan(int64_t rows, int64_t hidden, int64_t cols, int dtype);
 
 /*
