@@ -10,9 +10,10 @@
  *     without one are dense.  Pointers need the alignment of their element.
  *   - Sizes are >= 0 and <= INT32_MAX.  A call whose outputs have no elements
  *     returns GEMM_RELU_OK without touching the device.
- *   - Sums, means and statistics are fp32 (int32 where stated); results are
- *     rounded once, to nearest even.  Results are the same bits on every run:
- *     nothing is summed in an order that depends on timing.
+ *   - Sums, means and statistics are fp32 (int32 where stated), and so are the
+ *     operations behind them; results are then rounded to their type, to nearest
+ *     even.  Results are the same bits on every run: nothing is summed in an order
+ *     that depends on timing.
  *   - The call allocates nothing and is asynchronous on `stream` (a hipStream_t
  *     or NULL); it may be captured into a graph.  The library keeps no pointer.
  *     GEMM_RELU_SYNC=1 in the environment makes it synchronise and report.
@@ -125,7 +126,8 @@ int gemm_relu_quantize_rows(const void* x, int64_t x_stride, void* q, float* sca
 /*
  * 8-bit integer product: y_ij = (sum_k x_ik w_jk) x_scale_i w_scale_j for int8
  * x (rows x k) and w (n x k, one row per output channel), the sum exact in
- * int32.  y is rows x n of out_dtype (F16, BF16 or F32).  k <= 131071 (where no
+ * int32, then rounded to fp32, as are its products with x_scale and with w_scale
+ * (fp32 results so carry three roundings).  y is rows x n of out_dtype (F16, BF16 or F32).  k <= 131071 (where no
  * sum can overflow), else GEMM_RELU_EUNSUPPORTED.
  */
 int gemm_relu_i8(const void* x, int64_t x_stride, const float* x_scale, const void* w,
