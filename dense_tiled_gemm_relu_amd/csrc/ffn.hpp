@@ -78,7 +78,8 @@ struct NormArgs {
 };
 hipError_t launch_layer_norm(const NormArgs& a, int dt, int wdt, hipStream_t stream);
 // strips of rows the backward pass sums on their own before joining them
-int layer_norm_strips(int64_t rows, int64_t cols);
+// (bytes: of an element of x)
+int layer_norm_strips(int64_t rows, int64_t cols, int bytes);
 hipError_t launch_layer_norm_backward(const NormArgs& a, int dt, int wdt, hipStream_t stream);
 
 constexpr int kGradThreads = 512;          // of a workgroup, which takes a 64 x 64 tile

@@ -326,7 +326,8 @@ extern "C" int gemm_relu_layer_norm(const void* x, int64_t x_stride, const void*
 extern "C" int64_t gemm_relu_layer_norm_backward_workspace(int64_t rows, int64_t cols)
 {
     if (!size_ok(rows) || !size_ok(cols)) return GEMM_RELU_EINVAL;
-    return int64_t(layer_norm_strips(rows, cols)) * 2 * cols * 4;
+    // of the type that leaves more strips
+    return int64_t(std::max(layer_norm_strips(rows, cols, 2), layer_norm_strips(rows, cols, 4))) * 2 * cols * 4;
 }
 
 extern "C" int gemm_relu_layer_norm_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,

@@ -1077,16 +1077,18 @@ hipError_t launch_layer_norm(const NormArgs& a, int dt, int wdt, hipStream_t str
 }
 
 // Workgroups of the backward pass, each of which leaves one strip of sums: one a
-// CU (4097 x 3001 25 us, 32 with two), and two where a wave holds a row (12000 x 300
-// 14.6 us, 15.5 with one).
-int layer_norm_strips(int64_t rows, int64_t cols)
+// CU (4097 x 3001 25 us, 32 with two), and two where a wave holds a row, 1024 bytes
+// (12000 x 300 bf16 13.5 us, 14.0 with one; 50000 x 300 27.8 and 38.4; but fp32, two
+// waves a row, 19.5 and 15.2).
+int layer_norm_strips(int64_t rows, int64_t cols, int bytes)
 {
-    return rows == 0 ? 0 : even_grid(rows, cols <= 256 ? 4 : 2, cols <= 256 ? 512 : 256);
+    const bool wave = cols * bytes <= 1024;
+    return rows == 0 ? 0 : even_grid(rows, wave ? 4 : 2, wave ? 512 : 256);
 }
 
 hipError_t launch_layer_norm_backward(const NormArgs& a, int dt, int wdt, hipStream_t stream)
 {
-    const int strips = layer_norm_strips(a.rows, a.cols);
+    const int strips = layer_norm_strips(a.rows, a.cols, elem_size(dt));
     return with_types(dt, wdt, [&](auto x, auto w) {
         using T = decltype(x);
         using W = decltype(w);
