@@ -51,7 +51,9 @@ extern "C" {
  *   y_j = (x_j - mean) rstd weight_j + bias_j.
  * dtype (x, y): F16, BF16 or F32.  wdtype (weight, bias): dtype or F32.  bias
  * may be NULL (zero).  mean and rstd (rows floats each) are written unless NULL.
- * cols >= 1; eps >= 0.  A row with an infinity or NaN gives a row of NaN.
+ * cols >= 1; eps >= 0.  A row with an infinity or NaN gives a row of NaN, and
+ * so does one whose sum passes fp32; one whose squared distances from the mean pass
+ * it (distances above 1.8e19) has rstd 0.
  */
 int gemm_relu_layer_norm(const void* x, int64_t x_stride, const void* weight, const void* bias,
                          void* y, float* mean, float* rstd, int64_t rows, int64_t cols, int dtype,
