@@ -83,11 +83,9 @@ int layer_norm_strips(int64_t rows, int64_t cols, int bytes);
 hipError_t launch_layer_norm_backward(const NormArgs& a, int dt, int wdt, hipStream_t stream);
 
 constexpr int kGradThreads = 512;          // of a workgroup, which takes a 64 x 64 tile
-// What a tile of dg and du holds past float16's largest value: its rows, its units of
-// dg and its units of du, a bit each.
-struct GradOver {
-    unsigned long long rows, gate, up;
-};
+// What a tile of dg and du holds past float16's largest value, a bit each: its rows,
+// its units of dg and its units of du.
+typedef unsigned long long GradMask;
 struct GatedGradArgs {
     const float* gu;        // (rows, 2 hidden)
     const void* dh;
@@ -98,7 +96,7 @@ struct GatedGradArgs {
     int rows, hidden, act;
     unsigned* flags;        // `nflags` arrival counters to clear for a K split that follows
     int nflags;
-    GradOver* over;         // F16: one a tile, hidden fastest
+    GradMask* over;         // F16: every tile's rows (hidden fastest), then its units of dg, then of du
     // launch_gated_repair
     const void* x;
     const void* w;

@@ -288,7 +288,7 @@ GradPlan plan_grad(int64_t rows, int64_t hidden, int64_t cols, int64_t x_stride,
     g.sums_x = g.flags + uint64_t(round_up(4 * int64_t(g.nflags()), 256));
     g.sums_w = g.sums_x + sums(g.x);
     g.over = g.sums_w + sums(g.w);
-    g.bytes = g.over + uint64_t(ceil_div(rows, 64) * ceil_div(hidden, 64)) * sizeof(GradOver);
+    g.bytes = g.over + uint64_t(ceil_div(rows, 64) * ceil_div(hidden, 64)) * 3 * sizeof(GradMask);
     return g;
 }
 
@@ -454,7 +454,7 @@ extern "C" int gemm_relu_gated_backward(const void* dh, int64_t dh_stride, const
         g.act = act;
         g.flags = flags;
         g.nflags = p.nflags();
-        g.over = reinterpret_cast<GradOver*>(ws + p.over);
+        g.over = reinterpret_cast<GradMask*>(ws + p.over);
         g.x = x;
         g.w = weight;
         g.dx = dx;

@@ -670,9 +670,9 @@ template <int DT, int ACT> __global__ void __launch_bounds__(kGradThreads) gated
     constexpr int ROWS = 64 * 16 / kGradThreads;
     constexpr int PITCH = 68;                      // elements of a transposed row: 8-byte pieces on spread banks
     __shared__ __attribute__((aligned(16))) T tile[2][64][PITCH];
-    __shared__ GradOver over;
+    __shared__ GradMask over[3];
     if constexpr (DT == DT_F16) {
-        if (threadIdx.x == 0) over = GradOver{};
+        if (threadIdx.x < 3) over[threadIdx.x] = 0;
         __syncthreads();
     }
     const int htiles = (a.hidden + 63) / 64;
@@ -720,9 +720,9 @@ template <int DT, int ACT> __global__ void __launch_bounds__(kGradThreads) gated
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const bool in_gate = passes_half(gate[e]), in_up = passes_half(up[e]);
-                if (in_gate) atomicOr(&over.gate, 1ull << (c + e));
-                if (in_up) atomicOr(&over.up, 1ull << (c + e));
-                if (in_gate || in_up) atomicOr(&over.rows, 1ull << (q + k));
+                if (in_gate) atomicOr(&over[1], 1ull << (c + e));
+                if (in_up) atomicOr(&over[2], 1ull << (c + e));
+                if (in_gate || in_up) atomicOr(&over[0], 1ull << (q + k));
             }
         }
         const int r = r0 + q + k;
@@ -752,7 +752,7 @@ template <int DT, int ACT> __global__ void __launch_bounds__(kGradThreads) gated
     }
     __syncthreads();
     if constexpr (DT == DT_F16)
-        if (threadIdx.x == 0) a.over[blockIdx.x] = over;
+        if (threadIdx.x < 3) a.over[(size_t)threadIdx.x * gridDim.x + blockIdx.x] = over[threadIdx.x];
 #pragma unroll
     for (int k = 0; k < 1024 / kGradThreads; ++k) {
         const int p = k * kGradThreads + (int)threadIdx.x, half = p >> 9, hh = (p >> 3) & 63, rr = (p & 7) * 8;
@@ -772,13 +772,15 @@ template <int DT, int ACT> __global__ void __launch_bounds__(kGradThreads) gated
 // in fp32 from dg and du as they are.  A row counts if any of its elements passes the
 // range; the others keep the products' results, whatever shares their tile.
 //
-// One launch more for float16, which finds nothing to do but for gradients that large:
-// 2-3 us of a small call, 10 of 835 at 4096 x 7168 x 4096.  Otherwise it takes 0.8 ms at
-// 1027 x 2003 x 1501, 6.6 (one element) to 26 (all rows) at 4096 x 7168 x 4096, bound by
-// its steps' latency: 64 x 64 outputs a workgroup, 4 x 4 a thread, 16 K elements of
-// both operands a step in LDS, for a case that a loss scale meets once in a while.
+// One launch more for float16, whose workgroups read the notes of all tiles and end
+// there, 4 us (5 at 4096 x 7168 x 4096), but for gradients that large.  Then it takes
+// 0.5 ms (one element) to 1 ms at 1027 x 2003 x 1501, 3.3 to 26 at 4096 x 7168 x 4096,
+// bound by its steps' latency: 64 x 64 outputs a workgroup, 4 x 4 a thread, 16 K elements
+// of both operands a step in LDS, for a case that a loss scale meets once in a while.
+// Pieces are dealt out singly so that one large element occupies the device (with a few
+// workgroups a block of rows it took 6.6 ms, and 13 us where there is nothing to do).
 constexpr int kRepairK = 16;
-__device__ __forceinline__ unsigned long long group_or(unsigned long long v, unsigned long long* lds)
+__device__ __forceinline__ GradMask group_or(GradMask v, GradMask* lds)
 {
 #pragma unroll
     for (int step = 1; step < 64; step *= 2) v |= __shfl_xor(v, step);
@@ -786,33 +788,43 @@ __device__ __forceinline__ unsigned long long group_or(unsigned long long v, uns
     __syncthreads();
     return lds[0] | lds[1] | lds[2] | lds[3];
 }
-template <int ACT> __global__ void __launch_bounds__(kThreads) gated_repair_kernel(GatedGradArgs a, int parts)
+template <int ACT> __global__ void __launch_bounds__(kThreads) gated_repair_kernel(GatedGradArgs a)
 {
     using T = _Float16;
-    __shared__ unsigned long long masks[2][kThreads / 64];
+    __shared__ GradMask masks[2][kThreads / 64];
     __shared__ float left[2][kRepairK][64], right[2][kRepairK][64];
-    const int tid = (int)threadIdx.x, block = (int)blockIdx.x / parts, part = (int)blockIdx.x % parts;
-    const int htiles = (a.hidden + 63) / 64, rtiles = (a.rows + 63) / 64;
-    const bool of_dx = block < rtiles;
-    const int m0 = 64 * (of_dx ? block : block - rtiles);       // its first row of dx, or unit
-    // what the tiles along the other side found
-    unsigned long long gate = 0, up = 0;
-    if (of_dx) {
-        for (int t = tid; t < htiles; t += kThreads) gate |= a.over[(size_t)block * htiles + t].rows;
-    } else {
-        for (int t = tid; t < rtiles; t += kThreads) {
-            const GradOver& o = a.over[(size_t)t * htiles + (block - rtiles)];
-            gate |= o.gate;
-            up |= o.up;
-        }
-    }
-    gate = group_or(gate, masks[0]);
-    up = group_or(up, masks[1]);
-    if (!(gate | up)) return;
+    const int tid = (int)threadIdx.x, htiles = (a.hidden + 63) / 64, rtiles = (a.rows + 63) / 64, tiles = htiles * rtiles;
+    GradMask any = 0;
+#pragma unroll 8
+    for (int t = tid; t < tiles; t += kThreads) any |= a.over[t];
+    if (!group_or(any, masks[0])) return;
 
-    const int K = of_dx ? a.hidden : a.rows, mi = (tid >> 4) * 4, ni = (tid & 15) * 4;
-    constexpr int NL = 64 * kRepairK / kThreads, NR = 2 * NL;
-    for (int64_t n0 = (int64_t)part * 64; n0 < a.cols; n0 += (int64_t)parts * 64) {
+    // 64 columns of 64 rows of dx, or of a 64-unit block of dweight, at a time
+    const int col_tiles = (int)(((int64_t)a.cols + 63) / 64);
+    const int64_t pieces = (int64_t)(rtiles + htiles) * col_tiles;
+    for (int64_t piece = blockIdx.x; piece < pieces; piece += gridDim.x) {
+        const int block = (int)(piece / col_tiles);
+        const int64_t n0 = piece % col_tiles * 64;
+        const bool of_dx = block < rtiles;
+        const int m0 = 64 * (of_dx ? block : block - rtiles);       // its first row of dx, or unit
+        // what the tiles along the other side found
+        GradMask gate = 0, up = 0;
+        if (of_dx) {
+            for (int t = tid; t < htiles; t += kThreads) gate |= a.over[(size_t)block * htiles + t];
+        } else {
+            for (int t = tid; t < rtiles; t += kThreads) {
+                const size_t at = (size_t)t * htiles + (block - rtiles);
+                gate |= a.over[tiles + at];
+                up |= a.over[2 * (size_t)tiles + at];
+            }
+        }
+        __syncthreads();                        // the last piece's masks have been read
+        gate = group_or(gate, masks[0]);
+        up = group_or(up, masks[1]);
+        if (!(gate | up)) continue;
+
+        const int K = of_dx ? a.hidden : a.rows, mi = (tid >> 4) * 4, ni = (tid & 15) * 4;
+        constexpr int NL = 64 * kRepairK / kThreads, NR = 2 * NL;
         float sums[2][4][4] = {};           // dx: the first only
         for (int k0 = 0; k0 < K; k0 += kRepairK) {
             __syncthreads();                // the last step's reads are done
@@ -834,8 +846,8 @@ template <int ACT> __global__ void __launch_bounds__(kThreads) gated_repair_kern
             for (int i = 0; i < NR; ++i) {
                 const int e = i * kThreads + tid, k = (e / 64) % kRepairK, half = e / (64 * kRepairK);
                 const size_t row = (size_t)min(k0 + k, K - 1) + (of_dx && half ? (size_t)a.hidden : 0);
-                other[i] = (float)static_cast<const T*>(of_dx ? a.w : a.x)[row * (size_t)(of_dx ? a.w_stride : a.x_stride) +
-                                                                          (size_t)min(n0 + e % 64, (int64_t)a.cols - 1)];
+                const size_t col = (size_t)min(n0 + e % 64, (int64_t)a.cols - 1);
+                other[i] = (float)static_cast<const T*>(of_dx ? a.w : a.x)[row * (size_t)(of_dx ? a.w_stride : a.x_stride) + col];
             }
 #pragma unroll
             for (int i = 0; i < NL; ++i) {
@@ -1146,12 +1158,10 @@ hipError_t launch_gated_grad(const GatedGradArgs& a, int dt, hipStream_t stream)
 
 hipError_t launch_gated_repair(const GatedGradArgs& a, hipStream_t stream)
 {
-    // every 64 rows of dx and every 64 units of dweight, 64 of their columns a workgroup
-    // up to 2^13 workgroups: a single large element is spread over the device
-    const int64_t blocks = ceil_div(a.hidden, 64) + ceil_div(a.rows, 64);
-    const int parts = (int)std::max<int64_t>(1, std::min<int64_t>(ceil_div(a.cols, 64), (1 << 13) / blocks));
+    const int64_t pieces = (ceil_div(a.hidden, 64) + ceil_div(a.rows, 64)) * ceil_div(a.cols, 64);
     return with_act(a.act, [&](auto act) {
-        return start(&gated_repair_kernel<decltype(act)::value>, dim3((unsigned)(blocks * parts)), kThreads, stream, a, parts);
+        return start(&gated_repair_kernel<decltype(act)::value>, dim3((unsigned)std::min<int64_t>(pieces, 2 * kNumCUs)), kThreads,
+                     stream, a);
     });
 }
 
