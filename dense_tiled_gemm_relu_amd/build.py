@@ -37,7 +37,7 @@ LIB_SOURCES = ["gemm_relu_api.hip", "inst_f16_nn.hip", "inst_f16_nt.hip",
 PROBE_SOURCES = ["probe_layouts.hip", "probe_mfma_rate.hip", "probe_mfma16.hip", "probe_fp8.hip",
                  "probe_sparse.hip"]
 HEADERS = ["gemm_relu_kernel.hpp", "configs.hpp", "gemm_sp_relu_kernel.hpp", "api_common.hpp",
-           "ffn.hpp"]
+           "ffn.hpp", "linear_plan.hpp", "row_common.hpp"]
 
 # gfx950 only.  Packed fp32 ALU ops are switched off: the compiler otherwise
 # forms v_pk_* fp32 instructions from ordinary float code.
@@ -100,12 +100,13 @@ def _link(objs, out, verbose):
 def _front_end(force, verbose):
     """The CPython module: host code only, so the host compiler builds it."""
     src = os.path.join(CSRC, "ffn_torch.cpp")
-    if not force and not _newer(FFN_MODULE, [src, os.path.join(INCLUDE, "gemm_relu_ffn.h")]):
+    if not force and not _newer(FFN_MODULE, [src, os.path.join(CSRC, "torch_args.hpp"),
+                                             os.path.join(INCLUDE, "gemm_relu_ffn.h")]):
         return
     torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
     inc, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
     tmp = FFN_MODULE + ".tmp"
-    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden", "-I", INCLUDE,
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", "-fvisibility=hidden", "-I", INCLUDE, "-I", CSRC,
            "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"),
            "-isystem", sysconfig.get_paths()["include"], src, "-o", tmp, "-L", lib, "-lc10", "-ltorch_cpu",
            "-ltorch_python"]
