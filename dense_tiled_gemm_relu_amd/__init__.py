@@ -38,7 +38,8 @@ EXPORTS = ("gemm_relu", "gemm_relu_strerror", "gemm_relu_configs", "gemm_relu_pl
            "gemm_relu_layer_norm_backward_workspace", "gemm_relu_gated", "gemm_relu_gated_plan",
            "gemm_relu_gated_backward", "gemm_relu_gated_backward_workspace",
            "gemm_relu_gated_backward_plan", "gemm_relu_quantize_rows", "gemm_relu_i8",
-           "gemm_relu_i8_plan")
+           "gemm_relu_i8_plan", "gemm_relu_act", "gemm_relu_act_plan", "gemm_relu_act_backward",
+           "gemm_relu_act_backward_workspace", "gemm_relu_act_backward_plan")
 
 _lib = None
 
@@ -96,8 +97,9 @@ def library():
     lib.gemm_relu_sp_plan.argtypes = [vp, vp, vp, vp, i64, i64, i64, ctypes.c_int, ctypes.c_int,
                                       ctypes.c_int]
     lib.gemm_relu_sp_plan.restype = ctypes.c_char_p
-    from . import ffn
+    from . import block, ffn
     ffn.declare(lib)
+    block.declare(lib)
     _lib = lib
     return lib
 
@@ -289,3 +291,5 @@ def matmul_relu(A, B, transB=False, out_dtype=None, out=None, stream=None):
 # Operators of a feed-forward half layer (include/gemm_relu_ffn.h).
 from .ffn import (ACTIVATIONS, layer_norm, layer_norm_backward, matmul_gated,  # noqa: E402,F401
                   matmul_gated_backward, matmul_i8, quantize_rows)
+# Operators around it (include/gemm_relu_block.h).
+from .block import matmul_act, matmul_act_backward  # noqa: E402,F401

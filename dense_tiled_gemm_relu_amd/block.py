@@ -1,0 +1,89 @@
+"""Operators around a transformer's feed-forward half layer, on torch tensors.
+
+The product with bias, activation and residual in its epilogue, with its backward
+pass.  The work is done by the kernels behind include/gemm_relu_block.h, called
+through a small C++ module (csrc/block_torch.cpp); there is no CPU or PyTorch
+fallback.  Rows, strides, streams, results without autograd graphs: as in ffn.py.
+"""
+import ctypes
+import os
+
+from . import ffn
+
+ACTIVATIONS = {"none": 4, **ffn.ACTIVATIONS}
+
+_vp, _i64, _int, _u64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint64
+_SIGNATURES = {
+    "gemm_relu_act": ([_vp, _i64, _vp, _i64, _vp, _vp, _i64, _vp, _vp, _i64, _i64, _i64, _int, _int, _int, _vp], _int),
+    "gemm_relu_act_plan": ([_i64, _i64, _i64, _int], ctypes.c_char_p),
+    "gemm_relu_act_backward_workspace": ([_i64, _i64, _i64], _i64),
+    "gemm_relu_act_backward": ([_vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _int, _int,
+                                _int, _vp, _u64, _vp], _int),
+    "gemm_relu_act_backward_plan": ([_i64, _i64, _i64, _int], ctypes.c_char_p),
+}
+
+
+def declare(lib):
+    """Argument and result types of the functions of include/gemm_relu_block.h."""
+    for name, (args, res) in _SIGNATURES.items():
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = args, res
+
+
+MODULE_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_block.so")
+# the C functions the front end calls, in the order it takes them
+_BOUND = ("gemm_relu_act", "gemm_relu_act_backward_workspace", "gemm_relu_act_backward")
+
+_ops = _current_device = _raw_stream = _tensor = None
+
+
+def _load():
+    """The front end module, bound to the loaded library; raises if either has
+    not been built."""
+    global _ops, _current_device, _raw_stream, _tensor
+    import torch
+    ops = ffn.load_module("_block", MODULE_PATH, _BOUND)
+    _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+    _tensor = torch.Tensor
+    _ops = ops
+    return ops
+
+
+def _call(name, stream, *args):
+    return ffn.call_on(_ops or _load(), name, stream, args)
+
+
+def _activation(act):
+    code = ACTIVATIONS.get(act)
+    if code is None:
+        raise ValueError("act must be one of %s" % ", ".join(sorted(ACTIVATIONS)))
+    return code
+
+
+def matmul_act(x, weight, bias=None, act="none", residual=None, save=False, stream=None):
+    """Product with bias, activation and residual: y = act(x weight^T + bias) + residual.
+
+    x: (..., k) float16 or bfloat16; weight: (n, k); bias (n) of x's type or float32;
+    residual: (..., n), of x's type.  act: "none", "silu", "gelu", "gelu_tanh" or
+    "relu".  Returns y (..., n), or with ``save`` (y, z): z (..., n) holds the fp32
+    sums x weight^T + bias for matmul_act_backward (None without an activation, whose
+    gradient takes none).
+    """
+    code = _activation(act)
+    if stream is None and _ops is not None and isinstance(x, _tensor):
+        index = x.get_device()
+        if index >= 0 and _current_device() == index:
+            return _ops.matmul_act(x, weight, bias, code, residual, save, _raw_stream(index))
+    return _call("matmul_act", stream, x, weight, bias, code, residual, save)
+
+
+def matmul_act_backward(dy, z, x, weight, act="none", bias=None, stream=None):
+    """Gradients (dx, dweight, dbias) of matmul_act, given dy and the forward call's z
+    (None without an activation).  dx and dweight have x's type; dbias has the bias's,
+    and is None without one.  The residual's gradient is dy."""
+    code = _activation(act)
+    if stream is None and _ops is not None and isinstance(x, _tensor):
+        index = x.get_device()
+        if index >= 0 and _current_device() == index:
+            return _ops.matmul_act_backward(dy, z, x, weight, code, bias, _raw_stream(index))
+    return _call("matmul_act_backward", stream, dy, z, x, weight, code, bias)

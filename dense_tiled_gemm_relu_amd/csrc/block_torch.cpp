@@ -1,0 +1,151 @@
+// Tensor front end of the operators around the half layer, as a CPython module
+// (dense_tiled_gemm_relu_amd._block): argument checks, allocation of the results and
+// the workspaces, and the call into the C-ABI of include/gemm_relu_block.h.
+//
+// As in the feed-forward operators' module, the functions take their arguments by
+// position, and last the raw stream of the current device that the call runs on;
+// block.py holds the user's signatures.
+#include "gemm_relu_block.h"
+#include "torch_args.hpp"
+
+namespace {
+
+struct Api {
+    decltype(&gemm_relu_act) act;
+    decltype(&gemm_relu_act_backward_workspace) act_backward_workspace;
+    decltype(&gemm_relu_act_backward) act_backward;
+} api;
+
+// ---- arguments that may be None
+const at::Tensor* maybe(PyObject* o, const char* name) { return o == Py_None ? nullptr : &tensor(o, name); }
+const void* data(const at::Tensor* t) { return t ? t->data_ptr() : nullptr; }
+PyObject* give_all(std::initializer_list<const at::Tensor*> all)
+{
+    PyObject* out = PyTuple_New(Py_ssize_t(all.size()));
+    if (!out) throw python_error();
+    Py_ssize_t k = 0;
+    for (const at::Tensor* t : all) {
+        PyObject* item = Py_None;
+        if (t && t->defined())
+            item = THPVariable_Wrap(*t);
+        else
+            Py_INCREF(item);
+        PyTuple_SET_ITEM(out, k++, item);
+    }
+    return out;
+}
+int code_arg(PyObject* o)
+{
+    const long c = PyLong_AsLong(o);
+    if (c == -1 && PyErr_Occurred()) throw python_error();
+    return int(c);
+}
+
+// ---- product with bias, activation, residual
+struct Act {
+    Rows x, w;
+    int code, bias_code;
+};
+Act act_args(const at::Tensor& x, const at::Tensor& w, const at::Tensor* bias)
+{
+    Act a;
+    a.code = a.bias_code = code_of(x.scalar_type());
+    if (a.code < 0 || a.code == GEMM_RELU_F32 || w.scalar_type() != x.scalar_type())
+        refuse(PyExc_TypeError, "x and weight must share dtype float16 or bfloat16");
+    a.x = rows_of(x, "x");
+    a.w = matrix_of(w, "weight");
+    if (a.w.cols != a.x.cols) refuse(PyExc_ValueError, "inner dimensions differ: ", a.x.cols, " vs ", a.w.cols);
+    if (bias) {
+        expect_vector(*bias, "bias", a.w.rows, x.scalar_type(), at::kFloat);
+        a.bias_code = code_of(bias->scalar_type());
+    }
+    return a;
+}
+// dy, or the residual: of x's type, x's rows of n
+Rows output_rows(const at::Tensor& t, const char* name, const at::Tensor& x, int64_t n)
+{
+    if (t.scalar_type() != x.scalar_type()) refuse(PyExc_TypeError, name, " must have x's type");
+    if (t.sizes() != at::IntArrayRef(with_last(x, n)))
+        refuse(PyExc_ValueError, name, " must have the result's shape: x's, with ", n, " for the last dimension");
+    return rows_of(t, name);
+}
+
+// x, weight, bias or None, act (code), residual or None, save, stream
+PyObject* matmul_act(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    expect_args(n, 7);
+    const at::Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "weight");
+    const at::Tensor *bias = maybe(a[2], "bias"), *residual = maybe(a[4], "residual");
+    const int act = code_arg(a[3]);
+    const bool save = truth(a[5]);
+    const Act s = act_args(x, w, bias);
+    const Rows r = residual ? output_rows(*residual, "residual", x, s.w.rows) : Rows{};
+    warn_of_lost_gradients("matmul_act", {&x, &w, bias, residual});
+    expect_one_gpu({&x, &w, bias, residual});
+    at::Tensor y = make(x, with_last(x, s.w.rows), x.scalar_type()), z;
+    if (save && act != GEMM_RELU_ACT_NONE) z = make(x, with_last(x, s.w.rows), at::kFloat);
+    check(api.act(x.data_ptr(), s.x.ld, w.data_ptr(), s.w.ld, data(bias), data(residual), r.ld, y.data_ptr(),
+                  z.defined() ? floats(z) : nullptr, s.x.rows, s.w.rows, s.x.cols, s.code, s.bias_code, act, pointer(a[6])));
+    return save ? give_all({&y, &z}) : give(std::move(y));
+    END_HANDLE_TH_ERRORS
+}
+
+// dy, z or None, x, weight, act (code), bias or None, stream
+PyObject* matmul_act_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    expect_args(n, 7);
+    const at::Tensor &dy = tensor(a[0], "dy"), &x = tensor(a[2], "x"), &w = tensor(a[3], "weight");
+    const int act = code_arg(a[4]);
+    const at::Tensor *z = maybe(a[1], "z"), *bias = maybe(a[5], "bias");
+    const Act s = act_args(x, w, bias);
+    const Rows d = output_rows(dy, "dy", x, s.w.rows);
+    if (act == GEMM_RELU_ACT_NONE)
+        z = nullptr;
+    else if (!z)
+        refuse(PyExc_TypeError, "z must be a tensor, not NoneType: the gradient of an activation takes matmul_act's (save=True)");
+    else
+        expect_vector(*z, "z", s.x.rows * s.w.rows, at::kFloat, at::kFloat);
+    warn_of_lost_gradients("matmul_act_backward", {&x, &w, &dy, z, bias});
+    expect_one_gpu({&x, &w, &dy, z, bias});
+    at::Tensor dx = make(x, x.sizes(), x.scalar_type()), dw = make(w, w.sizes(), w.scalar_type()), db;
+    if (bias) db = make(*bias, bias->sizes(), bias->scalar_type());
+    const int64_t bytes = api.act_backward_workspace(s.x.rows, s.w.rows, s.x.cols);
+    const at::Tensor ws = workspace(x, bytes < 0 ? 0 : bytes);
+    check(api.act_backward(dy.data_ptr(), d.ld, z ? floats(*z) : nullptr, x.data_ptr(), s.x.ld, w.data_ptr(), s.w.ld,
+                           dx.data_ptr(), dw.data_ptr(), bias ? db.data_ptr() : nullptr, s.x.rows, s.w.rows, s.x.cols,
+                           s.code, s.bias_code, act, ws.data_ptr(), uint64_t(ws.numel()), pointer(a[6])));
+    return give_all({&dx, &dw, &db});
+    END_HANDLE_TH_ERRORS
+}
+
+// the status error, then the C functions' addresses in the order of Api
+PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    expect_args(n, 4);
+    Api b;
+    auto set = [&](auto& fn, int k) { fn = reinterpret_cast<std::remove_reference_t<decltype(fn)>>(pointer(a[k])); };
+    set(b.act, 1);
+    set(b.act_backward_workspace, 2);
+    set(b.act_backward, 3);
+    Py_INCREF(a[0]);
+    Py_XDECREF(status_error);
+    status_error = a[0];
+    api = b;
+    Py_RETURN_NONE;
+    END_HANDLE_TH_ERRORS
+}
+
+PyMethodDef methods[] = {
+    {"bind", method(bind), METH_FASTCALL, nullptr},
+    {"matmul_act", method(matmul_act), METH_FASTCALL, nullptr},
+    {"matmul_act_backward", method(matmul_act_backward), METH_FASTCALL, nullptr},
+    {nullptr, nullptr, 0, nullptr},
+};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_block", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__block() { return PyModule_Create(&module); }

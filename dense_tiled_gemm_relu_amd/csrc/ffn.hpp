@@ -56,7 +56,9 @@ typedef hipError_t (*PairLaunchFn)(const LinearPair& pair, int grid, hipStream_t
 PairLaunchFn launcher_cast_pair(int dt, int cfg);
 LinearLaunchFn launcher_gated(int dt, int cfg);                // B stored (N,K)
 LinearLaunchFn launcher_i8(int out_dt, int cfg);               // B stored (N,K)
-LinearLaunchFn launcher_skinny_gated(int dt, int cfg);         // the LIN_K* forms of both
+LinearLaunchFn launcher_act(int dt, int cfg);                  // B stored (N,K)
+LinearLaunchFn launcher_skinny_gated(int dt, int cfg);         // the LIN_K* forms of these
+LinearLaunchFn launcher_skinny_act(int dt, int cfg);
 LinearLaunchFn launcher_skinny_i8(int out_dt, int cfg);
 
 // ---- rows and element-wise work (ffn_rows.hip)

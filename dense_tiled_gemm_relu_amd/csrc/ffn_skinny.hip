@@ -1,5 +1,6 @@
-// Products with few rows of x, or few outputs, B stored (N,K): gated projections
-// and the scaled 8-bit product of a decode step or a small batch.
+// Products with few rows of x, or few outputs, B stored (N,K): gated projections, the
+// product with bias, activation and residual, and the scaled 8-bit product of a decode
+// step or a small batch.
 //
 // What bounds them is reading the weight once (M <= 64), or the latency of a
 // tile's K loop where the tiles do not fill the device.  A workgroup of four
@@ -178,6 +179,18 @@ __global__ void __launch_bounds__(kThreads) skinny_kernel(KernelArgs a)
                 }
             });
             mine = mine && g4 < 2;
+        } else if constexpr (EPI == EPI_ACT) {
+            c = c0 + 16 * j + 4 * g4;
+            const f32x4_t z = s + load_bias<IN>(a, c, cols);
+            if (a.GU && mine && c < cols) store_sums(a.GU + (size_t)m * (size_t)cols + c, z, c, cols);
+            u32x2_t r = {0u, 0u};
+            if (a.R)
+                r = load_half4(reinterpret_cast<const unsigned short*>(a.R) + (size_t)min(m, a.M - 1) * (size_t)a.ldr, c, cols);
+            with_activation_or_none(a.act, [&](auto kind) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = activation<decltype(kind)::value>(z[e]);
+            });
+            if (a.R) v += to_float4<IN>(r);
         } else {
             c = c0 + 16 * j + 4 * g4;
             const float sa = a.scale_a[min(m, a.M - 1)];
@@ -227,6 +240,11 @@ template <int IN, int OUT, int EPI> LinearLaunchFn pick(int cfg)
 LinearLaunchFn launcher_skinny_gated(int dt, int cfg)
 {
     return dt == DT_F16 ? pick<DT_F16, DT_F16, EPI_GATED>(cfg) : pick<DT_BF16, DT_BF16, EPI_GATED>(cfg);
+}
+
+LinearLaunchFn launcher_skinny_act(int dt, int cfg)
+{
+    return dt == DT_F16 ? pick<DT_F16, DT_F16, EPI_ACT>(cfg) : pick<DT_BF16, DT_BF16, EPI_ACT>(cfg);
 }
 
 LinearLaunchFn launcher_skinny_i8(int out_dt, int cfg)

@@ -51,11 +51,12 @@ enum : int { DT_I8 = 8 };   // signed 8-bit integers (EPI_I8 only), int32 accumu
 
 // What a tile does with its finished sums.  EPI_RELU: the fused GEMM + ReLU.
 // The others serve the feed-forward operators and take row strides of A and B:
-// EPI_CAST stores the rounded sums (A's rows are padded to lda, a multiple of 16
-// bytes, with zeros); EPI_GATED holds the sums g and u of a gate
+// EPI_CAST stores the rounded sums times alpha (A's rows are padded to lda, a multiple
+// of 16 bytes, with zeros); EPI_GATED holds the sums g and u of a gate
 // and an up projection side by side and stores act(g) u; EPI_I8 multiplies
-// integer sums by a scale per row of A and a scale per row of B.
-enum : int { EPI_RELU = 0, EPI_CAST = 1, EPI_GATED = 2, EPI_I8 = 3 };
+// integer sums by a scale per row of A and a scale per row of B; EPI_ACT adds a bias
+// per column, applies an activation and adds a residual.
+enum : int { EPI_RELU = 0, EPI_CAST = 1, EPI_GATED = 2, EPI_I8 = 3, EPI_ACT = 4 };
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
@@ -107,11 +108,18 @@ struct KernelArgs {
     // the `hidden` gate rows, then the `hidden` up rows; C is (M, hidden); GU,
     // unless null, receives the fp32 sums, M rows of hidden g then hidden u.
     // EPI_I8: one scale per row of A and per row of B.
+    // EPI_ACT: bias and R (M rows of N, ldr apart) may be null; GU, unless null,
+    // receives the fp32 sums with the bias, M rows of N.
     int lda, ldb;
     int hidden, act;
     float* GU;
     const float* scale_a;
     const float* scale_b;
+    float alpha;
+    const void* bias;
+    int bias_f32;             // the bias is fp32, else of A's type
+    int ldr;
+    const unsigned char* R;
 };
 
 // The tiles one configuration covers inside a launch: a grid of tiles_m x
@@ -326,7 +334,7 @@ __device__ __forceinline__ float relu(float x) { return x > 0.0f ? x : 0.0f; }
 // reciprocal are within a few fp32 ulps, far inside the 16-bit rounding of the
 // results.  The normal distribution function is taken from erfcf, which keeps
 // its relative accuracy in the lower tail where 1 + erf cancels.
-enum : int { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2, ACT_RELU = 3 };
+enum : int { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2, ACT_RELU = 3, ACT_NONE = 4 };
 // 1 / (1 + e^-z), as t / (1 + t) with t = e^z for negative z; e^-|z| is the
 // square of e^(-|z| / 2), since the hardware exponential alone would return 0
 // where the result is below the normal range
@@ -344,6 +352,7 @@ template <int ACT> __device__ __forceinline__ float activation(float g)
     if constexpr (ACT == ACT_GELU) return g * normal_cdf(g);
     // 0.5 (1 + tanh z) = 1 / (1 + e^-2z)
     if constexpr (ACT == ACT_GELU_TANH) return g * logistic(kTwoGeluC * (g + 0.044715f * g * g * g));
+    if constexpr (ACT == ACT_NONE) return g;
     return relu(g);
 }
 // f(the activation as a constant): one choice for a whole loop of elements, so that
@@ -357,6 +366,14 @@ template <class F> __device__ __forceinline__ void with_activation(int act, F&& 
     case ACT_GELU_TANH: f(std::integral_constant<int, ACT_GELU_TANH>{}); break;
     default: f(std::integral_constant<int, ACT_RELU>{}); break;
     }
+}
+// ... or none (the gated projections have one always)
+template <class F> __device__ __forceinline__ void with_activation_or_none(int act, F&& f)
+{
+    if (act == ACT_NONE)
+        f(std::integral_constant<int, ACT_NONE>{});
+    else
+        with_activation(act, f);
 }
 // value and slope of the activation at g
 template <int ACT> __device__ __forceinline__ void activation_slope(float g, float& value, float& slope)
@@ -374,6 +391,9 @@ template <int ACT> __device__ __forceinline__ void activation_slope(float g, flo
         value = g * s;
         // s (1 - s) is 0 long before the square is capped
         slope = s + g * s * (1.0f - s) * kTwoGeluC * (1.0f + 0.134145f * fminf(g * g, 1e30f));
+    } else if constexpr (ACT == ACT_NONE) {
+        value = g;
+        slope = 1.0f;
     } else {
         value = relu(g);
         slope = g > 0.0f ? 1.0f : 0.0f;
@@ -421,6 +441,58 @@ template <> struct OutTraits<DT_BF16> {
 template <> struct OutTraits<DT_F32> {
     static constexpr int bytes = 4;
 };
+
+// A 16-bit value, and four consecutive ones of a row whose columns n .. end at N (those
+// past the end are 0).
+template <int DT> __device__ __forceinline__ float to_float(unsigned short h)
+{
+    if constexpr (DT == DT_F16)
+        return (float)__builtin_bit_cast(_Float16, h);
+    else
+        return __builtin_bit_cast(float, (unsigned)h << 16);
+}
+template <int DT> __device__ __forceinline__ f32x4_t to_float4(u32x2_t w)
+{
+    return f32x4_t{to_float<DT>((unsigned short)w[0]), to_float<DT>((unsigned short)(w[0] >> 16)),
+                   to_float<DT>((unsigned short)w[1]), to_float<DT>((unsigned short)(w[1] >> 16))};
+}
+__device__ __forceinline__ u32x2_t load_half4(const unsigned short* row, int n, int N)
+{
+    u32x2_t w = {0u, 0u};
+    if (n + 4 <= N) {
+        __builtin_memcpy(&w, row + n, 8);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (n + e < N) w[e >> 1] |= (unsigned)row[n + e] << (16 * (e & 1));
+    }
+    return w;
+}
+// ... without a branch, for N >= 4: a group across the end is read moved back inside the
+// row and shifted down
+__device__ __forceinline__ u32x2_t load_half4_inside(const unsigned short* row, int n, int N)
+{
+    const int from = min(n, N - 4);
+    unsigned long long w;
+    __builtin_memcpy(&w, row + from, 8);
+    return __builtin_bit_cast(u32x2_t, w >> (16 * min(n - from, 3)));
+}
+// Four consecutive values of the bias (EPI_ACT): 0 without one, and past the end.
+template <int DT> __device__ __forceinline__ f32x4_t load_bias(const KernelArgs& args, int n, int N)
+{
+    f32x4_t v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (!args.bias) return v;
+    if (!args.bias_f32) return to_float4<DT>(load_half4(static_cast<const unsigned short*>(args.bias), n, N));
+    const float* b = static_cast<const float*>(args.bias);
+    if (n + 4 <= N) {
+        __builtin_memcpy(&v, b + n, 16);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (n + e < N) v[e] = b[n + e];
+    }
+    return v;
+}
 
 // ---------------------------------------------------------- configuration
 template <int IN_DT_, int OUT_DT_, bool TRANS_B_, int BM_, int BN_, int BK_, int WAVES_M_,
@@ -745,14 +817,14 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
     // loads with zero fill where it crosses the end of the row or the matrix,
     // then one 16 B LDS write per chunk.  The whole step of the register-staged
     // configurations; the K tail step of the direct ones.
-    constexpr bool MOVED_TAIL = C::EPI == EPI_GATED || C::EPI == EPI_I8;
+    constexpr bool MOVED_TAIL = C::EPI == EPI_GATED || C::EPI == EPI_I8 || C::EPI == EPI_ACT;
     u32x4_t ra[APT], rb[BPT];
     auto load_chunk = [&](const unsigned char* base, size_t row_off, int e0, int e_lim,
                           bool row_ok) -> u32x4_t {
         // EPC consecutive elements e0 .. e0+EPC-1 of one row; valid if e < e_lim.
         u32x4_t v = {0u, 0u, 0u, 0u};
         if (!row_ok) return v;
-        // gated and integer products: a chunk across the end of K is read from 16
+        // B stored (N,K), but for the GEMM + ReLU: a chunk across the end of K is read from 16
         // bytes before the end, with what the previous chunk holds cleared, in
         // both operands alike
         if (MOVED_TAIL && e_lim >= EPC) {
@@ -1689,6 +1761,55 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
             });
             return;
         }
+        if constexpr (C::EPI == EPI_ACT) {
+            auto col = [&](int j, int q) { return n0 + wn0 + MB * j + 4 * NG * q + 4 * g; };
+            f32x4_t bias[TN * NQ];
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+#pragma unroll
+                for (int q = 0; q < NQ; ++q) bias[j * NQ + q] = load_bias<C::IN_DT>(args, col(j, q), N);
+            // the next row's residual is on its way while a row is finished: no load
+            // stands behind a branch of its own (rows past the edge take the last one's)
+            u32x2_t next[TN * NQ] = {};
+            auto fetch = [&](int i) {
+                const unsigned short* row = reinterpret_cast<const unsigned short*>(args.R) +
+                                            (size_t)min(m0 + wm0 + MB * i + lr, M - 1) * (size_t)args.ldr;
+                if (N < 4) {
+#pragma unroll
+                    for (int b = 0; b < TN * NQ; ++b) next[b] = load_half4(row, col(b / NQ, b % NQ), N);
+                } else {
+#pragma unroll
+                    for (int b = 0; b < TN * NQ; ++b) next[b] = load_half4_inside(row, col(b / NQ, b % NQ), N);
+                }
+            };
+            if (args.R) fetch(0);
+            with_activation_or_none(args.act, [&](auto kind) {
+#pragma unroll
+                for (int i = 0; i < TM; ++i) {
+                    const int m = m0 + wm0 + MB * i + lr;
+                    u32x2_t r[TN * NQ];
+#pragma unroll
+                    for (int b = 0; b < TN * NQ; ++b) r[b] = next[b];
+                    if (args.R && i + 1 < TM) fetch(i + 1);
+#pragma unroll
+                    for (int j = 0; j < TN; ++j)
+#pragma unroll
+                        for (int q = 0; q < NQ; ++q) {
+                            f32x4_t z, v;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                z[e] = acc[i][j][4 * q + e] + bias[j * NQ + q][e];
+                                v[e] = activation<decltype(kind)::value>(z[e]);
+                            }
+                            const int n = col(j, q);
+                            if (args.GU && m < M && n < N) store_sums(args.GU + (size_t)m * (size_t)N + n, z, n, N);
+                            if (args.R) v += to_float4<C::IN_DT>(r[j * NQ + q]);
+                            put_group(i, j, q, v);
+                        }
+                }
+            });
+            return;
+        }
         // scales of the lane's rows and columns (rows and columns past the edge
         // take the last one's; their results are not stored)
         float sa[C::EPI == EPI_I8 ? TM : 1], sb[C::EPI == EPI_I8 ? TN * NQ : 1][4];
@@ -1715,6 +1836,7 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
 #pragma unroll
                         for (int e = 0; e < 4; ++e) x[e] = x[e] * sa[i] * sb[j * NQ + q][e];
                     }
+                    if constexpr (C::EPI == EPI_CAST) x *= args.alpha;
                     put_group(i, j, q, x);
                 }
     };

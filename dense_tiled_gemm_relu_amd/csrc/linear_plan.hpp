@@ -215,6 +215,7 @@ KernelArgs linear_args(const LinearPlan& p, const Linear& l, const void* A, cons
     a.split_steps = int(p.split_steps);
     a.panel = int(std::min<int64_t>(8, p.tiles_m));
     a.nxcd = 8;
+    a.alpha = 1.0f;
     return a;
 }
 

@@ -63,19 +63,24 @@ def _status_error(status):
 _ops = _current_device = _raw_stream = _tensor = None
 
 
-def _load():
-    """The front end module, bound to the loaded library; raises if either has
-    not been built."""
-    global _ops, _current_device, _raw_stream, _tensor
+def load_module(name, path, bound):
+    """The front end module `name`, bound to the `bound` functions of the loaded
+    library; raises if either has not been built."""
     from . import library
     lib = library()
-    if not os.path.exists(MODULE_PATH):
-        raise RuntimeError("front end %s is not built; run __graft_entry__.build()" % MODULE_PATH)
-    import torch
-    loader = importlib.machinery.ExtensionFileLoader("_ffn", MODULE_PATH)
-    ops = importlib.util.module_from_spec(importlib.util.spec_from_loader("_ffn", loader))
+    if not os.path.exists(path):
+        raise RuntimeError("front end %s is not built; run __graft_entry__.build()" % path)
+    loader = importlib.machinery.ExtensionFileLoader(name, path)
+    ops = importlib.util.module_from_spec(importlib.util.spec_from_loader(name, loader))
     loader.exec_module(ops)
-    ops.bind(_status_error, *(ctypes.cast(getattr(lib, name), _vp).value for name in _BOUND))
+    ops.bind(_status_error, *(ctypes.cast(getattr(lib, fn), _vp).value for fn in bound))
+    return ops
+
+
+def _load():
+    global _ops, _current_device, _raw_stream, _tensor
+    import torch
+    ops = load_module("_ffn", MODULE_PATH, _BOUND)
     _current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
     _tensor = torch.Tensor
     _ops = ops
@@ -93,9 +98,12 @@ def _as_torch_stream(stream, index):
 
 
 def _call(name, stream, *args):
-    """One call of the front end: on the tensors' GPU and `stream`, both made
+    return call_on(_ops or _load(), name, stream, args)
+
+
+def call_on(ops, name, stream, args):
+    """One call of the front end `ops`: on the tensors' GPU and `stream`, both made
     current for the allocations and the launches."""
-    ops = _ops or _load()
     first = next((a for a in args if hasattr(a, "get_device")), None)
     index = -1 if first is None else first.get_device()
     if index < 0:                                     # refused there, with the reason
@@ -103,7 +111,7 @@ def _call(name, stream, *args):
     import torch
     with torch.cuda.device(index):
         if stream is None:
-            return getattr(ops, name)(*args, _raw_stream(index))
+            return getattr(ops, name)(*args, torch._C._cuda_getCurrentRawStream(index))
         stream = _as_torch_stream(stream, index)
         with torch.cuda.stream(stream):
             out = getattr(ops, name)(*args, stream.cuda_stream)

@@ -1,0 +1,108 @@
+"""The operators around the half layer on the host: what they refuse, before any GPU call."""
+import pytest
+import torch
+
+import dense_tiled_gemm_relu_amd as gr
+
+# fake, well-aligned and disjoint addresses: validation inspects, never dereferences
+P = [i << 40 for i in range(1, 16)]
+X, W, B, R, Y, Z, DY, DX, DW, DB, WS, G, PW, S, ST = P
+F16, BF16, F32 = gr.F16, gr.BF16, gr.F32
+BIG = 2 ** 31
+
+
+def call(name, args, **over):
+    """The C function's status for `args` (a dict in argument order) with some replaced."""
+    assert set(over) <= set(args)
+    return getattr(gr.library(), name)(*{**args, **over}.values(), 0)
+
+
+ACT = dict(x=X, x_stride=8, w=W, w_stride=8, b=B, r=R, r_stride=6, y=Y, z=Z, rows=4, n=6, k=8, dtype=F16, bdtype=F32, act=0)
+ACT_BWD = dict(dy=DY, dy_stride=6, z=Z, x=X, x_stride=8, w=W, w_stride=8, dx=DX, dw=DW, db=DB, rows=4, n=6, k=8, dtype=F16,
+               bdtype=F16, act=0, ws=WS, ws_bytes=1 << 20)
+
+CASES = [("gemm_relu_act", ACT, o) for o in (
+    dict(rows=-1), dict(n=-1), dict(k=-1), dict(rows=BIG), dict(n=BIG), dict(dtype=F32), dict(dtype=3), dict(bdtype=BF16),
+    dict(act=-1), dict(act=5), dict(x_stride=7), dict(w_stride=7), dict(r_stride=5), dict(x_stride=BIG), dict(x=0), dict(w=0),
+    dict(y=0), dict(x=X + 1), dict(w=W + 1), dict(y=Y + 1), dict(b=B + 2), dict(r=R + 1), dict(z=Z + 2), dict(y=X), dict(y=W + 90),
+    dict(y=R), dict(z=R), dict(z=Y), dict(z=B), dict(y=B))]
+CASES += [("gemm_relu_act_backward", ACT_BWD, o) for o in (
+    dict(rows=-1), dict(n=BIG), dict(k=-1), dict(dtype=F32), dict(bdtype=BF16), dict(act=5), dict(dy_stride=5), dict(x_stride=1),
+    dict(dy=0), dict(z=0), dict(x=0), dict(w=0), dict(dx=0), dict(dw=0), dict(dx=X), dict(dw=W), dict(db=DW), dict(dx=DY),
+    dict(db=DY), dict(ws=0), dict(ws=WS + 64), dict(ws_bytes=100), dict(ws=W), dict(db=DB + 1))]
+
+
+@pytest.mark.parametrize("name,args,over", CASES)
+def test_invalid_arguments_fail_before_the_device(name, args, over):
+    assert call(name, args, **over) == gr.EINVAL
+
+
+@pytest.mark.parametrize("name,args,over", [
+    ("gemm_relu_act", ACT, dict(rows=0, x=0, y=0, r=0, z=0)), ("gemm_relu_act", ACT, dict(n=0, r_stride=0)),
+    ("gemm_relu_act_backward", ACT_BWD, dict(rows=0, n=0)), ("gemm_relu_act_backward", ACT_BWD, dict(n=0, k=0)),
+    ("gemm_relu_act_backward", ACT_BWD, dict(k=0, db=0)),
+])
+def test_calls_without_outputs_are_a_no_op(name, args, over):
+    assert call(name, args, **over) == gr.OK
+
+
+@pytest.mark.parametrize("name,args,over", [
+    ("gemm_relu_act", ACT, dict(k=BIG - 1, x_stride=BIG - 1, w_stride=BIG - 1)),
+    ("gemm_relu_act", ACT, dict(rows=BIG - 1, x=1 << 40, w=1 << 50, y=1 << 62, z=0, b=0, r=0, n=BIG - 1)),
+    ("gemm_relu_act_backward", ACT_BWD, dict(rows=2 ** 30 + 1)), ("gemm_relu_act_backward", ACT_BWD, dict(n=2 ** 30 + 1)),
+])
+def test_sizes_past_the_limits_are_refused(name, args, over):
+    assert call(name, args, **over) == gr.EUNSUPPORTED
+
+
+def test_workspaces_and_plans():
+    lib = gr.library()
+    # dz in both layouts and the sums of its 64-row tiles
+    assert lib.gemm_relu_act_backward_workspace(100, 20, 30) >= 2 * 2 * 100 * 20 + 2 * 20 * 4
+    assert lib.gemm_relu_act_backward_workspace(10, -20, 30) == gr.EINVAL
+    assert lib.gemm_relu_act_backward_workspace(2 ** 30 + 1, 1, 1) == gr.EUNSUPPORTED
+    assert lib.gemm_relu_act_backward_workspace(2 ** 20, 2 ** 20, 8) >= 2 ** 42          # grows without wrapping
+    assert lib.gemm_relu_act_plan(4, 6, 8, F32) is None
+    assert lib.gemm_relu_act_plan(0, 6, 8, F16) == b"none"
+    assert lib.gemm_relu_act_plan(4, 6, BIG - 1, F16) == b"unsupported"
+    assert lib.gemm_relu_act_plan(4, 6, 8, F16)
+    assert lib.gemm_relu_act_backward_plan(4, 6, 8, F32) is None
+    assert lib.gemm_relu_act_backward_plan(4, 6, 0, F16) == b"none"
+    assert lib.gemm_relu_act_backward_plan(2 ** 30 + 1, 6, 8, F16) == b"unsupported"
+    assert lib.gemm_relu_act_backward_plan(4, 6, 8, F16).count(b",") == 1
+
+
+# ---- the tensor front ends (CPU tensors: every refusal comes before the device is looked at, the last one is it)
+def t(*shape, dtype=torch.float16):
+    return torch.zeros(shape, dtype=dtype)
+
+
+F = torch.float32
+H = torch.bfloat16
+
+
+@pytest.mark.parametrize("error,fn", [
+    (ValueError, lambda: gr.matmul_act(t(4, 8), t(6, 8), act="swish")),
+    (TypeError, lambda: gr.matmul_act([1.0], t(6, 8))),
+    (TypeError, lambda: gr.matmul_act(t(4, 8, dtype=F), t(6, 8, dtype=F))),
+    (TypeError, lambda: gr.matmul_act(t(4, 8), t(6, 8, dtype=H))),
+    (ValueError, lambda: gr.matmul_act(t(4, 8), t(6, 9))),
+    (ValueError, lambda: gr.matmul_act(t(4, 8), t(8, 6).t())),
+    (ValueError, lambda: gr.matmul_act(t(4, 8), t(2, 3, 8))),
+    (ValueError, lambda: gr.matmul_act(t(4, 8), t(6, 8), t(8))),
+    (TypeError, lambda: gr.matmul_act(t(4, 8), t(6, 8), t(6, dtype=H))),
+    (TypeError, lambda: gr.matmul_act(t(4, 8), t(6, 8), residual=t(4, 6, dtype=F))),
+    (ValueError, lambda: gr.matmul_act(t(4, 8), t(6, 8), residual=t(4, 8))),
+    (ValueError, lambda: gr.matmul_act(t(4, 8), t(6, 8), residual=t(6, 4).t())),
+    (ValueError, lambda: gr.matmul_act(t(4, 8), t(6, 8), t(6), "gelu", t(4, 6))),          # not on a GPU
+    (TypeError, lambda: gr.matmul_act_backward(t(4, 6, dtype=H), t(4, 6, dtype=F), t(4, 8), t(6, 8), "silu")),
+    (ValueError, lambda: gr.matmul_act_backward(t(4, 5), t(4, 6, dtype=F), t(4, 8), t(6, 8), "silu")),
+    (TypeError, lambda: gr.matmul_act_backward(t(4, 6), None, t(4, 8), t(6, 8), "silu")),
+    (TypeError, lambda: gr.matmul_act_backward(t(4, 6), t(4, 6), t(4, 8), t(6, 8), "silu")),
+    (ValueError, lambda: gr.matmul_act_backward(t(4, 6), t(4, 5, dtype=F), t(4, 8), t(6, 8), "silu")),
+    (ValueError, lambda: gr.matmul_act_backward(t(4, 6), None, t(4, 8), t(6, 8), "none", t(5))),
+    (ValueError, lambda: gr.matmul_act_backward(t(4, 6), None, t(4, 8), t(6, 8), "none", t(6))),
+])
+def test_front_ends_refuse(error, fn):
+    with pytest.raises(error):
+        fn()
