@@ -1,7 +1,8 @@
 """Operators around a transformer's feed-forward half layer, on torch tensors.
 
-The product with bias, activation and residual in its epilogue, with its backward
-pass.  The work is done by the kernels behind include/gemm_relu_block.h, called
+The product with bias, activation and residual in its epilogue and the step from one
+block to the next (residual sum and norms), both with their backward passes.  The work
+is done by the kernels behind include/gemm_relu_block.h, called
 through a small C++ module (csrc/block_torch.cpp); there is no CPU or PyTorch
 fallback.  Rows, strides, streams, results without autograd graphs: as in ffn.py.
 """
@@ -11,6 +12,7 @@ import os
 from . import ffn
 
 ACTIVATIONS = {"none": 4, **ffn.ACTIVATIONS}
+NORMS = {"rms": 0, "layer": 1}
 
 _vp, _i64, _int, _u64 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint64
 _SIGNATURES = {
@@ -20,6 +22,11 @@ _SIGNATURES = {
     "gemm_relu_act_backward": ([_vp, _i64, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _int, _int,
                                 _int, _vp, _u64, _vp], _int),
     "gemm_relu_act_backward_plan": ([_i64, _i64, _i64, _int], ctypes.c_char_p),
+    "gemm_relu_add_norm": ([_vp, _i64, _vp, _i64, _vp, _i64] + [_vp] * 6 + [_i64, _i64, _int, _int, _int, ctypes.c_float,
+                           ctypes.c_float, _vp], _int),
+    "gemm_relu_add_norm_backward_workspace": ([_i64, _i64], _i64),
+    "gemm_relu_add_norm_backward": ([_vp, _i64] * 5 + [_vp] * 9 + [_i64, _i64, _int, _int, _int, ctypes.c_float, _vp, _u64,
+                                    _vp], _int),
 }
 
 
@@ -32,7 +39,8 @@ def declare(lib):
 
 MODULE_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_block.so")
 # the C functions the front end calls, in the order it takes them
-_BOUND = ("gemm_relu_act", "gemm_relu_act_backward_workspace", "gemm_relu_act_backward")
+_BOUND = ("gemm_relu_act", "gemm_relu_act_backward_workspace", "gemm_relu_act_backward", "gemm_relu_add_norm",
+          "gemm_relu_add_norm_backward_workspace", "gemm_relu_add_norm_backward")
 
 _ops = _current_device = _raw_stream = _tensor = None
 
@@ -87,3 +95,45 @@ def matmul_act_backward(dy, z, x, weight, act="none", bias=None, stream=None):
         if index >= 0 and _current_device() == index:
             return _ops.matmul_act_backward(dy, z, x, weight, code, bias, _raw_stream(index))
     return _call("matmul_act_backward", stream, dy, z, x, weight, code, bias)
+
+
+def _norm(norm):
+    code = NORMS.get(norm)
+    if code is None:
+        raise ValueError("norm must be one of %s" % ", ".join(sorted(NORMS)))
+    return code
+
+
+def add_norm(x, residual, weight=None, bias=None, gate=None, scale=1.0, post_weight=None, norm="rms", eps=1e-5, stats=False,
+             stream=None):
+    """From one block to the next: the residual sum s = residual + scale * gate * t, where
+    t is x, the block's output, or with ``post_weight`` norm(x) * post_weight; and the
+    next block's input y = norm(s) * weight + bias (y is None without a weight).
+
+    norm: "rms", v / sqrt(mean v^2 + eps), or "layer", which also takes the mean out.
+    x, residual and a gate of x's shape: float16, bfloat16 or float32, one type; weight,
+    bias, post_weight and a gate of one row (1-D, the same for all rows): x's type or
+    float32, one type.  Returns (s, y), or with ``stats`` (s, y, stats), the fp32
+    statistics (..., 4) of each row that the backward pass takes.
+    """
+    code = _norm(norm)
+    if stream is None and _ops is not None and isinstance(x, _tensor):
+        index = x.get_device()
+        if index >= 0 and _current_device() == index:
+            return _ops.add_norm(x, residual, weight, bias, gate, scale, post_weight, code, eps, stats, _raw_stream(index))
+    return _call("add_norm", stream, x, residual, weight, bias, gate, scale, post_weight, code, eps, stats)
+
+
+def add_norm_backward(dy, ds, x, residual, stats, weight=None, bias=None, gate=None, scale=1.0, post_weight=None, norm="rms",
+                      stream=None):
+    """Gradients (dx, dresidual, dweight, dbias, dgate, dpost_weight) of add_norm; those of
+    what was not given are None.  dy is the gradient of y (None without a weight), ds the
+    one that reaches s from elsewhere (or None).  Without gate and post_weight and with
+    scale 1, dx and dresidual are one tensor; without a weight dresidual is ds."""
+    code = _norm(norm)
+    if stream is None and _ops is not None and isinstance(x, _tensor):
+        index = x.get_device()
+        if index >= 0 and _current_device() == index:
+            return _ops.add_norm_backward(dy, ds, x, residual, stats, weight, bias, gate, scale, post_weight, code,
+                                          _raw_stream(index))
+    return _call("add_norm_backward", stream, dy, ds, x, residual, stats, weight, bias, gate, scale, post_weight, code)

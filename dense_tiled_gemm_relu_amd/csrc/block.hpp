@@ -7,7 +7,7 @@
 namespace gemm_relu_hip {
 
 // ---- column sums over strips of rows: out[s][j] = sum over strips of partial[strip][s cols + j]
-constexpr int kMaxSums = 5;
+constexpr int kMaxSums = 4;
 struct JoinArgs {
     const float* partial;       // strips x sums x cols
     void* out[kMaxSums];        // null: not wanted
@@ -31,5 +31,33 @@ struct ActGradArgs {
     int nflags;
 };
 hipError_t launch_act_grad(const ActGradArgs& a, int dt, hipStream_t stream);
+
+// ---- residual sum and norms (block_rows.hip)
+struct AddNormArgs {
+    const void* x;
+    const void* r;
+    const void* gate;           // null: 1
+    const void* pw;             // null: x is not normed
+    const void* w;              // null: no y
+    const void* b;
+    void* s;
+    void* y;
+    float* stats;               // 4 a row: mean and 1 / deviation of x, and of s
+    const void* dy;             // backward
+    const void* ds;
+    void* dx;
+    void* dr;
+    void* dgate;                // of a gate matrix; the sums over rows go to `partial`
+    float* partial;             // strips x 4 x cols: dweight, dbias, dgate, dpost_weight
+    float* row_sums;            // 2 a row: the means that dresidual takes (rows of any length)
+    int64_t x_stride, r_stride, gate_stride, dy_stride, ds_stride;    // gate_stride 0: one row
+    int rows, cols;
+    int layer;                  // layer norm, else root mean square
+    float scale, eps;
+};
+hipError_t launch_add_norm(const AddNormArgs& a, int dt, int wdt, hipStream_t stream);
+// strips of rows the backward pass sums on their own before launch_join
+int add_norm_strips(int64_t rows, int64_t cols, int bytes);
+hipError_t launch_add_norm_backward(const AddNormArgs& a, int dt, int wdt, hipStream_t stream);
 
 }  // namespace gemm_relu_hip

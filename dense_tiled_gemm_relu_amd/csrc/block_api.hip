@@ -157,3 +157,132 @@ extern "C" const char* gemm_relu_act_backward_plan(int64_t rows, int64_t n, int6
     static const PairNames names(',');
     return names.text[p.x.cfg][p.w.cfg];
 }
+
+// ------------------------------------------------- residual sum and norms
+static bool add_norm_ok(int64_t rows, int64_t cols, int64_t gate_stride, const void* gate, int dtype, int wdtype, int norm,
+                        float scale)
+{
+    return size_ok(rows) && size_ok(cols) && is_float(dtype) && (wdtype == dtype || wdtype == GEMM_RELU_F32) &&
+           (norm == GEMM_RELU_NORM_RMS || norm == GEMM_RELU_NORM_LAYER) && scale - scale == 0.0f &&
+           (!gate || gate_stride >= 0);
+}
+// a gate of one row, or a matrix
+static Mat gate_matrix(const void* gate, int64_t stride, int64_t rows, int64_t cols, int e, int we)
+{
+    if (!gate) return dense(nullptr, 0, 0, 1);
+    return stride ? Mat{gate, rows, cols, stride, e} : dense(gate, 1, cols, we);
+}
+
+extern "C" int gemm_relu_add_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                                  const void* gate, int64_t gate_stride, const void* post_weight, const void* weight,
+                                  const void* bias, void* s, void* y, float* stats, int64_t rows, int64_t cols, int dtype,
+                                  int wdtype, int norm, float scale, float eps, void* stream)
+{
+    if (!add_norm_ok(rows, cols, gate_stride, gate, dtype, wdtype, norm, scale) || !(eps >= 0.0f) || (rows > 0 && cols < 1) ||
+        (!weight && bias))
+        return GEMM_RELU_EINVAL;
+    if (rows == 0) return GEMM_RELU_OK;
+    const int e = elem_bytes(dtype), we = elem_bytes(wdtype);
+    const Mat m[] = {dense(s, rows, cols, e), dense(y, weight ? rows : 0, cols, e), dense(stats, stats ? rows : 0, 4, 4),
+                     {x, rows, cols, x_stride, e}, {residual, rows, cols, residual_stride, e},
+                     gate_matrix(gate, gate_stride, rows, cols, e, we), dense(post_weight, post_weight ? 1 : 0, cols, we),
+                     dense(weight, weight ? 1 : 0, cols, we), dense(bias, bias ? 1 : 0, cols, we)};
+    if (!mats_ok(m, 3)) return GEMM_RELU_EINVAL;
+    if (const int dev = check_device()) return dev;
+    AddNormArgs a{};
+    a.x = x;
+    a.r = residual;
+    a.gate = gate;
+    a.pw = post_weight;
+    a.w = weight;
+    a.b = bias;
+    a.s = s;
+    a.y = y;
+    a.stats = stats;
+    a.x_stride = x_stride;
+    a.r_stride = residual_stride;
+    a.gate_stride = gate ? gate_stride : 0;
+    a.rows = int(rows);
+    a.cols = int(cols);
+    a.layer = norm == GEMM_RELU_NORM_LAYER;
+    a.scale = scale;
+    a.eps = eps;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    return finish(launch_add_norm(a, dtype, wdtype, st), st);
+}
+
+// the strips' sums, then two sums a row
+static uint64_t add_norm_sums(int64_t rows, int64_t cols, int bytes)
+{
+    return uint64_t(round_up(int64_t(add_norm_strips(rows, cols, bytes)) * kMaxSums * cols * 4, 256));
+}
+extern "C" int64_t gemm_relu_add_norm_backward_workspace(int64_t rows, int64_t cols)
+{
+    if (!size_ok(rows) || !size_ok(cols)) return GEMM_RELU_EINVAL;
+    // of the type that leaves more strips
+    return int64_t(std::max(add_norm_sums(rows, cols, 2), add_norm_sums(rows, cols, 4))) + rows * 2 * 4;
+}
+
+extern "C" int gemm_relu_add_norm_backward(const void* dy, int64_t dy_stride, const void* ds, int64_t ds_stride, const void* x,
+                                           int64_t x_stride, const void* residual, int64_t residual_stride, const void* gate,
+                                           int64_t gate_stride, const void* post_weight, const void* weight,
+                                           const float* stats, void* dx, void* dresidual, void* dgate, void* dpost_weight,
+                                           void* dweight, void* dbias, int64_t rows, int64_t cols, int dtype, int wdtype,
+                                           int norm, float scale, void* workspace, uint64_t workspace_bytes, void* stream)
+{
+    if (!add_norm_ok(rows, cols, gate_stride, gate, dtype, wdtype, norm, scale) || (rows > 0 && cols < 1) ||
+        (!weight && (dweight || dbias)) || (!gate && dgate) || (!post_weight && dpost_weight))
+        return GEMM_RELU_EINVAL;
+    if (cols == 0) return GEMM_RELU_OK;
+    const int e = elem_bytes(dtype), we = elem_bytes(wdtype);
+    const uint64_t need = uint64_t(gemm_relu_add_norm_backward_workspace(rows, cols));
+    auto vector = [&](const void* p) { return dense(p, p ? 1 : 0, cols, we); };
+    auto output = [&](const void* p) { return dense(p, p ? rows : 0, cols, e); };
+    const Mat m[] = {output(dx), output(dresidual), gate && gate_stride ? output(dgate) : vector(dgate), vector(dpost_weight),
+                     vector(dweight), vector(dbias), bytes_of(workspace, need),
+                     weight ? Mat{dy, rows, cols, dy_stride, e} : dense(nullptr, 0, 0, e),
+                     ds ? Mat{ds, rows, cols, ds_stride, e} : dense(nullptr, 0, 0, e), {x, rows, cols, x_stride, e},
+                     {residual, rows, cols, residual_stride, e}, gate_matrix(gate, gate_stride, rows, cols, e, we),
+                     vector(post_weight), vector(weight), dense(stats, rows, 4, 4)};
+    if (!mats_ok(m, 7) || !workspace_ok(workspace, workspace_bytes, need)) return GEMM_RELU_EINVAL;
+    if (const int dev = check_device()) return dev;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    AddNormArgs a{};
+    a.x = x;
+    a.r = residual;
+    a.gate = gate;
+    a.pw = post_weight;
+    a.w = weight;
+    a.stats = const_cast<float*>(stats);
+    a.dy = dy;
+    a.ds = ds;
+    a.dx = dx;
+    a.dr = dresidual;
+    a.dgate = dgate;
+    a.partial = static_cast<float*>(workspace);
+    a.row_sums = reinterpret_cast<float*>(static_cast<char*>(workspace) + add_norm_sums(rows, cols, e));
+    a.x_stride = x_stride;
+    a.r_stride = residual_stride;
+    a.gate_stride = gate ? gate_stride : 0;
+    a.dy_stride = dy_stride;
+    a.ds_stride = ds_stride;
+    a.rows = int(rows);
+    a.cols = int(cols);
+    a.layer = norm == GEMM_RELU_NORM_LAYER;
+    a.scale = scale;
+    hipError_t err = launch_add_norm_backward(a, dtype, wdtype, st);
+    void* const row_gate = gate && !gate_stride ? dgate : nullptr;
+    if (err == hipSuccess && (dweight || dbias || row_gate || dpost_weight)) {
+        JoinArgs j{};
+        j.partial = a.partial;
+        j.out[0] = dweight;
+        j.out[1] = dbias;
+        j.out[2] = row_gate;
+        j.out[3] = dpost_weight;
+        j.sums = kMaxSums;
+        j.cols = int(cols);
+        j.strips = add_norm_strips(rows, cols, e);
+        err = launch_join(j, wdtype, st);
+    }
+    return finish(err, st);
+}

@@ -18,10 +18,14 @@ template <class W> __global__ void __launch_bounds__(1024) join_kernel(JoinArgs 
     __shared__ float part[16][64];
     const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
     const int64_t all = (int64_t)a.sums * a.cols;
-    for (int64_t j0 = (int64_t)blockIdx.x * 64; j0 < all; j0 += (int64_t)gridDim.x * 64) {
-        const int64_t j = j0 + lane;
+    const int blocks = (a.cols + 63) / 64;
+    for (int64_t u = blockIdx.x; u < (int64_t)a.sums * blocks; u += gridDim.x) {
+        const int which = (int)(u / blocks), c = (int)(u % blocks) * 64 + lane;
+        W* out = static_cast<W*>(which == 0 ? a.out[0] : which == 1 ? a.out[1] : which == 2 ? a.out[2] : a.out[3]);
+        if (!out) continue;
+        const int64_t j = (int64_t)which * a.cols + c;
         float s = 0.0f;
-        if (j < all) {
+        if (c < a.cols) {
             // a wave's strips in batches of 8, all loads of one in flight together
             // (strips past the end are the last one's, and count for nothing)
             for (int k = wave; k < a.strips; k += 16 * 8) {
@@ -35,15 +39,10 @@ template <class W> __global__ void __launch_bounds__(1024) join_kernel(JoinArgs 
         }
         part[wave][lane] = s;
         __syncthreads();
-        if (!wave && j < all) {
+        if (!wave && c < a.cols) {
 #pragma unroll
             for (int k = 1; k < 16; ++k) s += part[k][lane];
-            int64_t c = j;
-#pragma unroll
-            for (int k = 0; k < kMaxSums; ++k) {
-                if (c >= 0 && c < a.cols && a.out[k]) static_cast<W*>(a.out[k])[c] = (W)s;
-                c -= a.cols;
-            }
+            out[c] = (W)s;
         }
         __syncthreads();
     }
@@ -149,11 +148,534 @@ template <int DT, int ACT> __global__ void __launch_bounds__(kActGradThreads) ac
     __builtin_memcpy(out + 4, &hi, 8);
 }
 
+// ------------------------------------------------- residual sum and norms
+typedef float Stats __attribute__((ext_vector_type(4), aligned(4)));       // a row's statistics, at any float's address
+
+// One read of x and the residual, one write of s and y: the row stays in registers
+// between its sums; the next row is loaded meanwhile, and what is the same for all rows
+// stays in registers.  Bound by HBM.
+template <class T, class W, int G, int V> __global__ void __launch_bounds__(kGroupThreads<G>) add_norm_kernel(AddNormArgs a)
+{
+    constexpr int N = Chunk<T>::N;
+    using X = typename Chunk<T>::Vec;
+    using WV = typename VecN<W, N>::Vec;
+    __shared__ float lds[2][4][G / 64];
+    const RowMap<T, V> map(a.cols, (int)threadIdx.x % G, G);
+    const bool element_gate = a.gate && a.gate_stride, channel_gate = a.gate && !a.gate_stride;
+    WV w[V], b[V], pw[V], gate[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        w[v] = b[v] = pw[v] = gate[v] = WV{};
+        if (map.has(v)) {
+            if (a.w) w[v] = load_vec<WV>(static_cast<const W*>(a.w) + map.start[v]);
+            if (a.b) b[v] = load_vec<WV>(static_cast<const W*>(a.b) + map.start[v]);
+            if (a.pw) pw[v] = load_vec<WV>(static_cast<const W*>(a.pw) + map.start[v]);
+            if (channel_gate) gate[v] = load_vec<WV>(static_cast<const W*>(a.gate) + map.start[v]);
+        }
+    }
+    const int step = (int)gridDim.x * kGroups<G>;
+    int64_t row = group_index<G>();          // 64 bits: the last row's successor may pass 2^31
+    X nx[V], nr[V], ng[V];
+    auto fetch = [&](int64_t at) {
+        const T* x = static_cast<const T*>(a.x) + (size_t)at * (size_t)a.x_stride;
+        const T* r = static_cast<const T*>(a.r) + (size_t)at * (size_t)a.r_stride;
+        const T* g = static_cast<const T*>(a.gate) + (size_t)at * (size_t)a.gate_stride;
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (map.has(v)) {
+                nx[v] = load_vec<X>(x + map.start[v]);
+                nr[v] = load_vec<X>(r + map.start[v]);
+                if (element_gate) ng[v] = load_vec<X>(g + map.start[v]);
+            }
+    };
+#pragma unroll
+    for (int v = 0; v < V; ++v) nx[v] = nr[v] = ng[v] = X{};
+    if (row < a.rows) fetch(row);
+    const float n = (float)a.cols;
+    // mean (0 for the root mean square) and 1 / deviation of f
+    auto statistics = [&](const float(&f)[V][N], float(&buffers)[4][G / 64], int first, float& mean, float& rstd) {
+        float sum = 0.0f;
+        mean = 0.0f;
+        if (a.layer) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int e = 0; e < N; ++e) sum += map.owns(v, e) ? f[v][e] : 0.0f;
+            mean = group_all<G, Sum>(sum, buffers[first]) / n;
+            sum = 0.0f;
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                const float d = map.owns(v, e) ? f[v][e] - mean : 0.0f;
+                sum += d * d;
+            }
+        rstd = 1.0f / sqrtf(group_all<G, Sum>(sum, buffers[first + 1]) / n + a.eps);
+    };
+    for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
+        float f[V][N];
+        X r[V], g[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            r[v] = nr[v];
+            g[v] = ng[v];
+#pragma unroll
+            for (int e = 0; e < N; ++e) f[v][e] = (float)nx[v][e];
+        }
+        if (row < a.rows - step) fetch(row + step);
+        f32x4_t stats = {0.0f, 1.0f, 0.0f, 1.0f};
+        if (a.pw) {
+            float mean, rstd;
+            statistics(f, lds[turn], 0, mean, rstd);
+            stats[0] = mean;
+            stats[1] = rstd;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int e = 0; e < N; ++e) f[v][e] = (f[v][e] - mean) * rstd * (float)pw[v][e];
+        }
+        if (channel_gate) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int e = 0; e < N; ++e) f[v][e] *= (float)gate[v][e];
+        } else if (element_gate) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int e = 0; e < N; ++e) f[v][e] *= (float)g[v][e];
+        }
+        T* s = static_cast<T*>(a.s) + (size_t)row * (size_t)a.cols;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            X out;
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                f[v][e] = fmaf(a.scale, f[v][e], (float)r[v][e]);
+                out[e] = (T)f[v][e];
+            }
+            if (map.has(v)) __builtin_memcpy(s + map.start[v], &out, sizeof out);
+        }
+        if (a.w) {
+            float mean, rstd;
+            statistics(f, lds[turn], 2, mean, rstd);
+            stats[2] = mean;
+            stats[3] = rstd;
+            T* y = static_cast<T*>(a.y) + (size_t)row * (size_t)a.cols;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (map.has(v)) {
+                    X out;
+#pragma unroll
+                    for (int e = 0; e < N; ++e) out[e] = (T)((f[v][e] - mean) * rstd * (float)w[v][e] + (float)b[v][e]);
+                    __builtin_memcpy(y + map.start[v], &out, sizeof out);
+                }
+        }
+        if (a.stats && threadIdx.x % G == 0) *reinterpret_cast<Stats*>(a.stats + 4 * (size_t)row) = stats;
+    }
+}
+
+// The backward pass in one read of its inputs: s is computed again, the row's two sums
+// give dresidual, two more dx, and the thread's columns of the sums over rows stay in
+// registers over its rows.  A workgroup leaves one strip of partial sums; the join
+// kernel adds the strips in order.  `waves` waves a row, and as many rows at a time as
+// the workgroup holds.  Bound by HBM.
+template <class T, class W, int V>
+__global__ void __launch_bounds__(1024) add_norm_backward_kernel(AddNormArgs a, int waves)
+{
+    constexpr int N = Chunk<T>::N;
+    using X = typename Chunk<T>::Vec;
+    using WV = typename VecN<W, N>::Vec;
+    __shared__ float lds[2][4][16];
+    __shared__ float part[V == 1 ? 16 * N * 64 : 1];
+    const int lane = (int)(threadIdx.x & 63), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const int groups = (int)(blockDim.x >> 6) / waves, group = wave / waves, in_row = wave - group * waves;
+    const RowMap<T, V> map(a.cols, in_row * 64 + lane, 64 * waves);
+    const bool element_gate = a.gate && a.gate_stride, channel_gate = a.gate && !a.gate_stride;
+    WV w[V], pw[V], gate[V];
+    float dw[V][N], db[V][N], dg[V][N], dp[V][N];
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+        w[v] = pw[v] = gate[v] = WV{};
+        if (a.w) w[v] = load_vec<WV>(static_cast<const W*>(a.w) + map.start[v]);
+        if (a.pw) pw[v] = load_vec<WV>(static_cast<const W*>(a.pw) + map.start[v]);
+        if (channel_gate) gate[v] = load_vec<WV>(static_cast<const W*>(a.gate) + map.start[v]);
+#pragma unroll
+        for (int e = 0; e < N; ++e) dw[v][e] = db[v][e] = dg[v][e] = dp[v][e] = 0.0f;
+    }
+    const int64_t step = (int64_t)gridDim.x * groups;
+    const int64_t first_row = (int64_t)blockIdx.x * groups;
+    int64_t row = first_row + group;
+    // a missing chunk is the row's last, a row past the end the last one
+    X nx[V], nr[V], ny[V], nd[V], ng[V];
+    auto fetch = [&](int64_t to) {
+        const size_t at = (size_t)min(to, (int64_t)a.rows - 1);
+        const T* x = static_cast<const T*>(a.x) + at * (size_t)a.x_stride;
+        const T* r = static_cast<const T*>(a.r) + at * (size_t)a.r_stride;
+        const T* y = static_cast<const T*>(a.dy) + at * (size_t)a.dy_stride;
+        const T* d = static_cast<const T*>(a.ds) + at * (size_t)a.ds_stride;
+        const T* g = static_cast<const T*>(a.gate) + at * (size_t)a.gate_stride;
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            nx[v] = load_vec<X>(x + map.start[v]);
+            if (a.w) nr[v] = load_vec<X>(r + map.start[v]);
+            if (a.w) ny[v] = load_vec<X>(y + map.start[v]);
+            if (a.ds) nd[v] = load_vec<X>(d + map.start[v]);
+            if (element_gate) ng[v] = load_vec<X>(g + map.start[v]);
+        }
+    };
+#pragma unroll
+    for (int v = 0; v < V; ++v) nx[v] = nr[v] = ny[v] = nd[v] = ng[v] = X{};
+    fetch(row);
+    const float inv_n = 1.0f / (float)a.cols;
+    // one value for the whole wave: read through the scalar cache
+    typedef const __attribute__((address_space(4))) Stats* Scalars;
+    const Scalars all_stats = (Scalars)(uintptr_t)a.stats;
+    // means over the row of p and q
+    auto means = [&](float& p, float& q, float(&buffers)[4][16], int first) {
+        p = wave_all<Sum>(p);
+        q = wave_all<Sum>(q);
+        if (waves > 1) {
+            if (lane == 0) {
+                buffers[first][wave] = p;
+                buffers[first + 1][wave] = q;
+            }
+            __syncthreads();
+            p = q = 0.0f;
+            for (int k = 0; k < waves; ++k) {
+                p += buffers[first][group * waves + k];
+                q += buffers[first + 1][group * waves + k];
+            }
+        }
+        p = a.layer ? p * inv_n : 0.0f;
+        q *= inv_n;
+    };
+    // all rows of a workgroup meet at its barriers, so a row past the end runs along
+    // with nothing to add and nothing to store
+    for (int turn = 0; row - group < a.rows; row += step, turn ^= 1) {
+        const bool live = row < a.rows;
+        const f32x4_t stats = all_stats[min(row, (int64_t)a.rows - 1)];
+        float xhat[V][N], t[V][N], shat[V][N], dr[V][N];
+        X y[V], g[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            y[v] = ny[v];
+            g[v] = ng[v];
+#pragma unroll
+            for (int e = 0; e < N; ++e) {
+                xhat[v][e] = ((float)nx[v][e] - stats[0]) * stats[1];
+                t[v][e] = a.pw ? xhat[v][e] * (float)pw[v][e] : xhat[v][e];
+                const float gated = channel_gate ? t[v][e] * (float)gate[v][e] : element_gate ? t[v][e] * (float)g[v][e] : t[v][e];
+                shat[v][e] = (fmaf(a.scale, gated, (float)nr[v][e]) - stats[2]) * stats[3];
+                dr[v][e] = (float)nd[v][e];
+            }
+        }
+        fetch(row + step);
+        if (a.w) {
+            // c = dy weight
+            float p = 0.0f, q = 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    const float c = map.owns(v, e) ? (float)y[v][e] * (float)w[v][e] : 0.0f;
+                    p += c;
+                    q = fmaf(c, map.owns(v, e) ? shat[v][e] : 0.0f, q);
+                }
+            means(p, q, lds[turn], 0);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    const float d = (float)y[v][e];
+                    dr[v][e] = fmaf(stats[3], fmaf(-shat[v][e], q, fmaf(d, (float)w[v][e], -p)), dr[v][e]);
+                    if (live) {
+                        dw[v][e] = fmaf(d, shat[v][e], dw[v][e]);
+                        db[v][e] += d;
+                    }
+                }
+        }
+        const size_t at = (size_t)row * (size_t)a.cols;
+        if (a.dr) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (map.has(v) && live) {
+                    X out;
+#pragma unroll
+                    for (int e = 0; e < N; ++e) out[e] = (T)dr[v][e];
+                    __builtin_memcpy(static_cast<T*>(a.dr) + at + map.start[v], &out, sizeof out);
+                }
+        }
+        if (a.gate) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                X out;
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    const float d = a.scale * dr[v][e] * t[v][e];
+                    out[e] = (T)d;
+                    if (live) dg[v][e] += d;
+                }
+                if (element_gate && a.dgate && map.has(v) && live)
+                    __builtin_memcpy(static_cast<T*>(a.dgate) + at + map.start[v], &out, sizeof out);
+            }
+        }
+        // dt, in dr's place
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int e = 0; e < N; ++e)
+                dr[v][e] *= channel_gate ? a.scale * (float)gate[v][e] : element_gate ? a.scale * (float)g[v][e] : a.scale;
+        if (a.pw) {
+            float p = 0.0f, q = 0.0f;
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int e = 0; e < N; ++e) {
+                    if (live) dp[v][e] = fmaf(dr[v][e], xhat[v][e], dp[v][e]);
+                    dr[v][e] *= (float)pw[v][e];
+                    const float c = map.owns(v, e) ? dr[v][e] : 0.0f;
+                    p += c;
+                    q = fmaf(c, map.owns(v, e) ? xhat[v][e] : 0.0f, q);
+                }
+            means(p, q, lds[turn], 2);
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int e = 0; e < N; ++e) dr[v][e] = stats[1] * fmaf(-xhat[v][e], q, dr[v][e] - p);
+        }
+        if (a.dx) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+                if (map.has(v) && live) {
+                    X out;
+#pragma unroll
+                    for (int e = 0; e < N; ++e) out[e] = (T)dr[v][e];
+                    __builtin_memcpy(static_cast<T*>(a.dx) + at + map.start[v], &out, sizeof out);
+                }
+        }
+    }
+    // the groups' sums join first, in order
+    float* strip = a.partial + (size_t)blockIdx.x * kMaxSums * (size_t)a.cols;
+    const auto leave = [&](int which, float(&own)[V][N]) {
+        if constexpr (V == 1) {
+            if (groups > 1) {
+                __syncthreads();
+                if (group) {
+#pragma unroll
+                    for (int e = 0; e < N; ++e) part[(wave * N + e) * 64 + lane] = own[0][e];
+                }
+                __syncthreads();
+                if (group) return;
+                for (int k = 1; k < groups; ++k)
+#pragma unroll
+                    for (int e = 0; e < N; ++e) own[0][e] += part[((k * waves + in_row) * N + e) * 64 + lane];
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+            if (map.has(v)) {
+                float* to = strip + (size_t)which * (size_t)a.cols + map.start[v];
+                if (v < V - 1 || map.skip == 0) {
+#pragma unroll
+                    for (int e = 0; e < N; e += 4) {
+                        const f32x4_t four = {own[v][e], own[v][e + 1], own[v][e + 2], own[v][e + 3]};
+                        __builtin_memcpy(to + e, &four, 16);
+                    }
+                } else {
+#pragma unroll
+                    for (int e = 0; e < N; ++e)
+                        if (e >= map.skip) to[e] = own[v][e];
+                }
+            }
+    };
+    if (a.w) leave(0, dw);
+    if (a.w) leave(1, db);
+    if (channel_gate) leave(2, dg);
+    if (a.pw) leave(3, dp);
+}
+
+// ---- rows of any length: one workgroup a row, read once per use
+template <class T, class W> struct AnyRow {
+    const AddNormArgs& a;
+    const T *x, *r;
+    const T* g;
+    const W *pw, *gc;
+    float mean, rstd;          // of x
+    __device__ __forceinline__ AnyRow(const AddNormArgs& args, size_t row)
+        : a(args), x(static_cast<const T*>(args.x) + row * (size_t)args.x_stride),
+          r(static_cast<const T*>(args.r) + row * (size_t)args.r_stride),
+          g(args.gate && args.gate_stride ? static_cast<const T*>(args.gate) + row * (size_t)args.gate_stride : nullptr),
+          pw(static_cast<const W*>(args.pw)), gc(args.gate && !args.gate_stride ? static_cast<const W*>(args.gate) : nullptr),
+          mean(0.0f), rstd(1.0f)
+    {
+    }
+    __device__ __forceinline__ float gate(int64_t j) const { return g ? (float)g[j] : gc ? (float)gc[j] : 1.0f; }
+    __device__ __forceinline__ float xhat(int64_t j) const { return ((float)x[j] - mean) * rstd; }
+    __device__ __forceinline__ float t(int64_t j) const { return pw ? xhat(j) * (float)pw[j] : xhat(j); }
+    __device__ __forceinline__ float s(int64_t j) const { return fmaf(a.scale, t(j) * gate(j), (float)r[j]); }
+};
+template <class T, class W, bool SHORT> __global__ void __launch_bounds__(kThreads) add_norm_any_kernel(AddNormArgs a)
+{
+    __shared__ RowSums<1> lds[2][4][kThreads / 64];
+    const W* w = static_cast<const W*>(a.w);
+    const W* b = static_cast<const W*>(a.b);
+    int turn = 0;
+    for (size_t row = blockIdx.x; row < (size_t)a.rows; row += gridDim.x, turn ^= 1) {
+        AnyRow<T, W> in(a, row);
+        auto statistics = [&](auto&& at, int first, float& mean, float& rstd) {
+            float m = 0.0f;
+            if (a.layer) m = row_means<SHORT, 1>(a.cols, [&](int64_t j) { return Values<1>{at(j)}; }, lds[turn][first]).v[0];
+            const auto square = [&](int64_t j) {
+                const float d = at(j) - m;
+                return Values<1>{d * d};
+            };
+            rstd = 1.0f / sqrtf(row_means<SHORT, 1>(a.cols, square, lds[turn][first + 1]).v[0] + a.eps);
+            mean = m;
+        };
+        if (a.pw) {
+            float mean, rstd;
+            statistics([&](int64_t j) { return (float)in.x[j]; }, 0, mean, rstd);
+            in.mean = mean;
+            in.rstd = rstd;
+        }
+        T* s = static_cast<T*>(a.s) + row * (size_t)a.cols;
+        each_column<SHORT>(a.cols, [&](int64_t j) { return (T)in.s(j); }, [&](int64_t j, T v) { s[j] = v; });
+        float mean = 0.0f, rstd = 1.0f;
+        if (w) {
+            statistics([&](int64_t j) { return in.s(j); }, 2, mean, rstd);
+            T* y = static_cast<T*>(a.y) + row * (size_t)a.cols;
+            each_column<SHORT>(
+                a.cols, [&](int64_t j) { return (T)((in.s(j) - mean) * rstd * (float)w[j] + (b ? (float)b[j] : 0.0f)); },
+                [&](int64_t j, T v) { y[j] = v; });
+        }
+        if (a.stats && threadIdx.x == 0) {
+            const f32x4_t stats = {in.mean, in.rstd, mean, rstd};
+            *reinterpret_cast<Stats*>(a.stats + 4 * row) = stats;
+        }
+    }
+}
+// dresidual's value at column j of a row, given the means of c = dy weight and of c shat
+template <class T, class W> struct AnyGrad : AnyRow<T, W> {
+    const T *dy, *ds;
+    const W* w;
+    float smean, srstd, p, q;
+    __device__ __forceinline__ AnyGrad(const AddNormArgs& a, size_t row)
+        : AnyRow<T, W>(a, row), dy(a.w ? static_cast<const T*>(a.dy) + row * (size_t)a.dy_stride : nullptr),
+          ds(a.ds ? static_cast<const T*>(a.ds) + row * (size_t)a.ds_stride : nullptr), w(static_cast<const W*>(a.w)), p(0.0f),
+          q(0.0f)
+    {
+        const f32x4_t stats = *reinterpret_cast<const Stats*>(a.stats + 4 * row);
+        this->mean = stats[0];
+        this->rstd = stats[1];
+        smean = stats[2];
+        srstd = stats[3];
+    }
+    __device__ __forceinline__ float shat(int64_t j) const { return (this->s(j) - smean) * srstd; }
+    __device__ __forceinline__ float dr(int64_t j) const
+    {
+        const float d = ds ? (float)ds[j] : 0.0f;
+        return w ? fmaf(srstd, fmaf(-shat(j), q, fmaf((float)dy[j], (float)w[j], -p)), d) : d;
+    }
+};
+template <class T, class W, bool SHORT> __global__ void __launch_bounds__(kThreads) add_norm_dx_any_kernel(AddNormArgs a)
+{
+    __shared__ RowSums<2> lds[2][2][kThreads / 64];
+    int turn = 0;
+    for (size_t row = blockIdx.x; row < (size_t)a.rows; row += gridDim.x, turn ^= 1) {
+        AnyGrad<T, W> in(a, row);
+        if (a.w) {
+            const auto terms = [&](int64_t j) {
+                const float c = (float)in.dy[j] * (float)in.w[j];
+                return Values<2>{c, c * in.shat(j)};
+            };
+            const Values<2> m = row_means<SHORT, 2>(a.cols, terms, lds[turn][0]);
+            in.p = a.layer ? m.v[0] : 0.0f;
+            in.q = m.v[1];
+        }
+        if (threadIdx.x == 0) {
+            a.row_sums[2 * row] = in.p;
+            a.row_sums[2 * row + 1] = in.q;
+        }
+        const size_t at = row * (size_t)a.cols;
+        T *dr = static_cast<T*>(a.dr), *dg = in.g ? static_cast<T*>(a.dgate) : nullptr, *dx = static_cast<T*>(a.dx);
+        if (dr) each_column<SHORT>(a.cols, [&](int64_t j) { return (T)in.dr(j); }, [&](int64_t j, T v) { dr[at + j] = v; });
+        if (dg)
+            each_column<SHORT>(
+                a.cols, [&](int64_t j) { return (T)(a.scale * in.dr(j) * in.t(j)); }, [&](int64_t j, T v) { dg[at + j] = v; });
+        if (!dx) continue;
+        const auto c2 = [&](int64_t j) { return a.scale * in.gate(j) * in.dr(j) * (in.pw ? (float)in.pw[j] : 1.0f); };
+        float p = 0.0f, q = 0.0f;
+        if (in.pw) {
+            const auto terms = [&](int64_t j) {
+                const float c = c2(j);
+                return Values<2>{c, c * in.xhat(j)};
+            };
+            const Values<2> m = row_means<SHORT, 2>(a.cols, terms, lds[turn][1]);
+            p = a.layer ? m.v[0] : 0.0f;
+            q = m.v[1];
+        }
+        each_column<SHORT>(
+            a.cols, [&](int64_t j) { return (T)(in.pw ? in.rstd * fmaf(-in.xhat(j), q, c2(j) - p) : c2(j)); },
+            [&](int64_t j, T v) { dx[at + j] = v; });
+    }
+}
+// Column sums of one strip of rows: thread per column.
+template <class T, class W>
+__global__ void __launch_bounds__(kThreads) add_norm_strip_any_kernel(AddNormArgs a, int strip_rows)
+{
+    const int64_t j = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    if (j >= a.cols) return;
+    const int64_t r0 = (int64_t)blockIdx.y * strip_rows, r1 = min((int64_t)a.rows, r0 + strip_rows);
+    float dw = 0.0f, db = 0.0f, dg = 0.0f, dp = 0.0f;
+    for (int64_t r = r0; r < r1; ++r) {
+        AnyGrad<T, W> in(a, (size_t)r);
+        in.p = a.row_sums[2 * (size_t)r];
+        in.q = a.row_sums[2 * (size_t)r + 1];
+        if (a.w) {
+            const float d = (float)in.dy[j];
+            dw = fmaf(d, in.shat(j), dw);
+            db += d;
+        }
+        if (in.gc || in.pw) {
+            const float d = a.scale * in.dr(j);
+            dg = fmaf(d, in.t(j), dg);
+            dp = fmaf(d * in.gate(j), in.xhat(j), dp);
+        }
+    }
+    float* p = a.partial + (size_t)blockIdx.y * kMaxSums * (size_t)a.cols + j;
+    p[0] = dw;
+    p[(size_t)a.cols] = db;
+    p[2 * (size_t)a.cols] = dg;
+    p[3 * (size_t)a.cols] = dp;
+}
+
+// Threads that share a row and 16-byte chunks of it each, as row_shape, with at most two
+// chunks a thread: four vectors of weights stay in registers beside the row.
+RowShape add_norm_shape(int cols, int bytes)
+{
+    const int chunks = row_chunks(cols, bytes);
+    for (int g = 64; chunks > 0 && g <= 1024; g *= 2) {
+        const int v = (int)ceil_div(chunks, g);
+        if (v <= 2) return {g, v};
+    }
+    return {0, 0};
+}
+template <class F> hipError_t with_add_norm_shape(RowShape s, F&& f)
+{
+#define GR_SHAPE(G, V) \
+    if (s.g == G && s.v == V) return f(std::integral_constant<int, G>{}, std::integral_constant<int, V>{});
+    GR_SHAPE(64, 1) GR_SHAPE(64, 2) GR_SHAPE(128, 2) GR_SHAPE(256, 2) GR_SHAPE(512, 2) GR_SHAPE(1024, 2)
+#undef GR_SHAPE
+    return hipErrorInvalidValue;
+}
+
 }  // namespace
 
 hipError_t launch_join(const JoinArgs& a, int out_dt, hipStream_t stream)
 {
-    const dim3 grid((unsigned)std::min<int64_t>(ceil_div((int64_t)a.sums * a.cols, 64), kMaxRowGrid));
+    const dim3 grid((unsigned)std::min<int64_t>(a.sums * ceil_div(a.cols, 64), kMaxRowGrid));
     switch (out_dt) {
     case DT_F32: return start(&join_kernel<float>, grid, 1024, stream, a);
     case DT_F16: return start(&join_kernel<_Float16>, grid, 1024, stream, a);
@@ -176,6 +698,50 @@ hipError_t launch_act_grad(const ActGradArgs& a, int dt, hipStream_t stream)
     case ACT_RELU: return go(std::integral_constant<int, ACT_RELU>{});
     default: return go(std::integral_constant<int, ACT_NONE>{});
     }
+}
+
+hipError_t launch_add_norm(const AddNormArgs& a, int dt, int wdt, hipStream_t stream)
+{
+    const RowShape s = add_norm_shape(a.cols, elem_size(dt));
+    return with_types(dt, wdt, [&](auto x, auto w) {
+        using T = decltype(x);
+        using W = decltype(w);
+        if (!s.g)
+            return start(a.cols <= kThreads ? &add_norm_any_kernel<T, W, true> : &add_norm_any_kernel<T, W, false>,
+                         dim3(any_grid(a.rows)), kThreads, stream, a);
+        return with_add_norm_shape(s, [&](auto g, auto v) {
+            constexpr int G = decltype(g)::value;
+            const int grid = even_grid(a.rows, kGroups<G>, row_groups(a.rows, a.cols, sizeof(T), kGroupThreads<G>));
+            return start(&add_norm_kernel<T, W, G, decltype(v)::value>, dim3(grid), kGroupThreads<G>, stream, a);
+        });
+    });
+}
+
+// Workgroups of the backward pass, each of which leaves one strip of sums: one a CU.
+int add_norm_strips(int64_t rows, int64_t cols, int bytes)
+{
+    return rows == 0 ? 0 : even_grid(rows, 1, 256);
+}
+
+hipError_t launch_add_norm_backward(const AddNormArgs& a, int dt, int wdt, hipStream_t stream)
+{
+    if (a.rows == 0) return hipSuccess;
+    const int strips = add_norm_strips(a.rows, a.cols, elem_size(dt));
+    return with_types(dt, wdt, [&](auto x, auto w) {
+        using T = decltype(x);
+        using W = decltype(w);
+        const int chunks = row_chunks(a.cols, sizeof(T)), waves = (int)ceil_div(chunks, 64);
+        if (chunks > 0 && waves <= 16)
+            return start(&add_norm_backward_kernel<T, W, 1>, dim3(strips), 64 * waves * (16 / waves), stream, a, waves);
+        if (chunks > 0 && waves <= 32)
+            return start(&add_norm_backward_kernel<T, W, 2>, dim3(strips), 64 * ((waves + 1) / 2), stream, a, (waves + 1) / 2);
+        hipError_t e = start(a.cols <= kThreads ? &add_norm_dx_any_kernel<T, W, true> : &add_norm_dx_any_kernel<T, W, false>,
+                             dim3(any_grid(a.rows)), kThreads, stream, a);
+        if (e == hipSuccess)
+            e = start(&add_norm_strip_any_kernel<T, W>, dim3((unsigned)ceil_div(a.cols, kThreads), strips), kThreads, stream, a,
+                      (int)ceil_div(a.rows, strips));
+        return e;
+    });
 }
 
 }  // namespace gemm_relu_hip

@@ -14,6 +14,9 @@ struct Api {
     decltype(&gemm_relu_act) act;
     decltype(&gemm_relu_act_backward_workspace) act_backward_workspace;
     decltype(&gemm_relu_act_backward) act_backward;
+    decltype(&gemm_relu_add_norm) add_norm;
+    decltype(&gemm_relu_add_norm_backward_workspace) add_norm_backward_workspace;
+    decltype(&gemm_relu_add_norm_backward) add_norm_backward;
 } api;
 
 // ---- arguments that may be None
@@ -120,16 +123,129 @@ PyObject* matmul_act_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
+// ---- residual sum and norms
+double number(PyObject* o)
+{
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) throw python_error();
+    return v;
+}
+// a matrix like x
+Rows like_x(const at::Tensor& t, const char* name, const at::Tensor& x)
+{
+    if (t.scalar_type() != x.scalar_type()) refuse(PyExc_TypeError, name, " must have x's type");
+    if (t.sizes() != x.sizes()) refuse(PyExc_ValueError, name, " and x must have the same shape");
+    return rows_of(t, name);
+}
+struct AddNorm {
+    Rows x, r;
+    int code, wcode;
+    int64_t gate_stride = 0;                    // 0: a gate of one row
+    at::ScalarType wtype;
+};
+AddNorm add_norm_args(const at::Tensor& x, const at::Tensor& residual, const at::Tensor* w, const at::Tensor* bias,
+                      const at::Tensor* gate, const at::Tensor* post)
+{
+    AddNorm a;
+    a.code = float_code(x);
+    a.x = rows_of(x, "x");
+    a.r = like_x(residual, "residual", x);
+    if (bias && !w) refuse(PyExc_ValueError, "bias needs a weight");
+    const bool row_gate = gate && gate->dim() == 1;
+    // weight, bias, post_weight and a gate of one row share a type: x's or float32
+    const at::Tensor* const vectors[] = {w, bias, post, row_gate ? gate : nullptr};
+    const char* const names[] = {"weight", "bias", "post_weight", "gate"};
+    const at::Tensor* first = nullptr;
+    for (int k = 0; k < 4; ++k)
+        if (vectors[k]) {
+            if (!first) {
+                first = vectors[k];
+                expect_vector(*first, names[k], a.x.cols, x.scalar_type(), at::kFloat);
+            } else {
+                expect_vector(*vectors[k], names[k], a.x.cols, first->scalar_type(), first->scalar_type());
+            }
+        }
+    a.wtype = first ? first->scalar_type() : x.scalar_type();
+    a.wcode = code_of(a.wtype);
+    if (gate && !row_gate) a.gate_stride = like_x(*gate, "gate", x).ld;
+    return a;
+}
+
+// x, residual, weight, bias, gate, scale, post_weight (tensors or None), norm (code), eps, stats, stream
+PyObject* add_norm(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    expect_args(n, 11);
+    const at::Tensor &x = tensor(a[0], "x"), &residual = tensor(a[1], "residual");
+    const at::Tensor *w = maybe(a[2], "weight"), *bias = maybe(a[3], "bias"), *gate = maybe(a[4], "gate"),
+                     *post = maybe(a[6], "post_weight");
+    const double scale = number(a[5]), eps = number(a[8]);
+    const int norm = code_arg(a[7]);
+    const bool keep = truth(a[9]);
+    const AddNorm s = add_norm_args(x, residual, w, bias, gate, post);
+    warn_of_lost_gradients("add_norm", {&x, &residual, w, bias, gate, post});
+    expect_one_gpu({&x, &residual, w, bias, gate, post});
+    at::Tensor sum = make(x, x.sizes(), x.scalar_type()), y, stats;
+    if (w) y = make(x, x.sizes(), x.scalar_type());
+    if (keep) stats = make(x, with_last(x, 4), at::kFloat);
+    check(api.add_norm(x.data_ptr(), s.x.ld, residual.data_ptr(), s.r.ld, data(gate), s.gate_stride, data(post), data(w),
+                       data(bias), sum.data_ptr(), w ? y.data_ptr() : nullptr, keep ? floats(stats) : nullptr, s.x.rows,
+                       s.x.cols, s.code, s.wcode, norm, float(scale), float(eps), pointer(a[10])));
+    return keep ? give_all({&sum, &y, &stats}) : give_all({&sum, &y});
+    END_HANDLE_TH_ERRORS
+}
+
+// dy or None, ds or None, x, residual, stats, weight, bias, gate, scale, post_weight (tensors or None), norm (code), stream
+PyObject* add_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    expect_args(n, 12);
+    const at::Tensor *dy = maybe(a[0], "dy"), *ds = maybe(a[1], "ds"), *w = maybe(a[5], "weight"), *bias = maybe(a[6], "bias"),
+                     *gate = maybe(a[7], "gate"), *post = maybe(a[9], "post_weight");
+    const at::Tensor &x = tensor(a[2], "x"), &residual = tensor(a[3], "residual"), &stats = tensor(a[4], "stats");
+    const double scale = number(a[8]);
+    const int norm = code_arg(a[10]);
+    const AddNorm s = add_norm_args(x, residual, w, bias, gate, post);
+    if (bool(dy) != bool(w)) refuse(PyExc_ValueError, w ? "dy is missing: there is a weight" : "dy without a weight");
+    if (!w && !ds) refuse(PyExc_ValueError, "ds is missing: without a weight no gradient reaches the sum otherwise");
+    const int64_t dy_ld = dy ? like_x(*dy, "dy", x).ld : 0, ds_ld = ds ? like_x(*ds, "ds", x).ld : 0;
+    expect_vector(stats, "stats", 4 * s.x.rows, at::kFloat, at::kFloat);
+    warn_of_lost_gradients("add_norm_backward", {&x, &residual, dy, ds, &stats, w, bias, gate, post});
+    expect_one_gpu({&x, &residual, dy, ds, &stats, w, bias, gate, post});
+    // without gate and post_weight, and with scale 1, both gradients are the same
+    const bool same = !gate && !post && float(scale) == 1.0f;
+    at::Tensor dx, dr, dw, db, dg, dp;
+    const auto like = [](const at::Tensor& t) { return make(t, t.sizes(), t.scalar_type()); };
+    if (!same) dx = like(x);
+    dr = w ? like(x) : *ds;
+    if (w) dw = like(*w);
+    if (bias) db = like(*bias);
+    if (gate) dg = like(*gate);
+    if (post) dp = like(*post);
+    const auto out = [](const at::Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; };
+    const int64_t bytes = api.add_norm_backward_workspace(s.x.rows, s.x.cols);
+    const at::Tensor ws = workspace(x, bytes < 0 ? 0 : bytes);
+    check(api.add_norm_backward(data(dy), dy_ld, data(ds), ds_ld, x.data_ptr(), s.x.ld, residual.data_ptr(), s.r.ld, data(gate),
+                                s.gate_stride, data(post), data(w), floats(stats), out(dx), w ? out(dr) : nullptr, out(dg),
+                                out(dp), out(dw), out(db), s.x.rows, s.x.cols, s.code, s.wcode, norm, float(scale),
+                                ws.data_ptr(), uint64_t(ws.numel()), pointer(a[11])));
+    return give_all({same ? &dr : &dx, &dr, &dw, &db, &dg, &dp});
+    END_HANDLE_TH_ERRORS
+}
+
 // the status error, then the C functions' addresses in the order of Api
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
-    expect_args(n, 4);
+    expect_args(n, 7);
     Api b;
     auto set = [&](auto& fn, int k) { fn = reinterpret_cast<std::remove_reference_t<decltype(fn)>>(pointer(a[k])); };
     set(b.act, 1);
     set(b.act_backward_workspace, 2);
     set(b.act_backward, 3);
+    set(b.add_norm, 4);
+    set(b.add_norm_backward_workspace, 5);
+    set(b.add_norm_backward, 6);
     Py_INCREF(a[0]);
     Py_XDECREF(status_error);
     status_error = a[0];
@@ -142,6 +258,8 @@ PyMethodDef methods[] = {
     {"bind", method(bind), METH_FASTCALL, nullptr},
     {"matmul_act", method(matmul_act), METH_FASTCALL, nullptr},
     {"matmul_act_backward", method(matmul_act_backward), METH_FASTCALL, nullptr},
+    {"add_norm", method(add_norm), METH_FASTCALL, nullptr},
+    {"add_norm_backward", method(add_norm_backward), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_block", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -61,6 +61,53 @@ int gemm_relu_act_backward(const void* dy, int64_t dy_stride, const float* z, co
 /* Configuration names of its two products, "dx,dweight". */
 const char* gemm_relu_act_backward_plan(int64_t rows, int64_t n, int64_t k, int dtype);
 
+/* Norms of gemm_relu_add_norm: v / sqrt(mean v^2 + eps), and gemm_relu_layer_norm's. */
+#define GEMM_RELU_NORM_RMS   0
+#define GEMM_RELU_NORM_LAYER 1
+
+/*
+ * From one block to the next: the block's output x, normed first if post_weight is
+ * given, gated and scaled, is added to the residual stream, whose sum the next block's
+ * norm takes.  For each row of x and residual (rows x cols),
+ *   t = norm(x) post_weight, or x without one,
+ *   s = residual + scale gate t,
+ *   y = norm(s) weight + bias.
+ * gate: NULL (1), one row for all (gate_stride 0; cols elements of wdtype), or a matrix
+ * like x (gate_stride >= cols; of dtype).  weight NULL: no y (NULL too, as bias).  bias
+ * and post_weight may be NULL.  dtype (x, residual, s, y): F16, BF16 or F32; wdtype
+ * (weight, bias, post_weight): dtype or F32.  y is made of the fp32 s, not of the rounded
+ * one.  stats, unless NULL, receives 4 floats a row for the backward pass.  cols >= 1;
+ * eps >= 0; scale finite.
+ */
+int gemm_relu_add_norm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                       const void* gate, int64_t gate_stride, const void* post_weight,
+                       const void* weight, const void* bias, void* s, void* y, float* stats,
+                       int64_t rows, int64_t cols, int dtype, int wdtype, int norm, float scale,
+                       float eps, void* stream);
+
+/*
+ * Its backward pass, from dy (NULL without a weight), the gradient ds that reaches s from
+ * elsewhere (NULL: none) and the forward call's stats:
+ *   dresidual = ds + (the norm's gradient of dy weight at s),  dt = scale gate dresidual,
+ *   dgate = scale t dresidual (summed over rows for a gate of one row),
+ *   dpost_weight = sum over rows of dt (norm(x)),  dx = the norm's gradient of
+ *   dt post_weight at x, or dt,  dweight = sum over rows of dy (norm(s)),  dbias = sum over
+ *   rows of dy.
+ * s is computed again from x and residual, so nothing is lost in its rounding.  Every
+ * output may be NULL: not wanted (dx is dresidual without gate and post_weight and with
+ * scale 1; dresidual is ds without a weight).  dx, dresidual and a matrix's dgate have
+ * dtype, the others wdtype.  rows == 0 writes zeros to the sums over rows.
+ */
+int64_t gemm_relu_add_norm_backward_workspace(int64_t rows, int64_t cols);
+int gemm_relu_add_norm_backward(const void* dy, int64_t dy_stride, const void* ds, int64_t ds_stride,
+                                const void* x, int64_t x_stride, const void* residual,
+                                int64_t residual_stride, const void* gate, int64_t gate_stride,
+                                const void* post_weight, const void* weight, const float* stats,
+                                void* dx, void* dresidual, void* dgate, void* dpost_weight,
+                                void* dweight, void* dbias, int64_t rows, int64_t cols, int dtype,
+                                int wdtype, int norm, float scale, void* workspace,
+                                uint64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

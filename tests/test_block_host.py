@@ -21,6 +21,12 @@ ACT = dict(x=X, x_stride=8, w=W, w_stride=8, b=B, r=R, r_stride=6, y=Y, z=Z, row
 ACT_BWD = dict(dy=DY, dy_stride=6, z=Z, x=X, x_stride=8, w=W, w_stride=8, dx=DX, dw=DW, db=DB, rows=4, n=6, k=8, dtype=F16,
                bdtype=F16, act=0, ws=WS, ws_bytes=1 << 20)
 
+NORM = dict(x=X, x_stride=8, r=R, r_stride=8, gate=G, g_stride=0, pw=PW, w=W, b=B, s=S, y=Y, stats=ST, rows=4, cols=8,
+            dtype=BF16, wdtype=F32, norm=0, scale=1.0, eps=1e-5)
+NORM_BWD = dict(dy=DY, dy_stride=8, ds=Z, ds_stride=8, x=X, x_stride=8, r=R, r_stride=8, gate=G, g_stride=8, pw=PW, w=W,
+                stats=ST, dx=DX, dr=1 << 50, dgate=DB, dpw=1 << 51, dw=DW, db=1 << 52, rows=4, cols=8, dtype=F16, wdtype=F16,
+                norm=1, scale=1.0, ws=WS, ws_bytes=1 << 20)
+
 CASES = [("gemm_relu_act", ACT, o) for o in (
     dict(rows=-1), dict(n=-1), dict(k=-1), dict(rows=BIG), dict(n=BIG), dict(dtype=F32), dict(dtype=3), dict(bdtype=BF16),
     dict(act=-1), dict(act=5), dict(x_stride=7), dict(w_stride=7), dict(r_stride=5), dict(x_stride=BIG), dict(x=0), dict(w=0),
@@ -30,6 +36,18 @@ CASES += [("gemm_relu_act_backward", ACT_BWD, o) for o in (
     dict(rows=-1), dict(n=BIG), dict(k=-1), dict(dtype=F32), dict(bdtype=BF16), dict(act=5), dict(dy_stride=5), dict(x_stride=1),
     dict(dy=0), dict(z=0), dict(x=0), dict(w=0), dict(dx=0), dict(dw=0), dict(dx=X), dict(dw=W), dict(db=DW), dict(dx=DY),
     dict(db=DY), dict(ws=0), dict(ws=WS + 64), dict(ws_bytes=100), dict(ws=W), dict(db=DB + 1))]
+
+NAN, INF = float("nan"), float("inf")
+CASES += [("gemm_relu_add_norm", NORM, o) for o in (
+    dict(rows=-1), dict(cols=-1), dict(cols=0), dict(rows=BIG), dict(dtype=3), dict(wdtype=F16), dict(norm=2), dict(norm=-1),
+    dict(x_stride=7), dict(r_stride=7), dict(g_stride=7), dict(g_stride=-8), dict(g_stride=BIG), dict(x=0), dict(r=0), dict(s=0),
+    dict(y=0), dict(w=0), dict(x=X + 1), dict(r=R + 1), dict(gate=G + 2), dict(stats=ST + 2), dict(s=X), dict(s=R + 8),
+    dict(y=S), dict(y=W), dict(stats=PW), dict(s=G), dict(eps=-1.0), dict(eps=NAN), dict(scale=NAN), dict(scale=INF))]
+CASES += [("gemm_relu_add_norm_backward", NORM_BWD, o) for o in (
+    dict(rows=-1), dict(cols=0), dict(dtype=8), dict(wdtype=BF16), dict(norm=2), dict(scale=-INF), dict(dy=0), dict(x=0),
+    dict(r=0), dict(stats=0), dict(w=0), dict(gate=0), dict(pw=0), dict(dy_stride=7), dict(ds_stride=7), dict(g_stride=4),
+    dict(dx=DY), dict(dr=Z), dict(dx=X), dict(dr=R), dict(dgate=G), dict(dpw=PW), dict(dw=W), dict(db=DW), dict(dr=DX),
+    dict(ws=0), dict(ws=WS + 128), dict(ws_bytes=8), dict(ws=X), dict(dw=DW + 1))]
 
 
 @pytest.mark.parametrize("name,args,over", CASES)
@@ -41,6 +59,8 @@ def test_invalid_arguments_fail_before_the_device(name, args, over):
     ("gemm_relu_act", ACT, dict(rows=0, x=0, y=0, r=0, z=0)), ("gemm_relu_act", ACT, dict(n=0, r_stride=0)),
     ("gemm_relu_act_backward", ACT_BWD, dict(rows=0, n=0)), ("gemm_relu_act_backward", ACT_BWD, dict(n=0, k=0)),
     ("gemm_relu_act_backward", ACT_BWD, dict(k=0, db=0)),
+    ("gemm_relu_add_norm", NORM, dict(rows=0, x=0, r=0, s=0, y=0, stats=0)), ("gemm_relu_add_norm", NORM, dict(rows=0, cols=0)),
+    ("gemm_relu_add_norm_backward", NORM_BWD, dict(rows=0, cols=0)),
 ])
 def test_calls_without_outputs_are_a_no_op(name, args, over):
     assert call(name, args, **over) == gr.OK
@@ -70,6 +90,10 @@ def test_workspaces_and_plans():
     assert lib.gemm_relu_act_backward_plan(4, 6, 0, F16) == b"none"
     assert lib.gemm_relu_act_backward_plan(2 ** 30 + 1, 6, 8, F16) == b"unsupported"
     assert lib.gemm_relu_act_backward_plan(4, 6, 8, F16).count(b",") == 1
+    assert lib.gemm_relu_add_norm_backward_workspace(0, 100) == 0
+    assert lib.gemm_relu_add_norm_backward_workspace(1, 100) >= 4 * 100 * 4
+    assert lib.gemm_relu_add_norm_backward_workspace(-1, 100) == gr.EINVAL
+    assert lib.gemm_relu_add_norm_backward_workspace(BIG - 1, BIG - 1) >= 256 * 4 * 4 * (BIG - 1)
 
 
 # ---- the tensor front ends (CPU tensors: every refusal comes before the device is looked at, the last one is it)
@@ -102,6 +126,27 @@ H = torch.bfloat16
     (ValueError, lambda: gr.matmul_act_backward(t(4, 6), t(4, 5, dtype=F), t(4, 8), t(6, 8), "silu")),
     (ValueError, lambda: gr.matmul_act_backward(t(4, 6), None, t(4, 8), t(6, 8), "none", t(5))),
     (ValueError, lambda: gr.matmul_act_backward(t(4, 6), None, t(4, 8), t(6, 8), "none", t(6))),
+    (ValueError, lambda: gr.add_norm(t(4, 8), t(4, 8), t(8), norm="batch")),
+    (TypeError, lambda: gr.add_norm(t(4, 8, dtype=torch.int8), t(4, 8), t(8))),
+    (TypeError, lambda: gr.add_norm(t(4, 8), t(4, 8, dtype=F), t(8))),
+    (ValueError, lambda: gr.add_norm(t(4, 8), t(4, 7), t(8))),
+    (ValueError, lambda: gr.add_norm(t(4, 8), t(4, 8), t(7))),
+    (TypeError, lambda: gr.add_norm(t(4, 8), t(4, 8), t(8, dtype=H))),
+    (TypeError, lambda: gr.add_norm(t(4, 8), t(4, 8), t(8), t(8, dtype=F))),                   # one type for all of them
+    (TypeError, lambda: gr.add_norm(t(4, 8), t(4, 8), t(8), gate=t(8, dtype=F))),
+    (TypeError, lambda: gr.add_norm(t(4, 8), t(4, 8), t(8), post_weight=t(8, dtype=F))),
+    (TypeError, lambda: gr.add_norm(t(4, 8), t(4, 8), t(8, dtype=F), gate=t(4, 8, dtype=F))),
+    (ValueError, lambda: gr.add_norm(t(4, 8), t(4, 8), t(8), gate=t(4, 1))),
+    (ValueError, lambda: gr.add_norm(t(4, 8), t(4, 8), bias=t(8))),
+    (TypeError, lambda: gr.add_norm(t(4, 8), t(4, 8), t(8), scale="1")),
+    (ValueError, lambda: gr.add_norm(t(4, 8), t(4, 8), t(8))),                                 # not on a GPU
+    (ValueError, lambda: gr.add_norm_backward(None, t(4, 8), t(4, 8), t(4, 8), t(4, 4, dtype=F), t(8))),
+    (ValueError, lambda: gr.add_norm_backward(t(4, 8), t(4, 8), t(4, 8), t(4, 8), t(4, 4, dtype=F))),
+    (ValueError, lambda: gr.add_norm_backward(None, None, t(4, 8), t(4, 8), t(4, 4, dtype=F))),
+    (TypeError, lambda: gr.add_norm_backward(t(4, 8), t(4, 8, dtype=F), t(4, 8), t(4, 8), t(4, 4, dtype=F), t(8))),
+    (TypeError, lambda: gr.add_norm_backward(t(4, 8), t(4, 8), t(4, 8), t(4, 8), t(4, 4), t(8))),
+    (ValueError, lambda: gr.add_norm_backward(t(4, 8), t(4, 8), t(4, 8), t(4, 8), t(4, 2, dtype=F), t(8))),
+    (ValueError, lambda: gr.add_norm_backward(t(4, 8), t(4, 8), t(4, 8), t(4, 8), t(4, 4, dtype=F), t(8))),
 ])
 def test_front_ends_refuse(error, fn):
     with pytest.raises(error):
