@@ -40,7 +40,8 @@ EXPORTS = ("gemm_relu", "gemm_relu_strerror", "gemm_relu_configs", "gemm_relu_pl
            "gemm_relu_gated_backward_plan", "gemm_relu_quantize_rows", "gemm_relu_i8",
            "gemm_relu_i8_plan", "gemm_relu_act", "gemm_relu_act_plan", "gemm_relu_act_backward",
            "gemm_relu_act_backward_workspace", "gemm_relu_act_backward_plan", "gemm_relu_add_norm",
-           "gemm_relu_add_norm_backward", "gemm_relu_add_norm_backward_workspace")
+           "gemm_relu_add_norm_backward", "gemm_relu_add_norm_backward_workspace",
+           "gemm_relu_orthogonalize", "gemm_relu_orthogonalize_workspace")
 
 _lib = None
 
@@ -293,4 +294,4 @@ def matmul_relu(A, B, transB=False, out_dtype=None, out=None, stream=None):
 from .ffn import (ACTIVATIONS, layer_norm, layer_norm_backward, matmul_gated,  # noqa: E402,F401
                   matmul_gated_backward, matmul_i8, quantize_rows)
 # Operators around it (include/gemm_relu_block.h).
-from .block import add_norm, add_norm_backward, matmul_act, matmul_act_backward  # noqa: E402,F401
+from .block import add_norm, add_norm_backward, matmul_act, matmul_act_backward, orthogonalize  # noqa: E402,F401

@@ -1,12 +1,13 @@
 """Operators around a transformer's feed-forward half layer, on torch tensors.
 
 The product with bias, activation and residual in its epilogue and the step from one
-block to the next (residual sum and norms), both with their backward passes.  The work
-is done by the kernels behind include/gemm_relu_block.h, called
+block to the next (residual sum and norms), both with their backward passes, and the
+orthogonalisation of a weight's update.  The work is done by the kernels behind include/gemm_relu_block.h, called
 through a small C++ module (csrc/block_torch.cpp); there is no CPU or PyTorch
 fallback.  Rows, strides, streams, results without autograd graphs: as in ffn.py.
 """
 import ctypes
+import numbers
 import os
 
 from . import ffn
@@ -25,6 +26,8 @@ _SIGNATURES = {
     "gemm_relu_add_norm": ([_vp, _i64, _vp, _i64, _vp, _i64] + [_vp] * 6 + [_i64, _i64, _int, _int, _int, ctypes.c_float,
                            ctypes.c_float, _vp], _int),
     "gemm_relu_add_norm_backward_workspace": ([_i64, _i64], _i64),
+    "gemm_relu_orthogonalize_workspace": ([_i64, _i64, _i64], _i64),
+    "gemm_relu_orthogonalize": ([_vp, _i64, _i64, _vp, _i64, _i64, _i64, _int, _vp, _int, ctypes.c_float, _vp, _u64, _vp], _int),
     "gemm_relu_add_norm_backward": ([_vp, _i64] * 5 + [_vp] * 9 + [_i64, _i64, _int, _int, _int, ctypes.c_float, _vp, _u64,
                                     _vp], _int),
 }
@@ -40,7 +43,8 @@ def declare(lib):
 MODULE_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_block.so")
 # the C functions the front end calls, in the order it takes them
 _BOUND = ("gemm_relu_act", "gemm_relu_act_backward_workspace", "gemm_relu_act_backward", "gemm_relu_add_norm",
-          "gemm_relu_add_norm_backward_workspace", "gemm_relu_add_norm_backward")
+          "gemm_relu_add_norm_backward_workspace", "gemm_relu_add_norm_backward", "gemm_relu_orthogonalize_workspace",
+          "gemm_relu_orthogonalize")
 
 _ops = _current_device = _raw_stream = _tensor = None
 
@@ -137,3 +141,37 @@ def add_norm_backward(dy, ds, x, residual, stats, weight=None, bias=None, gate=N
             return _ops.add_norm_backward(dy, ds, x, residual, stats, weight, bias, gate, scale, post_weight, code,
                                           _raw_stream(index))
     return _call("add_norm_backward", stream, dy, ds, x, residual, stats, weight, bias, gate, scale, post_weight, code)
+
+
+# of a step whose slope at 0 is large: five of them bring singular values from 1e-3 of the
+# matrix's norm into 0.7 .. 1.2
+NEWTON_SCHULZ = (3.4445, -4.7750, 2.0315)
+
+
+def _coefficients(steps, coefficients):
+    c = tuple(coefficients)
+    if len(c) == 3 and all(isinstance(v, numbers.Real) for v in c):
+        return c * steps
+    if len(c) != steps or any(not hasattr(v, "__len__") or len(v) != 3 for v in c):
+        raise ValueError("coefficients must be (a, b, c), or one such triple for each of the %d steps" % steps)
+    return tuple(v for triple in c for v in triple)
+
+
+def orthogonalize(g, steps=5, coefficients=NEWTON_SCHULZ, eps=1e-7, stream=None):
+    """A matrix's update orthogonalised by Newton-Schulz steps: X = g / (|g| + eps), then
+    ``steps`` times X <- a X + (b A + c A^2) X with A = X X^T.  g's singular vectors stay,
+    its singular values tend to 1 (as far as the coefficients take them).
+
+    g: (m, n), or a batch (b, m, n) of matrices each on its own; float16, bfloat16 or
+    float32, with contiguous rows.  coefficients: (a, b, c), or a triple for each step.
+    Returns bfloat16 of g's shape; it is within 1e-3 of its norm before that rounding.
+    """
+    steps = int(steps)
+    if not 0 <= steps <= 64:
+        raise ValueError("steps must be from 0 to 64")
+    c = _coefficients(steps, coefficients)
+    if stream is None and _ops is not None and isinstance(g, _tensor):
+        index = g.get_device()
+        if index >= 0 and _current_device() == index:
+            return _ops.orthogonalize(g, c, eps, _raw_stream(index))
+    return _call("orthogonalize", stream, g, c, eps)

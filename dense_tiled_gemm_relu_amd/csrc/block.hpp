@@ -60,4 +60,35 @@ hipError_t launch_add_norm(const AddNormArgs& a, int dt, int wdt, hipStream_t st
 int add_norm_strips(int64_t rows, int64_t cols, int bytes);
 hipError_t launch_add_norm_backward(const AddNormArgs& a, int dt, int wdt, hipStream_t stream);
 
+// ---- orthogonalisation (ortho.hip)
+// X (p x q, p <= q) is padded to P x Q, multiples of 64, with zeros, which the steps
+// leave zeros.  The matrix instructions take float16: X times 2^8, A = X X^T without its
+// diagonal times 2^10 and B = b A + c A^2 without its diagonal times 2^8; the scales keep
+// what is far below a matrix's norm inside float16's normal range (its smallest value of
+// full precision, 2^-14, is 2^-22 of X's and B's norm and 2^-24 of A's), and leave room
+// for norms of 2^8, 2^6 and 2^8.
+constexpr float kOrthoX = 256.0f, kOrthoA = 1024.0f, kOrthoB = 256.0f;
+struct OrthoArgs {
+    const void* g;              // batch x rows x cols
+    int64_t g_stride, g_batch;  // elements from row to row, from matrix to matrix
+    void* out;                  // batch x rows x cols bfloat16
+    int rows, cols, batch;
+    int p, q, P, Q;             // q: the longer side
+    float eps;
+    double* squares;            // kOrthoParts sums of squares a matrix
+    float* x;                   // batch x P x Q
+    void* xh;                   // float16: batch x P x Q
+};
+constexpr int kOrthoParts = 64;
+hipError_t launch_ortho_start(const OrthoArgs& a, int dt, hipStream_t stream);
+hipError_t launch_ortho_end(const OrthoArgs& a, hipStream_t stream);
+// one of the products for every matrix of the batch
+struct OrthoProduct {
+    KernelArgs k;
+    uint64_t a, b, c, r;        // bytes from one matrix's A, B, C, R to the next's
+    uint64_t diag, x;           // floats from one matrix's diagonals, or X, to the next's
+};
+typedef hipError_t (*OrthoLaunchFn)(const OrthoProduct& p, int tiles, int batch, hipStream_t stream);
+OrthoLaunchFn launcher_ortho(int epi, int cfg);
+
 }  // namespace gemm_relu_hip

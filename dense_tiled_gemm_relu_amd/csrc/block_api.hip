@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <utility>
 
 #include "api_common.hpp"
 #include "block.hpp"
@@ -284,5 +285,163 @@ extern "C" int gemm_relu_add_norm_backward(const void* dy, int64_t dy_stride, co
         j.strips = add_norm_strips(rows, cols, e);
         err = launch_join(j, wdtype, st);
     }
+    return finish(err, st);
+}
+
+// --------------------------------------------------------- orthogonalisation
+namespace {
+
+constexpr int64_t kOrthoShort = int64_t(1) << 16, kOrthoLong = int64_t(1) << 22, kOrthoBatch = 65535;
+constexpr int kOrthoSteps = 64;
+
+struct OrthoPlan {
+    int64_t p, q, P, Q;
+    int gram, poly, step;                       // configurations of the products
+    uint64_t squares, x, xh[2], a, b, diag_a, diag_b, bytes;
+};
+// the configuration of least estimated time for `batch` products
+int ortho_config(const Linear& l, int64_t batch)
+{
+    int best = LIN_64;
+    for (int cfg : {LIN_128, LIN_128X2, LIN_256})
+        if (usable(cfg, l) && linear_time(cfg, l, batch) < linear_time(best, l, batch)) best = cfg;
+    return best;
+}
+OrthoPlan plan_ortho(int64_t batch, int64_t rows, int64_t cols)
+{
+    OrthoPlan o{};
+    o.p = std::min(rows, cols);
+    o.q = std::max(rows, cols);
+    o.P = round_up(o.p, 64);
+    o.Q = round_up(o.q, 64);
+    o.gram = ortho_config(Linear{o.P, o.P, o.Q, o.Q, o.Q, true}, batch);
+    o.poly = ortho_config(Linear{o.P, o.P, o.P, o.P, o.P, true}, batch);
+    o.step = ortho_config(Linear{o.P, o.Q, o.P, o.P, o.Q, false}, batch);
+    uint64_t at = 0;
+    const auto take = [&](uint64_t bytes) {
+        const uint64_t here = at;
+        at += (bytes + 255) & ~uint64_t(255);
+        return here;
+    };
+    const uint64_t PQ = uint64_t(o.P) * uint64_t(o.Q) * uint64_t(batch), PP = uint64_t(o.P) * uint64_t(o.P) * uint64_t(batch);
+    o.squares = take(uint64_t(batch) * kOrthoParts * 8);
+    o.x = take(PQ * 4);
+    o.xh[0] = take(PQ * 2);
+    o.xh[1] = take(PQ * 2);
+    o.a = take(PP * 2);
+    o.b = take(PP * 2);
+    o.diag_a = take(uint64_t(o.P) * uint64_t(batch) * 4);
+    o.diag_b = take(uint64_t(o.P) * uint64_t(batch) * 4);
+    o.bytes = at;
+    return o;
+}
+bool ortho_sizes_ok(int64_t batch, int64_t rows, int64_t cols) { return size_ok(batch) && size_ok(rows) && size_ok(cols); }
+bool ortho_supported(int64_t batch, int64_t rows, int64_t cols)
+{
+    return batch <= kOrthoBatch && std::min(rows, cols) <= kOrthoShort && std::max(rows, cols) <= kOrthoLong;
+}
+
+}  // namespace
+
+extern "C" int64_t gemm_relu_orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols)
+{
+    if (!ortho_sizes_ok(batch, rows, cols)) return GEMM_RELU_EINVAL;
+    if (batch == 0 || rows == 0 || cols == 0) return 0;
+    if (!ortho_supported(batch, rows, cols)) return GEMM_RELU_EUNSUPPORTED;
+    return int64_t(plan_ortho(batch, rows, cols).bytes);
+}
+
+extern "C" int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t g_batch_stride, void* out, int64_t batch,
+                                       int64_t rows, int64_t cols, int dtype, const float* coefficients, int steps, float eps,
+                                       void* workspace, uint64_t workspace_bytes, void* stream)
+{
+    if (!ortho_sizes_ok(batch, rows, cols) || !is_float(dtype) || steps < 0 || steps > kOrthoSteps || (steps > 0 && !coefficients) ||
+        !(eps >= 0.0f) || g_batch_stride < 0)
+        return GEMM_RELU_EINVAL;
+    if (batch == 0 || rows == 0 || cols == 0) return GEMM_RELU_OK;
+    if (!ortho_supported(batch, rows, cols)) return GEMM_RELU_EUNSUPPORTED;
+    const OrthoPlan o = plan_ortho(batch, rows, cols);
+    const int e = elem_bytes(dtype);
+    // the batch's matrices may lie in any order and overlap; the last one ends the furthest
+    Mat in{g, rows, cols, g_stride, e};
+    if (!in.ok()) return GEMM_RELU_EINVAL;
+    const uint64_t span = uint64_t(batch - 1) * uint64_t(g_batch_stride) * uint64_t(e) + in.span();
+    const uint64_t out_bytes = uint64_t(batch) * uint64_t(rows) * uint64_t(cols) * 2;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(out), ws_at = reinterpret_cast<uintptr_t>(workspace);
+    if (!out || (at & 1) || overlaps(at, out_bytes, in.at(), span) || overlaps(at, out_bytes, ws_at, o.bytes) ||
+        overlaps(ws_at, o.bytes, in.at(), span) || !workspace_ok(workspace, workspace_bytes, o.bytes))
+        return GEMM_RELU_EINVAL;
+    for (int k = 0; k < 3 * steps; ++k)
+        if (!(coefficients[k] - coefficients[k] == 0.0f)) return GEMM_RELU_EINVAL;
+    if (const int dev = check_device()) return dev;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    OrthoArgs a{};
+    a.g = g;
+    a.g_stride = g_stride;
+    a.g_batch = g_batch_stride;
+    a.out = out;
+    a.rows = int(rows);
+    a.cols = int(cols);
+    a.batch = int(batch);
+    a.p = int(o.p);
+    a.q = int(o.q);
+    a.P = int(o.P);
+    a.Q = int(o.Q);
+    a.eps = eps;
+    a.squares = reinterpret_cast<double*>(ws + o.squares);
+    a.x = reinterpret_cast<float*>(ws + o.x);
+    a.xh = ws + o.xh[0];
+    hipError_t err = launch_ortho_start(a, dtype, st);
+    const uint64_t PQ = uint64_t(o.P) * uint64_t(o.Q), PP = uint64_t(o.P) * uint64_t(o.P);
+    const Linear gram{o.P, o.P, o.Q, o.Q, o.Q, true}, poly{o.P, o.P, o.P, o.P, o.P, true}, next{o.P, o.Q, o.P, o.P, o.Q, false};
+    const auto product = [&](int epi, int cfg, const Linear& l, const void* A, const void* B, void* C) {
+        const LinearPlan p = plan_as(cfg, l);
+        OrthoProduct k{};
+        k.k = linear_args(p, l, A, B, C);
+        k.diag = uint64_t(o.P);
+        return std::make_pair(k, launcher_ortho(epi, cfg));
+    };
+    for (int s = 0; s < steps && err == hipSuccess; ++s) {
+        const void* xh = ws + o.xh[s % 2];
+        float* diag_a = reinterpret_cast<float*>(ws + o.diag_a);
+        float* diag_b = reinterpret_cast<float*>(ws + o.diag_b);
+        {
+            auto [k, launch] = product(EPI_GRAM, o.gram, gram, xh, xh, ws + o.a);
+            k.k.alpha = kOrthoA / (kOrthoX * kOrthoX);
+            k.k.beta = 1.0f / (kOrthoX * kOrthoX);
+            k.k.diag = diag_a;
+            k.a = k.b = PQ * 2;
+            k.c = PP * 2;
+            err = launch(k, int(k.k.tiles_m * k.k.tiles_n), int(batch), st);
+        }
+        if (err == hipSuccess) {
+            auto [k, launch] = product(EPI_POLY, o.poly, poly, ws + o.a, ws + o.a, ws + o.b);
+            k.k.alpha = kOrthoB;
+            k.k.beta = 1.0f / (kOrthoA * kOrthoA);
+            k.k.scale_o = 1.0f / kOrthoA;
+            k.k.pb = coefficients[3 * s + 1];
+            k.k.pc = coefficients[3 * s + 2];
+            k.k.diag = diag_a;
+            k.k.diag_out = diag_b;
+            k.k.R = ws + o.a;
+            k.k.ldr = int(o.P);
+            k.a = k.b = k.c = k.r = PP * 2;
+            err = launch(k, int(k.k.tiles_m * k.k.tiles_n), int(batch), st);
+        }
+        if (err == hipSuccess) {
+            auto [k, launch] = product(EPI_STEP, o.step, next, ws + o.b, xh, ws + o.xh[(s + 1) % 2]);
+            k.k.alpha = kOrthoX;
+            k.k.beta = 1.0f / (kOrthoB * kOrthoX);
+            k.k.pa = coefficients[3 * s];
+            k.k.diag = diag_b;
+            k.k.X = a.x;
+            k.a = PP * 2;
+            k.b = k.c = PQ * 2;
+            k.x = PQ;
+            err = launch(k, int(k.k.tiles_m * k.k.tiles_n), int(batch), st);
+        }
+    }
+    if (err == hipSuccess) err = launch_ortho_end(a, st);
     return finish(err, st);
 }

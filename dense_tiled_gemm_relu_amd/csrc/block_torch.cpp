@@ -17,6 +17,8 @@ struct Api {
     decltype(&gemm_relu_add_norm) add_norm;
     decltype(&gemm_relu_add_norm_backward_workspace) add_norm_backward_workspace;
     decltype(&gemm_relu_add_norm_backward) add_norm_backward;
+    decltype(&gemm_relu_orthogonalize_workspace) orthogonalize_workspace;
+    decltype(&gemm_relu_orthogonalize) orthogonalize;
 } api;
 
 // ---- arguments that may be None
@@ -233,11 +235,46 @@ PyObject* add_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
+// ---- orthogonalisation
+// g, coefficients (a tuple of 3 numbers a step), eps, stream
+PyObject* orthogonalize(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    expect_args(n, 4);
+    const at::Tensor& g = tensor(a[0], "g");
+    const int code = code_of(g.scalar_type());
+    if (code < 0) refuse(PyExc_TypeError, "g must be float16, bfloat16 or float32, not ", name_of(g.scalar_type()));
+    if (g.dim() != 2 && g.dim() != 3) refuse(PyExc_ValueError, "g must be a matrix, or a batch of them (3-D)");
+    const int64_t rows = g.size(-2), cols = g.size(-1), batch = g.dim() == 3 ? g.size(0) : 1;
+    int64_t row_stride = cols, batch_stride = rows * cols;
+    if (!g.is_contiguous()) {
+        // (a dimension of one element may have any stride)
+        row_stride = rows > 1 ? g.stride(-2) : cols;
+        batch_stride = batch > 1 ? g.stride(0) : 0;
+        if ((cols > 1 && g.stride(-1) != 1) || row_stride < cols) refuse(PyExc_ValueError, "g must have contiguous rows");
+    }
+    float coefficients[3 * 64];
+    const Py_ssize_t count = PyTuple_Check(a[1]) ? PyTuple_GET_SIZE(a[1]) : -1;
+    if (count < 0 || count % 3 || count > Py_ssize_t(sizeof coefficients / sizeof *coefficients))
+        refuse(PyExc_ValueError, "at most 64 steps of three coefficients");
+    for (Py_ssize_t k = 0; k < count; ++k) coefficients[k] = float(number(PyTuple_GET_ITEM(a[1], k)));
+    const double eps = number(a[2]);
+    warn_of_lost_gradients("orthogonalize", {&g});
+    expect_one_gpu({&g});
+    at::Tensor out = make(g, g.sizes(), at::kBFloat16);
+    const int64_t bytes = api.orthogonalize_workspace(batch, rows, cols);
+    const at::Tensor ws = workspace(g, bytes < 0 ? 0 : bytes);
+    check(api.orthogonalize(g.data_ptr(), row_stride, batch_stride, out.data_ptr(), batch, rows, cols, code, coefficients,
+                            int(count / 3), float(eps), ws.data_ptr(), uint64_t(ws.numel()), pointer(a[3])));
+    return give(std::move(out));
+    END_HANDLE_TH_ERRORS
+}
+
 // the status error, then the C functions' addresses in the order of Api
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
-    expect_args(n, 7);
+    expect_args(n, 9);
     Api b;
     auto set = [&](auto& fn, int k) { fn = reinterpret_cast<std::remove_reference_t<decltype(fn)>>(pointer(a[k])); };
     set(b.act, 1);
@@ -246,6 +283,8 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n)
     set(b.add_norm, 4);
     set(b.add_norm_backward_workspace, 5);
     set(b.add_norm_backward, 6);
+    set(b.orthogonalize_workspace, 7);
+    set(b.orthogonalize, 8);
     Py_INCREF(a[0]);
     Py_XDECREF(status_error);
     status_error = a[0];
@@ -260,6 +299,7 @@ PyMethodDef methods[] = {
     {"matmul_act_backward", method(matmul_act_backward), METH_FASTCALL, nullptr},
     {"add_norm", method(add_norm), METH_FASTCALL, nullptr},
     {"add_norm_backward", method(add_norm_backward), METH_FASTCALL, nullptr},
+    {"orthogonalize", method(orthogonalize), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_block", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

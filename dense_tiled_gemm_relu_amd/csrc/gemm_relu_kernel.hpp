@@ -55,8 +55,11 @@ enum : int { DT_I8 = 8 };   // signed 8-bit integers (EPI_I8 only), int32 accumu
 // of 16 bytes, with zeros); EPI_GATED holds the sums g and u of a gate
 // and an up projection side by side and stores act(g) u; EPI_I8 multiplies
 // integer sums by a scale per row of A and a scale per row of B; EPI_ACT adds a bias
-// per column, applies an activation and adds a residual.
-enum : int { EPI_RELU = 0, EPI_CAST = 1, EPI_GATED = 2, EPI_I8 = 3, EPI_ACT = 4 };
+// per column, applies an activation and adds a residual.  EPI_GRAM, EPI_POLY and
+// EPI_STEP are the three products of a Newton-Schulz step (ortho.hip).
+enum : int {
+    EPI_RELU = 0, EPI_CAST = 1, EPI_GATED = 2, EPI_I8 = 3, EPI_ACT = 4, EPI_GRAM = 5, EPI_POLY = 6, EPI_STEP = 7
+};
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
@@ -120,6 +123,15 @@ struct KernelArgs {
     int bias_f32;             // the bias is fp32, else of A's type
     int ldr;
     const unsigned char* R;
+    // Newton-Schulz products: alpha scales what C holds, beta the sums and scale_o what R
+    // holds to their true values.  EPI_GRAM writes the diagonal to diag and 0 in its place; EPI_POLY reads
+    // that and its operand R (ldr apart), and writes its own diagonal to diag_out;
+    // EPI_STEP reads diag and updates X (M rows of N, in place).  pa, pb, pc: the
+    // step's coefficients.
+    float beta, scale_o, pa, pb, pc;
+    float* diag;
+    float* diag_out;
+    float* X;
 };
 
 // The tiles one configuration covers inside a launch: a grid of tiles_m x
@@ -1808,6 +1820,92 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
                         }
                 }
             });
+            return;
+        }
+        if constexpr (C::EPI == EPI_GRAM) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+#pragma unroll
+                    for (int q = 0; q < NQ; ++q) {
+                        const int m = m0 + wm0 + MB * i + lr, n = n0 + wn0 + MB * j + 4 * NG * q + 4 * g;
+                        f32x4_t v;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float s = acc[i][j][4 * q + e];
+                            v[e] = s * args.alpha;
+                            if (m == n + e) {
+                                v[e] = 0.0f;
+                                if (m < M) args.diag[m] = s * args.beta;
+                            }
+                        }
+                        put_group(i, j, q, v);
+                    }
+            return;
+        }
+        if constexpr (C::EPI == EPI_POLY || C::EPI == EPI_STEP) {
+            // what a row needs is on its way while the one before is finished (rows and
+            // columns past the edge take the last ones; M and N are multiples of 64)
+            using In4 = std::conditional_t<C::EPI == EPI_POLY, u32x2_t, f32x4_t>;
+            In4 next[TN * NQ];
+            float next_diag;
+            auto col = [&](int b) { return n0 + wn0 + MB * (b / NQ) + 4 * NG * (b % NQ) + 4 * g; };
+            f32x4_t column[TN * NQ];
+            if constexpr (C::EPI == EPI_POLY) {
+#pragma unroll
+                for (int b = 0; b < TN * NQ; ++b)
+                    column[b] = *reinterpret_cast<const f32x4_t*>(args.diag + min(col(b), N - 4));
+            }
+            auto fetch = [&](int i) {
+                const int m = min(m0 + wm0 + MB * i + lr, M - 1);
+                next_diag = args.diag[m];
+#pragma unroll
+                for (int b = 0; b < TN * NQ; ++b) {
+                    const int n = min(col(b), N - 4);
+                    if constexpr (C::EPI == EPI_POLY)
+                        next[b] = *reinterpret_cast<const u32x2_t*>(args.R + ((size_t)m * (size_t)args.ldr + n) * 2);
+                    else
+                        next[b] = *reinterpret_cast<const f32x4_t*>(args.X + (size_t)m * (size_t)N + n);
+                }
+            };
+            fetch(0);
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+                const int m = m0 + wm0 + MB * i + lr;
+                In4 own[TN * NQ];
+                const float d = next_diag;
+#pragma unroll
+                for (int b = 0; b < TN * NQ; ++b) own[b] = next[b];
+                if (i + 1 < TM) fetch(i + 1);
+#pragma unroll
+                for (int b = 0; b < TN * NQ; ++b) {
+                    const int n = col(b);
+                    f32x4_t v;
+                    if constexpr (C::EPI == EPI_POLY) {
+                        // off the diagonal b O + c (O^2 + (d_m + d_n) O), O being A without
+                        // its diagonal d; on it b d + c (O^2 + d^2), in fp32
+                        const f32x4_t o = to_float4<DT_F16>(own[b]);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float s = acc[i][b / NQ][4 * (b % NQ) + e] * args.beta, a = o[e] * args.scale_o;
+                            v[e] = args.alpha * (args.pb * a + args.pc * (s + (d + column[b][e]) * a));
+                            if (m == n + e) {
+                                v[e] = 0.0f;
+                                if (m < M) args.diag_out[m] = args.pb * d + args.pc * (s + d * d);
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            v[e] = fmaf(args.pa + d, own[b][e], acc[i][b / NQ][4 * (b % NQ) + e] * args.beta);
+                        if (m < M && n >= n_own && n < N)
+                            *reinterpret_cast<f32x4_t*>(args.X + (size_t)m * (size_t)N + n) = v;
+                        v *= args.alpha;
+                    }
+                    put_group(i, b / NQ, b % NQ, v);
+                }
+            }
             return;
         }
         // scales of the lane's rows and columns (rows and columns past the edge

@@ -109,11 +109,11 @@ int64_t tiles_of(int cfg, const Linear& l)
 {
     return ceil_div(l.M, linear_info(cfg).bm) * ceil_div(l.N, linear_info(cfg).bn);
 }
-double linear_time(int cfg, const Linear& l)
+double linear_time(int cfg, const Linear& l, int64_t batch = 1)
 {
     const TileTime t = tile_time(cfg);
     const double one = t.per_byte * double(l.K) * l.bytes + t.fixed;
-    const int64_t tiles = tiles_of(cfg, l), rest = tiles % t.slots;
+    const int64_t tiles = tiles_of(cfg, l) * batch, rest = tiles % t.slots;
     return one * double(tiles / t.slots) + (rest == 0 ? 0.0 : rest <= kNumCUs ? t.alone * one : one);
 }
 

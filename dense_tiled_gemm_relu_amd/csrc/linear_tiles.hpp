@@ -28,13 +28,13 @@ template <class C> hipError_t launch(const KernelArgs& args, int grid, hipStream
 // 38); 64 x 64, gated 64 x 8192 x 8192 60 (LIN_128 83).  32 x 32 blocks with four
 // waves measured 3-15 % slower for LIN_128X2, and 556 us for the 8-bit 8192^3.
 //
-// Gated and integer products take B stored (N,K) and
-// 16x16 blocks everywhere: the two blocks a gated wave needs side by side fit
-// the small tiles, and the integer instruction has no other form here.
+// Products with B stored (N,K) take 16x16 blocks everywhere: the two blocks a gated wave
+// needs side by side fit the small tiles, and the integer instruction has no other form
+// here.
 template <int IN, int OUT, int EPI, int cfg> struct LinearCfg;
 template <int IN, int BK16> constexpr int bk = IN == DT_I8 ? 2 * BK16 : BK16;
-template <int EPI> constexpr bool nt = EPI != EPI_CAST;
-template <int EPI> constexpr int mb = EPI == EPI_CAST ? 32 : 16;
+template <int EPI> constexpr bool nt = EPI != EPI_CAST && EPI != EPI_STEP;
+template <int EPI> constexpr int mb = nt<EPI> ? 16 : 32;
 
 template <int IN, int OUT, int EPI> struct LinearCfg<IN, OUT, EPI, LIN_256> {
     using type = Cfg<IN, OUT, nt<EPI>, 256, 256, bk<IN, 32>, 2, 4, 4, true, true, 16, false, false, false, EPI>;

@@ -1,0 +1,165 @@
+// Orthogonalisation of a matrix by Newton-Schulz steps X <- a X + (b A + c A^2) X with
+// A = X X^T, from X = G / (|G| + eps): the passes over the matrix before and after, and
+// the three products of a step on the tile kernel.
+//
+// Precision.  The products' operands are float16, X itself and the diagonals of A and of
+// B = b A + c A^2 are fp32.  A step multiplies small singular values by a (485 times over
+// five steps of a = 3.4445), so a rounding of X would grow as much; a rounding of the
+// operands of A, B and B X is only ever multiplied by large singular vectors on one side
+// and stays small.  The diagonals are where A and B are largest near the end (A tends to
+// the identity), and rounding them would lose the most.  Against binary64 over spectra
+// from flat to ten decades the results are off by 1e-4 to 7e-4 of their norm; with X in
+// bfloat16, as such steps are often run, by 1e-2 to 0.5.
+#include "block.hpp"
+#include "linear_tiles.hpp"
+#include "row_common.hpp"
+
+namespace gemm_relu_hip {
+
+namespace {
+
+// ------------------------------------------------------- before the steps
+// Sums of squares in binary64 (the values may be any fp32 ones): kOrthoParts workgroups
+// a matrix take rows in turns.
+template <class T> __global__ void __launch_bounds__(kThreads) ortho_squares_kernel(OrthoArgs a)
+{
+    __shared__ double part[kThreads / 64];
+    const T* g = static_cast<const T*>(a.g) + (size_t)blockIdx.y * (size_t)a.g_batch;
+    double s = 0.0;
+    for (int64_t r = blockIdx.x; r < a.rows; r += kOrthoParts)
+        for (int64_t j = threadIdx.x; j < a.cols; j += kThreads) {
+            const double v = (double)(float)g[(size_t)r * (size_t)a.g_stride + j];
+            s = fma(v, v, s);
+        }
+#pragma unroll
+    for (int step = 1; step < 64; step *= 2) s += __shfl_xor(s, step);
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+#pragma unroll
+        for (int k = 1; k < kThreads / 64; ++k) s += part[k];
+        a.squares[(size_t)blockIdx.y * kOrthoParts + blockIdx.x] = s;
+    }
+}
+
+// X and its float16 copy, 64 x 64 a workgroup, transposed where the matrix is tall, with
+// zeros in the padding.
+template <class T> __global__ void __launch_bounds__(kThreads) ortho_start_kernel(OrthoArgs a)
+{
+    __shared__ float tile[64][65];
+    const size_t batch = blockIdx.y;
+    const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
+    double s = a.squares[batch * kOrthoParts + lane];
+    static_assert(kOrthoParts == 64, "one part a lane");
+#pragma unroll
+    for (int step = 1; step < 64; step *= 2) s += __shfl_xor(s, step);
+    const double scale = 1.0 / (sqrt(s) + (double)a.eps);
+    const int tiles = a.Q / 64, p0 = (int)(blockIdx.x / tiles) * 64, q0 = (int)(blockIdx.x % tiles) * 64;
+    const T* g = static_cast<const T*>(a.g) + batch * (size_t)a.g_batch;
+    const bool tall = a.rows > a.cols;
+    const int r0 = tall ? q0 : p0, c0 = tall ? p0 : q0;
+    float* x = a.x + batch * (size_t)a.P * (size_t)a.Q;
+    _Float16* xh = static_cast<_Float16*>(a.xh) + batch * (size_t)a.P * (size_t)a.Q;
+    const auto put = [&](int p, int q, float v) {
+        const size_t at = (size_t)p * (size_t)a.Q + q;
+        x[at] = v;
+        xh[at] = (_Float16)(v * kOrthoX);
+    };
+    for (int k = wave; k < 64; k += kThreads / 64) {
+        const int r = r0 + k, c = c0 + lane;
+        const float v = r < a.rows && c < a.cols ? (float)((double)(float)g[(size_t)r * (size_t)a.g_stride + c] * scale) : 0.0f;
+        if (tall)
+            tile[k][lane] = v;
+        else
+            put(r, c, v);
+    }
+    if (!tall) return;
+    __syncthreads();
+    for (int k = wave; k < 64; k += kThreads / 64) put(p0 + k, q0 + lane, tile[lane][k]);
+}
+
+// ------------------------------------------------------------- afterwards
+__global__ void __launch_bounds__(kThreads) ortho_end_kernel(OrthoArgs a)
+{
+    __shared__ float tile[64][65];
+    const size_t batch = blockIdx.y;
+    const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
+    const int tiles = a.Q / 64, p0 = (int)(blockIdx.x / tiles) * 64, q0 = (int)(blockIdx.x % tiles) * 64;
+    const bool tall = a.rows > a.cols;
+    const float* x = a.x + batch * (size_t)a.P * (size_t)a.Q;
+    __bf16* out = static_cast<__bf16*>(a.out) + batch * (size_t)a.rows * (size_t)a.cols;
+    for (int k = wave; k < 64; k += kThreads / 64) {
+        const int p = p0 + k, q = q0 + lane;
+        const float v = x[(size_t)p * (size_t)a.Q + q];
+        if (tall)
+            tile[k][lane] = v;
+        else if (p < a.p && q < a.q)
+            out[(size_t)p * (size_t)a.cols + q] = (__bf16)v;
+    }
+    if (!tall) return;
+    __syncthreads();
+    for (int k = wave; k < 64; k += kThreads / 64)
+        if (q0 + k < a.q && p0 + lane < a.p) out[(size_t)(q0 + k) * (size_t)a.cols + p0 + lane] = (__bf16)tile[lane][k];
+}
+
+// ------------------------------------------------------------ the products
+template <class C> __global__ void __launch_bounds__(C::NTHREADS, 1) ortho_product_kernel(OrthoProduct p)
+{
+    __shared__ __attribute__((aligned(1024))) unsigned char smem_raw[C::LDS_BYTES];
+    KernelArgs args = p.k;
+    const uint64_t batch = blockIdx.y;
+    args.A += batch * p.a;
+    args.B += batch * p.b;
+    args.C += batch * p.c;
+    args.R += batch * p.r;
+    args.diag += batch * p.diag;
+    args.diag_out += batch * p.diag;
+    args.X += batch * p.x;
+    gemm_relu_tile<C>(args, (int)blockIdx.x, (GR_LDS unsigned char*)(smem_raw), nullptr,
+                      Region{args.tiles_m, args.tiles_n, args.panel, 0});
+}
+template <class C> hipError_t launch_product(const OrthoProduct& p, int tiles, int batch, hipStream_t stream)
+{
+    void* params[] = {const_cast<OrthoProduct*>(&p)};
+    return hipLaunchKernel(reinterpret_cast<const void*>(&ortho_product_kernel<C>), dim3(tiles, batch), dim3(C::NTHREADS), params,
+                           0, stream);
+}
+template <int EPI> OrthoLaunchFn pick_product(int cfg)
+{
+    switch (cfg) {
+    case LIN_256: return &launch_product<typename LinearCfg<DT_F16, DT_F16, EPI, LIN_256>::type>;
+    case LIN_128: return &launch_product<typename LinearCfg<DT_F16, DT_F16, EPI, LIN_128>::type>;
+    case LIN_128X2: return &launch_product<typename LinearCfg<DT_F16, DT_F16, EPI, LIN_128X2>::type>;
+    case LIN_64: return &launch_product<typename LinearCfg<DT_F16, DT_F16, EPI, LIN_64>::type>;
+    default: return nullptr;
+    }
+}
+
+}  // namespace
+
+OrthoLaunchFn launcher_ortho(int epi, int cfg)
+{
+    switch (epi) {
+    case EPI_GRAM: return pick_product<EPI_GRAM>(cfg);
+    case EPI_POLY: return pick_product<EPI_POLY>(cfg);
+    case EPI_STEP: return pick_product<EPI_STEP>(cfg);
+    default: return nullptr;
+    }
+}
+
+hipError_t launch_ortho_start(const OrthoArgs& a, int dt, hipStream_t stream)
+{
+    return with_types(dt, dt, [&](auto x, auto) {
+        using T = decltype(x);
+        const hipError_t e = start(&ortho_squares_kernel<T>, dim3(kOrthoParts, a.batch), kThreads, stream, a);
+        if (e != hipSuccess) return e;
+        return start(&ortho_start_kernel<T>, dim3((unsigned)(a.P / 64) * (unsigned)(a.Q / 64), a.batch), kThreads, stream, a);
+    });
+}
+
+hipError_t launch_ortho_end(const OrthoArgs& a, hipStream_t stream)
+{
+    return start(&ortho_end_kernel, dim3((unsigned)(a.P / 64) * (unsigned)(a.Q / 64), a.batch), kThreads, stream, a);
+}
+
+}  // namespace gemm_relu_hip

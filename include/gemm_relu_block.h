@@ -108,6 +108,28 @@ int gemm_relu_add_norm_backward(const void* dy, int64_t dy_stride, const void* d
                                 int wdtype, int norm, float scale, void* workspace,
                                 uint64_t workspace_bytes, void* stream);
 
+/*
+ * Orthogonalisation of matrices by Newton-Schulz steps: each of the batch's matrices g
+ * (rows x cols, batch_stride elements apart, in any order) becomes
+ *   X = g / (|g| + eps), |g| the square root of the sum of squares,
+ *   X <- a X + (b A + c A^2) X,  A = X X^T,   once per step with its a, b, c,
+ * (with A = X^T X on the right where rows > cols: the same matrix).  The singular vectors
+ * stay, the singular values tend to 1.  coefficients: host memory, steps times a, b, c,
+ * read before the call returns; steps <= 64.  dtype (g): F16, BF16 or F32.  out is dense
+ * bfloat16 (batch x rows x cols).  The products' operands are rounded to float16, X itself
+ * is kept in fp32: results are off by less than 1e-3 of their norm before they are
+ * rounded.  Values of X and of b A + c A^2 past 2^8 in magnitude, and of A past 2^6, are
+ * past float16's range here and give infinities and NaN; coefficients that keep the
+ * singular values below 2 stay far from that.  A matrix of zeros gives zeros; an infinity or NaN in g gives
+ * NaN all over its matrix.  The shorter side <= 2^16, the longer <= 2^22, batch <= 65535,
+ * else GEMM_RELU_EUNSUPPORTED.
+ */
+int64_t gemm_relu_orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols);
+int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t batch_stride, void* out,
+                            int64_t batch, int64_t rows, int64_t cols, int dtype,
+                            const float* coefficients, int steps, float eps, void* workspace,
+                            uint64_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

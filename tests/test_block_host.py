@@ -1,4 +1,6 @@
 """The operators around the half layer on the host: what they refuse, before any GPU call."""
+import ctypes
+
 import pytest
 import torch
 
@@ -94,6 +96,41 @@ def test_workspaces_and_plans():
     assert lib.gemm_relu_add_norm_backward_workspace(1, 100) >= 4 * 100 * 4
     assert lib.gemm_relu_add_norm_backward_workspace(-1, 100) == gr.EINVAL
     assert lib.gemm_relu_add_norm_backward_workspace(BIG - 1, BIG - 1) >= 256 * 4 * 4 * (BIG - 1)
+    assert lib.gemm_relu_orthogonalize_workspace(0, 5, 5) == 0
+    assert lib.gemm_relu_orthogonalize_workspace(1, 64, 64) >= 64 * 64 * 12
+    assert lib.gemm_relu_orthogonalize_workspace(1, -1, 64) == gr.EINVAL
+    assert lib.gemm_relu_orthogonalize_workspace(65535, 2 ** 16, 2 ** 22) >= 65535 * 2 ** 41            # grows without wrapping
+    for sizes in ((1, 2 ** 16 + 1, 2 ** 17), (1, 4, 2 ** 22 + 1), (65536, 4, 4)):
+        assert lib.gemm_relu_orthogonalize_workspace(*sizes) == gr.EUNSUPPORTED
+
+
+class Coefficients(ctypes.Array):
+    _type_, _length_ = ctypes.c_float, 3
+
+
+STEP, BAD = Coefficients(3.0, -4.0, 2.0), Coefficients(3.0, float("inf"), 2.0)
+ORTHO = dict(g=X, stride=8, batch_stride=64, out=Y, batch=2, rows=8, cols=8, dtype=BF16, c=ctypes.addressof(STEP), steps=1,
+             eps=1e-7, ws=WS, ws_bytes=1 << 20)
+
+
+@pytest.mark.parametrize("over", [
+    dict(batch=-1), dict(rows=-1), dict(cols=BIG), dict(dtype=3), dict(stride=7), dict(stride=BIG), dict(batch_stride=-64),
+    dict(g=0), dict(g=X + 1), dict(out=0), dict(out=Y + 1), dict(out=X), dict(out=X + 250), dict(out=WS + 256), dict(c=0),
+    dict(c=ctypes.addressof(BAD)), dict(steps=-1), dict(steps=65), dict(eps=-1.0), dict(eps=NAN), dict(ws=0), dict(ws=WS + 8),
+    dict(ws_bytes=1000), dict(ws=X)])
+def test_orthogonalize_refuses(over):
+    assert call("gemm_relu_orthogonalize", ORTHO, **over) == gr.EINVAL
+
+
+@pytest.mark.parametrize("over", [dict(batch=0), dict(rows=0, g=0), dict(cols=0, g=0, out=0)])
+def test_orthogonalize_of_nothing(over):
+    assert call("gemm_relu_orthogonalize", ORTHO, **over) == gr.OK
+
+
+@pytest.mark.parametrize("over", [dict(rows=2 ** 16 + 1, cols=2 ** 17, stride=2 ** 17), dict(cols=2 ** 22 + 1, stride=2 ** 23),
+                                  dict(batch=65536)])
+def test_orthogonalize_past_the_limits(over):
+    assert call("gemm_relu_orthogonalize", ORTHO, **over) == gr.EUNSUPPORTED
 
 
 # ---- the tensor front ends (CPU tensors: every refusal comes before the device is looked at, the last one is it)
@@ -127,6 +164,18 @@ H = torch.bfloat16
     (ValueError, lambda: gr.matmul_act_backward(t(4, 6), None, t(4, 8), t(6, 8), "none", t(5))),
     (ValueError, lambda: gr.matmul_act_backward(t(4, 6), None, t(4, 8), t(6, 8), "none", t(6))),
     (ValueError, lambda: gr.add_norm(t(4, 8), t(4, 8), t(8), norm="batch")),
+    (TypeError, lambda: gr.orthogonalize(t(4, 8, dtype=torch.int8))),
+    (ValueError, lambda: gr.orthogonalize(t(8))),
+    (ValueError, lambda: gr.orthogonalize(t(2, 3, 4, 8))),
+    (ValueError, lambda: gr.orthogonalize(t(8, 4).t())),
+    (ValueError, lambda: gr.orthogonalize(t(4, 1).expand(4, 8))),
+    (ValueError, lambda: gr.orthogonalize(t(4, 8), 65)),
+    (ValueError, lambda: gr.orthogonalize(t(4, 8), -1)),
+    (ValueError, lambda: gr.orthogonalize(t(4, 8), 2, (1.0, 2.0))),
+    (ValueError, lambda: gr.orthogonalize(t(4, 8), 2, [(1.0, 2.0, 3.0)])),
+    (ValueError, lambda: gr.orthogonalize(t(4, 8), 2, [(1.0, 2.0, 3.0), (1.0, 2.0)])),
+    (TypeError, lambda: gr.orthogonalize(t(4, 8), 1, [("a", "b", "c")])),
+    (ValueError, lambda: gr.orthogonalize(t(4, 8))),                                           # not on a GPU
     (TypeError, lambda: gr.add_norm(t(4, 8, dtype=torch.int8), t(4, 8), t(8))),
     (TypeError, lambda: gr.add_norm(t(4, 8), t(4, 8, dtype=F), t(8))),
     (ValueError, lambda: gr.add_norm(t(4, 8), t(4, 7), t(8))),
