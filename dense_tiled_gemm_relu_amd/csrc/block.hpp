@@ -79,9 +79,9 @@ struct OrthoArgs {
     float* x;                   // batch x P x Q
     void* xh;                   // float16: batch x P x Q
 };
-constexpr int kOrthoParts = 64;
+constexpr int kOrthoParts = 256;
 hipError_t launch_ortho_start(const OrthoArgs& a, int dt, hipStream_t stream);
-hipError_t launch_ortho_end(const OrthoArgs& a, hipStream_t stream);
+hipError_t launch_ortho_copy(const OrthoArgs& a, hipStream_t stream);      // no steps: X as it is
 // one of the products for every matrix of the batch
 struct OrthoProduct {
     KernelArgs k;

@@ -4,7 +4,6 @@
 
 #include <algorithm>
 #include <cstdint>
-#include <utility>
 
 #include "api_common.hpp"
 #include "block.hpp"
@@ -291,7 +290,8 @@ extern "C" int gemm_relu_add_norm_backward(const void* dy, int64_t dy_stride, co
 // --------------------------------------------------------- orthogonalisation
 namespace {
 
-constexpr int64_t kOrthoShort = int64_t(1) << 16, kOrthoLong = int64_t(1) << 22, kOrthoBatch = 65535;
+// (the tiles' copies reach rows of 2^22 elements; a launch's work-items stay below 2^32)
+constexpr int64_t kOrthoShort = int64_t(1) << 16, kOrthoLong = int64_t(1) << 22, kOrthoSize = int64_t(1) << 34, kOrthoBatch = 65535;
 constexpr int kOrthoSteps = 64;
 
 struct OrthoPlan {
@@ -299,12 +299,19 @@ struct OrthoPlan {
     int gram, poly, step;                       // configurations of the products
     uint64_t squares, x, xh[2], a, b, diag_a, diag_b, bytes;
 };
-// the configuration of least estimated time for `batch` products
-int ortho_config(const Linear& l, int64_t batch)
+// tiles of one product: of a symmetric one those on and below the diagonal
+int64_t ortho_tiles(int cfg, const Linear& l, bool symmetric)
 {
+    const int64_t side = ceil_div(l.M, linear_info(cfg).bm);
+    return symmetric ? side * (side + 1) / 2 : tiles_of(cfg, l);
+}
+// the configuration of least estimated time for `batch` products
+int ortho_config(const Linear& l, int64_t batch, bool symmetric)
+{
+    const auto time = [&](int cfg) { return tiles_time(cfg, l, batch * ortho_tiles(cfg, l, symmetric)); };
     int best = LIN_64;
     for (int cfg : {LIN_128, LIN_128X2, LIN_256})
-        if (usable(cfg, l) && linear_time(cfg, l, batch) < linear_time(best, l, batch)) best = cfg;
+        if (usable(cfg, l) && time(cfg) < time(best)) best = cfg;
     return best;
 }
 OrthoPlan plan_ortho(int64_t batch, int64_t rows, int64_t cols)
@@ -314,9 +321,9 @@ OrthoPlan plan_ortho(int64_t batch, int64_t rows, int64_t cols)
     o.q = std::max(rows, cols);
     o.P = round_up(o.p, 64);
     o.Q = round_up(o.q, 64);
-    o.gram = ortho_config(Linear{o.P, o.P, o.Q, o.Q, o.Q, true}, batch);
-    o.poly = ortho_config(Linear{o.P, o.P, o.P, o.P, o.P, true}, batch);
-    o.step = ortho_config(Linear{o.P, o.Q, o.P, o.P, o.Q, false}, batch);
+    o.gram = ortho_config(Linear{o.P, o.P, o.Q, o.Q, o.Q, true}, batch, true);
+    o.poly = ortho_config(Linear{o.P, o.P, o.P, o.P, o.P, true}, batch, true);
+    o.step = ortho_config(Linear{o.P, o.Q, o.P, o.P, o.Q, false}, batch, false);
     uint64_t at = 0;
     const auto take = [&](uint64_t bytes) {
         const uint64_t here = at;
@@ -338,7 +345,8 @@ OrthoPlan plan_ortho(int64_t batch, int64_t rows, int64_t cols)
 bool ortho_sizes_ok(int64_t batch, int64_t rows, int64_t cols) { return size_ok(batch) && size_ok(rows) && size_ok(cols); }
 bool ortho_supported(int64_t batch, int64_t rows, int64_t cols)
 {
-    return batch <= kOrthoBatch && std::min(rows, cols) <= kOrthoShort && std::max(rows, cols) <= kOrthoLong;
+    return batch <= kOrthoBatch && std::min(rows, cols) <= kOrthoShort && std::max(rows, cols) <= kOrthoLong &&
+           rows * cols <= kOrthoSize;
 }
 
 }  // namespace
@@ -395,53 +403,55 @@ extern "C" int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t 
     hipError_t err = launch_ortho_start(a, dtype, st);
     const uint64_t PQ = uint64_t(o.P) * uint64_t(o.Q), PP = uint64_t(o.P) * uint64_t(o.P);
     const Linear gram{o.P, o.P, o.Q, o.Q, o.Q, true}, poly{o.P, o.P, o.P, o.P, o.P, true}, next{o.P, o.Q, o.P, o.P, o.Q, false};
-    const auto product = [&](int epi, int cfg, const Linear& l, const void* A, const void* B, void* C) {
-        const LinearPlan p = plan_as(cfg, l);
+    const auto launch = [&](int epi, int cfg, const Linear& l, OrthoProduct k) {
+        const bool symmetric = epi == EPI_GRAM || epi == EPI_POLY;
+        return launcher_ortho(epi, cfg)(k, int(ortho_tiles(cfg, l, symmetric)), int(batch), st);
+    };
+    const auto product = [&](int cfg, const Linear& l, const void* A, const void* B, void* C) {
         OrthoProduct k{};
-        k.k = linear_args(p, l, A, B, C);
+        k.k = linear_args(plan_as(cfg, l), l, A, B, C);
         k.diag = uint64_t(o.P);
-        return std::make_pair(k, launcher_ortho(epi, cfg));
+        return k;
     };
     for (int s = 0; s < steps && err == hipSuccess; ++s) {
         const void* xh = ws + o.xh[s % 2];
-        float* diag_a = reinterpret_cast<float*>(ws + o.diag_a);
-        float* diag_b = reinterpret_cast<float*>(ws + o.diag_b);
-        {
-            auto [k, launch] = product(EPI_GRAM, o.gram, gram, xh, xh, ws + o.a);
-            k.k.alpha = kOrthoA / (kOrthoX * kOrthoX);
-            k.k.beta = 1.0f / (kOrthoX * kOrthoX);
-            k.k.diag = diag_a;
-            k.a = k.b = PQ * 2;
-            k.c = PP * 2;
-            err = launch(k, int(k.k.tiles_m * k.k.tiles_n), int(batch), st);
-        }
-        if (err == hipSuccess) {
-            auto [k, launch] = product(EPI_POLY, o.poly, poly, ws + o.a, ws + o.a, ws + o.b);
-            k.k.alpha = kOrthoB;
-            k.k.beta = 1.0f / (kOrthoA * kOrthoA);
-            k.k.scale_o = 1.0f / kOrthoA;
-            k.k.pb = coefficients[3 * s + 1];
-            k.k.pc = coefficients[3 * s + 2];
-            k.k.diag = diag_a;
-            k.k.diag_out = diag_b;
-            k.k.R = ws + o.a;
-            k.k.ldr = int(o.P);
-            k.a = k.b = k.c = k.r = PP * 2;
-            err = launch(k, int(k.k.tiles_m * k.k.tiles_n), int(batch), st);
-        }
-        if (err == hipSuccess) {
-            auto [k, launch] = product(EPI_STEP, o.step, next, ws + o.b, xh, ws + o.xh[(s + 1) % 2]);
-            k.k.alpha = kOrthoX;
-            k.k.beta = 1.0f / (kOrthoB * kOrthoX);
-            k.k.pa = coefficients[3 * s];
-            k.k.diag = diag_b;
-            k.k.X = a.x;
-            k.a = PP * 2;
-            k.b = k.c = PQ * 2;
-            k.x = PQ;
-            err = launch(k, int(k.k.tiles_m * k.k.tiles_n), int(batch), st);
-        }
+        const bool last = s == steps - 1;
+        OrthoProduct k = product(o.gram, gram, xh, xh, ws + o.a);
+        k.k.alpha = kOrthoA / (kOrthoX * kOrthoX);
+        k.k.beta = 1.0f / (kOrthoX * kOrthoX);
+        k.k.diag = reinterpret_cast<float*>(ws + o.diag_a);
+        k.a = k.b = PQ * 2;
+        k.c = PP * 2;
+        err = launch(EPI_GRAM, o.gram, gram, k);
+        if (err != hipSuccess) break;
+        k = product(o.poly, poly, ws + o.a, ws + o.a, ws + o.b);
+        k.k.alpha = kOrthoB;
+        k.k.beta = 1.0f / (kOrthoA * kOrthoA);
+        k.k.scale_o = 1.0f / kOrthoA;
+        k.k.pb = coefficients[3 * s + 1];
+        k.k.pc = coefficients[3 * s + 2];
+        k.k.diag = reinterpret_cast<float*>(ws + o.diag_a);
+        k.k.diag_out = reinterpret_cast<float*>(ws + o.diag_b);
+        k.k.R = ws + o.a;
+        k.k.ldr = int(o.P);
+        k.a = k.b = k.c = k.r = PP * 2;
+        err = launch(EPI_POLY, o.poly, poly, k);
+        if (err != hipSuccess) break;
+        k = product(o.step, next, ws + o.b, xh, last ? out : ws + o.xh[(s + 1) % 2]);
+        k.k.alpha = kOrthoX;
+        k.k.beta = 1.0f / (kOrthoB * kOrthoX);
+        k.k.pa = coefficients[3 * s];
+        k.k.diag = reinterpret_cast<float*>(ws + o.diag_b);
+        k.k.X = a.x;
+        k.k.out_m = int(o.p);
+        k.k.out_n = int(o.q);
+        k.k.transposed = rows > cols;
+        k.a = PP * 2;
+        k.b = PQ * 2;
+        k.c = last ? uint64_t(rows) * uint64_t(cols) * 2 : PQ * 2;
+        k.x = PQ;
+        err = launch(last ? EPI_LAST : EPI_STEP, o.step, next, k);
     }
-    if (err == hipSuccess) err = launch_ortho_end(a, st);
+    if (err == hipSuccess && steps == 0) err = launch_ortho_copy(a, st);
     return finish(err, st);
 }

@@ -277,24 +277,31 @@ template <class T, class W, int G, int V> __global__ void __launch_bounds__(kGro
 }
 
 // The backward pass in one read of its inputs: s is computed again, the row's two sums
-// give dresidual, two more dx, and the thread's columns of the sums over rows stay in
-// registers over its rows.  A workgroup leaves one strip of partial sums; the join
-// kernel adds the strips in order.  `waves` waves a row, and as many rows at a time as
-// the workgroup holds.  Bound by HBM.
+// give dresidual, two more dx.  A workgroup takes rows in turns, `waves` waves a row and
+// as many rows at a time as 16 waves hold, and leaves one strip of sums over its rows; the
+// join kernel adds the strips in order.
+//
+// A thread's own sums over rows stand in LDS (with V N = 8 elements a thread; for longer
+// rows in registers, which then spill): four fp32 sums an element beside five streams, the
+// next row's among them, do not fit the 128 registers that 16 waves a CU leave.  They are
+// nobody else's, so they need no barrier, and they take a sixth of LDS's rate.  A chunk
+// moved back inside the row has its weights cleared where its neighbour owns the element:
+// the row's sums then need no test, and only what it owns is stored.
 template <class T, class W, int V>
 __global__ void __launch_bounds__(1024) add_norm_backward_kernel(AddNormArgs a, int waves)
 {
     constexpr int N = Chunk<T>::N;
     using X = typename Chunk<T>::Vec;
     using WV = typename VecN<W, N>::Vec;
+    constexpr bool IN_LDS = V * N <= 8;
+    constexpr int QUADS = V * N / 4;                  // of a thread's elements
     __shared__ float lds[2][4][16];
-    __shared__ float part[V == 1 ? 16 * N * 64 : 1];
+    __shared__ __attribute__((aligned(16))) f32x4_t sums_raw[IN_LDS ? kMaxSums * QUADS * 1024 : 1];
     const int lane = (int)(threadIdx.x & 63), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int groups = (int)(blockDim.x >> 6) / waves, group = wave / waves, in_row = wave - group * waves;
     const RowMap<T, V> map(a.cols, in_row * 64 + lane, 64 * waves);
     const bool element_gate = a.gate && a.gate_stride, channel_gate = a.gate && !a.gate_stride;
     WV w[V], pw[V], gate[V];
-    float dw[V][N], db[V][N], dg[V][N], dp[V][N];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         w[v] = pw[v] = gate[v] = WV{};
@@ -302,8 +309,21 @@ __global__ void __launch_bounds__(1024) add_norm_backward_kernel(AddNormArgs a, 
         if (a.pw) pw[v] = load_vec<WV>(static_cast<const W*>(a.pw) + map.start[v]);
         if (channel_gate) gate[v] = load_vec<WV>(static_cast<const W*>(a.gate) + map.start[v]);
 #pragma unroll
-        for (int e = 0; e < N; ++e) dw[v][e] = db[v][e] = dg[v][e] = dp[v][e] = 0.0f;
+        for (int e = 0; e < N; ++e)
+            if (!map.owns(v, e)) w[v][e] = pw[v][e] = (W)0.0f;
     }
+    // sum `which` of the thread's quad k of elements
+    f32x4_t in_registers[IN_LDS ? 1 : kMaxSums][IN_LDS ? 1 : QUADS];
+    const auto sum_at = [&](int which, int k) -> f32x4_t& {
+        if constexpr (IN_LDS)
+            return sums_raw[(which * QUADS + k) * 1024 + (int)threadIdx.x];
+        else
+            return in_registers[which][k];
+    };
+#pragma unroll
+    for (int which = 0; which < kMaxSums; ++which)
+#pragma unroll
+        for (int k = 0; k < QUADS; ++k) sum_at(which, k) = f32x4_t{};
     const int64_t step = (int64_t)gridDim.x * groups;
     const int64_t first_row = (int64_t)blockIdx.x * groups;
     int64_t row = first_row + group;
@@ -342,21 +362,38 @@ __global__ void __launch_bounds__(1024) add_norm_backward_kernel(AddNormArgs a, 
                 buffers[first + 1][wave] = q;
             }
             __syncthreads();
-            p = q = 0.0f;
-            for (int k = 0; k < waves; ++k) {
-                p += buffers[first][group * waves + k];
-                q += buffers[first + 1][group * waves + k];
-            }
+            // 16 lanes each add the waves'
+            const int k = lane & 15;
+            p = row16_sum(k < waves ? buffers[first][group * waves + k] : 0.0f);
+            q = row16_sum(k < waves ? buffers[first + 1][group * waves + k] : 0.0f);
         }
         p = a.layer ? p * inv_n : 0.0f;
         q *= inv_n;
+    };
+    // the row's values f of an output
+    auto store = [&](void* out, size_t at, const float(&f)[V][N]) {
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            X packed;
+#pragma unroll
+            for (int e = 0; e < N; ++e) packed[e] = (T)f[v][e];
+            T* to = static_cast<T*>(out) + at + map.start[v];
+            if (v < V - 1 || map.skip == 0) {
+                __builtin_memcpy(to, &packed, sizeof packed);
+            } else {
+#pragma unroll
+                for (int e = 0; e < N; ++e)
+                    if (e >= map.skip) to[e] = packed[e];
+            }
+        }
     };
     // all rows of a workgroup meet at its barriers, so a row past the end runs along
     // with nothing to add and nothing to store
     for (int turn = 0; row - group < a.rows; row += step, turn ^= 1) {
         const bool live = row < a.rows;
-        const f32x4_t stats = all_stats[min(row, (int64_t)a.rows - 1)];
-        float xhat[V][N], t[V][N], shat[V][N], dr[V][N];
+        const size_t at = (size_t)row * (size_t)a.cols;
+        const Stats stats = all_stats[min(row, (int64_t)a.rows - 1)];
+        float xhat[V][N], shat[V][N], dr[V][N];
         X y[V], g[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -365,13 +402,14 @@ __global__ void __launch_bounds__(1024) add_norm_backward_kernel(AddNormArgs a, 
 #pragma unroll
             for (int e = 0; e < N; ++e) {
                 xhat[v][e] = ((float)nx[v][e] - stats[0]) * stats[1];
-                t[v][e] = a.pw ? xhat[v][e] * (float)pw[v][e] : xhat[v][e];
-                const float gated = channel_gate ? t[v][e] * (float)gate[v][e] : element_gate ? t[v][e] * (float)g[v][e] : t[v][e];
-                shat[v][e] = (fmaf(a.scale, gated, (float)nr[v][e]) - stats[2]) * stats[3];
                 dr[v][e] = (float)nd[v][e];
             }
         }
-        fetch(row + step);
+        // t, and the gate's product with the scale, where they are wanted
+        const auto t = [&](int v, int e) { return a.pw ? xhat[v][e] * (float)pw[v][e] : xhat[v][e]; };
+        const auto scaled_gate = [&](int v, int e) {
+            return channel_gate ? a.scale * (float)gate[v][e] : element_gate ? a.scale * (float)g[v][e] : a.scale;
+        };
         if (a.w) {
             // c = dy weight
             float p = 0.0f, q = 0.0f;
@@ -379,65 +417,77 @@ __global__ void __launch_bounds__(1024) add_norm_backward_kernel(AddNormArgs a, 
             for (int v = 0; v < V; ++v)
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
-                    const float c = map.owns(v, e) ? (float)y[v][e] * (float)w[v][e] : 0.0f;
+                    const float gated = channel_gate ? t(v, e) * (float)gate[v][e]
+                                        : element_gate ? t(v, e) * (float)g[v][e]
+                                                       : t(v, e);
+                    shat[v][e] = (fmaf(a.scale, gated, (float)nr[v][e]) - stats[2]) * stats[3];
+                    const float c = (float)y[v][e] * (float)w[v][e];
                     p += c;
-                    q = fmaf(c, map.owns(v, e) ? shat[v][e] : 0.0f, q);
+                    q = fmaf(c, shat[v][e], q);
                 }
+            fetch(row + step);
             means(p, q, lds[turn], 0);
 #pragma unroll
             for (int v = 0; v < V; ++v)
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    const float d = (float)y[v][e];
-                    dr[v][e] = fmaf(stats[3], fmaf(-shat[v][e], q, fmaf(d, (float)w[v][e], -p)), dr[v][e]);
+                for (int h = 0; h < N / 4; ++h) {
+                    f32x4_t dw = sum_at(0, v * (N / 4) + h), db = sum_at(1, v * (N / 4) + h);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int e = 4 * h + u;
+                        const float d = (float)y[v][e];
+                        dr[v][e] = fmaf(stats[3], fmaf(-shat[v][e], q, fmaf(d, (float)w[v][e], -p)), dr[v][e]);
+                        dw[u] = fmaf(d, shat[v][e], dw[u]);
+                        db[u] += d;
+                    }
                     if (live) {
-                        dw[v][e] = fmaf(d, shat[v][e], dw[v][e]);
-                        db[v][e] += d;
+                        sum_at(0, v * (N / 4) + h) = dw;
+                        sum_at(1, v * (N / 4) + h) = db;
                     }
                 }
+        } else {
+            fetch(row + step);
         }
-        const size_t at = (size_t)row * (size_t)a.cols;
-        if (a.dr) {
+        if (a.dr && live) store(a.dr, at, dr);
+        if (channel_gate) {
 #pragma unroll
             for (int v = 0; v < V; ++v)
-                if (map.has(v) && live) {
-                    X out;
 #pragma unroll
-                    for (int e = 0; e < N; ++e) out[e] = (T)dr[v][e];
-                    __builtin_memcpy(static_cast<T*>(a.dr) + at + map.start[v], &out, sizeof out);
+                for (int h = 0; h < N / 4; ++h) {
+                    f32x4_t dg = sum_at(2, v * (N / 4) + h);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) dg[u] = fmaf(a.scale * dr[v][4 * h + u], t(v, 4 * h + u), dg[u]);
+                    if (live) sum_at(2, v * (N / 4) + h) = dg;
                 }
-        }
-        if (a.gate) {
+        } else if (element_gate && a.dgate && live) {
+            float dg[V][N];
 #pragma unroll
-            for (int v = 0; v < V; ++v) {
-                X out;
+            for (int v = 0; v < V; ++v)
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    const float d = a.scale * dr[v][e] * t[v][e];
-                    out[e] = (T)d;
-                    if (live) dg[v][e] += d;
-                }
-                if (element_gate && a.dgate && map.has(v) && live)
-                    __builtin_memcpy(static_cast<T*>(a.dgate) + at + map.start[v], &out, sizeof out);
-            }
+                for (int e = 0; e < N; ++e) dg[v][e] = a.scale * dr[v][e] * t(v, e);
+            store(a.dgate, at, dg);
         }
         // dt, in dr's place
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
-            for (int e = 0; e < N; ++e)
-                dr[v][e] *= channel_gate ? a.scale * (float)gate[v][e] : element_gate ? a.scale * (float)g[v][e] : a.scale;
+            for (int e = 0; e < N; ++e) dr[v][e] *= scaled_gate(v, e);
         if (a.pw) {
             float p = 0.0f, q = 0.0f;
 #pragma unroll
             for (int v = 0; v < V; ++v)
 #pragma unroll
-                for (int e = 0; e < N; ++e) {
-                    if (live) dp[v][e] = fmaf(dr[v][e], xhat[v][e], dp[v][e]);
-                    dr[v][e] *= (float)pw[v][e];
-                    const float c = map.owns(v, e) ? dr[v][e] : 0.0f;
-                    p += c;
-                    q = fmaf(c, map.owns(v, e) ? xhat[v][e] : 0.0f, q);
+                for (int h = 0; h < N / 4; ++h) {
+                    f32x4_t dp = sum_at(3, v * (N / 4) + h);
+#pragma unroll
+                    for (int u = 0; u < 4; ++u) {
+                        const int e = 4 * h + u;
+                        dp[u] = fmaf(dr[v][e], xhat[v][e], dp[u]);
+                        dr[v][e] *= (float)pw[v][e];
+                        p += dr[v][e];
+                        q = fmaf(dr[v][e], xhat[v][e], q);
+                    }
+                    if (live) sum_at(3, v * (N / 4) + h) = dp;
                 }
             means(p, q, lds[turn], 2);
 #pragma unroll
@@ -445,55 +495,31 @@ __global__ void __launch_bounds__(1024) add_norm_backward_kernel(AddNormArgs a, 
 #pragma unroll
                 for (int e = 0; e < N; ++e) dr[v][e] = stats[1] * fmaf(-xhat[v][e], q, dr[v][e] - p);
         }
-        if (a.dx) {
+        if (a.dx && live) store(a.dx, at, dr);
+    }
+    // the groups' sums join first, in order (with registers there is one group)
+    __syncthreads();
+    if (group) return;
+    float* strip = a.partial + (size_t)blockIdx.x * kMaxSums * (size_t)a.cols;
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-                if (map.has(v) && live) {
-                    X out;
+    for (int which = 0; which < kMaxSums; ++which) {
+        if (!(which < 2 ? a.w != nullptr : which == 2 ? channel_gate : a.pw != nullptr)) continue;
 #pragma unroll
-                    for (int e = 0; e < N; ++e) out[e] = (T)dr[v][e];
-                    __builtin_memcpy(static_cast<T*>(a.dx) + at + map.start[v], &out, sizeof out);
-                }
+        for (int k = 0; k < QUADS; ++k) {
+            f32x4_t s = sum_at(which, k);
+            if constexpr (IN_LDS)
+                for (int j = 1; j < groups; ++j) s += sums_raw[(which * QUADS + k) * 1024 + j * 64 * waves + (int)threadIdx.x];
+            const int v = k / (N / 4), e = 4 * (k % (N / 4));
+            float* to = strip + (size_t)which * (size_t)a.cols + map.start[v] + e;
+            if (v < V - 1 || map.skip == 0) {
+                __builtin_memcpy(to, &s, 16);
+            } else {
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+                    if (e + u >= map.skip) to[u] = s[u];
+            }
         }
     }
-    // the groups' sums join first, in order
-    float* strip = a.partial + (size_t)blockIdx.x * kMaxSums * (size_t)a.cols;
-    const auto leave = [&](int which, float(&own)[V][N]) {
-        if constexpr (V == 1) {
-            if (groups > 1) {
-                __syncthreads();
-                if (group) {
-#pragma unroll
-                    for (int e = 0; e < N; ++e) part[(wave * N + e) * 64 + lane] = own[0][e];
-                }
-                __syncthreads();
-                if (group) return;
-                for (int k = 1; k < groups; ++k)
-#pragma unroll
-                    for (int e = 0; e < N; ++e) own[0][e] += part[((k * waves + in_row) * N + e) * 64 + lane];
-            }
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            if (map.has(v)) {
-                float* to = strip + (size_t)which * (size_t)a.cols + map.start[v];
-                if (v < V - 1 || map.skip == 0) {
-#pragma unroll
-                    for (int e = 0; e < N; e += 4) {
-                        const f32x4_t four = {own[v][e], own[v][e + 1], own[v][e + 2], own[v][e + 3]};
-                        __builtin_memcpy(to + e, &four, 16);
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < N; ++e)
-                        if (e >= map.skip) to[e] = own[v][e];
-                }
-            }
-    };
-    if (a.w) leave(0, dw);
-    if (a.w) leave(1, db);
-    if (channel_gate) leave(2, dg);
-    if (a.pw) leave(3, dp);
 }
 
 // ---- rows of any length: one workgroup a row, read once per use

@@ -56,9 +56,12 @@ enum : int { DT_I8 = 8 };   // signed 8-bit integers (EPI_I8 only), int32 accumu
 // and an up projection side by side and stores act(g) u; EPI_I8 multiplies
 // integer sums by a scale per row of A and a scale per row of B; EPI_ACT adds a bias
 // per column, applies an activation and adds a residual.  EPI_GRAM, EPI_POLY and
-// EPI_STEP are the three products of a Newton-Schulz step (ortho.hip).
+// EPI_STEP are the three products of a Newton-Schulz step, EPI_LAST the last step's
+// (ortho.hip); the first two are symmetric, so that only the tiles on and below the
+// diagonal are contracted, and stored a second time transposed.
 enum : int {
-    EPI_RELU = 0, EPI_CAST = 1, EPI_GATED = 2, EPI_I8 = 3, EPI_ACT = 4, EPI_GRAM = 5, EPI_POLY = 6, EPI_STEP = 7
+    EPI_RELU = 0, EPI_CAST = 1, EPI_GATED = 2, EPI_I8 = 3, EPI_ACT = 4, EPI_GRAM = 5, EPI_POLY = 6, EPI_STEP = 7,
+    EPI_LAST = 8
 };
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
@@ -126,12 +129,14 @@ struct KernelArgs {
     // Newton-Schulz products: alpha scales what C holds, beta the sums and scale_o what R
     // holds to their true values.  EPI_GRAM writes the diagonal to diag and 0 in its place; EPI_POLY reads
     // that and its operand R (ldr apart), and writes its own diagonal to diag_out;
-    // EPI_STEP reads diag and updates X (M rows of N, in place).  pa, pb, pc: the
-    // step's coefficients.
+    // EPI_STEP reads diag and updates X (M rows of N, in place).  EPI_LAST reads diag and X
+    // and leaves its result in C, out_m rows of out_n (or transposed) of bfloat16.  pa, pb,
+    // pc: the step's coefficients.
     float beta, scale_o, pa, pb, pc;
     float* diag;
     float* diag_out;
     float* X;
+    int out_m, out_n, transposed;
 };
 
 // The tiles one configuration covers inside a launch: a grid of tiles_m x
@@ -677,6 +682,34 @@ __device__ __forceinline__ void tile_coords(int wg, int tiles_m, int tiles_n, in
     tn = within / rows;
 }
 
+// The same for the tiles on and below the diagonal of `tiles` x `tiles` ones: panels of
+// `panel` tile rows, each column by column up to its triangle, which goes row by row.
+__device__ __forceinline__ void triangle_coords(int wg, int tiles, int panel, int nxcd, int& tm, int& tn)
+{
+    const int total = tiles * (tiles + 1) / 2;
+    const int per = total / nxcd, rem = total % nxcd;
+    const int xcd = wg % nxcd, local = wg / nxcd;
+    const int logical = xcd < rem ? xcd * (per + 1) + local
+                                  : rem * (per + 1) + (xcd - rem) * per + local;
+    // the largest r with r (r + 1) / 2 <= l
+    auto row_of = [](int l) {
+        int r = (int)((sqrtf(8.0f * (float)l + 1.0f) - 1.0f) * 0.5f);
+        while (r * (r + 1) / 2 > l) --r;
+        while ((r + 1) * (r + 2) / 2 <= l) ++r;
+        return r;
+    };
+    const int first = row_of(logical) / panel * panel, rows = min(panel, tiles - first);
+    const int within = logical - first * (first + 1) / 2;
+    if (within < first * rows) {
+        tm = first + within % rows;
+        tn = within / rows;
+    } else {
+        const int rest = within - first * rows, r = row_of(rest);
+        tm = first + r;
+        tn = first + rest - r * (r + 1) / 2;
+    }
+}
+
 // One stream-K piece: the K steps [kt0, kt1) (of ceil(K / BK)) of a tile that
 // count pieces share.  Pieces are numbered in K order; piece p > 0 is the first
 // piece of unit first + p and keeps its partial in that unit's slot 2 (first +
@@ -727,7 +760,11 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
 
     int tm, tn;
-    tile_coords(wg, reg.tiles_m, reg.tiles_n, reg.panel, args.nxcd, tm, tn);
+    constexpr bool SYMMETRIC = C::EPI == EPI_GRAM || C::EPI == EPI_POLY;
+    if constexpr (SYMMETRIC)
+        triangle_coords(wg, reg.tiles_m, reg.panel, args.nxcd, tm, tn);
+    else
+        tile_coords(wg, reg.tiles_m, reg.tiles_n, reg.panel, args.nxcd, tm, tn);
     const int m0 = tm * BM;
     // (K,N) B on the direct path: the last tile column is moved back to end at N,
     // so every B chunk it copies lies inside its row.  The columns it shares with
@@ -1685,7 +1722,8 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
     // the gate sums (even j) or the up sums (odd j) of MB columns.
     constexpr int OB = OutTraits<C::OUT_DT>::bytes;
     constexpr int BNO = C::GATED ? BN / 2 : BN;       // columns of C in the tile
-    const int NC = C::GATED ? args.hidden : N;        // columns of C
+    const int NC = C::GATED ? args.hidden : C::EPI == EPI_LAST ? args.out_n : N;        // columns of C
+    const int MC = C::EPI == EPI_LAST ? args.out_m : M;                                 // and rows
     const int c0 = C::GATED ? n0 >> 1 : n0, c_own = C::GATED ? c0 : n_own, wc0 = C::GATED ? wn0 >> 1 : wn0;
     constexpr bool STAGED = OB == 2 && BM * BNO * 2 <= C::LDS_BYTES;
     constexpr int RB = BNO * 2, RCH = BNO / 8;        // staged: bytes and chunks per tile row
@@ -1844,7 +1882,7 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
                     }
             return;
         }
-        if constexpr (C::EPI == EPI_POLY || C::EPI == EPI_STEP) {
+        if constexpr (C::EPI == EPI_POLY || C::EPI == EPI_STEP || C::EPI == EPI_LAST) {
             // what a row needs is on its way while the one before is finished (rows and
             // columns past the edge take the last ones; M and N are multiples of 64)
             using In4 = std::conditional_t<C::EPI == EPI_POLY, u32x2_t, f32x4_t>;
@@ -1899,9 +1937,11 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             v[e] = fmaf(args.pa + d, own[b][e], acc[i][b / NQ][4 * (b % NQ) + e] * args.beta);
-                        if (m < M && n >= n_own && n < N)
-                            *reinterpret_cast<f32x4_t*>(args.X + (size_t)m * (size_t)N + n) = v;
-                        v *= args.alpha;
+                        if constexpr (C::EPI == EPI_STEP) {
+                            if (m < M && n >= n_own && n < N)
+                                *reinterpret_cast<f32x4_t*>(args.X + (size_t)m * (size_t)N + n) = v;
+                            v *= args.alpha;
+                        }
                     }
                     put_group(i, b / NQ, b % NQ, v);
                 }
@@ -1975,11 +2015,42 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
     } else {
         put_acc();
     }
+    // the staged tile's columns as rows of C from row c0 on: 4 x 16 blocks are read
+    // transposed, a lane's 8 consecutive rows of the tile are 16 bytes of such a row
+    auto store_transposed = [&](int rows, int cols) {
+        constexpr int RBLOCKS = BM / 32;
+        for (int idx = wave; idx < RBLOCKS * (BN / 16); idx += C::NWAVES) {
+            const int rb = idx % RBLOCKS * 32, cb = idx / RBLOCKS * 16, h = lane >> 4, i16 = lane & 15;
+            i16x4_t part[2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int r = rb + 8 * h + 4 * t + (i16 >> 2), c = cb + 4 * (i16 & 3);
+                part[t] = lds_read_tr16(smem + r * RB + (((c >> 3) ^ (r & XM)) << 4) + (c & 7) * 2);
+            }
+            const int n = c0 + cb + i16, m = m0 + rb + 8 * h;
+            if (n < c_own || n >= rows || m >= cols) continue;
+            unsigned short* dst = reinterpret_cast<unsigned short*>(args.C) + (size_t)n * (size_t)cols + m;
+            if (m + 8 <= cols) {
+                __builtin_memcpy(dst, part, 16);
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (m + e < cols) dst[e] = (unsigned short)part[e >> 2][e & 3];
+            }
+        }
+    };
     if constexpr (STAGED) {
         barrier_lds();
+        if constexpr (C::EPI == EPI_LAST)
+            if (args.transposed) {
+                store_transposed(NC, MC);
+                return;
+            }
+        if constexpr (SYMMETRIC)
+            if (tm != tn) store_transposed(N, M);
         auto store_chunk = [&](int r, int cc) {
             const int m = m0 + r, n = c0 + 8 * cc;
-            if (m >= M || n >= NC || n + 8 <= c_own) return;
+            if (m >= MC || n >= NC || n + 8 <= c_own) return;
             const u32x4_t v = *reinterpret_cast<const GR_LDS u32x4_t*>(
                 smem + r * RB + ((cc ^ (r & XM)) << 4));
             unsigned short* dst = reinterpret_cast<unsigned short*>(args.C) + (size_t)m * NC + n;

@@ -109,13 +109,15 @@ int64_t tiles_of(int cfg, const Linear& l)
 {
     return ceil_div(l.M, linear_info(cfg).bm) * ceil_div(l.N, linear_info(cfg).bn);
 }
-double linear_time(int cfg, const Linear& l, int64_t batch = 1)
+double tiles_time(int cfg, const Linear& l, int64_t tiles)
 {
     const TileTime t = tile_time(cfg);
     const double one = t.per_byte * double(l.K) * l.bytes + t.fixed;
-    const int64_t tiles = tiles_of(cfg, l) * batch, rest = tiles % t.slots;
+    const int64_t rest = tiles % t.slots;
     return one * double(tiles / t.slots) + (rest == 0 ? 0.0 : rest <= kNumCUs ? t.alone * one : one);
 }
+
+double linear_time(int cfg, const Linear& l) { return tiles_time(cfg, l, tiles_of(cfg, l)); }
 
 // Whether a configuration can take a product: the tiles' copies have 32-bit
 // offsets (256 rows of A, or of B stored (N,K), or a K step's rows of B stored

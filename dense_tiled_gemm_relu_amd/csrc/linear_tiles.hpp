@@ -33,7 +33,7 @@ template <class C> hipError_t launch(const KernelArgs& args, int grid, hipStream
 // here.
 template <int IN, int OUT, int EPI, int cfg> struct LinearCfg;
 template <int IN, int BK16> constexpr int bk = IN == DT_I8 ? 2 * BK16 : BK16;
-template <int EPI> constexpr bool nt = EPI != EPI_CAST && EPI != EPI_STEP;
+template <int EPI> constexpr bool nt = EPI != EPI_CAST && EPI != EPI_STEP && EPI != EPI_LAST;
 template <int EPI> constexpr int mb = nt<EPI> ? 16 : 32;
 
 template <int IN, int OUT, int EPI> struct LinearCfg<IN, OUT, EPI, LIN_256> {

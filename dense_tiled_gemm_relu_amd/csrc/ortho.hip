@@ -20,24 +20,46 @@ namespace {
 
 // ------------------------------------------------------- before the steps
 // Sums of squares in binary64 (the values may be any fp32 ones): kOrthoParts workgroups
-// a matrix take rows in turns.
-template <class T> __global__ void __launch_bounds__(kThreads) ortho_squares_kernel(OrthoArgs a)
+// a matrix take rows in turns, 16 bytes a thread.
+constexpr int kSquareThreads = 1024;
+template <class T> __global__ void __launch_bounds__(kSquareThreads) ortho_squares_kernel(OrthoArgs a)
 {
-    __shared__ double part[kThreads / 64];
+    constexpr int N = Chunk<T>::N;
+    using X = typename Chunk<T>::Vec;
+    __shared__ double part[kSquareThreads / 64];
     const T* g = static_cast<const T*>(a.g) + (size_t)blockIdx.y * (size_t)a.g_batch;
     double s = 0.0;
-    for (int64_t r = blockIdx.x; r < a.rows; r += kOrthoParts)
-        for (int64_t j = threadIdx.x; j < a.cols; j += kThreads) {
-            const double v = (double)(float)g[(size_t)r * (size_t)a.g_stride + j];
-            s = fma(v, v, s);
+    const auto add = [&](float v) { s = fma((double)v, (double)v, s); };
+    // short rows: several at a time
+    const int chunks = a.cols / N, wide = min(kSquareThreads, (chunks + 1 + 63) / 64 * 64), rows_here = kSquareThreads / wide;
+    const int t = (int)threadIdx.x % wide, own = (int)threadIdx.x / wide;
+    for (int64_t r = (int64_t)blockIdx.x * rows_here + own; own < rows_here && r < a.rows; r += kOrthoParts * rows_here) {
+        const T* row = g + (size_t)r * (size_t)a.g_stride;
+        constexpr int AHEAD = 4;
+        int j = t;
+        for (; j + (AHEAD - 1) * wide < chunks; j += AHEAD * wide) {
+            X v[AHEAD];
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u) v[u] = load_vec<X>(row + (size_t)(j + u * wide) * N);
+#pragma unroll
+            for (int u = 0; u < AHEAD; ++u)
+#pragma unroll
+                for (int e = 0; e < N; ++e) add((float)v[u][e]);
         }
+        for (; j < chunks; j += wide) {
+            const X v = load_vec<X>(row + (size_t)j * N);
+#pragma unroll
+            for (int e = 0; e < N; ++e) add((float)v[e]);
+        }
+        if (t < a.cols - chunks * N) add((float)row[(size_t)chunks * N + t]);
+    }
 #pragma unroll
     for (int step = 1; step < 64; step *= 2) s += __shfl_xor(s, step);
     if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = s;
     __syncthreads();
     if (threadIdx.x == 0) {
 #pragma unroll
-        for (int k = 1; k < kThreads / 64; ++k) s += part[k];
+        for (int k = 1; k < kSquareThreads / 64; ++k) s += part[k];
         a.squares[(size_t)blockIdx.y * kOrthoParts + blockIdx.x] = s;
     }
 }
@@ -49,8 +71,9 @@ template <class T> __global__ void __launch_bounds__(kThreads) ortho_start_kerne
     __shared__ float tile[64][65];
     const size_t batch = blockIdx.y;
     const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
-    double s = a.squares[batch * kOrthoParts + lane];
-    static_assert(kOrthoParts == 64, "one part a lane");
+    double s = 0.0;
+#pragma unroll
+    for (int k = 0; k < kOrthoParts; k += 64) s += a.squares[batch * kOrthoParts + k + lane];
 #pragma unroll
     for (int step = 1; step < 64; step *= 2) s += __shfl_xor(s, step);
     const double scale = 1.0 / (sqrt(s) + (double)a.eps);
@@ -78,8 +101,8 @@ template <class T> __global__ void __launch_bounds__(kThreads) ortho_start_kerne
     for (int k = wave; k < 64; k += kThreads / 64) put(p0 + k, q0 + lane, tile[lane][k]);
 }
 
-// ------------------------------------------------------------- afterwards
-__global__ void __launch_bounds__(kThreads) ortho_end_kernel(OrthoArgs a)
+// ------------------------------------------------------- without any step
+__global__ void __launch_bounds__(kThreads) ortho_copy_kernel(OrthoArgs a)
 {
     __shared__ float tile[64][65];
     const size_t batch = blockIdx.y;
@@ -126,11 +149,12 @@ template <class C> hipError_t launch_product(const OrthoProduct& p, int tiles, i
 }
 template <int EPI> OrthoLaunchFn pick_product(int cfg)
 {
+    constexpr int OUT = EPI == EPI_LAST ? DT_BF16 : DT_F16;
     switch (cfg) {
-    case LIN_256: return &launch_product<typename LinearCfg<DT_F16, DT_F16, EPI, LIN_256>::type>;
-    case LIN_128: return &launch_product<typename LinearCfg<DT_F16, DT_F16, EPI, LIN_128>::type>;
-    case LIN_128X2: return &launch_product<typename LinearCfg<DT_F16, DT_F16, EPI, LIN_128X2>::type>;
-    case LIN_64: return &launch_product<typename LinearCfg<DT_F16, DT_F16, EPI, LIN_64>::type>;
+    case LIN_256: return &launch_product<typename LinearCfg<DT_F16, OUT, EPI, LIN_256>::type>;
+    case LIN_128: return &launch_product<typename LinearCfg<DT_F16, OUT, EPI, LIN_128>::type>;
+    case LIN_128X2: return &launch_product<typename LinearCfg<DT_F16, OUT, EPI, LIN_128X2>::type>;
+    case LIN_64: return &launch_product<typename LinearCfg<DT_F16, OUT, EPI, LIN_64>::type>;
     default: return nullptr;
     }
 }
@@ -143,6 +167,7 @@ OrthoLaunchFn launcher_ortho(int epi, int cfg)
     case EPI_GRAM: return pick_product<EPI_GRAM>(cfg);
     case EPI_POLY: return pick_product<EPI_POLY>(cfg);
     case EPI_STEP: return pick_product<EPI_STEP>(cfg);
+    case EPI_LAST: return pick_product<EPI_LAST>(cfg);
     default: return nullptr;
     }
 }
@@ -151,15 +176,15 @@ hipError_t launch_ortho_start(const OrthoArgs& a, int dt, hipStream_t stream)
 {
     return with_types(dt, dt, [&](auto x, auto) {
         using T = decltype(x);
-        const hipError_t e = start(&ortho_squares_kernel<T>, dim3(kOrthoParts, a.batch), kThreads, stream, a);
+        const hipError_t e = start(&ortho_squares_kernel<T>, dim3(kOrthoParts, a.batch), kSquareThreads, stream, a);
         if (e != hipSuccess) return e;
         return start(&ortho_start_kernel<T>, dim3((unsigned)(a.P / 64) * (unsigned)(a.Q / 64), a.batch), kThreads, stream, a);
     });
 }
 
-hipError_t launch_ortho_end(const OrthoArgs& a, hipStream_t stream)
+hipError_t launch_ortho_copy(const OrthoArgs& a, hipStream_t stream)
 {
-    return start(&ortho_end_kernel, dim3((unsigned)(a.P / 64) * (unsigned)(a.Q / 64), a.batch), kThreads, stream, a);
+    return start(&ortho_copy_kernel, dim3((unsigned)(a.P / 64) * (unsigned)(a.Q / 64), a.batch), kThreads, stream, a);
 }
 
 }  // namespace gemm_relu_hip

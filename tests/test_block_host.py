@@ -99,8 +99,8 @@ def test_workspaces_and_plans():
     assert lib.gemm_relu_orthogonalize_workspace(0, 5, 5) == 0
     assert lib.gemm_relu_orthogonalize_workspace(1, 64, 64) >= 64 * 64 * 12
     assert lib.gemm_relu_orthogonalize_workspace(1, -1, 64) == gr.EINVAL
-    assert lib.gemm_relu_orthogonalize_workspace(65535, 2 ** 16, 2 ** 22) >= 65535 * 2 ** 41            # grows without wrapping
-    for sizes in ((1, 2 ** 16 + 1, 2 ** 17), (1, 4, 2 ** 22 + 1), (65536, 4, 4)):
+    assert lib.gemm_relu_orthogonalize_workspace(65535, 2 ** 14, 2 ** 20) >= 65535 * 2 ** 37            # grows without wrapping
+    for sizes in ((1, 2 ** 16 + 1, 2 ** 17), (1, 4, 2 ** 22 + 1), (1, 2 ** 15, 2 ** 20), (65536, 4, 4)):
         assert lib.gemm_relu_orthogonalize_workspace(*sizes) == gr.EUNSUPPORTED
 
 
