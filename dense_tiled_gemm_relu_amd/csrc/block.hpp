@@ -76,8 +76,8 @@ struct OrthoArgs {
     int p, q, P, Q;             // q: the longer side
     float eps;
     double* squares;            // kOrthoParts sums of squares a matrix
-    float* x;                   // batch x P x Q
-    void* xh;                   // float16: batch x P x Q
+    void* xh;                   // X times kOrthoX as float16: batch x P x Q
+    void* xl;                   // and kLowScale times what that loses
 };
 constexpr int kOrthoParts = 256;
 hipError_t launch_ortho_start(const OrthoArgs& a, int dt, hipStream_t stream);
@@ -85,8 +85,8 @@ hipError_t launch_ortho_copy(const OrthoArgs& a, hipStream_t stream);      // no
 // one of the products for every matrix of the batch
 struct OrthoProduct {
     KernelArgs k;
-    uint64_t a, b, c, r;        // bytes from one matrix's A, B, C, R to the next's
-    uint64_t diag, x;           // floats from one matrix's diagonals, or X, to the next's
+    uint64_t a, b, c, r;        // bytes from one matrix's A, B, C, R and L to the next's
+    uint64_t diag;              // floats from one matrix's diagonals to the next's
 };
 typedef hipError_t (*OrthoLaunchFn)(const OrthoProduct& p, int tiles, int batch, hipStream_t stream);
 OrthoLaunchFn launcher_ortho(int epi, int cfg);

@@ -32,7 +32,7 @@ extern "C" int gemm_relu_act(const void* x, int64_t x_stride, const void* weight
     const Mat m[] = {dense(y, rows, n, 2), dense(z, z ? rows : 0, n, 4), {x, rows, k, x_stride, 2},
                      {weight, n, k, weight_stride, 2}, dense(bias, bias ? 1 : 0, n, elem_bytes(bias_dtype)), r};
     if (!mats_ok(m, 2)) return GEMM_RELU_EINVAL;
-    const RowsPlan p = plan_rows(Linear{rows, n, k, x_stride, weight_stride, true});
+    const RowsPlan p = plan_rows(Linear{rows, n, k, x_stride, weight_stride, true}, true);
     if (k > kMaxK || p.p.grid() > kMaxGrid) return GEMM_RELU_EUNSUPPORTED;
     if (const int dev = check_device()) return dev;
     hipStream_t st = static_cast<hipStream_t>(stream);
@@ -57,7 +57,7 @@ extern "C" const char* gemm_relu_act_plan(int64_t rows, int64_t n, int64_t k, in
     if (!act_sizes_ok(rows, n, k, dtype)) return nullptr;
     if (rows == 0 || n == 0) return "none";
     if (k > kMaxK) return "unsupported";
-    return rows_plan_name(plan_rows(Linear{rows, n, k, k, k, true}));
+    return rows_plan_name(plan_rows(Linear{rows, n, k, k, k, true}, true));
 }
 
 // the products' plan, behind whose workspace the sums of dz over each 64 rows lie
@@ -297,7 +297,7 @@ constexpr int kOrthoSteps = 64;
 struct OrthoPlan {
     int64_t p, q, P, Q;
     int gram, poly, step;                       // configurations of the products
-    uint64_t squares, x, xh[2], a, b, diag_a, diag_b, bytes;
+    uint64_t squares, xl, xh[2], a, b, diag_a, diag_b, bytes;
 };
 // tiles of one product: of a symmetric one those on and below the diagonal
 int64_t ortho_tiles(int cfg, const Linear& l, bool symmetric)
@@ -332,7 +332,7 @@ OrthoPlan plan_ortho(int64_t batch, int64_t rows, int64_t cols)
     };
     const uint64_t PQ = uint64_t(o.P) * uint64_t(o.Q) * uint64_t(batch), PP = uint64_t(o.P) * uint64_t(o.P) * uint64_t(batch);
     o.squares = take(uint64_t(batch) * kOrthoParts * 8);
-    o.x = take(PQ * 4);
+    o.xl = take(PQ * 2);
     o.xh[0] = take(PQ * 2);
     o.xh[1] = take(PQ * 2);
     o.a = take(PP * 2);
@@ -398,8 +398,8 @@ extern "C" int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t 
     a.Q = int(o.Q);
     a.eps = eps;
     a.squares = reinterpret_cast<double*>(ws + o.squares);
-    a.x = reinterpret_cast<float*>(ws + o.x);
     a.xh = ws + o.xh[0];
+    a.xl = ws + o.xl;
     hipError_t err = launch_ortho_start(a, dtype, st);
     const uint64_t PQ = uint64_t(o.P) * uint64_t(o.Q), PP = uint64_t(o.P) * uint64_t(o.P);
     const Linear gram{o.P, o.P, o.Q, o.Q, o.Q, true}, poly{o.P, o.P, o.P, o.P, o.P, true}, next{o.P, o.Q, o.P, o.P, o.Q, false};
@@ -438,18 +438,20 @@ extern "C" int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t 
         err = launch(EPI_POLY, o.poly, poly, k);
         if (err != hipSuccess) break;
         k = product(o.step, next, ws + o.b, xh, last ? out : ws + o.xh[(s + 1) % 2]);
-        k.k.alpha = kOrthoX;
-        k.k.beta = 1.0f / (kOrthoB * kOrthoX);
+        k.k.alpha = 1.0f / kOrthoX;             // of the last step's result
+        k.k.beta = 1.0f / kOrthoB;
         k.k.pa = coefficients[3 * s];
         k.k.diag = reinterpret_cast<float*>(ws + o.diag_b);
-        k.k.X = a.x;
+        k.k.R = static_cast<const unsigned char*>(xh);
+        k.k.L = ws + o.xl;
+        k.k.ldr = int(o.Q);
         k.k.out_m = int(o.p);
         k.k.out_n = int(o.q);
         k.k.transposed = rows > cols;
         k.a = PP * 2;
         k.b = PQ * 2;
         k.c = last ? uint64_t(rows) * uint64_t(cols) * 2 : PQ * 2;
-        k.x = PQ;
+        k.r = PQ * 2;
         err = launch(last ? EPI_LAST : EPI_STEP, o.step, next, k);
     }
     if (err == hipSuccess && steps == 0) err = launch_ortho_copy(a, st);

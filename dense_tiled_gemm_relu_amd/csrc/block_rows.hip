@@ -98,7 +98,7 @@ template <int DT, int ACT> __global__ void __launch_bounds__(kActGradThreads) ac
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             float value, slope;
-            activation_slope<ACT>(z[k][e], value, slope);
+            activation_slope<ACT, true>(z[k][e], value, slope);
             const float g = (float)d[k][e] * slope;
             column[e] += g;
             dz[k][e] = (T)(g * a.scale);
@@ -153,14 +153,19 @@ typedef float Stats __attribute__((ext_vector_type(4), aligned(4)));       // a 
 
 // One read of x and the residual, one write of s and y: the row stays in registers
 // between its sums; the next row is loaded meanwhile, and what is the same for all rows
-// stays in registers.  Bound by HBM.
-template <class T, class W, int G, int V> __global__ void __launch_bounds__(kGroupThreads<G>) add_norm_kernel(AddNormArgs a)
+// stays in registers.  One wave a row and four rows a workgroup, or `waves` waves a row:
+// one chunk a thread (two where 16 waves would not hold the row), since four vectors of
+// fp32 weights beside two chunks leave a CU three waves a SIMD (4097 x 3001 fp16, norms on
+// both sides, 28 us so).  Bound by HBM.
+template <class T, class W, bool ONE, int V>
+__global__ void __launch_bounds__(ONE ? kThreads : 1024) add_norm_kernel(AddNormArgs a, int waves)
 {
     constexpr int N = Chunk<T>::N;
     using X = typename Chunk<T>::Vec;
     using WV = typename VecN<W, N>::Vec;
-    __shared__ float lds[2][4][G / 64];
-    const RowMap<T, V> map(a.cols, (int)threadIdx.x % G, G);
+    __shared__ float lds[2][4][16];
+    const int lane = (int)(threadIdx.x & 63), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+    const RowMap<T, V> map(a.cols, ONE ? lane : (int)threadIdx.x, ONE ? 64 : 64 * waves);
     const bool element_gate = a.gate && a.gate_stride, channel_gate = a.gate && !a.gate_stride;
     WV w[V], b[V], pw[V], gate[V];
 #pragma unroll
@@ -173,8 +178,9 @@ template <class T, class W, int G, int V> __global__ void __launch_bounds__(kGro
             if (channel_gate) gate[v] = load_vec<WV>(static_cast<const W*>(a.gate) + map.start[v]);
         }
     }
-    const int step = (int)gridDim.x * kGroups<G>;
-    int64_t row = group_index<G>();          // 64 bits: the last row's successor may pass 2^31
+    constexpr int ROWS = ONE ? kThreads / 64 : 1;
+    const int step = (int)gridDim.x * ROWS;
+    int64_t row = (int64_t)blockIdx.x * ROWS + (ONE ? wave : 0);          // 64 bits: the last row's successor may pass 2^31
     X nx[V], nr[V], ng[V];
     auto fetch = [&](int64_t at) {
         const T* x = static_cast<const T*>(a.x) + (size_t)at * (size_t)a.x_stride;
@@ -192,8 +198,20 @@ template <class T, class W, int G, int V> __global__ void __launch_bounds__(kGro
     for (int v = 0; v < V; ++v) nx[v] = nr[v] = ng[v] = X{};
     if (row < a.rows) fetch(row);
     const float n = (float)a.cols;
+    // the sum over the row; the waves alternate between buffers, so that whoever writes one
+    // again has passed the barrier of another, behind every read
+    auto row_sum = [&](float v, float(&buffer)[16]) {
+        v = wave_all<Sum>(v);
+        if constexpr (!ONE) {
+            if (lane == 0) buffer[wave] = v;
+            __syncthreads();
+            const int k = lane & 15;
+            v = row16_sum(k < waves ? buffer[k] : 0.0f);
+        }
+        return v;
+    };
     // mean (0 for the root mean square) and 1 / deviation of f
-    auto statistics = [&](const float(&f)[V][N], float(&buffers)[4][G / 64], int first, float& mean, float& rstd) {
+    auto statistics = [&](const float(&f)[V][N], float(&buffers)[4][16], int first, float& mean, float& rstd) {
         float sum = 0.0f;
         mean = 0.0f;
         if (a.layer) {
@@ -201,7 +219,7 @@ template <class T, class W, int G, int V> __global__ void __launch_bounds__(kGro
             for (int v = 0; v < V; ++v)
 #pragma unroll
                 for (int e = 0; e < N; ++e) sum += map.owns(v, e) ? f[v][e] : 0.0f;
-            mean = group_all<G, Sum>(sum, buffers[first]) / n;
+            mean = row_sum(sum, buffers[first]) / n;
             sum = 0.0f;
         }
 #pragma unroll
@@ -211,7 +229,7 @@ template <class T, class W, int G, int V> __global__ void __launch_bounds__(kGro
                 const float d = map.owns(v, e) ? f[v][e] - mean : 0.0f;
                 sum += d * d;
             }
-        rstd = 1.0f / sqrtf(group_all<G, Sum>(sum, buffers[first + 1]) / n + a.eps);
+        rstd = 1.0f / sqrtf(row_sum(sum, buffers[first + 1]) / n + a.eps);
     };
     for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
         float f[V][N];
@@ -272,7 +290,7 @@ template <class T, class W, int G, int V> __global__ void __launch_bounds__(kGro
                     __builtin_memcpy(y + map.start[v], &out, sizeof out);
                 }
         }
-        if (a.stats && threadIdx.x % G == 0) *reinterpret_cast<Stats*>(a.stats + 4 * (size_t)row) = stats;
+        if (a.stats && (ONE ? lane : (int)threadIdx.x) == 0) *reinterpret_cast<Stats*>(a.stats + 4 * (size_t)row) = stats;
     }
 }
 
@@ -677,26 +695,6 @@ __global__ void __launch_bounds__(kThreads) add_norm_strip_any_kernel(AddNormArg
     p[3 * (size_t)a.cols] = dp;
 }
 
-// Threads that share a row and 16-byte chunks of it each, as row_shape, with at most two
-// chunks a thread: four vectors of weights stay in registers beside the row.
-RowShape add_norm_shape(int cols, int bytes)
-{
-    const int chunks = row_chunks(cols, bytes);
-    for (int g = 64; chunks > 0 && g <= 1024; g *= 2) {
-        const int v = (int)ceil_div(chunks, g);
-        if (v <= 2) return {g, v};
-    }
-    return {0, 0};
-}
-template <class F> hipError_t with_add_norm_shape(RowShape s, F&& f)
-{
-#define GR_SHAPE(G, V) \
-    if (s.g == G && s.v == V) return f(std::integral_constant<int, G>{}, std::integral_constant<int, V>{});
-    GR_SHAPE(64, 1) GR_SHAPE(64, 2) GR_SHAPE(128, 2) GR_SHAPE(256, 2) GR_SHAPE(512, 2) GR_SHAPE(1024, 2)
-#undef GR_SHAPE
-    return hipErrorInvalidValue;
-}
-
 }  // namespace
 
 hipError_t launch_join(const JoinArgs& a, int out_dt, hipStream_t stream)
@@ -728,18 +726,21 @@ hipError_t launch_act_grad(const ActGradArgs& a, int dt, hipStream_t stream)
 
 hipError_t launch_add_norm(const AddNormArgs& a, int dt, int wdt, hipStream_t stream)
 {
-    const RowShape s = add_norm_shape(a.cols, elem_size(dt));
     return with_types(dt, wdt, [&](auto x, auto w) {
         using T = decltype(x);
         using W = decltype(w);
-        if (!s.g)
+        const int chunks = row_chunks(a.cols, sizeof(T)), waves = (int)ceil_div(chunks, 64);
+        if (chunks == 0 || waves > 32)
             return start(a.cols <= kThreads ? &add_norm_any_kernel<T, W, true> : &add_norm_any_kernel<T, W, false>,
                          dim3(any_grid(a.rows)), kThreads, stream, a);
-        return with_add_norm_shape(s, [&](auto g, auto v) {
-            constexpr int G = decltype(g)::value;
-            const int grid = even_grid(a.rows, kGroups<G>, row_groups(a.rows, a.cols, sizeof(T), kGroupThreads<G>));
-            return start(&add_norm_kernel<T, W, G, decltype(v)::value>, dim3(grid), kGroupThreads<G>, stream, a);
-        });
+        const auto go = [&](auto kernel, int rows_here, int row_waves) {
+            const int threads = 64 * rows_here * row_waves;
+            const int grid = even_grid(a.rows, rows_here, row_groups(a.rows, a.cols, sizeof(T), threads));
+            return start(kernel, dim3(grid), threads, stream, a, row_waves);
+        };
+        return waves == 1    ? go(&add_norm_kernel<T, W, true, 1>, kThreads / 64, 1)
+               : waves <= 16 ? go(&add_norm_kernel<T, W, false, 1>, 1, waves)
+                             : go(&add_norm_kernel<T, W, false, 2>, 1, (waves + 1) / 2);
     });
 }
 

@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kThreads) skinny_kernel(KernelArgs a)
                 r = load_half4(reinterpret_cast<const unsigned short*>(a.R) + (size_t)min(m, a.M - 1) * (size_t)a.ldr, c, cols);
             with_activation_or_none(a.act, [&](auto kind) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = activation<decltype(kind)::value>(z[e]);
+                for (int e = 0; e < 4; ++e) v[e] = activation<decltype(kind)::value, true>(z[e]);
             });
             if (a.R) v += to_float4<IN>(r);
         } else {
@@ -231,6 +231,9 @@ template <int IN, int OUT, int EPI> LinearLaunchFn pick(int cfg)
     case LIN_K32: return &launch<IN, OUT, EPI, 2, 2, 128, 4>;
     case LIN_K32X48: return &launch<IN, OUT, EPI, 2, 3, 128, 3>;
     case LIN_K48X32: return &launch<IN, OUT, EPI, 3, 2, 128, 3>;
+    case LIN_K64X32:
+        if constexpr (EPI == EPI_ACT) return &launch<IN, OUT, EPI, 4, 2, 128, 3>;
+        return nullptr;
     default: return nullptr;
     }
 }

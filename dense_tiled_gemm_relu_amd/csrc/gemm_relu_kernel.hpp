@@ -126,16 +126,16 @@ struct KernelArgs {
     int bias_f32;             // the bias is fp32, else of A's type
     int ldr;
     const unsigned char* R;
-    // Newton-Schulz products: alpha scales what C holds, beta the sums and scale_o what R
-    // holds to their true values.  EPI_GRAM writes the diagonal to diag and 0 in its place; EPI_POLY reads
+    // Newton-Schulz products: beta scales the sums, scale_o what R holds, alpha what C
+    // receives.  EPI_GRAM writes the diagonal to diag and 0 in its place; EPI_POLY reads
     // that and its operand R (ldr apart), and writes its own diagonal to diag_out;
-    // EPI_STEP reads diag and updates X (M rows of N, in place).  EPI_LAST reads diag and X
-    // and leaves its result in C, out_m rows of out_n (or transposed) of bfloat16.  pa, pb,
-    // pc: the step's coefficients.
+    // EPI_STEP reads diag and X as R + L / kLowScale (ldr apart), and writes the new X to C
+    // and L.  EPI_LAST reads the same and leaves its result in C, out_m rows of out_n (or
+    // transposed) of bfloat16.  pa, pb, pc: the step's coefficients.
     float beta, scale_o, pa, pb, pc;
     float* diag;
     float* diag_out;
-    float* X;
+    unsigned char* L;
     int out_m, out_n, transposed;
 };
 
@@ -362,11 +362,27 @@ __device__ __forceinline__ float logistic(float z)
     return z < 0.0f ? t * r : r;
 }
 __device__ __forceinline__ float normal_cdf(float z) { return 0.5f * erfcf(z * -0.70710678118654752440f); }
+// The same in a quarter of erfcf's instructions, for the product with bias, activation
+// and residual: erfc(a) = t exp(-a^2 + p(t)), t = 1 / (1 + a / 2), with the polynomial of
+// Press et al., Numerical Recipes, whose relative error is below 1.2e-7 everywhere; the
+// exponential as in logistic.  (1027 x 2003 x 1501 fp16 with everything in the epilogue
+// 31.1 us with erfcf, 27.5 with this; the gated projections keep their bits.)
+__device__ __forceinline__ float normal_cdf_short(float z)
+{
+    const float a = fabsf(z) * 0.70710678118654752440f, t = __builtin_amdgcn_rcpf(fmaf(0.5f, a, 1.0f));
+    constexpr float c[] = {0.17087277f, -0.82215223f, 1.48851587f, -1.13520398f, 0.27886807f,
+                           -0.18628806f, 0.09678418f, 0.37409196f, 1.00002368f, -1.26551223f};
+    float p = c[0];
+#pragma unroll
+    for (int k = 1; k < 10; ++k) p = fmaf(p, t, c[k]);
+    const float e = __expf(0.5f * fmaf(-a, a, p)), tail = 0.5f * t * e * e;
+    return z < 0.0f ? tail : 1.0f - tail;
+}
 constexpr float kTwoGeluC = 1.5957691216057307f;     // 2 sqrt(2 / pi)
-template <int ACT> __device__ __forceinline__ float activation(float g)
+template <int ACT, bool SHORT = false> __device__ __forceinline__ float activation(float g)
 {
     if constexpr (ACT == ACT_SILU) return g * logistic(g);
-    if constexpr (ACT == ACT_GELU) return g * normal_cdf(g);
+    if constexpr (ACT == ACT_GELU) return g * (SHORT ? normal_cdf_short(g) : normal_cdf(g));
     // 0.5 (1 + tanh z) = 1 / (1 + e^-2z)
     if constexpr (ACT == ACT_GELU_TANH) return g * logistic(kTwoGeluC * (g + 0.044715f * g * g * g));
     if constexpr (ACT == ACT_NONE) return g;
@@ -393,14 +409,14 @@ template <class F> __device__ __forceinline__ void with_activation_or_none(int a
         with_activation(act, f);
 }
 // value and slope of the activation at g
-template <int ACT> __device__ __forceinline__ void activation_slope(float g, float& value, float& slope)
+template <int ACT, bool SHORT = false> __device__ __forceinline__ void activation_slope(float g, float& value, float& slope)
 {
     if constexpr (ACT == ACT_SILU) {
         const float s = logistic(g);
         value = g * s;
         slope = s * (1.0f + g * (1.0f - s));
     } else if constexpr (ACT == ACT_GELU) {
-        const float p = normal_cdf(g);
+        const float p = SHORT ? normal_cdf_short(g) : normal_cdf(g);
         value = g * p;
         slope = p + g * 0.39894228040143267794f * __expf(-0.5f * g * g);      // 1 / sqrt(2 pi)
     } else if constexpr (ACT == ACT_GELU_TANH) {
@@ -427,6 +443,9 @@ __device__ __forceinline__ u32x4_t clear_front(u32x4_t v, int zeros)
     }
     return v;
 }
+
+// What a float16 x loses of a value v is kept as a second float16, kLowScale (v - x).
+constexpr float kLowScale = 2048.0f;
 
 // Four consecutive fp32 values of a row whose columns n .. end at N.
 __device__ __forceinline__ void store_sums(float* dst, const f32x4_t& v, int n, int N)
@@ -1025,6 +1044,44 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
 
     using Acc = typename In::Acc;
     constexpr int NACC = In::NACC;
+    // Newton-Schulz products: what the epilogue needs of the lane's elements, 4 columns a
+    // group (rows and columns past the edge take the last ones'; M and N are multiples of
+    // 64).  All of it is loaded before the main loop where registers allow (not where two
+    // workgroups share a CU): the loop of a small product is as short as the loads' way.
+    constexpr bool NS = C::EPI == EPI_POLY || C::EPI == EPI_STEP || C::EPI == EPI_LAST;
+    constexpr bool NS_EARLY = NS && BM * BN < 256 * 256 && (BM * BN < 128 * 128 || C::LDS_BYTES > 80 * 1024);
+    constexpr int NS_GROUPS = NS ? TN * NACC / 4 : 1;
+    struct NsRow {
+        float d;
+        u32x2_t hi[NS_GROUPS], lo[C::EPI == EPI_POLY ? 1 : NS_GROUPS];
+    };
+    constexpr int NS_AHEAD = 2;            // rows on their way otherwise
+    NsRow ns_rows[NS_EARLY ? TM : NS_AHEAD];
+    f32x4_t ns_columns[NS_GROUPS];
+    auto ns_col = [&](int b) { return n0 + wn0 + MB * (b / (NACC / 4)) + 4 * NG * (b % (NACC / 4)) + 4 * g; };
+    auto ns_fetch = [&](int i) {
+        const int m = min(m0 + wm0 + MB * i + lr, M - 1);
+        NsRow& row = ns_rows[NS_EARLY ? i : i % NS_AHEAD];
+        row.d = args.diag[m];
+#pragma unroll
+        for (int b = 0; b < NS_GROUPS; ++b) {
+            const size_t at = ((size_t)m * (size_t)args.ldr + min(ns_col(b), N - 4)) * 2;
+            row.hi[b] = *reinterpret_cast<const u32x2_t*>(args.R + at);
+            if constexpr (C::EPI != EPI_POLY) row.lo[b] = *reinterpret_cast<const u32x2_t*>(args.L + at);
+        }
+    };
+    auto ns_fetch_columns = [&] {
+        if constexpr (C::EPI == EPI_POLY) {
+#pragma unroll
+            for (int b = 0; b < NS_GROUPS; ++b)
+                ns_columns[b] = *reinterpret_cast<const f32x4_t*>(args.diag + min(ns_col(b), N - 4));
+        }
+    };
+    if constexpr (NS_EARLY) {
+#pragma unroll
+        for (int i = 0; i < TM; ++i) ns_fetch(i);
+    }
+
     Acc acc[TM][TN];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
@@ -1818,29 +1875,30 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
             for (int j = 0; j < TN; ++j)
 #pragma unroll
                 for (int q = 0; q < NQ; ++q) bias[j * NQ + q] = load_bias<C::IN_DT>(args, col(j, q), N);
-            // the next row's residual is on its way while a row is finished: no load
-            // stands behind a branch of its own (rows past the edge take the last one's)
-            u32x2_t next[TN * NQ] = {};
+            // all of the residual's loads are in flight before the first of z's stores: one
+            // that stood behind them would wait for them (256 x 256, 4096 x 4096 x 7168
+            // bf16 with both, row by row: 250 us).  No load has a branch of its own; rows
+            // past the edge take the last one's.
+            u32x2_t residual[TM][TN * NQ] = {};
             auto fetch = [&](int i) {
                 const unsigned short* row = reinterpret_cast<const unsigned short*>(args.R) +
                                             (size_t)min(m0 + wm0 + MB * i + lr, M - 1) * (size_t)args.ldr;
                 if (N < 4) {
 #pragma unroll
-                    for (int b = 0; b < TN * NQ; ++b) next[b] = load_half4(row, col(b / NQ, b % NQ), N);
+                    for (int b = 0; b < TN * NQ; ++b) residual[i][b] = load_half4(row, col(b / NQ, b % NQ), N);
                 } else {
 #pragma unroll
-                    for (int b = 0; b < TN * NQ; ++b) next[b] = load_half4_inside(row, col(b / NQ, b % NQ), N);
+                    for (int b = 0; b < TN * NQ; ++b) residual[i][b] = load_half4_inside(row, col(b / NQ, b % NQ), N);
                 }
             };
-            if (args.R) fetch(0);
+            if (args.R) {
+#pragma unroll
+                for (int i = 0; i < TM; ++i) fetch(i);
+            }
             with_activation_or_none(args.act, [&](auto kind) {
 #pragma unroll
                 for (int i = 0; i < TM; ++i) {
                     const int m = m0 + wm0 + MB * i + lr;
-                    u32x2_t r[TN * NQ];
-#pragma unroll
-                    for (int b = 0; b < TN * NQ; ++b) r[b] = next[b];
-                    if (args.R && i + 1 < TM) fetch(i + 1);
 #pragma unroll
                     for (int j = 0; j < TN; ++j)
 #pragma unroll
@@ -1849,13 +1907,16 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
                                 z[e] = acc[i][j][4 * q + e] + bias[j * NQ + q][e];
-                                v[e] = activation<decltype(kind)::value>(z[e]);
+                                v[e] = activation<decltype(kind)::value, true>(z[e]);
                             }
                             const int n = col(j, q);
                             if (args.GU && m < M && n < N) store_sums(args.GU + (size_t)m * (size_t)N + n, z, n, N);
-                            if (args.R) v += to_float4<C::IN_DT>(r[j * NQ + q]);
+                            u32x2_t& r = residual[i][j * NQ + q];
+                            asm volatile("" : "+v"(r));                  // unpacked here, not before
+                            if (args.R) v += to_float4<C::IN_DT>(r);
                             put_group(i, j, q, v);
                         }
+                    __builtin_amdgcn_sched_barrier(0);       // rows mixed by the scheduler spill
                 }
             });
             return;
@@ -1883,63 +1944,48 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
             return;
         }
         if constexpr (C::EPI == EPI_POLY || C::EPI == EPI_STEP || C::EPI == EPI_LAST) {
-            // what a row needs is on its way while the one before is finished (rows and
-            // columns past the edge take the last ones; M and N are multiples of 64)
-            using In4 = std::conditional_t<C::EPI == EPI_POLY, u32x2_t, f32x4_t>;
-            In4 next[TN * NQ];
-            float next_diag;
-            auto col = [&](int b) { return n0 + wn0 + MB * (b / NQ) + 4 * NG * (b % NQ) + 4 * g; };
-            f32x4_t column[TN * NQ];
-            if constexpr (C::EPI == EPI_POLY) {
+            ns_fetch_columns();
+            if constexpr (!NS_EARLY) {
 #pragma unroll
-                for (int b = 0; b < TN * NQ; ++b)
-                    column[b] = *reinterpret_cast<const f32x4_t*>(args.diag + min(col(b), N - 4));
+                for (int i = 0; i < min(TM, NS_AHEAD); ++i) ns_fetch(i);
             }
-            auto fetch = [&](int i) {
-                const int m = min(m0 + wm0 + MB * i + lr, M - 1);
-                next_diag = args.diag[m];
-#pragma unroll
-                for (int b = 0; b < TN * NQ; ++b) {
-                    const int n = min(col(b), N - 4);
-                    if constexpr (C::EPI == EPI_POLY)
-                        next[b] = *reinterpret_cast<const u32x2_t*>(args.R + ((size_t)m * (size_t)args.ldr + n) * 2);
-                    else
-                        next[b] = *reinterpret_cast<const f32x4_t*>(args.X + (size_t)m * (size_t)N + n);
-                }
-            };
-            fetch(0);
 #pragma unroll
             for (int i = 0; i < TM; ++i) {
                 const int m = m0 + wm0 + MB * i + lr;
-                In4 own[TN * NQ];
-                const float d = next_diag;
+                const NsRow own = ns_rows[NS_EARLY ? i : i % NS_AHEAD];
+                if constexpr (!NS_EARLY)
+                    if (i + NS_AHEAD < TM) ns_fetch(i + NS_AHEAD);
 #pragma unroll
-                for (int b = 0; b < TN * NQ; ++b) own[b] = next[b];
-                if (i + 1 < TM) fetch(i + 1);
-#pragma unroll
-                for (int b = 0; b < TN * NQ; ++b) {
-                    const int n = col(b);
+                for (int b = 0; b < NS_GROUPS; ++b) {
+                    const int n = ns_col(b);
                     f32x4_t v;
+                    const f32x4_t o = to_float4<DT_F16>(own.hi[b]);
                     if constexpr (C::EPI == EPI_POLY) {
                         // off the diagonal b O + c (O^2 + (d_m + d_n) O), O being A without
                         // its diagonal d; on it b d + c (O^2 + d^2), in fp32
-                        const f32x4_t o = to_float4<DT_F16>(own[b]);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             const float s = acc[i][b / NQ][4 * (b % NQ) + e] * args.beta, a = o[e] * args.scale_o;
-                            v[e] = args.alpha * (args.pb * a + args.pc * (s + (d + column[b][e]) * a));
+                            v[e] = args.alpha * (args.pb * a + args.pc * (s + (own.d + ns_columns[b][e]) * a));
                             if (m == n + e) {
                                 v[e] = 0.0f;
-                                if (m < M) args.diag_out[m] = args.pb * d + args.pc * (s + d * d);
+                                if (m < M) args.diag_out[m] = args.pb * own.d + args.pc * (s + own.d * own.d);
                             }
                         }
                     } else {
+                        const f32x4_t low = to_float4<DT_F16>(own.lo[b]);
+                        unsigned short h[4];
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            v[e] = fmaf(args.pa + d, own[b][e], acc[i][b / NQ][4 * (b % NQ) + e] * args.beta);
+                        for (int e = 0; e < 4; ++e) {
+                            const float x = fmaf(low[e], 1.0f / kLowScale, o[e]);
+                            v[e] = fmaf(args.pa + own.d, x, acc[i][b / NQ][4 * (b % NQ) + e] * args.beta);
+                            h[e] = OutTraits<DT_F16>::cvt((v[e] - (float)(_Float16)v[e]) * kLowScale);
+                        }
                         if constexpr (C::EPI == EPI_STEP) {
+                            const u32x2_t rest = {h[0] | ((unsigned)h[1] << 16), h[2] | ((unsigned)h[3] << 16)};
                             if (m < M && n >= n_own && n < N)
-                                *reinterpret_cast<f32x4_t*>(args.X + (size_t)m * (size_t)N + n) = v;
+                                *reinterpret_cast<u32x2_t*>(args.L + ((size_t)m * (size_t)N + n) * 2) = rest;
+                        } else {
                             v *= args.alpha;
                         }
                     }

@@ -102,6 +102,7 @@ TileTime tile_time(int cfg)
     case LIN_K32: return {1.4, 800, kNumCUs, 1.0};
     case LIN_K32X48:
     case LIN_K48X32: return {1.75, 900, kNumCUs, 1.0};
+    case LIN_K64X32: return {2.0, 900, kNumCUs, 1.0};
     default: return {15.0, 4000, 2 * kNumCUs, 0.6};      // LIN_G64
     }
 }
@@ -143,11 +144,11 @@ LinearPlan plan_as(int cfg, const Linear& l)
 // register-staged tile is never the fastest but where rows are too far apart for the
 // other tiles and K is short (1024 x 512 x 32 gated, rows 2^22 + 8 apart, 5.9 us, 9.3 on
 // 32 x 32; 1024 x 512 x 512 14.2 and 11.3).
-LinearPlan plan_linear(const Linear& l)
+LinearPlan plan_linear(const Linear& l, bool k64x32 = false)
 {
     int best = LIN_G64;
-    for (int cfg : {LIN_K16, LIN_K32, LIN_K32X48, LIN_K48X32, LIN_64, LIN_128, LIN_128X2, LIN_256})
-        if (usable(cfg, l) && linear_time(cfg, l) < linear_time(best, l)) best = cfg;
+    for (int cfg : {LIN_K16, LIN_K32, LIN_K32X48, LIN_K48X32, LIN_K64X32, LIN_64, LIN_128, LIN_128X2, LIN_256})
+        if ((cfg != LIN_K64X32 || k64x32) && usable(cfg, l) && linear_time(cfg, l) < linear_time(best, l)) best = cfg;
     return plan_as(best, l);
 }
 
@@ -164,9 +165,9 @@ struct RowsPlan {
     LinearPlan p, q;            // q: of the rest, if it has rows
 };
 constexpr int64_t kRestRows = 32;
-RowsPlan plan_rows(const Linear& l)
+RowsPlan plan_rows(const Linear& l, bool k64x32 = false)
 {
-    RowsPlan r{l, l, plan_linear(l), {}};
+    RowsPlan r{l, l, plan_linear(l, k64x32), {}};
     r.rest.M = 0;
     double best = linear_time(r.p.cfg, l);
     for (int cfg : {LIN_128, LIN_128X2, LIN_256}) {
@@ -174,7 +175,7 @@ RowsPlan plan_rows(const Linear& l)
         rest.M = l.M % linear_info(cfg).bm;
         top.M = l.M - rest.M;
         if (top.M == 0 || rest.M == 0 || rest.M > kRestRows || !usable(cfg, l)) continue;
-        const LinearPlan q = plan_linear(rest);
+        const LinearPlan q = plan_linear(rest, k64x32);
         if (q.grid() > kMaxGrid) continue;
         const double t = linear_time(cfg, top) + linear_time(q.cfg, rest) + 3000.0;    // a second launch
         if (t < best) {

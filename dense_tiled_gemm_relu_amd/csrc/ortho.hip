@@ -2,8 +2,9 @@
 // A = X X^T, from X = G / (|G| + eps): the passes over the matrix before and after, and
 // the three products of a step on the tile kernel.
 //
-// Precision.  The products' operands are float16, X itself and the diagonals of A and of
-// B = b A + c A^2 are fp32.  A step multiplies small singular values by a (485 times over
+// Precision.  The products' operands are float16; X itself is the sum of two float16 (22
+// bits: fp32 would be 2 bytes more to write), of which the larger is the operand, and the
+// diagonals of A and of B = b A + c A^2 are fp32.  A step multiplies small singular values by a (485 times over
 // five steps of a = 3.4445), so a rounding of X would grow as much; a rounding of the
 // operands of A, B and B X is only ever multiplied by large singular vectors on one side
 // and stays small.  The diagonals are where A and B are largest near the end (A tends to
@@ -64,8 +65,7 @@ template <class T> __global__ void __launch_bounds__(kSquareThreads) ortho_squar
     }
 }
 
-// X and its float16 copy, 64 x 64 a workgroup, transposed where the matrix is tall, with
-// zeros in the padding.
+// X, 64 x 64 a workgroup, transposed where the matrix is tall, with zeros in the padding.
 template <class T> __global__ void __launch_bounds__(kThreads) ortho_start_kernel(OrthoArgs a)
 {
     __shared__ float tile[64][65];
@@ -76,17 +76,18 @@ template <class T> __global__ void __launch_bounds__(kThreads) ortho_start_kerne
     for (int k = 0; k < kOrthoParts; k += 64) s += a.squares[batch * kOrthoParts + k + lane];
 #pragma unroll
     for (int step = 1; step < 64; step *= 2) s += __shfl_xor(s, step);
-    const double scale = 1.0 / (sqrt(s) + (double)a.eps);
+    const double scale = (double)kOrthoX / (sqrt(s) + (double)a.eps);
     const int tiles = a.Q / 64, p0 = (int)(blockIdx.x / tiles) * 64, q0 = (int)(blockIdx.x % tiles) * 64;
     const T* g = static_cast<const T*>(a.g) + batch * (size_t)a.g_batch;
     const bool tall = a.rows > a.cols;
     const int r0 = tall ? q0 : p0, c0 = tall ? p0 : q0;
-    float* x = a.x + batch * (size_t)a.P * (size_t)a.Q;
     _Float16* xh = static_cast<_Float16*>(a.xh) + batch * (size_t)a.P * (size_t)a.Q;
+    _Float16* xl = static_cast<_Float16*>(a.xl) + batch * (size_t)a.P * (size_t)a.Q;
     const auto put = [&](int p, int q, float v) {
         const size_t at = (size_t)p * (size_t)a.Q + q;
-        x[at] = v;
-        xh[at] = (_Float16)(v * kOrthoX);
+        const _Float16 hi = (_Float16)v;
+        xh[at] = hi;
+        xl[at] = (_Float16)((v - (float)hi) * kLowScale);
     };
     for (int k = wave; k < 64; k += kThreads / 64) {
         const int r = r0 + k, c = c0 + lane;
@@ -109,11 +110,13 @@ __global__ void __launch_bounds__(kThreads) ortho_copy_kernel(OrthoArgs a)
     const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
     const int tiles = a.Q / 64, p0 = (int)(blockIdx.x / tiles) * 64, q0 = (int)(blockIdx.x % tiles) * 64;
     const bool tall = a.rows > a.cols;
-    const float* x = a.x + batch * (size_t)a.P * (size_t)a.Q;
+    const _Float16* xh = static_cast<const _Float16*>(a.xh) + batch * (size_t)a.P * (size_t)a.Q;
+    const _Float16* xl = static_cast<const _Float16*>(a.xl) + batch * (size_t)a.P * (size_t)a.Q;
     __bf16* out = static_cast<__bf16*>(a.out) + batch * (size_t)a.rows * (size_t)a.cols;
     for (int k = wave; k < 64; k += kThreads / 64) {
         const int p = p0 + k, q = q0 + lane;
-        const float v = x[(size_t)p * (size_t)a.Q + q];
+        const size_t at = (size_t)p * (size_t)a.Q + q;
+        const float v = fmaf((float)xl[at], 1.0f / kLowScale, (float)xh[at]) / kOrthoX;
         if (tall)
             tile[k][lane] = v;
         else if (p < a.p && q < a.q)
@@ -135,9 +138,9 @@ template <class C> __global__ void __launch_bounds__(C::NTHREADS, 1) ortho_produ
     args.B += batch * p.b;
     args.C += batch * p.c;
     args.R += batch * p.r;
+    args.L += batch * p.r;
     args.diag += batch * p.diag;
     args.diag_out += batch * p.diag;
-    args.X += batch * p.x;
     gemm_relu_tile<C>(args, (int)blockIdx.x, (GR_LDS unsigned char*)(smem_raw), nullptr,
                       Region{args.tiles_m, args.tiles_n, args.panel, 0});
 }

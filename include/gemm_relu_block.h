@@ -117,7 +117,7 @@ int gemm_relu_add_norm_backward(const void* dy, int64_t dy_stride, const void* d
  * stay, the singular values tend to 1.  coefficients: host memory, steps times a, b, c,
  * read before the call returns; steps <= 64.  dtype (g): F16, BF16 or F32.  out is dense
  * bfloat16 (batch x rows x cols).  The products' operands are rounded to float16, X itself
- * is kept in fp32: results are off by less than 1e-3 of their norm before they are
+ * is kept in twice that: results are off by less than 1e-3 of their norm before they are
  * rounded.  Values of X and of b A + c A^2 past 2^8 in magnitude, and of A past 2^6, are
  * past float16's range here and give infinities and NaN; coefficients that keep the
  * singular values below 2 stay far from that.  A matrix of zeros gives zeros; an infinity or NaN in g gives

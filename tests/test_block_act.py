@@ -18,7 +18,8 @@ SIZES = [(1, 1, 1), (1, 64, 64), (2, 33, 100), (5, 7, 513), (3, 3, 40), (16, 100
          (64, 128, 192), (65, 64, 33), (100, 260, 130), (130, 67, 1000), (257, 129, 64), (300, 200, 333)]
 # sizes that take each kernel configuration
 BIG = [(1, 5000, 1024), (64, 2050, 2048), (48, 515, 3000), (200, 2060, 640), (1000, 2200, 520), (2050, 4100, 264),
-       (2048, 8192, 264), (2003, 2006, 2003), (77, 3001, 2500), (100, 3000, 3000)]
+       (2048, 8192, 264), (2003, 2006, 2003), (77, 3001, 2500), (100, 3000, 3000),
+       (50, 8100, 333), (128, 4096, 520)]
 
 
 def inputs(rows, n, k, dtype, seed, bias_dtype=None):
@@ -72,7 +73,8 @@ def test_every_configuration_is_taken():
         names.update(lib.gemm_relu_act_plan(rows, n, k, gr.BF16).decode().split("+"))
         grads.update(lib.gemm_relu_act_backward_plan(rows, n, k, gr.BF16).decode().split(","))
     tiles = {"d256x256x32_s4_i16w8", "d128x128x64_s4_i16w8", "d64x64x64_s4"}
-    assert names >= tiles | {"d128x128x64_s2w8", "k16x16x64_s4", "k32x32x64_s4", "k32x48x64_s3"}, names
+    assert names >= tiles | {"d128x128x64_s2w8", "k16x16x64_s4", "k32x32x64_s4", "k32x48x64_s3",
+                     "k64x32x64_s3"}, names
     assert grads >= tiles | {"g64x64x64"}, grads
 
 
@@ -257,3 +259,15 @@ def test_largest_float16_gradients_stay_finite(act):
     w, x = w * 2.0 ** -8, x * 2.0 ** -8
     assert (dy.to(F64) * act_ref(z.to(F64), act)[1]).abs().max() > 65520
     grad_check(dy, z, x, w, act, None, *gr.matmul_act_backward(dy, z, x, w, act))
+
+
+@pytest.mark.parametrize("act", ACTS)
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_activations_over_their_range(dtype, act):
+    # sums from -40 to 40 and the far ends, and their slopes (dy = 1)
+    g = torch.cat([torch.linspace(-40, 40, 1601), torch.tensor([-60000.0, -1000.0, 1000.0, 60000.0])]).to(dtype).cuda()[:, None]
+    w = torch.ones(1, 1, device="cuda", dtype=dtype)
+    y, z = gr.matmul_act(g, w, None, act, save=True)
+    check(y, g, w, None, act, None, z)
+    z = g.float()
+    grad_check(torch.ones_like(g), z, g, w, act, None, *gr.matmul_act_backward(torch.ones_like(g), z, g, w, act))

@@ -97,9 +97,9 @@ def test_workspaces_and_plans():
     assert lib.gemm_relu_add_norm_backward_workspace(-1, 100) == gr.EINVAL
     assert lib.gemm_relu_add_norm_backward_workspace(BIG - 1, BIG - 1) >= 256 * 4 * 4 * (BIG - 1)
     assert lib.gemm_relu_orthogonalize_workspace(0, 5, 5) == 0
-    assert lib.gemm_relu_orthogonalize_workspace(1, 64, 64) >= 64 * 64 * 12
+    assert lib.gemm_relu_orthogonalize_workspace(1, 64, 64) >= 64 * 64 * 10
     assert lib.gemm_relu_orthogonalize_workspace(1, -1, 64) == gr.EINVAL
-    assert lib.gemm_relu_orthogonalize_workspace(65535, 2 ** 14, 2 ** 20) >= 65535 * 2 ** 37            # grows without wrapping
+    assert lib.gemm_relu_orthogonalize_workspace(65535, 2 ** 14, 2 ** 20) >= 65535 * 2 ** 36            # grows without wrapping
     for sizes in ((1, 2 ** 16 + 1, 2 ** 17), (1, 4, 2 ** 22 + 1), (1, 2 ** 15, 2 ** 20), (65536, 4, 4)):
         assert lib.gemm_relu_orthogonalize_workspace(*sizes) == gr.EUNSUPPORTED
 
