@@ -6,12 +6,18 @@
 
 namespace gemm_relu_hip {
 
-// ---- column sums over strips of rows: out[s][j] = sum over strips of partial[strip][s cols + j]
-constexpr int kMaxSums = 4;
+// ---- column sums over strips of rows: column j of result k is scale factor_j times the sum
+// over strips of partial[strip][of cols + j]
+constexpr int kMaxResults = 4;
 struct JoinArgs {
     const float* partial;       // strips x sums x cols
-    void* out[kMaxSums];        // null: not wanted
-    int sums, cols, strips;
+    struct Result {
+        void* out;              // null: not wanted
+        int of;
+        const void* factor;     // of the results' type; null: 1
+        float scale;
+    } result[kMaxResults];
+    int results, sums, cols, strips;
 };
 hipError_t launch_join(const JoinArgs& a, int out_dt, hipStream_t stream);
 
@@ -33,6 +39,10 @@ struct ActGradArgs {
 hipError_t launch_act_grad(const ActGradArgs& a, int dt, hipStream_t stream);
 
 // ---- residual sum and norms (block_rows.hip)
+// The sums over rows that the backward pass leaves in strips: of dy norm(s), of dy, and of
+// dresidual norm(x) (norm(x): x itself without a post_weight), from which dgate and
+// dpost_weight both follow; with a matrix for a gate, of dt norm(x).
+constexpr int kNormSums = 3;
 struct AddNormArgs {
     const void* x;
     const void* r;
@@ -48,7 +58,8 @@ struct AddNormArgs {
     void* dx;
     void* dr;
     void* dgate;                // of a gate matrix; the sums over rows go to `partial`
-    float* partial;             // strips x 4 x cols: dweight, dbias, dgate, dpost_weight
+    const void* db;             // null: not wanted
+    float* partial;             // strips x kNormSums x cols
     float* row_sums;            // 2 a row: the means that dresidual takes (rows of any length)
     int64_t x_stride, r_stride, gate_stride, dy_stride, ds_stride;    // gate_stride 0: one row
     int rows, cols;

@@ -139,8 +139,8 @@ extern "C" int gemm_relu_act_backward(const void* dy, int64_t dy_stride, const f
     if (e == hipSuccess && dbias && n > 0) {
         JoinArgs j{};
         j.partial = reinterpret_cast<const float*>(ws + p.more);
-        j.out[0] = dbias;
-        j.sums = 1;
+        j.result[0] = {dbias, 0, nullptr, 1.0f};
+        j.results = j.sums = 1;
         j.cols = int(n);
         j.strips = int(ceil_div(rows, 64));
         e = launch_join(j, bias_dtype, st);
@@ -214,7 +214,7 @@ extern "C" int gemm_relu_add_norm(const void* x, int64_t x_stride, const void* r
 // the strips' sums, then two sums a row
 static uint64_t add_norm_sums(int64_t rows, int64_t cols, int bytes)
 {
-    return uint64_t(round_up(int64_t(add_norm_strips(rows, cols, bytes)) * kMaxSums * cols * 4, 256));
+    return uint64_t(round_up(int64_t(add_norm_strips(rows, cols, bytes)) * kNormSums * cols * 4, 256));
 }
 extern "C" int64_t gemm_relu_add_norm_backward_workspace(int64_t rows, int64_t cols)
 {
@@ -259,6 +259,7 @@ extern "C" int gemm_relu_add_norm_backward(const void* dy, int64_t dy_stride, co
     a.dx = dx;
     a.dr = dresidual;
     a.dgate = dgate;
+    a.db = dbias;
     a.partial = static_cast<float*>(workspace);
     a.row_sums = reinterpret_cast<float*>(static_cast<char*>(workspace) + add_norm_sums(rows, cols, e));
     a.x_stride = x_stride;
@@ -275,11 +276,13 @@ extern "C" int gemm_relu_add_norm_backward(const void* dy, int64_t dy_stride, co
     if (err == hipSuccess && (dweight || dbias || row_gate || dpost_weight)) {
         JoinArgs j{};
         j.partial = a.partial;
-        j.out[0] = dweight;
-        j.out[1] = dbias;
-        j.out[2] = row_gate;
-        j.out[3] = dpost_weight;
-        j.sums = kMaxSums;
+        j.result[0] = {dweight, 0, nullptr, 1.0f};
+        j.result[1] = {dbias, 1, nullptr, 1.0f};
+        // the third sum is of dresidual norm(x), with a matrix for a gate times it
+        j.result[2] = {row_gate, 2, post_weight, scale};
+        j.result[3] = {dpost_weight, 2, gate && !gate_stride ? gate : nullptr, scale};
+        j.results = kMaxResults;
+        j.sums = kNormSums;
         j.cols = int(cols);
         j.strips = add_norm_strips(rows, cols, e);
         err = launch_join(j, wdtype, st);

@@ -18,12 +18,12 @@ template <class W> __global__ void __launch_bounds__(1024) join_kernel(JoinArgs 
     __shared__ float part[16][64];
     const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
     const int64_t all = (int64_t)a.sums * a.cols;
-    const int blocks = (a.cols + 63) / 64;
-    for (int64_t u = blockIdx.x; u < (int64_t)a.sums * blocks; u += gridDim.x) {
-        const int which = (int)(u / blocks), c = (int)(u % blocks) * 64 + lane;
-        W* out = static_cast<W*>(which == 0 ? a.out[0] : which == 1 ? a.out[1] : which == 2 ? a.out[2] : a.out[3]);
-        if (!out) continue;
-        const int64_t j = (int64_t)which * a.cols + c;
+    const int blocks = (int)(((int64_t)a.cols + 63) / 64);
+    for (int64_t u = blockIdx.x; u < (int64_t)a.results * blocks; u += gridDim.x) {
+        const int k = (int)(u / blocks);
+        const JoinArgs::Result r = a.result[k];
+        if (!r.out) continue;
+        const int64_t c = u % blocks * 64 + lane, j = (int64_t)r.of * a.cols + c;
         float s = 0.0f;
         if (c < a.cols) {
             // a wave's strips in batches of 8, all loads of one in flight together
@@ -42,7 +42,9 @@ template <class W> __global__ void __launch_bounds__(1024) join_kernel(JoinArgs 
         if (!wave && c < a.cols) {
 #pragma unroll
             for (int k = 1; k < 16; ++k) s += part[k][lane];
-            out[c] = (W)s;
+            s *= r.scale;
+            if (r.factor) s *= (float)static_cast<const W*>(r.factor)[c];
+            static_cast<W*>(r.out)[c] = (W)s;
         }
         __syncthreads();
     }
@@ -153,10 +155,10 @@ typedef float Stats __attribute__((ext_vector_type(4), aligned(4)));       // a 
 
 // One read of x and the residual, one write of s and y: the row stays in registers
 // between its sums; the next row is loaded meanwhile, and what is the same for all rows
-// stays in registers.  One wave a row and four rows a workgroup, or `waves` waves a row:
-// one chunk a thread (two where 16 waves would not hold the row), since four vectors of
-// fp32 weights beside two chunks leave a CU three waves a SIMD (4097 x 3001 fp16, norms on
-// both sides, 28 us so).  Bound by HBM.
+// stays in registers, gate, post_weight and scale as one product.  One wave a row and four
+// rows a workgroup, or `waves` waves a row: one chunk a thread (two where 16 waves would
+// not hold the row).  Bound by HBM where there is one norm (16384 x 8192 bf16 194 us, 5.5
+// TB/s); with norms on both sides the vector unit works nearly as long.
 template <class T, class W, bool ONE, int V>
 __global__ void __launch_bounds__(ONE ? kThreads : 1024) add_norm_kernel(AddNormArgs a, int waves)
 {
@@ -166,17 +168,24 @@ __global__ void __launch_bounds__(ONE ? kThreads : 1024) add_norm_kernel(AddNorm
     __shared__ float lds[2][4][16];
     const int lane = (int)(threadIdx.x & 63), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const RowMap<T, V> map(a.cols, ONE ? lane : (int)threadIdx.x, ONE ? 64 : 64 * waves);
+    // whether a lane of the wave holds elements that its neighbour owns: only then do the
+    // sums look at each element's owner
+    const bool edge = __any(map.skip != 0);
     const bool element_gate = a.gate && a.gate_stride, channel_gate = a.gate && !a.gate_stride;
-    WV w[V], b[V], pw[V], gate[V];
+    WV w[V], b[V];
+    float k[V][N];                // scale gate post_weight
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        w[v] = b[v] = pw[v] = gate[v] = WV{};
+        w[v] = b[v] = WV{};
+        WV pw = WV{}, gate = WV{};
         if (map.has(v)) {
             if (a.w) w[v] = load_vec<WV>(static_cast<const W*>(a.w) + map.start[v]);
             if (a.b) b[v] = load_vec<WV>(static_cast<const W*>(a.b) + map.start[v]);
-            if (a.pw) pw[v] = load_vec<WV>(static_cast<const W*>(a.pw) + map.start[v]);
-            if (channel_gate) gate[v] = load_vec<WV>(static_cast<const W*>(a.gate) + map.start[v]);
+            if (a.pw) pw = load_vec<WV>(static_cast<const W*>(a.pw) + map.start[v]);
+            if (channel_gate) gate = load_vec<WV>(static_cast<const W*>(a.gate) + map.start[v]);
         }
+#pragma unroll
+        for (int e = 0; e < N; ++e) k[v][e] = a.scale * (channel_gate ? (float)gate[e] : 1.0f) * (a.pw ? (float)pw[e] : 1.0f);
     }
     constexpr int ROWS = ONE ? kThreads / 64 : 1;
     const int step = (int)gridDim.x * ROWS;
@@ -205,30 +214,38 @@ __global__ void __launch_bounds__(ONE ? kThreads : 1024) add_norm_kernel(AddNorm
         if constexpr (!ONE) {
             if (lane == 0) buffer[wave] = v;
             __syncthreads();
-            const int k = lane & 15;
-            v = row16_sum(k < waves ? buffer[k] : 0.0f);
+            const int j = lane & 15;
+            v = row16_sum(j < waves ? buffer[j] : 0.0f);
         }
         return v;
+    };
+    // f((its elements as they count in sums))
+    auto each = [&](auto&& f) {
+        if (edge) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int e = 0; e < N; ++e) f(v, e, map.owns(v, e));
+        } else {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int e = 0; e < N; ++e) f(v, e, true);
+        }
     };
     // mean (0 for the root mean square) and 1 / deviation of f
     auto statistics = [&](const float(&f)[V][N], float(&buffers)[4][16], int first, float& mean, float& rstd) {
         float sum = 0.0f;
         mean = 0.0f;
         if (a.layer) {
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-#pragma unroll
-                for (int e = 0; e < N; ++e) sum += map.owns(v, e) ? f[v][e] : 0.0f;
+            each([&](int v, int e, bool own) { sum += own ? f[v][e] : 0.0f; });
             mean = row_sum(sum, buffers[first]) / n;
             sum = 0.0f;
         }
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-            for (int e = 0; e < N; ++e) {
-                const float d = map.owns(v, e) ? f[v][e] - mean : 0.0f;
-                sum += d * d;
-            }
+        each([&](int v, int e, bool own) {
+            const float d = own ? f[v][e] - mean : 0.0f;
+            sum = fmaf(d, d, sum);
+        });
         rstd = 1.0f / sqrtf(row_sum(sum, buffers[first + 1]) / n + a.eps);
     };
     for (int turn = 0; row < a.rows; row += step, turn ^= 1) {
@@ -251,14 +268,9 @@ __global__ void __launch_bounds__(ONE ? kThreads : 1024) add_norm_kernel(AddNorm
 #pragma unroll
             for (int v = 0; v < V; ++v)
 #pragma unroll
-                for (int e = 0; e < N; ++e) f[v][e] = (f[v][e] - mean) * rstd * (float)pw[v][e];
+                for (int e = 0; e < N; ++e) f[v][e] = (f[v][e] - mean) * rstd;
         }
-        if (channel_gate) {
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-#pragma unroll
-                for (int e = 0; e < N; ++e) f[v][e] *= (float)gate[v][e];
-        } else if (element_gate) {
+        if (element_gate) {
 #pragma unroll
             for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -270,7 +282,7 @@ __global__ void __launch_bounds__(ONE ? kThreads : 1024) add_norm_kernel(AddNorm
             X out;
 #pragma unroll
             for (int e = 0; e < N; ++e) {
-                f[v][e] = fmaf(a.scale, f[v][e], (float)r[v][e]);
+                f[v][e] = fmaf(k[v][e], f[v][e], (float)r[v][e]);
                 out[e] = (T)f[v][e];
             }
             if (map.has(v)) __builtin_memcpy(s + map.start[v], &out, sizeof out);
@@ -286,7 +298,7 @@ __global__ void __launch_bounds__(ONE ? kThreads : 1024) add_norm_kernel(AddNorm
                 if (map.has(v)) {
                     X out;
 #pragma unroll
-                    for (int e = 0; e < N; ++e) out[e] = (T)((f[v][e] - mean) * rstd * (float)w[v][e] + (float)b[v][e]);
+                    for (int e = 0; e < N; ++e) out[e] = (T)fmaf((f[v][e] - mean) * rstd, (float)w[v][e], (float)b[v][e]);
                     __builtin_memcpy(y + map.start[v], &out, sizeof out);
                 }
         }
@@ -300,11 +312,13 @@ __global__ void __launch_bounds__(ONE ? kThreads : 1024) add_norm_kernel(AddNorm
 // join kernel adds the strips in order.
 //
 // A thread's own sums over rows stand in LDS (with V N = 8 elements a thread; for longer
-// rows in registers, which then spill): four fp32 sums an element beside five streams, the
+// rows in registers, which then spill): three fp32 sums an element beside five streams, the
 // next row's among them, do not fit the 128 registers that 16 waves a CU leave.  They are
 // nobody else's, so they need no barrier, and they take a sixth of LDS's rate.  A chunk
 // moved back inside the row has its weights cleared where its neighbour owns the element:
-// the row's sums then need no test, and only what it owns is stored.
+// the row's sums then need no test, and only what it owns is stored.  Bound by HBM, with
+// the vector unit close behind: 16384 x 4096 bf16, eight streams, 204 us (5.3 TB/s; 440
+// with the sums in registers).
 template <class T, class W, int V>
 __global__ void __launch_bounds__(1024) add_norm_backward_kernel(AddNormArgs a, int waves)
 {
@@ -314,34 +328,41 @@ __global__ void __launch_bounds__(1024) add_norm_backward_kernel(AddNormArgs a, 
     constexpr bool IN_LDS = V * N <= 8;
     constexpr int QUADS = V * N / 4;                  // of a thread's elements
     __shared__ float lds[2][4][16];
-    __shared__ __attribute__((aligned(16))) f32x4_t sums_raw[IN_LDS ? kMaxSums * QUADS * 1024 : 1];
+    __shared__ __attribute__((aligned(16))) f32x4_t sums_raw[IN_LDS ? kNormSums * QUADS * 1024 : 1];
     const int lane = (int)(threadIdx.x & 63), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int groups = (int)(blockDim.x >> 6) / waves, group = wave / waves, in_row = wave - group * waves;
     const RowMap<T, V> map(a.cols, in_row * 64 + lane, 64 * waves);
     const bool element_gate = a.gate && a.gate_stride, channel_gate = a.gate && !a.gate_stride;
-    WV w[V], pw[V], gate[V];
+    WV w[V];
+    float k[V][N];                // scale gate post_weight
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-        w[v] = pw[v] = gate[v] = WV{};
+        w[v] = WV{};
+        WV pw = WV{}, gate = WV{};
         if (a.w) w[v] = load_vec<WV>(static_cast<const W*>(a.w) + map.start[v]);
-        if (a.pw) pw[v] = load_vec<WV>(static_cast<const W*>(a.pw) + map.start[v]);
-        if (channel_gate) gate[v] = load_vec<WV>(static_cast<const W*>(a.gate) + map.start[v]);
+        if (a.pw) pw = load_vec<WV>(static_cast<const W*>(a.pw) + map.start[v]);
+        if (channel_gate) gate = load_vec<WV>(static_cast<const W*>(a.gate) + map.start[v]);
 #pragma unroll
-        for (int e = 0; e < N; ++e)
-            if (!map.owns(v, e)) w[v][e] = pw[v][e] = (W)0.0f;
+        for (int e = 0; e < N; ++e) {
+            k[v][e] = a.scale * (channel_gate ? (float)gate[e] : 1.0f) * (a.pw ? (float)pw[e] : 1.0f);
+            if (!map.owns(v, e)) {
+                w[v][e] = (W)0.0f;
+                k[v][e] = 0.0f;
+            }
+        }
     }
-    // sum `which` of the thread's quad k of elements
-    f32x4_t in_registers[IN_LDS ? 1 : kMaxSums][IN_LDS ? 1 : QUADS];
-    const auto sum_at = [&](int which, int k) -> f32x4_t& {
+    // sum `which` of the thread's quad q of elements
+    f32x4_t in_registers[IN_LDS ? 1 : kNormSums][IN_LDS ? 1 : QUADS];
+    const auto sum_at = [&](int which, int q) -> f32x4_t& {
         if constexpr (IN_LDS)
-            return sums_raw[(which * QUADS + k) * 1024 + (int)threadIdx.x];
+            return sums_raw[(which * QUADS + q) * 1024 + (int)threadIdx.x];
         else
-            return in_registers[which][k];
+            return in_registers[which][q];
     };
 #pragma unroll
-    for (int which = 0; which < kMaxSums; ++which)
+    for (int which = 0; which < kNormSums; ++which)
 #pragma unroll
-        for (int k = 0; k < QUADS; ++k) sum_at(which, k) = f32x4_t{};
+        for (int q = 0; q < QUADS; ++q) sum_at(which, q) = f32x4_t{};
     const int64_t step = (int64_t)gridDim.x * groups;
     const int64_t first_row = (int64_t)blockIdx.x * groups;
     int64_t row = first_row + group;
@@ -370,10 +391,10 @@ __global__ void __launch_bounds__(1024) add_norm_backward_kernel(AddNormArgs a, 
     // one value for the whole wave: read through the scalar cache
     typedef const __attribute__((address_space(4))) Stats* Scalars;
     const Scalars all_stats = (Scalars)(uintptr_t)a.stats;
-    // means over the row of p and q
+    // means over the row of p (0 for the root mean square) and q
     auto means = [&](float& p, float& q, float(&buffers)[4][16], int first) {
-        p = wave_all<Sum>(p);
         q = wave_all<Sum>(q);
+        if (a.layer) p = wave_all<Sum>(p);
         if (waves > 1) {
             if (lane == 0) {
                 buffers[first][wave] = p;
@@ -381,9 +402,9 @@ __global__ void __launch_bounds__(1024) add_norm_backward_kernel(AddNormArgs a, 
             }
             __syncthreads();
             // 16 lanes each add the waves'
-            const int k = lane & 15;
-            p = row16_sum(k < waves ? buffers[first][group * waves + k] : 0.0f);
-            q = row16_sum(k < waves ? buffers[first + 1][group * waves + k] : 0.0f);
+            const int j = lane & 15;
+            if (a.layer) p = row16_sum(j < waves ? buffers[first][group * waves + j] : 0.0f);
+            q = row16_sum(j < waves ? buffers[first + 1][group * waves + j] : 0.0f);
         }
         p = a.layer ? p * inv_n : 0.0f;
         q *= inv_n;
@@ -411,11 +432,10 @@ __global__ void __launch_bounds__(1024) add_norm_backward_kernel(AddNormArgs a, 
         const bool live = row < a.rows;
         const size_t at = (size_t)row * (size_t)a.cols;
         const Stats stats = all_stats[min(row, (int64_t)a.rows - 1)];
-        float xhat[V][N], shat[V][N], dr[V][N];
-        X y[V], g[V];
+        float xhat[V][N], dr[V][N];
+        X g[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            y[v] = ny[v];
             g[v] = ng[v];
 #pragma unroll
             for (int e = 0; e < N; ++e) {
@@ -423,111 +443,104 @@ __global__ void __launch_bounds__(1024) add_norm_backward_kernel(AddNormArgs a, 
                 dr[v][e] = (float)nd[v][e];
             }
         }
-        // t, and the gate's product with the scale, where they are wanted
-        const auto t = [&](int v, int e) { return a.pw ? xhat[v][e] * (float)pw[v][e] : xhat[v][e]; };
-        const auto scaled_gate = [&](int v, int e) {
-            return channel_gate ? a.scale * (float)gate[v][e] : element_gate ? a.scale * (float)g[v][e] : a.scale;
-        };
         if (a.w) {
             // c = dy weight
-            float p = 0.0f, q = 0.0f;
+            float shat[V][N], c[V][N], p = 0.0f, q = 0.0f;
+            X y[V];
 #pragma unroll
-            for (int v = 0; v < V; ++v)
+            for (int v = 0; v < V; ++v) {
+                y[v] = ny[v];
 #pragma unroll
                 for (int e = 0; e < N; ++e) {
-                    const float gated = channel_gate ? t(v, e) * (float)gate[v][e]
-                                        : element_gate ? t(v, e) * (float)g[v][e]
-                                                       : t(v, e);
-                    shat[v][e] = (fmaf(a.scale, gated, (float)nr[v][e]) - stats[2]) * stats[3];
-                    const float c = (float)y[v][e] * (float)w[v][e];
-                    p += c;
-                    q = fmaf(c, shat[v][e], q);
+                    const float gated = element_gate ? xhat[v][e] * (float)g[v][e] : xhat[v][e];
+                    shat[v][e] = (fmaf(k[v][e], gated, (float)nr[v][e]) - stats[2]) * stats[3];
+                    c[v][e] = (float)y[v][e] * (float)w[v][e];
+                    p += c[v][e];
+                    q = fmaf(c[v][e], shat[v][e], q);
                 }
+            }
             fetch(row + step);
             means(p, q, lds[turn], 0);
+            p *= -stats[3];
+            q *= -stats[3];
 #pragma unroll
             for (int v = 0; v < V; ++v)
 #pragma unroll
                 for (int h = 0; h < N / 4; ++h) {
-                    f32x4_t dw = sum_at(0, v * (N / 4) + h), db = sum_at(1, v * (N / 4) + h);
+                    f32x4_t dw = sum_at(0, v * (N / 4) + h);
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         const int e = 4 * h + u;
-                        const float d = (float)y[v][e];
-                        dr[v][e] = fmaf(stats[3], fmaf(-shat[v][e], q, fmaf(d, (float)w[v][e], -p)), dr[v][e]);
-                        dw[u] = fmaf(d, shat[v][e], dw[u]);
-                        db[u] += d;
+                        dr[v][e] = fmaf(shat[v][e], q, fmaf(c[v][e], stats[3], dr[v][e] + p));
+                        dw[u] = fmaf((float)y[v][e], shat[v][e], dw[u]);
                     }
-                    if (live) {
-                        sum_at(0, v * (N / 4) + h) = dw;
-                        sum_at(1, v * (N / 4) + h) = db;
+                    if (live) sum_at(0, v * (N / 4) + h) = dw;
+                    if (a.db) {
+                        f32x4_t db = sum_at(1, v * (N / 4) + h);
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) db[u] += (float)y[v][4 * h + u];
+                        if (live) sum_at(1, v * (N / 4) + h) = db;
                     }
                 }
         } else {
             fetch(row + step);
         }
         if (a.dr && live) store(a.dr, at, dr);
-        if (channel_gate) {
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-#pragma unroll
-                for (int h = 0; h < N / 4; ++h) {
-                    f32x4_t dg = sum_at(2, v * (N / 4) + h);
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) dg[u] = fmaf(a.scale * dr[v][4 * h + u], t(v, 4 * h + u), dg[u]);
-                    if (live) sum_at(2, v * (N / 4) + h) = dg;
-                }
-        } else if (element_gate && a.dgate && live) {
+        if (element_gate) {
+            // t's other factor beside xhat, and dt without the rest of it
             float dg[V][N];
 #pragma unroll
             for (int v = 0; v < V; ++v)
 #pragma unroll
-                for (int e = 0; e < N; ++e) dg[v][e] = a.scale * dr[v][e] * t(v, e);
-            store(a.dgate, at, dg);
+                for (int e = 0; e < N; ++e) {
+                    dg[v][e] = dr[v][e] * xhat[v][e] * k[v][e];
+                    dr[v][e] *= (float)g[v][e];
+                }
+            if (a.dgate && live) store(a.dgate, at, dg);
         }
-        // dt, in dr's place
+        float p = 0.0f, q = 0.0f;
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
-            for (int e = 0; e < N; ++e) dr[v][e] *= scaled_gate(v, e);
-        if (a.pw) {
-            float p = 0.0f, q = 0.0f;
+            for (int h = 0; h < N / 4; ++h) {
+                if (a.gate || a.pw) {
+                    f32x4_t sum = sum_at(2, v * (N / 4) + h);
 #pragma unroll
-            for (int v = 0; v < V; ++v)
-#pragma unroll
-                for (int h = 0; h < N / 4; ++h) {
-                    f32x4_t dp = sum_at(3, v * (N / 4) + h);
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int e = 4 * h + u;
-                        dp[u] = fmaf(dr[v][e], xhat[v][e], dp[u]);
-                        dr[v][e] *= (float)pw[v][e];
-                        p += dr[v][e];
-                        q = fmaf(dr[v][e], xhat[v][e], q);
-                    }
-                    if (live) sum_at(3, v * (N / 4) + h) = dp;
+                    for (int u = 0; u < 4; ++u) sum[u] = fmaf(dr[v][4 * h + u], xhat[v][4 * h + u], sum[u]);
+                    if (live) sum_at(2, v * (N / 4) + h) = sum;
                 }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const int e = 4 * h + u;
+                    dr[v][e] *= k[v][e];
+                    p += dr[v][e];
+                    q = fmaf(dr[v][e], xhat[v][e], q);
+                }
+            }
+        if (a.pw) {
             means(p, q, lds[turn], 2);
+            p *= -stats[1];
+            q *= -stats[1];
 #pragma unroll
             for (int v = 0; v < V; ++v)
 #pragma unroll
-                for (int e = 0; e < N; ++e) dr[v][e] = stats[1] * fmaf(-xhat[v][e], q, dr[v][e] - p);
+                for (int e = 0; e < N; ++e) dr[v][e] = fmaf(xhat[v][e], q, fmaf(dr[v][e], stats[1], p));
         }
         if (a.dx && live) store(a.dx, at, dr);
     }
     // the groups' sums join first, in order (with registers there is one group)
     __syncthreads();
     if (group) return;
-    float* strip = a.partial + (size_t)blockIdx.x * kMaxSums * (size_t)a.cols;
+    float* strip = a.partial + (size_t)blockIdx.x * kNormSums * (size_t)a.cols;
 #pragma unroll
-    for (int which = 0; which < kMaxSums; ++which) {
-        if (!(which < 2 ? a.w != nullptr : which == 2 ? channel_gate : a.pw != nullptr)) continue;
+    for (int which = 0; which < kNormSums; ++which) {
+        if (!(which == 0 ? a.w != nullptr : which == 1 ? a.db != nullptr : a.gate || a.pw)) continue;
 #pragma unroll
-        for (int k = 0; k < QUADS; ++k) {
-            f32x4_t s = sum_at(which, k);
+        for (int q = 0; q < QUADS; ++q) {
+            f32x4_t s = sum_at(which, q);
             if constexpr (IN_LDS)
-                for (int j = 1; j < groups; ++j) s += sums_raw[(which * QUADS + k) * 1024 + j * 64 * waves + (int)threadIdx.x];
-            const int v = k / (N / 4), e = 4 * (k % (N / 4));
+                for (int j = 1; j < groups; ++j) s += sums_raw[(which * QUADS + q) * 1024 + j * 64 * waves + (int)threadIdx.x];
+            const int v = q / (N / 4), e = 4 * (q % (N / 4));
             float* to = strip + (size_t)which * (size_t)a.cols + map.start[v] + e;
             if (v < V - 1 || map.skip == 0) {
                 __builtin_memcpy(to, &s, 16);
@@ -672,7 +685,7 @@ __global__ void __launch_bounds__(kThreads) add_norm_strip_any_kernel(AddNormArg
     const int64_t j = (int64_t)blockIdx.x * kThreads + threadIdx.x;
     if (j >= a.cols) return;
     const int64_t r0 = (int64_t)blockIdx.y * strip_rows, r1 = min((int64_t)a.rows, r0 + strip_rows);
-    float dw = 0.0f, db = 0.0f, dg = 0.0f, dp = 0.0f;
+    float dw = 0.0f, db = 0.0f, sum = 0.0f;
     for (int64_t r = r0; r < r1; ++r) {
         AnyGrad<T, W> in(a, (size_t)r);
         in.p = a.row_sums[2 * (size_t)r];
@@ -682,24 +695,19 @@ __global__ void __launch_bounds__(kThreads) add_norm_strip_any_kernel(AddNormArg
             dw = fmaf(d, in.shat(j), dw);
             db += d;
         }
-        if (in.gc || in.pw) {
-            const float d = a.scale * in.dr(j);
-            dg = fmaf(d, in.t(j), dg);
-            dp = fmaf(d * in.gate(j), in.xhat(j), dp);
-        }
+        if (in.gc || in.pw) sum = fmaf(in.g ? in.dr(j) * in.gate(j) : in.dr(j), in.xhat(j), sum);
     }
-    float* p = a.partial + (size_t)blockIdx.y * kMaxSums * (size_t)a.cols + j;
+    float* p = a.partial + (size_t)blockIdx.y * kNormSums * (size_t)a.cols + j;
     p[0] = dw;
     p[(size_t)a.cols] = db;
-    p[2 * (size_t)a.cols] = dg;
-    p[3 * (size_t)a.cols] = dp;
+    p[2 * (size_t)a.cols] = sum;
 }
 
 }  // namespace
 
 hipError_t launch_join(const JoinArgs& a, int out_dt, hipStream_t stream)
 {
-    const dim3 grid((unsigned)std::min<int64_t>(a.sums * ceil_div(a.cols, 64), kMaxRowGrid));
+    const dim3 grid((unsigned)std::min<int64_t>(a.results * ceil_div(a.cols, 64), kMaxRowGrid));
     switch (out_dt) {
     case DT_F32: return start(&join_kernel<float>, grid, 1024, stream, a);
     case DT_F16: return start(&join_kernel<_Float16>, grid, 1024, stream, a);
@@ -733,10 +741,12 @@ hipError_t launch_add_norm(const AddNormArgs& a, int dt, int wdt, hipStream_t st
         if (chunks == 0 || waves > 32)
             return start(a.cols <= kThreads ? &add_norm_any_kernel<T, W, true> : &add_norm_any_kernel<T, W, false>,
                          dim3(any_grid(a.rows)), kThreads, stream, a);
+        // as many workgroups as a device holds of these kernels' 20 waves a CU (4097 x 3001
+        // fp16 29.5 us; with four times as many, each of fewer rows, 34; 16384 x 8192 bf16
+        // 194 and 217)
         const auto go = [&](auto kernel, int rows_here, int row_waves) {
-            const int threads = 64 * rows_here * row_waves;
-            const int grid = even_grid(a.rows, rows_here, row_groups(a.rows, a.cols, sizeof(T), threads));
-            return start(kernel, dim3(grid), threads, stream, a, row_waves);
+            const int grid = even_grid(a.rows, rows_here, kNumCUs * std::max(1, 20 / (rows_here * row_waves)));
+            return start(kernel, dim3(grid), 64 * rows_here * row_waves, stream, a, row_waves);
         };
         return waves == 1    ? go(&add_norm_kernel<T, W, true, 1>, kThreads / 64, 1)
                : waves <= 16 ? go(&add_norm_kernel<T, W, false, 1>, 1, waves)

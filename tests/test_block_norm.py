@@ -117,7 +117,9 @@ class Case:
             dyd, w = self.dy.to(f), self.w.to(f)
             c = (dyd * w, U * (dyd * w).abs())
             v, e = self.through(c, self.shat, self.sr)
-            total = (d + v, e + U * (d + v).abs())
+            # the norm's terms are added to ds one at a time: each rounding is of a partial
+            # sum below |ds| and those terms, whose share `through` counts
+            total = (d + v, e + 3 * U * d.abs() + U * (d + v).abs())
             out[2] = summed(dyd * self.shat[0], dyd.abs() * self.shat[1])
             if self.b is not None:
                 out[3] = summed(dyd, 0 * dyd)
