@@ -93,6 +93,18 @@ struct OrthoArgs {
 constexpr int kOrthoParts = 256;
 hipError_t launch_ortho_start(const OrthoArgs& a, int dt, hipStream_t stream);
 hipError_t launch_ortho_copy(const OrthoArgs& a, hipStream_t stream);      // no steps: X as it is
+// all steps of small matrices in one launch (ortho_small.hip): the shorter side at most 128
+// and padded to 64 or 128, the longer padded to a multiple of 128, at most 2^15 elements
+struct OrthoSteps {
+    float v[3 * 64];
+    int steps;
+};
+inline bool ortho_is_small(int64_t p, int64_t q)
+{
+    const int64_t P = p <= 64 ? 64 : 128;
+    return p <= 128 && (q + 127) / 128 * 128 * P <= (int64_t(1) << 15);
+}
+hipError_t launch_ortho_small(const OrthoArgs& a, const OrthoSteps& c, int dt, hipStream_t stream);
 // one of the products for every matrix of the batch
 struct OrthoProduct {
     KernelArgs k;

@@ -295,7 +295,7 @@ namespace {
 
 // (the tiles' copies reach rows of 2^22 elements; a launch's work-items stay below 2^32)
 constexpr int64_t kOrthoShort = int64_t(1) << 16, kOrthoLong = int64_t(1) << 22, kOrthoSize = int64_t(1) << 34, kOrthoBatch = 65535;
-constexpr int kOrthoSteps = 64;
+constexpr int kOrthoSteps = int(sizeof(OrthoSteps::v) / (3 * sizeof(float)));
 
 struct OrthoPlan {
     int64_t p, q, P, Q;
@@ -324,6 +324,7 @@ OrthoPlan plan_ortho(int64_t batch, int64_t rows, int64_t cols)
     o.q = std::max(rows, cols);
     o.P = round_up(o.p, 64);
     o.Q = round_up(o.q, 64);
+    if (ortho_is_small(o.p, o.q)) return o;
     o.gram = ortho_config(Linear{o.P, o.P, o.Q, o.Q, o.Q, true}, batch, true);
     o.poly = ortho_config(Linear{o.P, o.P, o.P, o.P, o.P, true}, batch, true);
     o.step = ortho_config(Linear{o.P, o.Q, o.P, o.P, o.Q, false}, batch, false);
@@ -403,6 +404,12 @@ extern "C" int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t 
     a.squares = reinterpret_cast<double*>(ws + o.squares);
     a.xh = ws + o.xh[0];
     a.xl = ws + o.xl;
+    if (ortho_is_small(o.p, o.q)) {
+        OrthoSteps c{};
+        c.steps = steps;
+        std::copy_n(coefficients, 3 * steps, c.v);
+        return finish(launch_ortho_small(a, c, dtype, st), st);
+    }
     hipError_t err = launch_ortho_start(a, dtype, st);
     const uint64_t PQ = uint64_t(o.P) * uint64_t(o.Q), PP = uint64_t(o.P) * uint64_t(o.P);
     const Linear gram{o.P, o.P, o.Q, o.Q, o.Q, true}, poly{o.P, o.P, o.P, o.P, o.P, true}, next{o.P, o.Q, o.P, o.P, o.Q, false};

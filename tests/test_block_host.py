@@ -97,7 +97,8 @@ def test_workspaces_and_plans():
     assert lib.gemm_relu_add_norm_backward_workspace(-1, 100) == gr.EINVAL
     assert lib.gemm_relu_add_norm_backward_workspace(BIG - 1, BIG - 1) >= 256 * 3 * 4 * (BIG - 1)
     assert lib.gemm_relu_orthogonalize_workspace(0, 5, 5) == 0
-    assert lib.gemm_relu_orthogonalize_workspace(1, 64, 64) >= 64 * 64 * 10
+    assert lib.gemm_relu_orthogonalize_workspace(1, 64, 64) == 0                      # one launch, all in LDS
+    assert lib.gemm_relu_orthogonalize_workspace(1, 256, 256) >= 256 * 256 * 10
     assert lib.gemm_relu_orthogonalize_workspace(1, -1, 64) == gr.EINVAL
     assert lib.gemm_relu_orthogonalize_workspace(65535, 2 ** 14, 2 ** 20) >= 65535 * 2 ** 36            # grows without wrapping
     for sizes in ((1, 2 ** 16 + 1, 2 ** 17), (1, 4, 2 ** 22 + 1), (1, 2 ** 15, 2 ** 20), (65536, 4, 4)):
@@ -109,13 +110,13 @@ class Coefficients(ctypes.Array):
 
 
 STEP, BAD = Coefficients(3.0, -4.0, 2.0), Coefficients(3.0, float("inf"), 2.0)
-ORTHO = dict(g=X, stride=8, batch_stride=64, out=Y, batch=2, rows=8, cols=8, dtype=BF16, c=ctypes.addressof(STEP), steps=1,
-             eps=1e-7, ws=WS, ws_bytes=1 << 20)
+ORTHO = dict(g=X, stride=200, batch_stride=40000, out=Y, batch=2, rows=200, cols=200, dtype=BF16, c=ctypes.addressof(STEP), steps=1,
+             eps=1e-7, ws=WS, ws_bytes=1 << 24)
 
 
 @pytest.mark.parametrize("over", [
-    dict(batch=-1), dict(rows=-1), dict(cols=BIG), dict(dtype=3), dict(stride=7), dict(stride=BIG), dict(batch_stride=-64),
-    dict(g=0), dict(g=X + 1), dict(out=0), dict(out=Y + 1), dict(out=X), dict(out=X + 250), dict(out=WS + 256), dict(c=0),
+    dict(batch=-1), dict(rows=-1), dict(cols=BIG), dict(dtype=3), dict(stride=199), dict(stride=BIG), dict(batch_stride=-64),
+    dict(g=0), dict(g=X + 1), dict(out=0), dict(out=Y + 1), dict(out=X), dict(out=X + 159998), dict(out=WS + 256), dict(c=0),
     dict(c=ctypes.addressof(BAD)), dict(steps=-1), dict(steps=65), dict(eps=-1.0), dict(eps=NAN), dict(ws=0), dict(ws=WS + 8),
     dict(ws_bytes=1000), dict(ws=X)])
 def test_orthogonalize_refuses(over):

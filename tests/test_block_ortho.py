@@ -16,7 +16,8 @@ from tests.block_helpers import BF16, F16, F32, F64, ints, rnd
 pytestmark = pytest.mark.gpu
 
 QUINTIC = (3.4445, -4.7750, 2.0315)
-SIZES = [(1, 1), (1, 64), (64, 1), (2, 3), (64, 64), (65, 200), (200, 65), (128, 130), (256, 256), (300, 1001), (1001, 300),
+SIZES = [(1, 1), (1, 64), (64, 1), (2, 3), (64, 64), (17, 300), (400, 33), (64, 512), (512, 64), (64, 513), (65, 65), (65, 200),
+         (200, 65), (128, 128), (128, 256), (256, 128), (128, 257), (129, 129), (128, 130), (256, 256), (300, 1001), (1001, 300),
          (520, 520), (129, 2050), (1030, 1024), (2100, 2100), (4100, 700)]
 
 
@@ -92,7 +93,8 @@ def scattered(m, n, k, seed):
 
 
 @pytest.mark.parametrize("dtype", [F16, BF16, F32])
-@pytest.mark.parametrize("m,n,k", [(1, 1, 0), (1, 64, 2), (64, 1, 2), (5, 7, 2), (64, 64, 4), (65, 200, 4), (200, 65, 4),
+@pytest.mark.parametrize("m,n,k", [(1, 1, 0), (1, 64, 2), (64, 1, 2), (5, 7, 2), (64, 64, 4), (60, 500, 4), (500, 60, 4),
+                                   (30, 300, 3), (300, 30, 3), (33, 100, 3), (128, 128, 4), (100, 250, 4), (250, 100, 4), (65, 200, 4), (200, 65, 4),
                                    (130, 131, 4), (256, 256, 5), (300, 1001, 5), (1001, 300, 5), (520, 520, 5), (129, 2050, 5),
                                    (1030, 1024, 5), (2100, 2100, 6), (4100, 700, 6), (700, 9000, 6)])
 def test_exact_step(m, n, k, dtype):
@@ -138,7 +140,7 @@ def test_coefficients_of_each_step():
     assert torch.equal(gr.orthogonalize(g, 3, schedule[:3]), gr.orthogonalize(g, 3))
 
 
-@pytest.mark.parametrize("m,n", [(100, 70), (70, 100), (256, 512), (1100, 1200)])
+@pytest.mark.parametrize("m,n", [(50, 31), (100, 70), (70, 100), (200, 300), (300, 200), (256, 512), (1100, 1200)])
 def test_batches_and_strides(m, n):
     g = rnd(5, 5, m, n).to(BF16)
     g[1] *= 1e-20
