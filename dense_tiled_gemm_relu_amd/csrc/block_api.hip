@@ -88,7 +88,7 @@ extern "C" int gemm_relu_act_backward(const void* dy, int64_t dy_stride, const f
                      bytes_of(workspace, p.bytes), {dy, rows, n, dy_stride, 2}, dense(z, slopes ? rows : 0, n, 4),
                      {x, rows, k, x_stride, 2}, {weight, n, k, weight_stride, 2}};
     if (!mats_ok(m, 4) || !workspace_ok(workspace, workspace_bytes, p.bytes)) return GEMM_RELU_EINVAL;
-    if (p.x.grid() + p.w.grid() > kMaxGrid || ceil_div(n, 64) * ceil_div(rows, 64) * kActGradThreads >= (int64_t(1) << 32))
+    if (p.x.grid() + p.w.grid() + ceil_div(n, 64) > kMaxGrid || ceil_div(n, 64) * ceil_div(rows, 64) * kActGradThreads >= (int64_t(1) << 32))
         return GEMM_RELU_EUNSUPPORTED;
     if (const int dev = check_device()) return dev;
     hipStream_t st = static_cast<hipStream_t>(stream);
@@ -131,19 +131,14 @@ extern "C" int gemm_relu_act_backward(const void* dy, int64_t dy_stride, const f
     gw.flags = flags + (p.x.splits > 1 ? p.x.tiles() : 0);
     gw.ws = reinterpret_cast<float*>(ws + p.sums_w);
     const int nx = rows > 0 && k > 0 ? int(p.x.grid()) : 0, nw = n > 0 && k > 0 ? int(p.w.grid()) : 0;
-    if (e == hipSuccess && nx + nw > 0) {
+    // dbias in the same launch, behind the products
+    const LinearSums sums{reinterpret_cast<const float*>(ws + p.more), dbias, int(n), int(ceil_div(rows, 64)), bias_dtype};
+    const int ns = dbias ? int(ceil_div(n, 64)) : 0;
+    if (e == hipSuccess && nx + nw + ns > 0) {
         // the product whose tiles take longest first
         const bool x_first = p.lx.K * p.w.splits >= p.lw.K * p.x.splits;
-        e = launcher_cast_pair(dtype, p.x.cfg)(x_first ? LinearPair{gx, gw, nx} : LinearPair{gw, gx, nw}, nx + nw, st);
-    }
-    if (e == hipSuccess && dbias && n > 0) {
-        JoinArgs j{};
-        j.partial = reinterpret_cast<const float*>(ws + p.more);
-        j.result[0] = {dbias, 0, nullptr, 1.0f};
-        j.results = j.sums = 1;
-        j.cols = int(n);
-        j.strips = int(ceil_div(rows, 64));
-        e = launch_join(j, bias_dtype, st);
+        const LinearPair pair = x_first ? LinearPair{gx, gw, nx} : LinearPair{gw, gx, nw};
+        e = launcher_cast_pair_sums(dtype, p.x.cfg)(LinearPairSums{pair, nx + nw, sums}, nx + nw + ns, st);
     }
     return finish(e, st);
 }

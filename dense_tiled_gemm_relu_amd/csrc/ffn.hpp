@@ -55,6 +55,20 @@ struct LinearPair {
 };
 typedef hipError_t (*PairLaunchFn)(const LinearPair& pair, int grid, hipStream_t stream);
 PairLaunchFn launcher_cast_pair(int dt, int cfg);
+// the same with the sums of a matrix's rows over strips, 64 columns a workgroup behind the
+// products' (inst_act.hip)
+struct LinearSums {
+    const float* partial;   // strips x cols
+    void* out;              // cols; null: none
+    int cols, strips, out_dt;
+};
+struct LinearPairSums {
+    LinearPair pair;
+    int products;           // workgroups of both
+    LinearSums sums;
+};
+typedef hipError_t (*PairSumsLaunchFn)(const LinearPairSums& p, int grid, hipStream_t stream);
+PairSumsLaunchFn launcher_cast_pair_sums(int dt, int cfg);
 LinearLaunchFn launcher_gated(int dt, int cfg);                // B stored (N,K)
 LinearLaunchFn launcher_i8(int out_dt, int cfg);               // B stored (N,K)
 LinearLaunchFn launcher_act(int dt, int cfg);                  // B stored (N,K)

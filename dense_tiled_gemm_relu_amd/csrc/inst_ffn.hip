@@ -9,12 +9,7 @@ namespace {
 template <class C> __global__ void __launch_bounds__(C::NTHREADS, 1) linear_pair_kernel(LinearPair pair)
 {
     __shared__ __attribute__((aligned(1024))) unsigned char smem_raw[C::LDS_BYTES];
-    const bool second = (int)blockIdx.x >= pair.first;
-    const KernelArgs& args = second ? pair.b : pair.a;
-    const int wg = (int)blockIdx.x - (second ? pair.first : 0), tiles = args.tiles_m * args.tiles_n;
-    // a K split's workgroups take part wg / tiles of tile wg % tiles
-    gemm_relu_tile<C>(args, C::SPLITK ? wg % tiles : wg, (GR_LDS unsigned char*)(smem_raw), nullptr,
-                      Region{args.tiles_m, args.tiles_n, args.panel, 0, C::SPLITK ? wg / tiles : 0});
+    pair_tile<C>(pair, (GR_LDS unsigned char*)(smem_raw));
 }
 
 template <class C> hipError_t launch_pair(const LinearPair& pair, int grid, hipStream_t stream)

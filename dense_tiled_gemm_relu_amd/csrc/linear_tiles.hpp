@@ -21,6 +21,17 @@ template <class C> hipError_t launch(const KernelArgs& args, int grid, hipStream
                            params, 0, stream);
 }
 
+// workgroup blockIdx.x of a pair of products
+template <class C> __device__ __forceinline__ void pair_tile(const LinearPair& pair, GR_LDS unsigned char* smem)
+{
+    const bool second = (int)blockIdx.x >= pair.first;
+    const KernelArgs& args = second ? pair.b : pair.a;
+    const int wg = (int)blockIdx.x - (second ? pair.first : 0), tiles = args.tiles_m * args.tiles_n;
+    // a K split's workgroups take part wg / tiles of tile wg % tiles
+    gemm_relu_tile<C>(args, C::SPLITK ? wg % tiles : wg, smem, nullptr,
+                      Region{args.tiles_m, args.tiles_n, args.panel, 0, C::SPLITK ? wg / tiles : 0});
+}
+
 // EPI over inputs IN.  What a configuration measured, in us: 256 x 256, gated 4096 x
 // 7168 x 4096 bf16 395 (1.22 PFLOP/s; 128 x 128 485-500) and 8-bit 8192^3 443 (2.48
 // POP/s); LIN_128, gated 1024 x 2048 x 1536, one round, 15.4 (LIN_128X2 23, 64 x 64

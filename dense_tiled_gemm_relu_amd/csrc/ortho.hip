@@ -66,40 +66,75 @@ template <class T> __global__ void __launch_bounds__(kSquareThreads) ortho_squar
 }
 
 // X, 64 x 64 a workgroup, transposed where the matrix is tall, with zeros in the padding.
+// Four rows of four elements a thread, all loads in flight together.  Bound by HBM: 8192 x
+// 8192 bf16, 0.4 GB.
 template <class T> __global__ void __launch_bounds__(kThreads) ortho_start_kernel(OrthoArgs a)
 {
+    typedef T T4 __attribute__((ext_vector_type(4)));
+    typedef _Float16 H4 __attribute__((ext_vector_type(4)));
+    constexpr int ROWS = 64 * 16 / kThreads;
     __shared__ float tile[64][65];
     const size_t batch = blockIdx.y;
-    const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
+    const int lane = (int)(threadIdx.x & 63), c4 = (int)(threadIdx.x & 15) * 4, row = (int)(threadIdx.x >> 4);
+    const int tiles = a.Q / 64, p0 = (int)(blockIdx.x / tiles) * 64, q0 = (int)(blockIdx.x % tiles) * 64;
+    const T* g = static_cast<const T*>(a.g) + batch * (size_t)a.g_batch;
+    const bool tall = a.rows > a.cols;
+    const int r0 = tall ? q0 : p0, c = (tall ? p0 : q0) + c4;
+    T4 raw[ROWS];
+    if (c + 4 <= a.cols) {
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k)
+            raw[k] = load_vec<T4>(g + (size_t)min(r0 + row + 64 / ROWS * k, a.rows - 1) * (size_t)a.g_stride + c);
+    } else {
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                raw[k][e] = g[(size_t)min(r0 + row + 64 / ROWS * k, a.rows - 1) * (size_t)a.g_stride + min(c + e, a.cols - 1)];
+    }
     double s = 0.0;
 #pragma unroll
     for (int k = 0; k < kOrthoParts; k += 64) s += a.squares[batch * kOrthoParts + k + lane];
 #pragma unroll
     for (int step = 1; step < 64; step *= 2) s += __shfl_xor(s, step);
-    const double scale = (double)kOrthoX / (sqrt(s) + (double)a.eps);
-    const int tiles = a.Q / 64, p0 = (int)(blockIdx.x / tiles) * 64, q0 = (int)(blockIdx.x % tiles) * 64;
-    const T* g = static_cast<const T*>(a.g) + batch * (size_t)a.g_batch;
-    const bool tall = a.rows > a.cols;
-    const int r0 = tall ? q0 : p0, c0 = tall ? p0 : q0;
+    // the scale as an fp32 number times a power of two: it may be past fp32's range
+    int power;
+    const float factor = (float)frexp((double)kOrthoX / (sqrt(s) + (double)a.eps), &power);
     _Float16* xh = static_cast<_Float16*>(a.xh) + batch * (size_t)a.P * (size_t)a.Q;
     _Float16* xl = static_cast<_Float16*>(a.xl) + batch * (size_t)a.P * (size_t)a.Q;
-    const auto put = [&](int p, int q, float v) {
+    const auto put = [&](int p, int q, const float(&v)[4]) {
         const size_t at = (size_t)p * (size_t)a.Q + q;
-        const _Float16 hi = (_Float16)v;
-        xh[at] = hi;
-        xl[at] = (_Float16)((v - (float)hi) * kLowScale);
+        H4 hi, lo;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            hi[e] = (_Float16)v[e];
+            lo[e] = (_Float16)((v[e] - (float)hi[e]) * kLowScale);
+        }
+        *reinterpret_cast<H4*>(xh + at) = hi;
+        *reinterpret_cast<H4*>(xl + at) = lo;
     };
-    for (int k = wave; k < 64; k += kThreads / 64) {
-        const int r = r0 + k, c = c0 + lane;
-        const float v = r < a.rows && c < a.cols ? (float)((double)(float)g[(size_t)r * (size_t)a.g_stride + c] * scale) : 0.0f;
-        if (tall)
-            tile[k][lane] = v;
-        else
-            put(r, c, v);
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+        const int r = row + 64 / ROWS * k;
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            v[e] = r0 + r < a.rows && c + e < a.cols ? ldexpf((float)raw[k][e] * factor, power) : 0.0f;
+        if (tall) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) tile[r][c4 + e] = v[e];
+        } else {
+            put(p0 + r, q0 + c4, v);
+        }
     }
     if (!tall) return;
     __syncthreads();
-    for (int k = wave; k < 64; k += kThreads / 64) put(p0 + k, q0 + lane, tile[lane][k]);
+#pragma unroll
+    for (int k = 0; k < ROWS; ++k) {
+        const int p = row + 64 / ROWS * k;
+        const float v[4] = {tile[c4][p], tile[c4 + 1][p], tile[c4 + 2][p], tile[c4 + 3][p]};
+        put(p0 + p, q0 + c4, v);
+    }
 }
 
 // ------------------------------------------------------- without any step
