@@ -89,6 +89,8 @@ struct OrthoArgs {
     double* squares;            // kOrthoParts sums of squares a matrix
     void* xh;                   // X times kOrthoX as float16: batch x P x Q
     void* xl;                   // and kLowScale times what that loses
+    unsigned* flags;            // nflags counters a matrix, to clear
+    int nflags;
 };
 constexpr int kOrthoParts = 256;
 hipError_t launch_ortho_start(const OrthoArgs& a, int dt, hipStream_t stream);
@@ -109,7 +111,7 @@ hipError_t launch_ortho_small(const OrthoArgs& a, const OrthoSteps& c, int dt, h
 struct OrthoProduct {
     KernelArgs k;
     uint64_t a, b, c, r;        // bytes from one matrix's A, B, C, R and L to the next's
-    uint64_t diag;              // floats from one matrix's diagonals to the next's
+    uint64_t diag, ws, flags;   // values from one matrix's diagonals, partial sums, counters to the next's
 };
 typedef hipError_t (*OrthoLaunchFn)(const OrthoProduct& p, int tiles, int batch, hipStream_t stream);
 OrthoLaunchFn launcher_ortho(int epi, int cfg);

@@ -295,7 +295,8 @@ constexpr int kOrthoSteps = int(sizeof(OrthoSteps::v) / (3 * sizeof(float)));
 struct OrthoPlan {
     int64_t p, q, P, Q;
     int gram, poly, step;                       // configurations of the products
-    uint64_t squares, xl, xh[2], a, b, diag_a, diag_b, bytes;
+    int64_t parts = 1, split_steps = 0;         // of A's K, with LIN_64: steps each
+    uint64_t squares, xl, xh[2], a, b, diag_a, diag_b, flags, sums, bytes;
 };
 // tiles of one product: of a symmetric one those on and below the diagonal
 int64_t ortho_tiles(int cfg, const Linear& l, bool symmetric)
@@ -312,6 +313,25 @@ int ortho_config(const Linear& l, int64_t batch, bool symmetric)
         if (usable(cfg, l) && time(cfg) < time(best)) best = cfg;
     return best;
 }
+// A = X X^T has the longest K and, of a short X, few tiles: its K is cut into parts where
+// the estimate says so (3001 x 1000, 136 tiles of 47 steps: 16 us in one part).  Two
+// workgroups that share a CU slow each other down from 0.55 of their time together.
+void split_gram(OrthoPlan& o, const Linear& l, int64_t batch)
+{
+    const int64_t steps = ceil_div(l.K, kSplitStep), tiles = ortho_tiles(LIN_64, l, true) * batch;
+    const TileTime t = tile_time(LIN_64);
+    double best = tiles_time(o.gram, l, batch * ortho_tiles(o.gram, l, true));
+    for (int64_t parts = 2; parts <= 8; ++parts) {
+        if (tiles > kNumCUs || tiles * parts > 2 * kNumCUs || steps < 4 * parts) break;
+        const double share = t.alone + (1.0 - t.alone) * double(std::max<int64_t>(0, tiles * parts - kNumCUs)) / kNumCUs;
+        const double time = share * (t.per_byte * double(l.K) * l.bytes / double(parts) + t.fixed) + 3000.0;
+        if (time >= best) continue;
+        best = time;
+        o.gram = LIN_64;
+        o.split_steps = ceil_div(steps, parts);
+        o.parts = ceil_div(steps, o.split_steps);
+    }
+}
 OrthoPlan plan_ortho(int64_t batch, int64_t rows, int64_t cols)
 {
     OrthoPlan o{};
@@ -323,6 +343,7 @@ OrthoPlan plan_ortho(int64_t batch, int64_t rows, int64_t cols)
     o.gram = ortho_config(Linear{o.P, o.P, o.Q, o.Q, o.Q, true}, batch, true);
     o.poly = ortho_config(Linear{o.P, o.P, o.P, o.P, o.P, true}, batch, true);
     o.step = ortho_config(Linear{o.P, o.Q, o.P, o.P, o.Q, false}, batch, false);
+    split_gram(o, Linear{o.P, o.P, o.Q, o.Q, o.Q, true}, batch);
     uint64_t at = 0;
     const auto take = [&](uint64_t bytes) {
         const uint64_t here = at;
@@ -338,6 +359,9 @@ OrthoPlan plan_ortho(int64_t batch, int64_t rows, int64_t cols)
     o.b = take(PP * 2);
     o.diag_a = take(uint64_t(o.P) * uint64_t(batch) * 4);
     o.diag_b = take(uint64_t(o.P) * uint64_t(batch) * 4);
+    const uint64_t tiles = o.parts > 1 ? uint64_t(ortho_tiles(LIN_64, Linear{o.P, o.P, 0, 0, 0, true}, true)) * uint64_t(batch) : 0;
+    o.flags = take(tiles * 4);
+    o.sums = take(tiles * uint64_t(o.parts) * 64 * 64 * 4);
     o.bytes = at;
     return o;
 }
@@ -399,6 +423,9 @@ extern "C" int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t 
     a.squares = reinterpret_cast<double*>(ws + o.squares);
     a.xh = ws + o.xh[0];
     a.xl = ws + o.xl;
+    const int64_t gram_tiles = ortho_tiles(o.gram, Linear{o.P, o.P, o.Q, o.Q, o.Q, true}, true);
+    a.flags = reinterpret_cast<unsigned*>(ws + o.flags);
+    a.nflags = o.parts > 1 ? int(gram_tiles) : 0;
     if (ortho_is_small(o.p, o.q)) {
         OrthoSteps c{};
         c.steps = steps;
@@ -410,7 +437,7 @@ extern "C" int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t 
     const Linear gram{o.P, o.P, o.Q, o.Q, o.Q, true}, poly{o.P, o.P, o.P, o.P, o.P, true}, next{o.P, o.Q, o.P, o.P, o.Q, false};
     const auto launch = [&](int epi, int cfg, const Linear& l, OrthoProduct k) {
         const bool symmetric = epi == EPI_GRAM || epi == EPI_POLY;
-        return launcher_ortho(epi, cfg)(k, int(ortho_tiles(cfg, l, symmetric)), int(batch), st);
+        return launcher_ortho(epi, cfg)(k, int(ortho_tiles(cfg, l, symmetric) * k.k.splits), int(batch), st);
     };
     const auto product = [&](int cfg, const Linear& l, const void* A, const void* B, void* C) {
         OrthoProduct k{};
@@ -427,6 +454,14 @@ extern "C" int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t 
         k.k.diag = reinterpret_cast<float*>(ws + o.diag_a);
         k.a = k.b = PQ * 2;
         k.c = PP * 2;
+        if (o.gram == LIN_64) {
+            k.k.splits = int(o.parts);
+            k.k.split_steps = int(o.parts > 1 ? o.split_steps : ceil_div(o.Q, kSplitStep));
+            k.k.ws = reinterpret_cast<float*>(ws + o.sums);
+            k.k.flags = a.flags;
+            k.ws = uint64_t(gram_tiles) * uint64_t(o.parts) * 64 * 64;
+            k.flags = uint64_t(gram_tiles);
+        }
         err = launch(EPI_GRAM, o.gram, gram, k);
         if (err != hipSuccess) break;
         k = product(o.poly, poly, ws + o.a, ws + o.a, ws + o.b);

@@ -1689,7 +1689,7 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
     // consecutive bytes).
     if constexpr (C::SPLITK) if (C::EPI == EPI_RELU || args.splits > 1) {
         constexpr int NQS = NACC / 4, NV = TM * TN * NQS;
-        const int tiles = reg.tiles_m * reg.tiles_n;
+        const int tiles = SYMMETRIC ? reg.tiles_m * (reg.tiles_m + 1) / 2 : reg.tiles_m * reg.tiles_n;
         const int tile = wg;
         auto slot = [&](int p) { return args.ws + ((size_t)(p * tiles + tile) * (BM * BN) + tid); };
         float* own = slot(split);

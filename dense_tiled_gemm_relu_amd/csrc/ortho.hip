@@ -80,6 +80,9 @@ template <class T> __global__ void __launch_bounds__(kThreads) ortho_start_kerne
     const T* g = static_cast<const T*>(a.g) + batch * (size_t)a.g_batch;
     const bool tall = a.rows > a.cols;
     const int r0 = tall ? q0 : p0, c = (tall ? p0 : q0) + c4;
+    // the arrival counters of a K split that follows
+    if (blockIdx.x == 0)
+        for (int k = threadIdx.x; k < a.nflags; k += kThreads) a.flags[batch * (size_t)a.nflags + k] = 0u;
     T4 raw[ROWS];
     if (c + 4 <= a.cols) {
 #pragma unroll
@@ -176,8 +179,12 @@ template <class C> __global__ void __launch_bounds__(C::NTHREADS, 1) ortho_produ
     args.L += batch * p.r;
     args.diag += batch * p.diag;
     args.diag_out += batch * p.diag;
-    gemm_relu_tile<C>(args, (int)blockIdx.x, (GR_LDS unsigned char*)(smem_raw), nullptr,
-                      Region{args.tiles_m, args.tiles_n, args.panel, 0});
+    args.ws += batch * p.ws;
+    args.flags += batch * p.flags;
+    // a K split's workgroups take part wg / tiles of tile wg % tiles
+    const int wg = (int)blockIdx.x, tiles = C::SPLITK ? (int)gridDim.x / args.splits : 1;
+    gemm_relu_tile<C>(args, C::SPLITK ? wg % tiles : wg, (GR_LDS unsigned char*)(smem_raw), nullptr,
+                      Region{args.tiles_m, args.tiles_n, args.panel, 0, C::SPLITK ? wg / tiles : 0});
 }
 template <class C> hipError_t launch_product(const OrthoProduct& p, int tiles, int batch, hipStream_t stream)
 {
