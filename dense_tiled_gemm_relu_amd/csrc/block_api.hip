@@ -290,6 +290,7 @@ namespace {
 
 // (the tiles' copies reach rows of 2^22 elements; a launch's work-items stay below 2^32)
 constexpr int64_t kOrthoShort = int64_t(1) << 16, kOrthoLong = int64_t(1) << 22, kOrthoSize = int64_t(1) << 34, kOrthoBatch = 65535;
+constexpr int64_t kOrthoBatchStride = int64_t(1) << 40;      // more than any memory; what lies behind could wrap
 constexpr int kOrthoSteps = int(sizeof(OrthoSteps::v) / (3 * sizeof(float)));
 
 struct OrthoPlan {
@@ -387,7 +388,7 @@ extern "C" int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t 
                                        void* workspace, uint64_t workspace_bytes, void* stream)
 {
     if (!ortho_sizes_ok(batch, rows, cols) || !is_float(dtype) || steps < 0 || steps > kOrthoSteps || (steps > 0 && !coefficients) ||
-        !(eps >= 0.0f) || g_batch_stride < 0)
+        !(eps >= 0.0f) || g_batch_stride < 0 || g_batch_stride > kOrthoBatchStride)
         return GEMM_RELU_EINVAL;
     if (batch == 0 || rows == 0 || cols == 0) return GEMM_RELU_OK;
     if (!ortho_supported(batch, rows, cols)) return GEMM_RELU_EUNSUPPORTED;

@@ -311,10 +311,11 @@ __global__ void __launch_bounds__(ONE ? kThreads : 1024) add_norm_kernel(AddNorm
 // as many rows at a time as 16 waves hold, and leaves one strip of sums over its rows; the
 // join kernel adds the strips in order.
 //
-// A thread's own sums over rows stand in LDS (with V N = 8 elements a thread; for longer
-// rows in registers, which then spill): three fp32 sums an element beside five streams, the
-// next row's among them, do not fit the 128 registers that 16 waves a CU leave.  They are
-// nobody else's, so they need no barrier, and they take a sixth of LDS's rate.  A chunk
+// A thread's own sums over rows stand in LDS: three fp32 sums an element beside five
+// streams, the next row's among them, do not fit the 128 registers that 16 waves a CU
+// leave.  They are nobody else's, so they need no barrier, and they take a sixth of LDS's
+// rate.  16-bit rows of more than 1024 chunks have more than LDS holds: their sums over
+// rows are left to add_norm_strip_any_kernel.  A chunk
 // moved back inside the row has its weights cleared where its neighbour owns the element:
 // the row's sums then need no test, and only what it owns is stored.  Bound by HBM, with
 // the vector unit close behind: 16384 x 4096 bf16, eight streams, 204 us (5.3 TB/s; 440
@@ -325,10 +326,10 @@ __global__ void __launch_bounds__(1024) add_norm_backward_kernel(AddNormArgs a, 
     constexpr int N = Chunk<T>::N;
     using X = typename Chunk<T>::Vec;
     using WV = typename VecN<W, N>::Vec;
-    constexpr bool IN_LDS = V * N <= 8;
+    constexpr bool SUMS = V * N <= 8;
     constexpr int QUADS = V * N / 4;                  // of a thread's elements
     __shared__ float lds[2][4][16];
-    __shared__ __attribute__((aligned(16))) f32x4_t sums_raw[IN_LDS ? kNormSums * QUADS * 1024 : 1];
+    __shared__ __attribute__((aligned(16))) f32x4_t sums_raw[SUMS ? kNormSums * QUADS * 1024 : 1];
     const int lane = (int)(threadIdx.x & 63), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int groups = (int)(blockDim.x >> 6) / waves, group = wave / waves, in_row = wave - group * waves;
     const RowMap<T, V> map(a.cols, in_row * 64 + lane, 64 * waves);
@@ -352,17 +353,13 @@ __global__ void __launch_bounds__(1024) add_norm_backward_kernel(AddNormArgs a, 
         }
     }
     // sum `which` of the thread's quad q of elements
-    f32x4_t in_registers[IN_LDS ? 1 : kNormSums][IN_LDS ? 1 : QUADS];
-    const auto sum_at = [&](int which, int q) -> f32x4_t& {
-        if constexpr (IN_LDS)
-            return sums_raw[(which * QUADS + q) * 1024 + (int)threadIdx.x];
-        else
-            return in_registers[which][q];
-    };
+    const auto sum_at = [&](int which, int q) -> f32x4_t& { return sums_raw[(which * QUADS + q) * 1024 + (int)threadIdx.x]; };
+    if constexpr (SUMS) {
 #pragma unroll
-    for (int which = 0; which < kNormSums; ++which)
+        for (int which = 0; which < kNormSums; ++which)
 #pragma unroll
-        for (int q = 0; q < QUADS; ++q) sum_at(which, q) = f32x4_t{};
+            for (int q = 0; q < QUADS; ++q) sum_at(which, q) = f32x4_t{};
+    }
     const int64_t step = (int64_t)gridDim.x * groups;
     const int64_t first_row = (int64_t)blockIdx.x * groups;
     int64_t row = first_row + group;
@@ -461,19 +458,24 @@ __global__ void __launch_bounds__(1024) add_norm_backward_kernel(AddNormArgs a, 
             }
             fetch(row + step);
             means(p, q, lds[turn], 0);
+            if (!SUMS && live && in_row == 0 && lane == 0) {
+                a.row_sums[2 * row] = p;
+                a.row_sums[2 * row + 1] = q;
+            }
             p *= -stats[3];
             q *= -stats[3];
 #pragma unroll
             for (int v = 0; v < V; ++v)
 #pragma unroll
+                for (int e = 0; e < N; ++e) dr[v][e] = fmaf(shat[v][e], q, fmaf(c[v][e], stats[3], dr[v][e] + p));
+            if constexpr (SUMS) {
+#pragma unroll
+                for (int v = 0; v < V; ++v)
+#pragma unroll
                 for (int h = 0; h < N / 4; ++h) {
                     f32x4_t dw = sum_at(0, v * (N / 4) + h);
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int e = 4 * h + u;
-                        dr[v][e] = fmaf(shat[v][e], q, fmaf(c[v][e], stats[3], dr[v][e] + p));
-                        dw[u] = fmaf((float)y[v][e], shat[v][e], dw[u]);
-                    }
+                    for (int u = 0; u < 4; ++u) dw[u] = fmaf((float)y[v][4 * h + u], shat[v][4 * h + u], dw[u]);
                     if (live) sum_at(0, v * (N / 4) + h) = dw;
                     if (a.db) {
                         f32x4_t db = sum_at(1, v * (N / 4) + h);
@@ -482,6 +484,7 @@ __global__ void __launch_bounds__(1024) add_norm_backward_kernel(AddNormArgs a, 
                         if (live) sum_at(1, v * (N / 4) + h) = db;
                     }
                 }
+            }
         } else {
             fetch(row + step);
         }
@@ -503,7 +506,7 @@ __global__ void __launch_bounds__(1024) add_norm_backward_kernel(AddNormArgs a, 
         for (int v = 0; v < V; ++v)
 #pragma unroll
             for (int h = 0; h < N / 4; ++h) {
-                if (a.gate || a.pw) {
+                if (SUMS && (a.gate || a.pw)) {
                     f32x4_t sum = sum_at(2, v * (N / 4) + h);
 #pragma unroll
                     for (int u = 0; u < 4; ++u) sum[u] = fmaf(dr[v][4 * h + u], xhat[v][4 * h + u], sum[u]);
@@ -528,7 +531,8 @@ __global__ void __launch_bounds__(1024) add_norm_backward_kernel(AddNormArgs a, 
         }
         if (a.dx && live) store(a.dx, at, dr);
     }
-    // the groups' sums join first, in order (with registers there is one group)
+    // the groups' sums join first, in order
+    if constexpr (!SUMS) return;
     __syncthreads();
     if (group) return;
     float* strip = a.partial + (size_t)blockIdx.x * kNormSums * (size_t)a.cols;
@@ -538,8 +542,7 @@ __global__ void __launch_bounds__(1024) add_norm_backward_kernel(AddNormArgs a, 
 #pragma unroll
         for (int q = 0; q < QUADS; ++q) {
             f32x4_t s = sum_at(which, q);
-            if constexpr (IN_LDS)
-                for (int j = 1; j < groups; ++j) s += sums_raw[(which * QUADS + q) * 1024 + j * 64 * waves + (int)threadIdx.x];
+            for (int j = 1; j < groups; ++j) s += sums_raw[(which * QUADS + q) * 1024 + j * 64 * waves + (int)threadIdx.x];
             const int v = q / (N / 4), e = 4 * (q % (N / 4));
             float* to = strip + (size_t)which * (size_t)a.cols + map.start[v] + e;
             if (v < V - 1 || map.skip == 0) {
@@ -651,7 +654,7 @@ template <class T, class W, bool SHORT> __global__ void __launch_bounds__(kThrea
             in.p = a.layer ? m.v[0] : 0.0f;
             in.q = m.v[1];
         }
-        if (threadIdx.x == 0) {
+        if (a.w && threadIdx.x == 0) {
             a.row_sums[2 * row] = in.p;
             a.row_sums[2 * row + 1] = in.q;
         }
@@ -686,10 +689,13 @@ __global__ void __launch_bounds__(kThreads) add_norm_strip_any_kernel(AddNormArg
     if (j >= a.cols) return;
     const int64_t r0 = (int64_t)blockIdx.y * strip_rows, r1 = min((int64_t)a.rows, r0 + strip_rows);
     float dw = 0.0f, db = 0.0f, sum = 0.0f;
+#pragma unroll 4
     for (int64_t r = r0; r < r1; ++r) {
         AnyGrad<T, W> in(a, (size_t)r);
-        in.p = a.row_sums[2 * (size_t)r];
-        in.q = a.row_sums[2 * (size_t)r + 1];
+        if (a.w) {
+            in.p = a.row_sums[2 * (size_t)r];
+            in.q = a.row_sums[2 * (size_t)r + 1];
+        }
         if (a.w) {
             const float d = (float)in.dy[j];
             dw = fmaf(d, in.shat(j), dw);
@@ -770,11 +776,15 @@ hipError_t launch_add_norm_backward(const AddNormArgs& a, int dt, int wdt, hipSt
         const int chunks = row_chunks(a.cols, sizeof(T)), waves = (int)ceil_div(chunks, 64);
         if (chunks > 0 && waves <= 16)
             return start(&add_norm_backward_kernel<T, W, 1>, dim3(strips), 64 * waves * (16 / waves), stream, a, waves);
-        if (chunks > 0 && waves <= 32)
-            return start(&add_norm_backward_kernel<T, W, 2>, dim3(strips), 64 * ((waves + 1) / 2), stream, a, (waves + 1) / 2);
-        hipError_t e = start(a.cols <= kThreads ? &add_norm_dx_any_kernel<T, W, true> : &add_norm_dx_any_kernel<T, W, false>,
-                             dim3(any_grid(a.rows)), kThreads, stream, a);
-        if (e == hipSuccess)
+        hipError_t e;
+        if (chunks > 0 && waves <= 32) {
+            e = start(&add_norm_backward_kernel<T, W, 2>, dim3(strips), 64 * ((waves + 1) / 2), stream, a, (waves + 1) / 2);
+            if (sizeof(T) == 4) return e;
+        } else {
+            e = start(a.cols <= kThreads ? &add_norm_dx_any_kernel<T, W, true> : &add_norm_dx_any_kernel<T, W, false>,
+                      dim3(any_grid(a.rows)), kThreads, stream, a);
+        }
+        if (e == hipSuccess && (a.w || a.gate || a.pw))
             e = start(&add_norm_strip_any_kernel<T, W>, dim3((unsigned)ceil_div(a.cols, kThreads), strips), kThreads, stream, a,
                       (int)ceil_div(a.rows, strips));
         return e;

@@ -68,7 +68,7 @@ const char* gemm_relu_act_backward_plan(int64_t rows, int64_t n, int64_t k, int 
 /*
  * From one block to the next: the block's output x, normed first if post_weight is
  * given, gated and scaled, is added to the residual stream, whose sum the next block's
- * norm takes.  For each row of x and residual (rows x cols),
+ * norm takes (rows past fp32's range: as gemm_relu_layer_norm).  For each row of x and residual (rows x cols),
  *   t = norm(x) post_weight, or x without one,
  *   s = residual + scale gate t,
  *   y = norm(s) weight + bias.
@@ -110,7 +110,7 @@ int gemm_relu_add_norm_backward(const void* dy, int64_t dy_stride, const void* d
 
 /*
  * Orthogonalisation of matrices by Newton-Schulz steps: each of the batch's matrices g
- * (rows x cols, batch_stride elements apart, in any order) becomes
+ * (rows x cols, batch_stride elements apart, 0 to 2^40) becomes
  *   X = g / (|g| + eps), |g| the square root of the sum of squares,
  *   X <- a X + (b A + c A^2) X,  A = X X^T,   once per step with its a, b, c,
  * (with A = X^T X on the right where rows > cols: the same matrix).  The singular vectors

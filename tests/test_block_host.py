@@ -115,7 +115,7 @@ ORTHO = dict(g=X, stride=200, batch_stride=40000, out=Y, batch=2, rows=200, cols
 
 
 @pytest.mark.parametrize("over", [
-    dict(batch=-1), dict(rows=-1), dict(cols=BIG), dict(dtype=3), dict(stride=199), dict(stride=BIG), dict(batch_stride=-64),
+    dict(batch=-1), dict(rows=-1), dict(cols=BIG), dict(dtype=3), dict(stride=199), dict(stride=BIG), dict(batch_stride=-64), dict(batch_stride=2 ** 40 + 1),
     dict(g=0), dict(g=X + 1), dict(out=0), dict(out=Y + 1), dict(out=X), dict(out=X + 159998), dict(out=WS + 256), dict(c=0),
     dict(c=ctypes.addressof(BAD)), dict(steps=-1), dict(steps=65), dict(eps=-1.0), dict(eps=NAN), dict(ws=0), dict(ws=WS + 8),
     dict(ws_bytes=1000), dict(ws=X)])
