@@ -41,7 +41,8 @@ EXPORTS = ("gemm_relu", "gemm_relu_strerror", "gemm_relu_configs", "gemm_relu_pl
            "gemm_relu_i8_plan", "gemm_relu_act", "gemm_relu_act_plan", "gemm_relu_act_backward",
            "gemm_relu_act_backward_workspace", "gemm_relu_act_backward_plan", "gemm_relu_add_norm",
            "gemm_relu_add_norm_backward", "gemm_relu_add_norm_backward_workspace",
-           "gemm_relu_orthogonalize", "gemm_relu_orthogonalize_workspace")
+           "gemm_relu_orthogonalize", "gemm_relu_orthogonalize_workspace",
+           "gemm_relu_orthogonalize_plan")
 
 _lib = None
 

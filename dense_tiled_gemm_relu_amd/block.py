@@ -27,6 +27,7 @@ _SIGNATURES = {
                            ctypes.c_float, _vp], _int),
     "gemm_relu_add_norm_backward_workspace": ([_i64, _i64], _i64),
     "gemm_relu_orthogonalize_workspace": ([_i64, _i64, _i64], _i64),
+    "gemm_relu_orthogonalize_plan": ([_i64, _i64, _i64], ctypes.c_char_p),
     "gemm_relu_orthogonalize": ([_vp, _i64, _i64, _vp, _i64, _i64, _i64, _int, _vp, _int, ctypes.c_float, _vp, _u64, _vp], _int),
     "gemm_relu_add_norm_backward": ([_vp, _i64] * 5 + [_vp] * 9 + [_i64, _i64, _int, _int, _int, ctypes.c_float, _vp, _u64,
                                     _vp], _int),

@@ -293,25 +293,54 @@ constexpr int64_t kOrthoShort = int64_t(1) << 16, kOrthoLong = int64_t(1) << 22,
 constexpr int64_t kOrthoBatchStride = int64_t(1) << 40;      // more than any memory; what lies behind could wrap
 constexpr int kOrthoSteps = int(sizeof(OrthoSteps::v) / (3 * sizeof(float)));
 
+// A symmetric product's configuration, and that of its diagonal tiles where they take a launch
+// of their own in smaller tiles (-1: they do not): half of such a tile is wasted, and their few
+// can cost a whole round (8192 x 8192, 528 tiles of 256 x 256 on 256 CUs: 560 us; 496 and the
+// diagonal 461).
+struct Symmetric {
+    int cfg, diagonal;
+};
 struct OrthoPlan {
     int64_t p, q, P, Q;
-    int gram, poly, step;                       // configurations of the products
+    Symmetric gram, poly;                       // configurations of the products
+    int step;
     int64_t parts = 1, split_steps = 0;         // of A's K, with LIN_64: steps each
     uint64_t squares, xl, xh[2], a, b, diag_a, diag_b, flags, sums, bytes;
 };
-// tiles of one product: of a symmetric one those on and below the diagonal
-int64_t ortho_tiles(int cfg, const Linear& l, bool symmetric)
+int64_t triangle(int64_t side) { return side * (side + 1) / 2; }
+int64_t side_of(int cfg, const Linear& l) { return ceil_div(l.M, linear_info(cfg).bm); }
+// the configurations of least estimated time for `batch` products
+int ortho_config(const Linear& l, int64_t batch)
 {
-    const int64_t side = ceil_div(l.M, linear_info(cfg).bm);
-    return symmetric ? side * (side + 1) / 2 : tiles_of(cfg, l);
-}
-// the configuration of least estimated time for `batch` products
-int ortho_config(const Linear& l, int64_t batch, bool symmetric)
-{
-    const auto time = [&](int cfg) { return tiles_time(cfg, l, batch * ortho_tiles(cfg, l, symmetric)); };
+    const auto time = [&](int cfg) { return tiles_time(cfg, l, batch * tiles_of(cfg, l)); };
     int best = LIN_64;
     for (int cfg : {LIN_128, LIN_128X2, LIN_256})
         if (usable(cfg, l) && time(cfg) < time(best)) best = cfg;
+    return best;
+}
+int64_t diagonal_tiles(const Symmetric& s, const Linear& l)
+{
+    return side_of(s.cfg, l) * triangle(linear_info(s.cfg).bm / linear_info(s.diagonal).bm);
+}
+double symmetric_time(const Symmetric& s, const Linear& l, int64_t batch)
+{
+    const int64_t side = side_of(s.cfg, l);
+    if (s.diagonal < 0) return tiles_time(s.cfg, l, batch * triangle(side));
+    return tiles_time(s.cfg, l, batch * triangle(side - 1)) + tiles_time(s.diagonal, l, batch * diagonal_tiles(s, l)) +
+           3000.0;                                                                    // a second launch
+}
+Symmetric symmetric_config(const Linear& l, int64_t batch)
+{
+    Symmetric best{LIN_64, -1};
+    const auto consider = [&](Symmetric s) {
+        if (usable(s.cfg, l) && symmetric_time(s, l, batch) < symmetric_time(best, l, batch)) best = s;
+    };
+    for (int cfg : {LIN_128, LIN_128X2, LIN_256}) {
+        consider({cfg, -1});
+        if (side_of(cfg, l) > 1)
+            for (int diagonal : {LIN_64, LIN_128})
+                if (linear_info(diagonal).bm < linear_info(cfg).bm) consider({cfg, diagonal});
+    }
     return best;
 }
 // A = X X^T has the longest K and, of a short X, few tiles: its K is cut into parts where
@@ -319,16 +348,16 @@ int ortho_config(const Linear& l, int64_t batch, bool symmetric)
 // workgroups that share a CU slow each other down from 0.55 of their time together.
 void split_gram(OrthoPlan& o, const Linear& l, int64_t batch)
 {
-    const int64_t steps = ceil_div(l.K, kSplitStep), tiles = ortho_tiles(LIN_64, l, true) * batch;
+    const int64_t steps = ceil_div(l.K, kSplitStep), tiles = triangle(side_of(LIN_64, l)) * batch;
     const TileTime t = tile_time(LIN_64);
-    double best = tiles_time(o.gram, l, batch * ortho_tiles(o.gram, l, true));
+    double best = symmetric_time(o.gram, l, batch);
     for (int64_t parts = 2; parts <= 8; ++parts) {
         if (tiles > kNumCUs || tiles * parts > 2 * kNumCUs || steps < 4 * parts) break;
         const double share = t.alone + (1.0 - t.alone) * double(std::max<int64_t>(0, tiles * parts - kNumCUs)) / kNumCUs;
         const double time = share * (t.per_byte * double(l.K) * l.bytes / double(parts) + t.fixed) + 3000.0;
         if (time >= best) continue;
         best = time;
-        o.gram = LIN_64;
+        o.gram = Symmetric{LIN_64, -1};
         o.split_steps = ceil_div(steps, parts);
         o.parts = ceil_div(steps, o.split_steps);
     }
@@ -341,9 +370,9 @@ OrthoPlan plan_ortho(int64_t batch, int64_t rows, int64_t cols)
     o.P = round_up(o.p, 64);
     o.Q = round_up(o.q, 64);
     if (ortho_is_small(o.p, o.q)) return o;
-    o.gram = ortho_config(Linear{o.P, o.P, o.Q, o.Q, o.Q, true}, batch, true);
-    o.poly = ortho_config(Linear{o.P, o.P, o.P, o.P, o.P, true}, batch, true);
-    o.step = ortho_config(Linear{o.P, o.Q, o.P, o.P, o.Q, false}, batch, false);
+    o.gram = symmetric_config(Linear{o.P, o.P, o.Q, o.Q, o.Q, true}, batch);
+    o.poly = symmetric_config(Linear{o.P, o.P, o.P, o.P, o.P, true}, batch);
+    o.step = ortho_config(Linear{o.P, o.Q, o.P, o.P, o.Q, false}, batch);
     split_gram(o, Linear{o.P, o.P, o.Q, o.Q, o.Q, true}, batch);
     uint64_t at = 0;
     const auto take = [&](uint64_t bytes) {
@@ -360,7 +389,7 @@ OrthoPlan plan_ortho(int64_t batch, int64_t rows, int64_t cols)
     o.b = take(PP * 2);
     o.diag_a = take(uint64_t(o.P) * uint64_t(batch) * 4);
     o.diag_b = take(uint64_t(o.P) * uint64_t(batch) * 4);
-    const uint64_t tiles = o.parts > 1 ? uint64_t(ortho_tiles(LIN_64, Linear{o.P, o.P, 0, 0, 0, true}, true)) * uint64_t(batch) : 0;
+    const uint64_t tiles = o.parts > 1 ? uint64_t(triangle(o.P / 64)) * uint64_t(batch) : 0;
     o.flags = take(tiles * 4);
     o.sums = take(tiles * uint64_t(o.parts) * 64 * 64 * 4);
     o.bytes = at;
@@ -381,6 +410,41 @@ extern "C" int64_t gemm_relu_orthogonalize_workspace(int64_t batch, int64_t rows
     if (batch == 0 || rows == 0 || cols == 0) return 0;
     if (!ortho_supported(batch, rows, cols)) return GEMM_RELU_EUNSUPPORTED;
     return int64_t(plan_ortho(batch, rows, cols).bytes);
+}
+
+extern "C" const char* gemm_relu_orthogonalize_plan(int64_t batch, int64_t rows, int64_t cols)
+{
+    if (!ortho_sizes_ok(batch, rows, cols)) return nullptr;
+    if (batch == 0 || rows == 0 || cols == 0) return "none";
+    if (!ortho_supported(batch, rows, cols)) return "unsupported";
+    if (ortho_is_small(std::min(rows, cols), std::max(rows, cols))) return "small";
+    // every plan's name, kept for good: three products, of which two may name the tiles on
+    // their diagonal
+    constexpr int CFGS = LIN_64 + 1, DIAGONALS = 3;
+    struct Names {
+        char text[CFGS * DIAGONALS][CFGS * DIAGONALS][CFGS][160];
+        static int put(char* to, size_t room, int k)
+        {
+            static constexpr int diagonals[DIAGONALS] = {-1, LIN_128, LIN_64};
+            const int d = diagonals[k % DIAGONALS];
+            return std::snprintf(to, room, d < 0 ? "%s," : "%s/%s,", linear_info(k / DIAGONALS).name, d < 0 ? "" : linear_info(d).name);
+        }
+        Names()
+        {
+            for (int a = 0; a < CFGS * DIAGONALS; ++a)
+                for (int b = 0; b < CFGS * DIAGONALS; ++b)
+                    for (int c = 0; c < CFGS; ++c) {
+                        char* to = text[a][b][c];
+                        size_t at = size_t(put(to, sizeof text[a][b][c], a));
+                        at += size_t(put(to + at, sizeof text[a][b][c] - at, b));
+                        std::snprintf(to + at, sizeof text[a][b][c] - at, "%s", linear_info(c).name);
+                    }
+        }
+    };
+    static const Names names;
+    const OrthoPlan o = plan_ortho(batch, rows, cols);
+    const auto index = [](const Symmetric& s) { return s.cfg * DIAGONALS + (s.diagonal < 0 ? 0 : s.diagonal == LIN_128 ? 1 : 2); };
+    return names.text[index(o.gram)][index(o.poly)][o.step];
 }
 
 extern "C" int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t g_batch_stride, void* out, int64_t batch,
@@ -424,7 +488,7 @@ extern "C" int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t 
     a.squares = reinterpret_cast<double*>(ws + o.squares);
     a.xh = ws + o.xh[0];
     a.xl = ws + o.xl;
-    const int64_t gram_tiles = ortho_tiles(o.gram, Linear{o.P, o.P, o.Q, o.Q, o.Q, true}, true);
+    const int64_t gram_tiles = triangle(o.P / 64);             // of a cut product
     a.flags = reinterpret_cast<unsigned*>(ws + o.flags);
     a.nflags = o.parts > 1 ? int(gram_tiles) : 0;
     if (ortho_is_small(o.p, o.q)) {
@@ -436,36 +500,45 @@ extern "C" int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t 
     hipError_t err = launch_ortho_start(a, dtype, st);
     const uint64_t PQ = uint64_t(o.P) * uint64_t(o.Q), PP = uint64_t(o.P) * uint64_t(o.P);
     const Linear gram{o.P, o.P, o.Q, o.Q, o.Q, true}, poly{o.P, o.P, o.P, o.P, o.P, true}, next{o.P, o.Q, o.P, o.P, o.Q, false};
-    const auto launch = [&](int epi, int cfg, const Linear& l, OrthoProduct k) {
-        const bool symmetric = epi == EPI_GRAM || epi == EPI_POLY;
-        return launcher_ortho(epi, cfg)(k, int(ortho_tiles(cfg, l, symmetric) * k.k.splits), int(batch), st);
-    };
     const auto product = [&](int cfg, const Linear& l, const void* A, const void* B, void* C) {
         OrthoProduct k{};
         k.k = linear_args(plan_as(cfg, l), l, A, B, C);
+        k.k.split_steps = int(ceil_div(l.K, kSplitStep));      // one part, where the configuration can cut K
         k.diag = uint64_t(o.P);
         return k;
+    };
+    // a symmetric product in one launch, or its tiles below the diagonal and then those on it
+    const auto symmetric = [&](int epi, const Symmetric& c, const Linear& l, OrthoProduct k) {
+        const int64_t side = side_of(c.cfg, l);
+        if (c.diagonal < 0) return launcher_ortho(epi, c.cfg)(k, int(triangle(side)) * k.k.splits, int(batch), st);
+        k.k.triangle = 1;
+        const hipError_t e = launcher_ortho(epi, c.cfg)(k, int(triangle(side - 1)), int(batch), st);
+        if (e != hipSuccess) return e;
+        k.k.triangle = 2;
+        k.k.sub = linear_info(c.cfg).bm / linear_info(c.diagonal).bm;
+        k.k.tiles_m = k.k.tiles_n = int(side_of(c.diagonal, l));
+        return launcher_ortho(epi, c.diagonal)(k, int(diagonal_tiles(c, l)), int(batch), st);
     };
     for (int s = 0; s < steps && err == hipSuccess; ++s) {
         const void* xh = ws + o.xh[s % 2];
         const bool last = s == steps - 1;
-        OrthoProduct k = product(o.gram, gram, xh, xh, ws + o.a);
+        OrthoProduct k = product(o.gram.cfg, gram, xh, xh, ws + o.a);
         k.k.alpha = kOrthoA / (kOrthoX * kOrthoX);
         k.k.beta = 1.0f / (kOrthoX * kOrthoX);
         k.k.diag = reinterpret_cast<float*>(ws + o.diag_a);
         k.a = k.b = PQ * 2;
         k.c = PP * 2;
-        if (o.gram == LIN_64) {
+        if (o.parts > 1) {
             k.k.splits = int(o.parts);
-            k.k.split_steps = int(o.parts > 1 ? o.split_steps : ceil_div(o.Q, kSplitStep));
+            k.k.split_steps = int(o.split_steps);
             k.k.ws = reinterpret_cast<float*>(ws + o.sums);
             k.k.flags = a.flags;
             k.ws = uint64_t(gram_tiles) * uint64_t(o.parts) * 64 * 64;
             k.flags = uint64_t(gram_tiles);
         }
-        err = launch(EPI_GRAM, o.gram, gram, k);
+        err = symmetric(EPI_GRAM, o.gram, gram, k);
         if (err != hipSuccess) break;
-        k = product(o.poly, poly, ws + o.a, ws + o.a, ws + o.b);
+        k = product(o.poly.cfg, poly, ws + o.a, ws + o.a, ws + o.b);
         k.k.alpha = kOrthoB;
         k.k.beta = 1.0f / (kOrthoA * kOrthoA);
         k.k.scale_o = 1.0f / kOrthoA;
@@ -476,7 +549,7 @@ extern "C" int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t 
         k.k.R = ws + o.a;
         k.k.ldr = int(o.P);
         k.a = k.b = k.c = k.r = PP * 2;
-        err = launch(EPI_POLY, o.poly, poly, k);
+        err = symmetric(EPI_POLY, o.poly, poly, k);
         if (err != hipSuccess) break;
         k = product(o.step, next, ws + o.b, xh, last ? out : ws + o.xh[(s + 1) % 2]);
         k.k.alpha = 1.0f / kOrthoX;             // of the last step's result
@@ -493,7 +566,7 @@ extern "C" int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t 
         k.b = PQ * 2;
         k.c = last ? uint64_t(rows) * uint64_t(cols) * 2 : PQ * 2;
         k.r = PQ * 2;
-        err = launch(last ? EPI_LAST : EPI_STEP, o.step, next, k);
+        err = launcher_ortho(last ? EPI_LAST : EPI_STEP, o.step)(k, int(tiles_of(o.step, next)), int(batch), st);
     }
     if (err == hipSuccess && steps == 0) err = launch_ortho_copy(a, st);
     return finish(err, st);

@@ -137,6 +137,10 @@ struct KernelArgs {
     float* diag_out;
     unsigned char* L;
     int out_m, out_n, transposed;
+    // EPI_GRAM and EPI_POLY: which tiles of the symmetric product a launch takes.  0: those on
+    // and below the diagonal; 1: those below it; 2: those on and below it inside diagonal
+    // blocks of `sub` x `sub` tiles.
+    int triangle, sub;
 };
 
 // The tiles one configuration covers inside a launch: a grid of tiles_m x
@@ -701,6 +705,14 @@ __device__ __forceinline__ void tile_coords(int wg, int tiles_m, int tiles_n, in
     tn = within / rows;
 }
 
+// The largest r with r (r + 1) / 2 <= l.
+__device__ __forceinline__ int triangle_row(int l)
+{
+    int r = (int)((sqrtf(8.0f * (float)l + 1.0f) - 1.0f) * 0.5f);
+    while (r * (r + 1) / 2 > l) --r;
+    while ((r + 1) * (r + 2) / 2 <= l) ++r;
+    return r;
+}
 // The same for the tiles on and below the diagonal of `tiles` x `tiles` ones: panels of
 // `panel` tile rows, each column by column up to its triangle, which goes row by row.
 __device__ __forceinline__ void triangle_coords(int wg, int tiles, int panel, int nxcd, int& tm, int& tn)
@@ -710,20 +722,13 @@ __device__ __forceinline__ void triangle_coords(int wg, int tiles, int panel, in
     const int xcd = wg % nxcd, local = wg / nxcd;
     const int logical = xcd < rem ? xcd * (per + 1) + local
                                   : rem * (per + 1) + (xcd - rem) * per + local;
-    // the largest r with r (r + 1) / 2 <= l
-    auto row_of = [](int l) {
-        int r = (int)((sqrtf(8.0f * (float)l + 1.0f) - 1.0f) * 0.5f);
-        while (r * (r + 1) / 2 > l) --r;
-        while ((r + 1) * (r + 2) / 2 <= l) ++r;
-        return r;
-    };
-    const int first = row_of(logical) / panel * panel, rows = min(panel, tiles - first);
+    const int first = triangle_row(logical) / panel * panel, rows = min(panel, tiles - first);
     const int within = logical - first * (first + 1) / 2;
     if (within < first * rows) {
         tm = first + within % rows;
         tn = within / rows;
     } else {
-        const int rest = within - first * rows, r = row_of(rest);
+        const int rest = within - first * rows, r = triangle_row(rest);
         tm = first + r;
         tn = first + rest - r * (r + 1) / 2;
     }
@@ -780,9 +785,18 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
 
     int tm, tn;
     constexpr bool SYMMETRIC = C::EPI == EPI_GRAM || C::EPI == EPI_POLY;
-    if constexpr (SYMMETRIC)
-        triangle_coords(wg, reg.tiles_m, reg.panel, args.nxcd, tm, tn);
-    else
+    if constexpr (SYMMETRIC) {
+        if (args.triangle == 2) {
+            const int per = args.sub * (args.sub + 1) / 2, block = wg / per * args.sub, k = wg % per, i = triangle_row(k);
+            tm = block + i;
+            tn = block + k - i * (i + 1) / 2;
+            if (tm >= reg.tiles_m) return;                  // the last block's tiles past the edge
+        } else {
+            const int below = args.triangle;
+            triangle_coords(wg, reg.tiles_m - below, reg.panel, args.nxcd, tm, tn);
+            tm += below;
+        }
+    } else
         tile_coords(wg, reg.tiles_m, reg.tiles_n, reg.panel, args.nxcd, tm, tn);
     const int m0 = tm * BM;
     // (K,N) B on the direct path: the last tile column is moved back to end at N,
@@ -1689,7 +1703,7 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
     // consecutive bytes).
     if constexpr (C::SPLITK) if (C::EPI == EPI_RELU || args.splits > 1) {
         constexpr int NQS = NACC / 4, NV = TM * TN * NQS;
-        const int tiles = SYMMETRIC ? reg.tiles_m * (reg.tiles_m + 1) / 2 : reg.tiles_m * reg.tiles_n;
+        const int tiles = SYMMETRIC ? reg.tiles_m * (reg.tiles_m + 1) / 2 : reg.tiles_m * reg.tiles_n;   // (triangle 0)
         const int tile = wg;
         auto slot = [&](int p) { return args.ws + ((size_t)(p * tiles + tile) * (BM * BN) + tid); };
         float* own = slot(split);

@@ -130,6 +130,11 @@ int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t batch_strid
                             const float* coefficients, int steps, float eps, void* workspace,
                             uint64_t workspace_bytes, void* stream);
 
+/* Configuration names of a step's products, "A,B,X" ("t/d" where a symmetric one's tiles on
+ * the diagonal take another configuration d; "small" where one launch does all steps, "none",
+ * "unsupported" and NULL as for the others).  The text stays valid.  Host-only. */
+const char* gemm_relu_orthogonalize_plan(int64_t batch, int64_t rows, int64_t cols);
+
 #ifdef __cplusplus
 }
 #endif

@@ -105,6 +105,14 @@ def test_workspaces_and_plans():
         assert lib.gemm_relu_orthogonalize_workspace(*sizes) == gr.EUNSUPPORTED
 
 
+def test_orthogonalize_plans():
+    plan = gr.library().gemm_relu_orthogonalize_plan
+    assert plan(1, -1, 4) is None and plan(0, 4, 4) == b"none" and plan(1, 2 ** 16 + 1, 2 ** 17) == b"unsupported"
+    assert plan(1, 128, 256) == plan(1, 512, 64) == b"small"
+    names = {plan(b, m, n): None for b in (1, 4, 8) for m in range(200, 9000, 200) for n in (m, m + 1000)}
+    assert all(len(name.split(b",")) == 3 for name in names) and any(b"/" in name for name in names)
+
+
 class Coefficients(ctypes.Array):
     _type_, _length_ = ctypes.c_float, 3
 

@@ -176,3 +176,25 @@ def test_non_finite_matrices_stay_apart():
 def test_empty_sizes():
     for shape in ((0, 5), (5, 0), (0, 4, 5), (3, 0, 5)):
         assert gr.orthogonalize(torch.zeros(shape, device="cuda")).shape == shape
+
+
+@pytest.mark.parametrize("batch,m,n,names", [
+    (1, 2900, 2890, "d128x128x64_s4_i16w8/d64x64x64_s4"), (2, 2880, 3000, "d128x128x64_s2w8/d64x64x64_s4"),
+    (3, 3300, 3264, "d256x256x32_s4_i16w8/d128x128x64_s4_i16w8"), (1, 5900, 5800, "d256x256x32_s4_i16w8/d64x64x64_s4")])
+def test_diagonal_tiles_in_a_launch_of_their_own(batch, m, n, names):
+    # exact as in test_exact_step: the products' tiles below the diagonal and those on it, the
+    # last ones past the edge
+    assert names in gr.library().gemm_relu_orthogonalize_plan(batch, m, n).decode()
+    k = 6
+    g = torch.stack([scattered(m, n, k, 7 * i) for i in range(batch)])
+    for a, b, c in ((1.5, -0.5, 0.0), (1.0, 0.0, 4.0 ** k)):
+        got = gr.orthogonalize(g.to(BF16), 1, (a, b, c), 0.0)
+        for x, y in zip(g.to(F64) / 2 ** k, got.to(F64)):
+            x, y = (x.t(), y.t()) if m > n else (x, y)
+            gram = x @ x.t()
+            assert ((gram * 4 ** k) @ (gram * 4 ** k)).abs().max() < 2 ** 9
+            assert torch.equal(y, (a * x + (b * gram + c * gram @ gram) @ x).to(BF16).to(F64))
+    want = torch.stack([gr.orthogonalize(v) for v in rnd(1, batch, m, n)])
+    if batch == 1:
+        ref, err = steps_of(rnd(1, batch, m, n)[0], 5, QUINTIC)
+        assert (want[0].to(F64) - ref).norm() <= (1e-3 + 2.0 ** -8) * ref.norm()
