@@ -296,7 +296,7 @@ constexpr int kOrthoSteps = int(sizeof(OrthoSteps::v) / (3 * sizeof(float)));
 // A symmetric product's configuration, and that of its diagonal tiles where they take a launch
 // of their own in smaller tiles (-1: they do not): half of such a tile is wasted, and their few
 // can cost a whole round (8192 x 8192, 528 tiles of 256 x 256 on 256 CUs: 560 us; 496 and the
-// diagonal 461).
+// diagonal 422 + 53).
 struct Symmetric {
     int cfg, diagonal;
 };
@@ -344,7 +344,7 @@ Symmetric symmetric_config(const Linear& l, int64_t batch)
     return best;
 }
 // A = X X^T has the longest K and, of a short X, few tiles: its K is cut into parts where
-// the estimate says so (3001 x 1000, 136 tiles of 47 steps: 16 us in one part).  Two
+// the estimate says so (3001 x 1000, 136 tiles of 47 steps: 16 us in one part, 14 in three).  Two
 // workgroups that share a CU slow each other down from 0.55 of their time together.
 void split_gram(OrthoPlan& o, const Linear& l, int64_t batch)
 {

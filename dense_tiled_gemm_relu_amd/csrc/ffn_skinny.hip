@@ -22,7 +22,10 @@
 // weight the tiles' fewer bytes from the L2 win: 64 x 8192 x 8192 gated 89 against 60.
 // 32 x 48 and 48 x 32 are for what just misses one round of smaller ones: 77 x 3001 x
 // 5003 8-bit 13.3 against 19, 100 x 3000 x 3000 7.2 against 10; elsewhere they are
-// slower (64 x 4096 x 8192 10.4 against 9.2).
+// slower (64 x 4096 x 8192 10.4 against 9.2).  64 x 32 reads a wide weight once for up to 64
+// rows and just fits one round where 32 x 32 takes two: with bias, activation and residual,
+// weights from HBM, 64 x 8192 x 8192 35 us (47 on 32 x 32; HBM's share 26), 64 x 7168 x 4096
+// 13.8 (18.4 on 64 x 64), 128 x 4096 x 4096 12.4 (18.4).
 #include "api_common.hpp"
 #include "ffn.hpp"
 

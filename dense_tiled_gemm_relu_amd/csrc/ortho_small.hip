@@ -9,8 +9,9 @@
 //
 // A step is bound by LDS: a wave's blocks share their operands' reads (2 x 4 blocks of A
 // take 6 reads of 16 bytes a lane for 8 matrix instructions).  The matrix comes and goes
-// through LDS in short loops: a workgroup runs such code once, and 61 KB of unrolled loads
-// and stores took 27 us to fetch.
+// through LDS in short loops: a workgroup runs such code once, and with 61 KB of unrolled
+// loads and stores 128 x 256 without any step took 27 us, with the loops 11.  Five steps: 128
+// x 256 bf16 43 us, 64 x 512 29, 64 x 128 14; on the tile kernel 85 to 90.
 #include "block.hpp"
 #include "row_common.hpp"
 
