@@ -120,8 +120,8 @@ int gemm_relu_add_norm_backward(const void* dy, int64_t dy_stride, const void* d
  * is kept in twice that: results are off by less than 1e-3 of their norm before they are
  * rounded.  Values of X and of b A + c A^2 past 2^8 in magnitude, and of A past 2^6, are
  * past float16's range here and give infinities and NaN; coefficients that keep the
- * singular values below 2 stay far from that.  A matrix of zeros gives zeros; an infinity or NaN in g gives
- * NaN all over its matrix.  The shorter side <= 2^16, the longer <= 2^22, rows x cols <=
+ * singular values below 2 stay far from that.  A matrix of zeros gives zeros (with eps == 0 NaN, 0 / 0); a
+ * NaN in g, or with at least one step an infinity, gives NaN all over its matrix.  The shorter side <= 2^16, the longer <= 2^22, rows x cols <=
  * 2^34, batch <= 65535, else GEMM_RELU_EUNSUPPORTED.
  */
 int64_t gemm_relu_orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols);

@@ -249,6 +249,27 @@ def test_non_finite_values_stay_in_their_rows(rows, n, k):
     assert torch.equal(y[:, keep], good[:, keep])
 
 
+@pytest.mark.parametrize("act", ["none", "silu"])
+@pytest.mark.parametrize("rows,n,k", [(3, 64, 70), (70, 72, 40), (40, 41, 33), (300, 192, 900), (1500, 1600, 72), (2048, 2048, 512)])
+def test_non_finite_gradients_stay_in_their_rows(rows, n, k, act):
+    # a row of dx takes its row of dy, a row of dweight its column; nothing of the next row, and
+    # nothing between rows that are further apart than they are long
+    x, w, b, _ = inputs(rows, n, k, F16, 61)
+    z = None if act == "none" else x.float() @ w.float().t()
+    dy = rnd(62, rows, n).to(F16)
+    clean = gr.matmul_act_backward(dy, z, x, w, act, b)
+    for pad in (8, 3):
+        for got, want in zip(gr.matmul_act_backward(strided(dy, pad), z, x, w, act, b), clean):
+            assert torch.equal(got, want)
+    bad = dy.clone()
+    bad[1, 0], bad[1, n - 1] = float("inf"), float("nan")
+    dx, dw, db = gr.matmul_act_backward(bad, z, x, w, act, b)
+    assert torch.isnan(dx[1]).all() and torch.isnan(dw[n - 1]).all() and torch.isnan(db[n - 1]) and not torch.isfinite(dw[0]).any()
+    others, inner = [i for i in range(rows) if i != 1], slice(1, n - 1)
+    assert torch.equal(dx[others], clean[0][others])
+    assert torch.equal(dw[inner], clean[1][inner]) and torch.equal(db[inner], clean[2][inner])
+
+
 @pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
 def test_largest_float16_gradients_stay_finite(act):
     # slopes pass 1 (at most 1.13), so dz can pass float16's largest value; dx and dw here do not

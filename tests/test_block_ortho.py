@@ -173,6 +173,17 @@ def test_non_finite_matrices_stay_apart():
     assert torch.equal(got[[0, 3]], clean[[0, 3]])
 
 
+@pytest.mark.parametrize("m,n", [(20, 30), (100, 300), (300, 100)])
+def test_without_steps_or_norm(m, n):
+    # no steps: the normed matrix itself, where an infinity stays at its place; 0 / 0 with eps 0
+    g = rnd(8, m, n)
+    g[3, 4] = float("inf")
+    got = gr.orthogonalize(g, 0)
+    assert torch.isnan(got[3, 4]) and int(torch.isnan(got).sum()) == 1 and int(got.count_nonzero()) == 1
+    zero = torch.zeros(m, n, device="cuda")
+    assert not gr.orthogonalize(zero).any() and torch.isnan(gr.orthogonalize(zero, eps=0.0)).all()
+
+
 def test_empty_sizes():
     for shape in ((0, 5), (5, 0), (0, 4, 5), (3, 0, 5)):
         assert gr.orthogonalize(torch.zeros(shape, device="cuda")).shape == shape
