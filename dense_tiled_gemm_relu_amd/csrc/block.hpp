@@ -106,6 +106,27 @@ inline bool ortho_is_small(int64_t p, int64_t q)
     const int64_t P = p <= 64 ? 64 : 128;
     return p <= 128 && (q + 127) / 128 * 128 * P <= (int64_t(1) << 15);
 }
+// ... and one launch a step of longer ones, in parts of 256 along the longer side, where
+// every workgroup adds the parts' A = X X^T and makes B of it by itself.  That costs more the
+// more parts there are and the larger A is, so the tile kernel takes the longest ones, and
+// batches that would be more than a round of workgroups.  Five steps in bf16, here and there:
+// 64 x 1024 40 us and 76, 64 x 16384 106 and 130, 64 of 64 x 1024 114 and 190; 128 x 512 72
+// and 85, 128 x 2048 97 and 97, 128 x 4096 126 and 104.
+struct OrthoLong {
+    float* x;                   // X times kOrthoX: batch x parts x what a workgroup's lanes hold
+    float *in, *out;            // A's sums of each part, before the step and after
+    int first, last;
+    float ca, cb, cc;
+};
+constexpr int kOrthoPart = 256;
+inline int ortho_parts(int64_t q) { return int((q + kOrthoPart - 1) / kOrthoPart); }
+inline bool ortho_is_long(int64_t batch, int64_t p, int64_t q)
+{
+    const int64_t P = p <= 64 ? 64 : 128;
+    return p <= 128 && !ortho_is_small(p, q) && ortho_parts(q) * P * P * P <= (int64_t(1) << 24) && ortho_parts(q) * batch <= 256;
+}
+hipError_t launch_ortho_squares(const OrthoArgs& a, int dt, hipStream_t stream);
+hipError_t launch_ortho_long(const OrthoArgs& a, const OrthoSteps& c, float* x, float* sums, int dt, hipStream_t stream);
 hipError_t launch_ortho_small(const OrthoArgs& a, const OrthoSteps& c, int dt, hipStream_t stream);
 // one of the products for every matrix of the batch
 struct OrthoProduct {

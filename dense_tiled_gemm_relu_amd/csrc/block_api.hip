@@ -370,6 +370,13 @@ OrthoPlan plan_ortho(int64_t batch, int64_t rows, int64_t cols)
     o.P = round_up(o.p, 64);
     o.Q = round_up(o.q, 64);
     if (ortho_is_small(o.p, o.q)) return o;
+    if (ortho_is_long(batch, o.p, o.q)) {
+        const uint64_t parts = uint64_t(ortho_parts(o.q)) * uint64_t(batch), P = uint64_t(o.P);
+        o.xl = uint64_t(batch) * kOrthoParts * 8;                       // X of the parts' lanes
+        o.a = o.xl + parts * P * kOrthoPart * 4;                        // two steps' sums
+        o.bytes = o.a + 2 * parts * P * P * 4;
+        return o;
+    }
     o.gram = symmetric_config(Linear{o.P, o.P, o.Q, o.Q, o.Q, true}, batch);
     o.poly = symmetric_config(Linear{o.P, o.P, o.P, o.P, o.P, true}, batch);
     o.step = ortho_config(Linear{o.P, o.Q, o.P, o.P, o.Q, false}, batch);
@@ -418,6 +425,7 @@ extern "C" const char* gemm_relu_orthogonalize_plan(int64_t batch, int64_t rows,
     if (batch == 0 || rows == 0 || cols == 0) return "none";
     if (!ortho_supported(batch, rows, cols)) return "unsupported";
     if (ortho_is_small(std::min(rows, cols), std::max(rows, cols))) return "small";
+    if (ortho_is_long(batch, std::min(rows, cols), std::max(rows, cols))) return "long";
     // every plan's name, kept for good: three products, of which two may name the tiles on
     // their diagonal
     constexpr int CFGS = LIN_64 + 1, DIAGONALS = 3;
@@ -491,11 +499,13 @@ extern "C" int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t 
     const int64_t gram_tiles = triangle(o.P / 64);             // of a cut product
     a.flags = reinterpret_cast<unsigned*>(ws + o.flags);
     a.nflags = o.parts > 1 ? int(gram_tiles) : 0;
-    if (ortho_is_small(o.p, o.q)) {
+    const bool small = ortho_is_small(o.p, o.q);
+    if (small || ortho_is_long(batch, o.p, o.q)) {
         OrthoSteps c{};
         c.steps = steps;
         std::copy_n(coefficients, 3 * steps, c.v);
-        return finish(launch_ortho_small(a, c, dtype, st), st);
+        float *const x = reinterpret_cast<float*>(ws + o.xl), *const sums = reinterpret_cast<float*>(ws + o.a);
+        return finish(small ? launch_ortho_small(a, c, dtype, st) : launch_ortho_long(a, c, x, sums, dtype, st), st);
     }
     hipError_t err = launch_ortho_start(a, dtype, st);
     const uint64_t PQ = uint64_t(o.P) * uint64_t(o.Q), PP = uint64_t(o.P) * uint64_t(o.P);

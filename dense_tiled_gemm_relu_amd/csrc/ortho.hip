@@ -221,12 +221,20 @@ OrthoLaunchFn launcher_ortho(int epi, int cfg)
     }
 }
 
-hipError_t launch_ortho_start(const OrthoArgs& a, int dt, hipStream_t stream)
+hipError_t launch_ortho_squares(const OrthoArgs& a, int dt, hipStream_t stream)
 {
     return with_types(dt, dt, [&](auto x, auto) {
         using T = decltype(x);
-        const hipError_t e = start(&ortho_squares_kernel<T>, dim3(kOrthoParts, a.batch), kSquareThreads, stream, a);
-        if (e != hipSuccess) return e;
+        return start(&ortho_squares_kernel<T>, dim3(kOrthoParts, a.batch), kSquareThreads, stream, a);
+    });
+}
+
+hipError_t launch_ortho_start(const OrthoArgs& a, int dt, hipStream_t stream)
+{
+    const hipError_t e = launch_ortho_squares(a, dt, stream);
+    if (e != hipSuccess) return e;
+    return with_types(dt, dt, [&](auto x, auto) {
+        using T = decltype(x);
         return start(&ortho_start_kernel<T>, dim3((unsigned)(a.P / 64) * (unsigned)(a.Q / 64), a.batch), kThreads, stream, a);
     });
 }

@@ -1,8 +1,8 @@
-// Orthogonalisation of small matrices: all steps of one in one workgroup.
+// Orthogonalisation where the shorter side is at most 128: all steps of a small matrix in one
+// workgroup, one launch a step of a long one.
 //
 // A step's three products on the tile kernel are three launches of 5 us whatever the
-// size.  Where the shorter side is at most 128 and a padded matrix has at most 32768
-// elements, eight waves hold X in fp32 registers (64 a lane), its float16 copy and A and B
+// size.  Where a padded matrix has at most 32768 elements, eight waves hold X in fp32 registers (64 a lane), its float16 copy and A and B
 // = b A + c A^2 without their diagonals in LDS, so a call is one launch.  Arithmetic and
 // scales are those of ortho.hip, but for X, which is fp32 here.  Rows in LDS are padded by
 // 16 bytes, which puts the 16 rows of a matrix operand on different banks.
@@ -12,6 +12,10 @@
 // through LDS in short loops: a workgroup runs such code once, and with 61 KB of unrolled
 // loads and stores 128 x 256 without any step took 27 us, with the loops 11.  Five steps: 128
 // x 256 bf16 43 us, 64 x 512 29, 64 x 128 14; on the tile kernel 85 to 90.
+//
+// A long matrix's step is such a step of each part of 256 columns, between launches that
+// exchange the parts' sums of A: 7 to 13 us, of which 3 the launch, 1 to 3 the sums, 1 to 2 X
+// from and to memory, and the rest as above.
 #include "block.hpp"
 #include "row_common.hpp"
 
@@ -22,8 +26,9 @@ namespace {
 constexpr int kSmallThreads = 512, kSmallWaves = kSmallThreads / 64;
 
 // P: the padded shorter side; CB: blocks of 16 columns of X a wave has, the padded longer
-// side being 128 CB
-template <int P, int CB> __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(OrthoArgs a, OrthoSteps c, int dt)
+// side being 128 CB, or with LONG a workgroup's part of it
+template <int P, int CB, bool LONG>
+__global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(OrthoArgs a, OrthoSteps c, OrthoLong part_of, int dt)
 {
     using In = InTraits<DT_F16, 16>;
     using Op = typename In::Op;
@@ -40,8 +45,10 @@ template <int P, int CB> __global__ void __launch_bounds__(kSmallThreads) ortho_
     __shared__ double part[kSmallWaves];
     const int lane = (int)(threadIdx.x & 63), wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
     const int r16 = lane & 15, g4 = lane >> 4;
-    const size_t batch = blockIdx.x;
+    const size_t batch = LONG ? blockIdx.y : blockIdx.x;
+    const int q0 = LONG ? (int)blockIdx.x * Q : 0;
     const bool tall = a.rows > a.cols;
+    const int row0 = tall ? q0 : 0, col0 = tall ? 0 : q0;
 
     // in: |g| in binary64 (the values may be any fp32 ones) on the way, zeros around it
     double s = 0.0;
@@ -58,14 +65,15 @@ template <int P, int CB> __global__ void __launch_bounds__(kSmallThreads) ortho_
                 for (int u = 0; u < ROWS; ++u)
 #pragma unroll
                     for (int k = 0; k < COLS; ++k)
-                        v[u][k] = g[(size_t)min(r0 + u * kSmallWaves, a.rows - 1) * (size_t)a.g_stride + min(64 * k + lane, a.cols - 1)];
+                        v[u][k] = g[(size_t)min(row0 + r0 + u * kSmallWaves, a.rows - 1) * (size_t)a.g_stride +
+                                    min(col0 + 64 * k + lane, a.cols - 1)];
 #pragma unroll
                 for (int u = 0; u < ROWS; ++u)
 #pragma unroll
                     for (int k = 0; k < COLS; ++k) {
                         const int r = r0 + u * kSmallWaves, j = 64 * k + lane;
-                        const float in = r < a.rows && j < a.cols ? (float)v[u][k] : 0.0f;
-                        s = fma((double)in, (double)in, s);
+                        const float in = row0 + r < a.rows && col0 + j < a.cols ? (float)v[u][k] : 0.0f;
+                        if constexpr (!LONG) s = fma((double)in, (double)in, s);
                         raw[tall ? j * RP + r : r * RP + j] = in;
                     }
             }
@@ -75,37 +83,44 @@ template <int P, int CB> __global__ void __launch_bounds__(kSmallThreads) ortho_
         else
             rows_of(std::integral_constant<int, Q>{}, std::integral_constant<int, P>{});
     };
-    if (dt == DT_F32)
-        load_all(0.0f);
-    else if (dt == DT_F16)
-        load_all((_Float16)0.0f);
-    else
-        load_all((__bf16)0.0f);
-#pragma unroll
-    for (int step = 1; step < 64; step *= 2) s += __shfl_xor(s, step);
-    if (lane == 0) part[wave] = s;
-    __syncthreads();
-    s = part[0];
-#pragma unroll
-    for (int k = 1; k < kSmallWaves; ++k) s += part[k];
-    // the scale as an fp32 number times a power of two: it may be past fp32's range
-    const double scale = (double)kOrthoX / (sqrt(s) + (double)a.eps);
-    int power;
-    const float factor = (float)frexp(scale, &power);
-
     // element (p, q) of X, q the longer side; a lane has rows 16 i + r16, columns 4 g4 .. +3
     // of its wave's CB blocks
     f32x4_t x[RB][CB];
     const auto column = [&](int j) { return (wave * CB + j) * 16 + 4 * g4; };
+    const auto start_x = [&] {
+        if (dt == DT_F32)
+            load_all(0.0f);
+        else if (dt == DT_F16)
+            load_all((_Float16)0.0f);
+        else
+            load_all((__bf16)0.0f);
+        if constexpr (LONG) {
 #pragma unroll
-    for (int i = 0; i < RB; ++i)
-#pragma unroll
-        for (int j = 0; j < CB; ++j) {
-            x[i][j] = *reinterpret_cast<const f32x4_t*>(raw + (16 * i + r16) * RP + column(j));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[i][j][e] = ldexpf(x[i][j][e] * factor, power);
+            for (int k = 0; k < kOrthoParts; k += 64) s += a.squares[batch * kOrthoParts + k + lane];
         }
-    __syncthreads();                                            // read, so xh may take its place
+#pragma unroll
+        for (int step = 1; step < 64; step *= 2) s += __shfl_xor(s, step);
+        if (!LONG && lane == 0) part[wave] = s;
+        __syncthreads();
+        if constexpr (!LONG) {
+            s = part[0];
+#pragma unroll
+            for (int k = 1; k < kSmallWaves; ++k) s += part[k];
+        }
+        // the scale as an fp32 number times a power of two: it may be past fp32's range
+        const double scale = (double)kOrthoX / (sqrt(s) + (double)a.eps);
+        int power;
+        const float factor = (float)frexp(scale, &power);
+#pragma unroll
+        for (int i = 0; i < RB; ++i)
+#pragma unroll
+            for (int j = 0; j < CB; ++j) {
+                x[i][j] = *reinterpret_cast<const f32x4_t*>(raw + (16 * i + r16) * RP + column(j));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[i][j][e] = ldexpf(x[i][j][e] * factor, power);
+            }
+        __syncthreads();                                        // read, so xh may take its place
+    };
     const auto put_x = [&] {
 #pragma unroll
         for (int i = 0; i < RB; ++i)
@@ -117,7 +132,6 @@ template <int P, int CB> __global__ void __launch_bounds__(kSmallThreads) ortho_
                 *reinterpret_cast<H4*>(&xh[(16 * i + r16) * XP + column(j)]) = h;
             }
     };
-    put_x();
 
     // rows 16 b .. of a matrix whose rows run along k, k-step s
     const auto row_operand = [&](const _Float16* m, int pitch, int b, int s) {
@@ -145,10 +159,8 @@ template <int P, int CB> __global__ void __launch_bounds__(kSmallThreads) ortho_
         }
     };
 
-    for (int step = 0; step < c.steps; ++step) {
-        const float ca = c.v[3 * step], cb = c.v[3 * step + 1], cc = c.v[3 * step + 2];
-        __syncthreads();
-        square(xh, XP, Q / 32);
+    // the rest of a step from the sums of A = X X^T in acc; xh holds X
+    const auto rest_of_step = [&](float ca, float cb, float cc) {
 #pragma unroll
         for (int i = 0; i < GR; ++i)
 #pragma unroll
@@ -229,11 +241,70 @@ template <int P, int CB> __global__ void __launch_bounds__(kSmallThreads) ortho_
                 for (int e = 0; e < 4; ++e) x[i][j][e] = fmaf(d, x[i][j][e], y[i][j][e] * (1.0f / kOrthoB));
         }
         __syncthreads();                                        // every wave has read xh
-        put_x();
+    };
+
+    if constexpr (!LONG) {
+        start_x();
+        for (int step = 0; step < c.steps; ++step) {
+            put_x();
+            __syncthreads();
+            square(xh, XP, Q / 32);
+            rest_of_step(c.v[3 * step], c.v[3 * step + 1], c.v[3 * step + 2]);
+        }
+    } else {
+        // Where a lane's values lie: its own ones of X, and those of A of each part of the
+        // matrix, which it adds in order.
+        f32x4_t* const own = reinterpret_cast<f32x4_t*>(part_of.x) + ((batch * gridDim.x + blockIdx.x) * (RB * CB)) * kSmallThreads + threadIdx.x;
+        const auto sums_of = [&](float* p, size_t chunk) {
+            return reinterpret_cast<f32x4_t*>(p) + ((batch * gridDim.x + chunk) * (GR * GC)) * kSmallThreads + threadIdx.x;
+        };
+        if (part_of.first) {
+            start_x();
+            if (!part_of.last) put_x();
+        } else {
+#pragma unroll
+            for (int i = 0; i < RB; ++i)
+#pragma unroll
+                for (int j = 0; j < CB; ++j) x[i][j] = own[(i * CB + j) * kSmallThreads];
+#pragma unroll
+            for (int i = 0; i < GR; ++i)
+#pragma unroll
+                for (int j = 0; j < GC; ++j) acc[i][j] = f32x4_t{};
+            constexpr int AHEAD = P == 64 ? 4 : 2;
+            for (int k = 0; k < (int)gridDim.x; k += AHEAD) {
+                f32x4_t v[AHEAD][GR * GC];
+#pragma unroll
+                for (int u = 0; u < AHEAD; ++u) {
+                    const f32x4_t* from = sums_of(part_of.in, min(k + u, (int)gridDim.x - 1));
+#pragma unroll
+                    for (int b = 0; b < GR * GC; ++b) v[u][b] = from[b * kSmallThreads];
+                }
+#pragma unroll
+                for (int u = 0; u < AHEAD; ++u)
+                    if (k + u < (int)gridDim.x) {
+#pragma unroll
+                        for (int b = 0; b < GR * GC; ++b) acc[b / GC][b % GC] += v[u][b];
+                    }
+            }
+            put_x();
+            rest_of_step(part_of.ca, part_of.cb, part_of.cc);
+            if (!part_of.last) put_x();
+        }
+        if (!part_of.last) {
+            __syncthreads();
+            square(xh, XP, Q / 32);
+            f32x4_t* to = sums_of(part_of.out, blockIdx.x);
+#pragma unroll
+            for (int b = 0; b < GR * GC; ++b) to[b * kSmallThreads] = acc[b / GC][b % GC];
+#pragma unroll
+            for (int i = 0; i < RB; ++i)
+#pragma unroll
+                for (int j = 0; j < CB; ++j) own[(i * CB + j) * kSmallThreads] = x[i][j];
+            return;
+        }
     }
 
     // out, through LDS again
-    __syncthreads();
     typedef __bf16 B4 __attribute__((ext_vector_type(4)));
     __bf16* const staged = reinterpret_cast<__bf16*>(memory);
 #pragma unroll
@@ -247,10 +318,11 @@ template <int P, int CB> __global__ void __launch_bounds__(kSmallThreads) ortho_
         }
     __syncthreads();
     __bf16* out = static_cast<__bf16*>(a.out) + batch * (size_t)a.rows * (size_t)a.cols;
-    for (int r = wave; r < a.rows; r += kSmallWaves)
+    const int rows = min(a.rows - row0, tall ? Q : P), cols = min(a.cols - col0, tall ? P : Q);
+    for (int r = wave; r < rows; r += kSmallWaves)
 #pragma unroll 4
-        for (int j = lane; j < a.cols; j += 64)
-            out[(size_t)r * (size_t)a.cols + j] = tall ? staged[j * XP + r] : staged[r * XP + j];
+        for (int j = lane; j < cols; j += 64)
+            out[(size_t)(row0 + r) * (size_t)a.cols + col0 + j] = tall ? staged[j * XP + r] : staged[r * XP + j];
 }
 
 }  // namespace
@@ -258,21 +330,40 @@ template <int P, int CB> __global__ void __launch_bounds__(kSmallThreads) ortho_
 hipError_t launch_ortho_small(const OrthoArgs& a, const OrthoSteps& c, int dt, hipStream_t stream)
 {
     const int blocks = (a.q + 127) / 128;
-    const auto go = [&](auto kernel) { return start(kernel, dim3(a.batch), kSmallThreads, stream, a, c, dt); };
+    const auto go = [&](auto kernel) { return start(kernel, dim3(a.batch), kSmallThreads, stream, a, c, OrthoLong{}, dt); };
     if (a.p <= 64) {
         switch (blocks) {
-        case 1: return go(&ortho_small_kernel<64, 1>);
-        case 2: return go(&ortho_small_kernel<64, 2>);
-        case 3: return go(&ortho_small_kernel<64, 3>);
-        case 4: return go(&ortho_small_kernel<64, 4>);
+        case 1: return go(&ortho_small_kernel<64, 1, false>);
+        case 2: return go(&ortho_small_kernel<64, 2, false>);
+        case 3: return go(&ortho_small_kernel<64, 3, false>);
+        case 4: return go(&ortho_small_kernel<64, 4, false>);
         default: return hipErrorInvalidValue;
         }
     }
     switch (blocks) {
-    case 1: return go(&ortho_small_kernel<128, 1>);
-    case 2: return go(&ortho_small_kernel<128, 2>);
+    case 1: return go(&ortho_small_kernel<128, 1, false>);
+    case 2: return go(&ortho_small_kernel<128, 2, false>);
     default: return hipErrorInvalidValue;
     }
+}
+
+hipError_t launch_ortho_long(const OrthoArgs& a, const OrthoSteps& c, float* x, float* sums, int dt, hipStream_t stream)
+{
+    hipError_t e = launch_ortho_squares(a, dt, stream);
+    const int parts = ortho_parts(a.q);
+    const size_t size = (size_t)a.batch * (size_t)parts * (size_t)a.P * (size_t)a.P;
+    // the launch before the first step leaves X and the parts' A, each step the next's
+    for (int step = -1; step < c.steps && e == hipSuccess; ++step) {
+        OrthoLong part_of{x, sums + (step & 1 ? 0 : size), sums + (step & 1 ? size : 0), step < 0, step == c.steps - 1, 0.0f, 0.0f, 0.0f};
+        if (step >= 0) {
+            part_of.ca = c.v[3 * step];
+            part_of.cb = c.v[3 * step + 1];
+            part_of.cc = c.v[3 * step + 2];
+        }
+        e = start(a.p <= 64 ? &ortho_small_kernel<64, 2, true> : &ortho_small_kernel<128, 2, true>, dim3(parts, a.batch),
+                  kSmallThreads, stream, a, OrthoSteps{}, part_of, dt);
+    }
+    return e;
 }
 
 }  // namespace gemm_relu_hip

@@ -7,6 +7,8 @@ Frobenius, ||.|| the largest singular value,
   E_X' <= L E_X + ||X|| E_B + u ||B|| |X|,  L the largest slope |a| + 3 |b| s^2 + 5 |c| s^4
 at s = ||X||, to which a tenth is added for the products of errors and the fp32 sums.
 """
+import ctypes
+
 import pytest
 import torch
 
@@ -18,7 +20,8 @@ pytestmark = pytest.mark.gpu
 QUINTIC = (3.4445, -4.7750, 2.0315)
 SIZES = [(1, 1), (1, 64), (64, 1), (2, 3), (64, 64), (17, 300), (400, 33), (64, 512), (512, 64), (64, 513), (65, 65), (65, 200),
          (200, 65), (128, 128), (128, 256), (256, 128), (128, 257), (129, 129), (128, 130), (256, 256), (300, 1001), (1001, 300),
-         (520, 520), (129, 2050), (1030, 1024), (2100, 2100), (4100, 700)]
+         (520, 520), (129, 2050), (1030, 1024), (2100, 2100), (4100, 700), (1, 700), (33, 5000), (16384, 64), (64, 16385), (128, 2048), (128, 4096),
+         (4095, 90), (65, 1111)]
 
 
 def largest(a):
@@ -96,7 +99,8 @@ def scattered(m, n, k, seed):
 @pytest.mark.parametrize("m,n,k", [(1, 1, 0), (1, 64, 2), (64, 1, 2), (5, 7, 2), (64, 64, 4), (60, 500, 4), (500, 60, 4),
                                    (30, 300, 3), (300, 30, 3), (33, 100, 3), (128, 128, 4), (100, 250, 4), (250, 100, 4), (65, 200, 4), (200, 65, 4),
                                    (130, 131, 4), (256, 256, 5), (300, 1001, 5), (1001, 300, 5), (520, 520, 5), (129, 2050, 5),
-                                   (1030, 1024, 5), (2100, 2100, 6), (4100, 700, 6), (700, 9000, 6)])
+                                   (1030, 1024, 5), (2100, 2100, 6), (4100, 700, 6), (700, 9000, 6), (50, 4001, 4), (16384, 64, 4),
+                                   (128, 2048, 4), (128, 4096, 4), (3000, 100, 4), (70, 300, 4)])
 def test_exact_step(m, n, k, dtype):
     # few entries a row: A and A^2 are whole numbers of at most 9 bits times a power of two,
     # and so is B where it is a multiple of one of them
@@ -140,7 +144,7 @@ def test_coefficients_of_each_step():
     assert torch.equal(gr.orthogonalize(g, 3, schedule[:3]), gr.orthogonalize(g, 3))
 
 
-@pytest.mark.parametrize("m,n", [(50, 31), (100, 70), (70, 100), (200, 300), (300, 200), (256, 512), (1100, 1200)])
+@pytest.mark.parametrize("m,n", [(50, 31), (50, 1000), (1500, 100), (100, 70), (70, 100), (200, 300), (300, 200), (256, 512), (1100, 1200)])
 def test_batches_and_strides(m, n):
     g = rnd(5, 5, m, n).to(BF16)
     g[1] *= 1e-20
@@ -165,12 +169,35 @@ def test_scale_does_not_matter():
 
 
 def test_non_finite_matrices_stay_apart():
-    g = rnd(7, 4, 100, 130)
-    clean = gr.orthogonalize(g)
-    g[1, 99, 129], g[2, 0, 0] = float("nan"), float("inf")
-    got = gr.orthogonalize(g)
-    assert torch.isnan(got[1]).all() and torch.isnan(got[2]).all()
-    assert torch.equal(got[[0, 3]], clean[[0, 3]])
+    for m, n in ((100, 130), (300, 130), (100, 600), (3000, 40)):
+        g = rnd(7, 4, m, n)
+        clean = gr.orthogonalize(g)
+        g[1, m - 1, n - 1], g[2, 0, 0] = float("nan"), float("inf")
+        got = gr.orthogonalize(g)
+        assert torch.isnan(got[1]).all() and torch.isnan(got[2]).all()
+        assert torch.equal(got[[0, 3]], clean[[0, 3]])
+
+
+def test_plans_by_size():
+    plan = lambda *size: gr.library().gemm_relu_orthogonalize_plan(*size).decode()
+    assert plan(1, 64, 512) == plan(1000, 256, 128) == "small"
+    assert plan(1, 64, 513) == plan(85, 600, 20) == plan(1, 128, 2048) == plan(4, 16384, 64) == "long"
+    assert all("," in plan(*size) for size in ((1, 129, 300), (1, 128, 2049), (5, 16384, 64), (1, 64, 16385)))
+
+
+def test_long_workspace_with_nothing_behind_it():
+    # sizes at the ends of the rule: what lies behind each of its parts stays as it is
+    g = rnd(9, 3, 100, 700)
+    want = gr.orthogonalize(g)
+    lib = gr.library()
+    need = lib.gemm_relu_orthogonalize_workspace(3, 100, 700)
+    ws = torch.full((need + 4096,), 77, dtype=torch.uint8, device="cuda")
+    out = torch.full((3 * 100 * 700 + 512,), 5.0, dtype=BF16, device="cuda")
+    c = (ctypes.c_float * 15)(*(QUINTIC * 5))
+    status = lib.gemm_relu_orthogonalize(g.data_ptr(), 700, 70000, out.data_ptr(), 3, 100, 700, 2, c, 5, 1e-7,
+                                         ws.data_ptr(), need, torch.cuda.current_stream().cuda_stream)
+    assert status == 0 and torch.equal(out[:210000].view(3, 100, 700), want)
+    assert (out[210000:] == 5).all() and (ws[need:] == 77).all()
 
 
 @pytest.mark.parametrize("m,n", [(20, 30), (100, 300), (300, 100)])
