@@ -111,7 +111,8 @@ inline bool ortho_is_small(int64_t p, int64_t q)
 // more parts there are and the larger A is, so the tile kernel takes the longest ones, and
 // batches that would be more than a round of workgroups.  Five steps in bf16, here and there:
 // 64 x 1024 40 us and 76, 64 x 16384 106 and 130, 64 of 64 x 1024 114 and 190; 128 x 512 72
-// and 85, 128 x 2048 97 and 97, 128 x 4096 126 and 104.
+// and 85, 128 x 2048 97 and 97, 128 x 4096 126 and 104.  (Parts of 128 columns of 128 rows: 128
+// x 512 62 us, but 64 of them 167 instead of 139, 32 of 128 x 1024 187 instead of 132.)
 struct OrthoLong {
     float* x;                   // X times kOrthoX: batch x parts x what a workgroup's lanes hold
     float *in, *out;            // A's sums of each part, before the step and after
