@@ -86,13 +86,15 @@ struct OrthoArgs {
     int rows, cols, batch;
     int p, q, P, Q;             // q: the longer side
     float eps;
-    double* squares;            // kOrthoParts sums of squares a matrix
+    double* squares;            // sums of squares: `parts` a matrix, kOrthoParts apart
+    int parts;
     void* xh;                   // X times kOrthoX as float16: batch x P x Q
     void* xl;                   // and kLowScale times what that loses
     unsigned* flags;            // nflags counters a matrix, to clear
     int nflags;
 };
 constexpr int kOrthoParts = 256;
+int ortho_square_parts(int64_t rows, int64_t cols, int dt);
 hipError_t launch_ortho_start(const OrthoArgs& a, int dt, hipStream_t stream);
 hipError_t launch_ortho_copy(const OrthoArgs& a, hipStream_t stream);      // no steps: X as it is
 // all steps of small matrices in one launch (ortho_small.hip): the shorter side at most 128
@@ -110,9 +112,9 @@ inline bool ortho_is_small(int64_t p, int64_t q)
 // every workgroup adds the parts' A = X X^T and makes B of it by itself.  That costs more the
 // more parts there are and the larger A is, so the tile kernel takes the longest ones, and
 // batches that would be more than a round of workgroups.  Five steps in bf16, here and there:
-// 64 x 1024 40 us and 76, 64 x 16384 106 and 130, 64 of 64 x 1024 114 and 190; 128 x 512 72
+// 64 x 1024 40 us and 76, 64 x 16384 106 and 130, 64 of 64 x 1024 73 and 150; 128 x 512 72
 // and 85, 128 x 2048 97 and 97, 128 x 4096 126 and 104.  (Parts of 128 columns of 128 rows: 128
-// x 512 62 us, but 64 of them 167 instead of 139, 32 of 128 x 1024 187 instead of 132.)
+// x 512 62 us, but 64 of them 28 more, 32 of 128 x 1024 55 more.)
 struct OrthoLong {
     float* x;                   // X times kOrthoX: batch x parts x what a workgroup's lanes hold
     float *in, *out;            // A's sums of each part, before the step and after

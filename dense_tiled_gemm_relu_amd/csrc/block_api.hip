@@ -494,6 +494,7 @@ extern "C" int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t 
     a.Q = int(o.Q);
     a.eps = eps;
     a.squares = reinterpret_cast<double*>(ws + o.squares);
+    a.parts = ortho_square_parts(rows, cols, dtype);
     a.xh = ws + o.xh[0];
     a.xl = ws + o.xl;
     const int64_t gram_tiles = triangle(o.P / 64);             // of a cut product

@@ -20,9 +20,12 @@ namespace gemm_relu_hip {
 namespace {
 
 // ------------------------------------------------------- before the steps
-// Sums of squares in binary64 (the values may be any fp32 ones): kOrthoParts workgroups
-// a matrix take rows in turns, 16 bytes a thread.
+// Sums of squares in binary64 (the values may be any fp32 ones): workgroups take rows in
+// turns, 16 bytes a thread; of short rows up to four turns each (8 of 1792 x 36 bf16 in 32
+// workgroups each 5 us, 10 in 256 of which 144 have nothing).
 constexpr int kSquareThreads = 1024;
+// threads that share a row of so many pieces of 16 bytes
+__host__ __device__ constexpr int square_threads(int chunks) { return chunks + 64 < kSquareThreads ? (chunks + 64) / 64 * 64 : kSquareThreads; }
 template <class T> __global__ void __launch_bounds__(kSquareThreads) ortho_squares_kernel(OrthoArgs a)
 {
     constexpr int N = Chunk<T>::N;
@@ -32,9 +35,9 @@ template <class T> __global__ void __launch_bounds__(kSquareThreads) ortho_squar
     double s = 0.0;
     const auto add = [&](float v) { s = fma((double)v, (double)v, s); };
     // short rows: several at a time
-    const int chunks = a.cols / N, wide = min(kSquareThreads, (chunks + 1 + 63) / 64 * 64), rows_here = kSquareThreads / wide;
+    const int chunks = a.cols / N, wide = square_threads(chunks), rows_here = kSquareThreads / wide;
     const int t = (int)threadIdx.x % wide, own = (int)threadIdx.x / wide;
-    for (int64_t r = (int64_t)blockIdx.x * rows_here + own; own < rows_here && r < a.rows; r += kOrthoParts * rows_here) {
+    for (int64_t r = (int64_t)blockIdx.x * rows_here + own; own < rows_here && r < a.rows; r += (int64_t)gridDim.x * rows_here) {
         const T* row = g + (size_t)r * (size_t)a.g_stride;
         constexpr int AHEAD = 4;
         int j = t;
@@ -97,7 +100,7 @@ template <class T> __global__ void __launch_bounds__(kThreads) ortho_start_kerne
     }
     double s = 0.0;
 #pragma unroll
-    for (int k = 0; k < kOrthoParts; k += 64) s += a.squares[batch * kOrthoParts + k + lane];
+    for (int k = 0; k < kOrthoParts; k += 64) s += k + lane < a.parts ? a.squares[batch * kOrthoParts + k + lane] : 0.0;
 #pragma unroll
     for (int step = 1; step < 64; step *= 2) s += __shfl_xor(s, step);
     // the scale as an fp32 number times a power of two: it may be past fp32's range
@@ -221,11 +224,19 @@ OrthoLaunchFn launcher_ortho(int epi, int cfg)
     }
 }
 
+int ortho_square_parts(int64_t rows, int64_t cols, int dt)
+{
+    const int rows_here = kSquareThreads / square_threads(int(cols / (16 / elem_size(dt))));
+    int64_t parts = ceil_div(rows, rows_here);
+    if (rows_here >= 4 && parts > 32) parts = std::max<int64_t>(32, ceil_div(parts, 4));
+    return int(std::min<int64_t>(parts, kOrthoParts));
+}
+
 hipError_t launch_ortho_squares(const OrthoArgs& a, int dt, hipStream_t stream)
 {
     return with_types(dt, dt, [&](auto x, auto) {
         using T = decltype(x);
-        return start(&ortho_squares_kernel<T>, dim3(kOrthoParts, a.batch), kSquareThreads, stream, a);
+        return start(&ortho_squares_kernel<T>, dim3(a.parts, a.batch), kSquareThreads, stream, a);
     });
 }
 

@@ -96,7 +96,7 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(OrthoArgs a,
             load_all((__bf16)0.0f);
         if constexpr (LONG) {
 #pragma unroll
-            for (int k = 0; k < kOrthoParts; k += 64) s += a.squares[batch * kOrthoParts + k + lane];
+            for (int k = 0; k < kOrthoParts; k += 64) s += k + lane < a.parts ? a.squares[batch * kOrthoParts + k + lane] : 0.0;
         }
 #pragma unroll
         for (int step = 1; step < 64; step *= 2) s += __shfl_xor(s, step);
