@@ -165,7 +165,9 @@ def orthogonalize(g, steps=5, coefficients=NEWTON_SCHULZ, eps=1e-7, stream=None)
 
     g: (m, n), or a batch (b, m, n) of matrices each on its own; float16, bfloat16 or
     float32, with contiguous rows.  coefficients: (a, b, c), or a triple for each step.
-    Returns bfloat16 of g's shape; it is within 1e-3 of its norm before that rounding.
+    Returns bfloat16 of g's shape.  Before that rounding it is within 3e-3 of its norm for up
+    to 6 steps of the default coefficients where the shorter side is at least 16 (1e-2 for
+    up to 5 below that), whatever g's singular values; include/gemm_relu_block.h says more.
     """
     steps = int(steps)
     if not 0 <= steps <= 64:

@@ -88,8 +88,10 @@ struct OrthoArgs {
     float eps;
     double* squares;            // sums of squares: `parts` a matrix, kOrthoParts apart
     int parts;
-    void* xh;                   // X times kOrthoX as float16: batch x P x Q
-    void* xl;                   // and kLowScale times what that loses
+    // X times kOrthoX as float16 (xh) and kLowScale times what that loses (xl): P x Q each, one
+    // matrix's 2 P Q values from the next's, so that [xl; xh] is one operand of 2 P rows
+    void* xh;
+    void* xl;
     unsigned* flags;            // nflags counters a matrix, to clear
     int nflags;
 };
@@ -112,9 +114,9 @@ inline bool ortho_is_small(int64_t p, int64_t q)
 // every workgroup adds the parts' A = X X^T and makes B of it by itself.  That costs more the
 // more parts there are and the larger A is, so the tile kernel takes the longest ones, and
 // batches that would be more than a round of workgroups.  Five steps in bf16, here and there:
-// 64 x 1024 40 us and 76, 64 x 16384 106 and 130, 64 of 64 x 1024 73 and 150; 128 x 512 72
-// and 85, 128 x 2048 97 and 97, 128 x 4096 126 and 104.  (Parts of 128 columns of 128 rows: 128
-// x 512 62 us, but 64 of them 28 more, 32 of 128 x 1024 55 more.)
+// 64 x 1024 49 us and 97, 64 x 16384 112 and 130, 64 of 64 x 1024 80 and 150; 128 x 512 85
+// and 94, 128 x 2048 109 and 105, 8 of them 124 and 133.  (Parts of 128 columns of 128 rows, before
+// X's low half was an operand: 128 x 512 62 us for 72, but 64 of them 28 more, 32 of 128 x 1024 55 more.)
 struct OrthoLong {
     float* x;                   // X times kOrthoX: batch x parts x what a workgroup's lanes hold
     float *in, *out;            // A's sums of each part, before the step and after
@@ -134,7 +136,7 @@ hipError_t launch_ortho_small(const OrthoArgs& a, const OrthoSteps& c, int dt, h
 // one of the products for every matrix of the batch
 struct OrthoProduct {
     KernelArgs k;
-    uint64_t a, b, c, r;        // bytes from one matrix's A, B, C, R and L to the next's
+    uint64_t a, b, c, r, low;   // bytes from one matrix's A, B, C, R and L, low to the next's
     uint64_t diag, ws, flags;   // values from one matrix's diagonals, partial sums, counters to the next's
 };
 typedef hipError_t (*OrthoLaunchFn)(const OrthoProduct& p, int tiles, int batch, hipStream_t stream);

@@ -305,7 +305,7 @@ struct OrthoPlan {
     Symmetric gram, poly;                       // configurations of the products
     int step;
     int64_t parts = 1, split_steps = 0;         // of A's K, with LIN_64: steps each
-    uint64_t squares, xl, xh[2], a, b, diag_a, diag_b, flags, sums, bytes;
+    uint64_t squares, x[2], a, b, diag_a, diag_b, flags, sums, bytes;
 };
 int64_t triangle(int64_t side) { return side * (side + 1) / 2; }
 int64_t side_of(int cfg, const Linear& l) { return ceil_div(l.M, linear_info(cfg).bm); }
@@ -372,14 +372,14 @@ OrthoPlan plan_ortho(int64_t batch, int64_t rows, int64_t cols)
     if (ortho_is_small(o.p, o.q)) return o;
     if (ortho_is_long(batch, o.p, o.q)) {
         const uint64_t parts = uint64_t(ortho_parts(o.q)) * uint64_t(batch), P = uint64_t(o.P);
-        o.xl = uint64_t(batch) * kOrthoParts * 8;                       // X of the parts' lanes
-        o.a = o.xl + parts * P * kOrthoPart * 4;                        // two steps' sums
+        o.x[0] = uint64_t(batch) * kOrthoParts * 8;                     // X of the parts' lanes
+        o.a = o.x[0] + parts * P * kOrthoPart * 4;                        // two steps' sums
         o.bytes = o.a + 2 * parts * P * P * 4;
         return o;
     }
     o.gram = symmetric_config(Linear{o.P, o.P, o.Q, o.Q, o.Q, true}, batch);
     o.poly = symmetric_config(Linear{o.P, o.P, o.P, o.P, o.P, true}, batch);
-    o.step = ortho_config(Linear{o.P, o.Q, o.P, o.P, o.Q, false}, batch);
+    o.step = ortho_config(Linear{o.P, o.Q, 2 * o.P, 2 * o.P, o.Q, false}, batch);
     split_gram(o, Linear{o.P, o.P, o.Q, o.Q, o.Q, true}, batch);
     uint64_t at = 0;
     const auto take = [&](uint64_t bytes) {
@@ -389,11 +389,10 @@ OrthoPlan plan_ortho(int64_t batch, int64_t rows, int64_t cols)
     };
     const uint64_t PQ = uint64_t(o.P) * uint64_t(o.Q) * uint64_t(batch), PP = uint64_t(o.P) * uint64_t(o.P) * uint64_t(batch);
     o.squares = take(uint64_t(batch) * kOrthoParts * 8);
-    o.xl = take(PQ * 2);
-    o.xh[0] = take(PQ * 2);
-    o.xh[1] = take(PQ * 2);
+    o.x[0] = take(PQ * 4);                      // [xl; xh], before a step and after
+    o.x[1] = take(PQ * 4);
     o.a = take(PP * 2);
-    o.b = take(PP * 2);
+    o.b = take(PP * 4);                         // [B / kLowScale, B]
     o.diag_a = take(uint64_t(o.P) * uint64_t(batch) * 4);
     o.diag_b = take(uint64_t(o.P) * uint64_t(batch) * 4);
     const uint64_t tiles = o.parts > 1 ? uint64_t(triangle(o.P / 64)) * uint64_t(batch) : 0;
@@ -495,8 +494,9 @@ extern "C" int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t 
     a.eps = eps;
     a.squares = reinterpret_cast<double*>(ws + o.squares);
     a.parts = ortho_square_parts(rows, cols, dtype);
-    a.xh = ws + o.xh[0];
-    a.xl = ws + o.xl;
+    const uint64_t PQ = uint64_t(o.P) * uint64_t(o.Q), PP = uint64_t(o.P) * uint64_t(o.P);
+    a.xl = ws + o.x[0];
+    a.xh = ws + o.x[0] + PQ * 2;
     const int64_t gram_tiles = triangle(o.P / 64);             // of a cut product
     a.flags = reinterpret_cast<unsigned*>(ws + o.flags);
     a.nflags = o.parts > 1 ? int(gram_tiles) : 0;
@@ -505,12 +505,11 @@ extern "C" int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t 
         OrthoSteps c{};
         c.steps = steps;
         std::copy_n(coefficients, 3 * steps, c.v);
-        float *const x = reinterpret_cast<float*>(ws + o.xl), *const sums = reinterpret_cast<float*>(ws + o.a);
+        float *const x = reinterpret_cast<float*>(ws + o.x[0]), *const sums = reinterpret_cast<float*>(ws + o.a);
         return finish(small ? launch_ortho_small(a, c, dtype, st) : launch_ortho_long(a, c, x, sums, dtype, st), st);
     }
     hipError_t err = launch_ortho_start(a, dtype, st);
-    const uint64_t PQ = uint64_t(o.P) * uint64_t(o.Q), PP = uint64_t(o.P) * uint64_t(o.P);
-    const Linear gram{o.P, o.P, o.Q, o.Q, o.Q, true}, poly{o.P, o.P, o.P, o.P, o.P, true}, next{o.P, o.Q, o.P, o.P, o.Q, false};
+    const Linear gram{o.P, o.P, o.Q, o.Q, o.Q, true}, poly{o.P, o.P, o.P, o.P, o.P, true}, next{o.P, o.Q, 2 * o.P, 2 * o.P, o.Q, false};
     const auto product = [&](int cfg, const Linear& l, const void* A, const void* B, void* C) {
         OrthoProduct k{};
         k.k = linear_args(plan_as(cfg, l), l, A, B, C);
@@ -531,13 +530,14 @@ extern "C" int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t 
         return launcher_ortho(epi, c.diagonal)(k, int(diagonal_tiles(c, l)), int(batch), st);
     };
     for (int s = 0; s < steps && err == hipSuccess; ++s) {
-        const void* xh = ws + o.xh[s % 2];
+        const unsigned char *const xl = ws + o.x[s % 2], *const xh = xl + PQ * 2;
+        unsigned char* const to = ws + o.x[(s + 1) % 2];
         const bool last = s == steps - 1;
         OrthoProduct k = product(o.gram.cfg, gram, xh, xh, ws + o.a);
         k.k.alpha = kOrthoA / (kOrthoX * kOrthoX);
         k.k.beta = 1.0f / (kOrthoX * kOrthoX);
         k.k.diag = reinterpret_cast<float*>(ws + o.diag_a);
-        k.a = k.b = PQ * 2;
+        k.a = k.b = PQ * 4;
         k.c = PP * 2;
         if (o.parts > 1) {
             k.k.splits = int(o.parts);
@@ -559,24 +559,26 @@ extern "C" int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t 
         k.k.diag_out = reinterpret_cast<float*>(ws + o.diag_b);
         k.k.R = ws + o.a;
         k.k.ldr = int(o.P);
-        k.a = k.b = k.c = k.r = PP * 2;
+        k.a = k.b = k.r = PP * 2;
+        k.c = PP * 4;
         err = symmetric(EPI_POLY, o.poly, poly, k);
         if (err != hipSuccess) break;
-        k = product(o.step, next, ws + o.b, xh, last ? out : ws + o.xh[(s + 1) % 2]);
+        // [B / kLowScale, B] [xl; xh]
+        k = product(o.step, next, ws + o.b, xl, last ? out : to + PQ * 2);
         k.k.alpha = 1.0f / kOrthoX;             // of the last step's result
         k.k.beta = 1.0f / kOrthoB;
         k.k.pa = coefficients[3 * s];
         k.k.diag = reinterpret_cast<float*>(ws + o.diag_b);
-        k.k.R = static_cast<const unsigned char*>(xh);
-        k.k.L = ws + o.xl;
+        k.k.R = xh;
+        k.k.L = xl;
+        k.k.low = to;
         k.k.ldr = int(o.Q);
         k.k.out_m = int(o.p);
         k.k.out_n = int(o.q);
         k.k.transposed = rows > cols;
-        k.a = PP * 2;
-        k.b = PQ * 2;
-        k.c = last ? uint64_t(rows) * uint64_t(cols) * 2 : PQ * 2;
-        k.r = PQ * 2;
+        k.a = PP * 4;
+        k.b = k.r = k.low = PQ * 4;
+        k.c = last ? uint64_t(rows) * uint64_t(cols) * 2 : PQ * 4;
         err = launcher_ortho(last ? EPI_LAST : EPI_STEP, o.step)(k, int(tiles_of(o.step, next)), int(batch), st);
     }
     if (err == hipSuccess && steps == 0) err = launch_ortho_copy(a, st);

@@ -128,14 +128,16 @@ struct KernelArgs {
     const unsigned char* R;
     // Newton-Schulz products: beta scales the sums, scale_o what R holds, alpha what C
     // receives.  EPI_GRAM writes the diagonal to diag and 0 in its place; EPI_POLY reads
-    // that and its operand R (ldr apart), and writes its own diagonal to diag_out;
+    // that and its operand R (ldr apart), writes its own diagonal to diag_out, and leaves
+    // each row twice in C: over kLowScale, then as it is;
     // EPI_STEP reads diag and X as R + L / kLowScale (ldr apart), and writes the new X to C
-    // and L.  EPI_LAST reads the same and leaves its result in C, out_m rows of out_n (or
+    // and low.  EPI_LAST reads the same and leaves its result in C, out_m rows of out_n (or
     // transposed) of bfloat16.  pa, pb, pc: the step's coefficients.
     float beta, scale_o, pa, pb, pc;
     float* diag;
     float* diag_out;
-    unsigned char* L;
+    const unsigned char* L;
+    unsigned char* low;
     int out_m, out_n, transposed;
     // EPI_GRAM and EPI_POLY: which tiles of the symmetric product a launch takes.  0: those on
     // and below the diagonal; 1: those below it; 2: those on and below it inside diagonal
@@ -2000,7 +2002,7 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
                         if constexpr (C::EPI == EPI_STEP) {
                             const u32x2_t rest = {h[0] | ((unsigned)h[1] << 16), h[2] | ((unsigned)h[3] << 16)};
                             if (m < M && n >= n_own && n < N)
-                                *reinterpret_cast<u32x2_t*>(args.L + ((size_t)m * (size_t)N + n) * 2) = rest;
+                                *reinterpret_cast<u32x2_t*>(args.low + ((size_t)m * (size_t)N + n) * 2) = rest;
                         } else {
                             v *= args.alpha;
                         }
@@ -2077,6 +2079,13 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
     } else {
         put_acc();
     }
+    // EPI_POLY: eight float16 of row m from column n on, twice
+    auto put_twice = [&](size_t m, int n, u32x4_t v) {
+        const f16x8_t low = __builtin_bit_cast(f16x8_t, v) * (_Float16)(1.0f / kLowScale);
+        unsigned short* row = reinterpret_cast<unsigned short*>(args.C) + m * 2 * (size_t)N + n;
+        __builtin_memcpy(row, &low, 16);
+        __builtin_memcpy(row + N, &v, 16);
+    };
     // the staged tile's columns as rows of C from row c0 on: 4 x 16 blocks are read
     // transposed, a lane's 8 consecutive rows of the tile are 16 bytes of such a row
     auto store_transposed = [&](int rows, int cols) {
@@ -2091,6 +2100,10 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
             }
             const int n = c0 + cb + i16, m = m0 + rb + 8 * h;
             if (n < c_own || n >= rows || m >= cols) continue;
+            if constexpr (C::EPI == EPI_POLY) {             // (whole pieces: sides are multiples of 64)
+                put_twice((size_t)n, m, __builtin_bit_cast(u32x4_t, __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7)));
+                continue;
+            }
             unsigned short* dst = reinterpret_cast<unsigned short*>(args.C) + (size_t)n * (size_t)cols + m;
             if (m + 8 <= cols) {
                 __builtin_memcpy(dst, part, 16);
@@ -2115,6 +2128,10 @@ __device__ __forceinline__ void gemm_relu_tile(const KernelArgs& args, int wg,
             if (m >= MC || n >= NC || n + 8 <= c_own) return;
             const u32x4_t v = *reinterpret_cast<const GR_LDS u32x4_t*>(
                 smem + r * RB + ((cc ^ (r & XM)) << 4));
+            if constexpr (C::EPI == EPI_POLY) {
+                put_twice((size_t)m, n, v);
+                return;
+            }
             unsigned short* dst = reinterpret_cast<unsigned short*>(args.C) + (size_t)m * NC + n;
             if (n >= c_own && n + 8 <= NC) {
                 // streaming store: C is not read again, so its lines should not

@@ -2,15 +2,18 @@
 // A = X X^T, from X = G / (|G| + eps): the passes over the matrix before and after, and
 // the three products of a step on the tile kernel.
 //
-// Precision.  The products' operands are float16; X itself is the sum of two float16 (22
-// bits: fp32 would be 2 bytes more to write), of which the larger is the operand, and the
-// diagonals of A and of B = b A + c A^2 are fp32.  A step multiplies small singular values by a (485 times over
-// five steps of a = 3.4445), so a rounding of X would grow as much; a rounding of the
-// operands of A, B and B X is only ever multiplied by large singular vectors on one side
-// and stays small.  The diagonals are where A and B are largest near the end (A tends to
-// the identity), and rounding them would lose the most.  Against binary64 over spectra
-// from flat to ten decades the results are off by 1e-4 to 7e-4 of their norm; with X in
-// bfloat16, as such steps are often run, by 1e-2 to 0.5.
+// Precision.  X is the sum of two float16, x = xh + xl (22 bits: fp32 would be 2 bytes more
+// to write), and the diagonals of A and of B = b A + c A^2 are fp32; the other values of A
+// and B are float16 operands, and A is made of xh alone.  A step multiplies small singular
+// values by a (485 times over five steps of a = 3.4445), so a rounding of X would grow as
+// much.  B multiplies xh and xl: so every rounding in A and B is a factor (a + B + error) on
+// X's left, and takes the same share of a small singular direction as of a large one.  B xh
+// alone would leave B xl out, whose right side is any direction; with A's rounding, whose
+// left side is, it couples the small directions among each other, which a then multiplies:
+// off by 2e-2 after five steps of 16 x 16 of one direction over noise of 1e-3, by 0.3 after
+// eight.  As it is, over spectra from flat to six decades, 2e-4 to 2e-3 (shorter sides from
+// 16 on) after five or six.  The diagonals are where A and B are largest near the end (A
+// tends to the identity), and rounding them would lose the most.
 #include "block.hpp"
 #include "linear_tiles.hpp"
 #include "row_common.hpp"
@@ -106,8 +109,8 @@ template <class T> __global__ void __launch_bounds__(kThreads) ortho_start_kerne
     // the scale as an fp32 number times a power of two: it may be past fp32's range
     int power;
     const float factor = (float)frexp((double)kOrthoX / (sqrt(s) + (double)a.eps), &power);
-    _Float16* xh = static_cast<_Float16*>(a.xh) + batch * (size_t)a.P * (size_t)a.Q;
-    _Float16* xl = static_cast<_Float16*>(a.xl) + batch * (size_t)a.P * (size_t)a.Q;
+    _Float16* xh = static_cast<_Float16*>(a.xh) + batch * 2 * (size_t)a.P * (size_t)a.Q;
+    _Float16* xl = static_cast<_Float16*>(a.xl) + batch * 2 * (size_t)a.P * (size_t)a.Q;
     const auto put = [&](int p, int q, const float(&v)[4]) {
         const size_t at = (size_t)p * (size_t)a.Q + q;
         H4 hi, lo;
@@ -151,8 +154,8 @@ __global__ void __launch_bounds__(kThreads) ortho_copy_kernel(OrthoArgs a)
     const int lane = (int)(threadIdx.x & 63), wave = (int)(threadIdx.x >> 6);
     const int tiles = a.Q / 64, p0 = (int)(blockIdx.x / tiles) * 64, q0 = (int)(blockIdx.x % tiles) * 64;
     const bool tall = a.rows > a.cols;
-    const _Float16* xh = static_cast<const _Float16*>(a.xh) + batch * (size_t)a.P * (size_t)a.Q;
-    const _Float16* xl = static_cast<const _Float16*>(a.xl) + batch * (size_t)a.P * (size_t)a.Q;
+    const _Float16* xh = static_cast<const _Float16*>(a.xh) + batch * 2 * (size_t)a.P * (size_t)a.Q;
+    const _Float16* xl = static_cast<const _Float16*>(a.xl) + batch * 2 * (size_t)a.P * (size_t)a.Q;
     __bf16* out = static_cast<__bf16*>(a.out) + batch * (size_t)a.rows * (size_t)a.cols;
     for (int k = wave; k < 64; k += kThreads / 64) {
         const int p = p0 + k, q = q0 + lane;
@@ -170,10 +173,13 @@ __global__ void __launch_bounds__(kThreads) ortho_copy_kernel(OrthoArgs a)
 }
 
 // ------------------------------------------------------------ the products
-// What a step of 8192 x 8192 takes: A 475 us and A^2 485 (half of their products; 1160 TFLOP/s
-// for those), B X 895 (1228 TFLOP/s), whose epilogue reads and writes 8 bytes an element while
-// the matrix units wait: one tile fills a CU.  8 x 1024 x 2048: 43, 31 and 63 us, of which
-// 25 are such an epilogue (one round of tiles); with X in fp32 it was the same.
+// B X is one product over 2 P values of K: [B / kLowScale, B] [xl; xh], the lesser terms first
+// (xl holds kLowScale times what xh loses, B / kLowScale loses nothing that counts beside B
+// xh).  What a step of 8192 x 8192 takes: A 476 us and A^2 511 (half of their products; 1150
+// and 1075 TFLOP/s for those), B X 1664 (1320 TFLOP/s; 895 without xl), whose epilogue
+// reads and writes 8 bytes an element while the matrix units wait: one tile fills a CU.  8 x
+// 1024 x 2048: 43, 35 and 88 us (63 without xl), of which 25 are such an epilogue (one round
+// of tiles); with X in fp32 it was the same.
 template <class C> __global__ void __launch_bounds__(C::NTHREADS, 1) ortho_product_kernel(OrthoProduct p)
 {
     __shared__ __attribute__((aligned(1024))) unsigned char smem_raw[C::LDS_BYTES];
@@ -184,6 +190,7 @@ template <class C> __global__ void __launch_bounds__(C::NTHREADS, 1) ortho_produ
     args.C += batch * p.c;
     args.R += batch * p.r;
     args.L += batch * p.r;
+    args.low += batch * p.low;
     args.diag += batch * p.diag;
     args.diag_out += batch * p.diag;
     args.ws += batch * p.ws;

@@ -11,10 +11,11 @@
 // take 6 reads of 16 bytes a lane for 8 matrix instructions).  The matrix comes and goes
 // through LDS in short loops: a workgroup runs such code once, and with 61 KB of unrolled
 // loads and stores 128 x 256 without any step took 27 us, with the loops 11.  Five steps: 128
-// x 256 bf16 43 us, 64 x 512 29, 64 x 128 14; on the tile kernel 85 to 90.
+// x 256 bf16 53 us, 64 x 512 37, 64 x 128 16 (41, 28 and 12 with B times X's larger half
+// alone); on the tile kernel 87 to 94.
 //
 // A long matrix's step is such a step of each part of 256 columns, between launches that
-// exchange the parts' sums of A: 7 to 13 us, of which 3 the launch, 1 to 3 the sums, 1 to 2 X
+// exchange the parts' sums of A: 8 to 16 us, of which 3 the launch, 1 to 3 the sums, 1 to 2 X
 // from and to memory, and the rest as above.
 #include "block.hpp"
 #include "row_common.hpp"
@@ -121,17 +122,25 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(OrthoArgs a,
             }
         __syncthreads();                                        // read, so xh may take its place
     };
-    const auto put_x = [&] {
+    // X as float16, or LOW kLowScale times what that loses
+    const auto put_x = [&](auto low) {
+        constexpr bool LOW = decltype(low)::value;
 #pragma unroll
         for (int i = 0; i < RB; ++i)
 #pragma unroll
             for (int j = 0; j < CB; ++j) {
                 H4 h;
+                if constexpr (LOW) asm volatile("" : "+v"(x[i][j]));    // converted again, not kept since the step began (spills)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) h[e] = (_Float16)x[i][j][e];
+                for (int e = 0; e < 4; ++e) {
+                    h[e] = (_Float16)x[i][j][e];
+                    if constexpr (LOW) h[e] = (_Float16)((x[i][j][e] - (float)h[e]) * kLowScale);
+                }
                 *reinterpret_cast<H4*>(&xh[(16 * i + r16) * XP + column(j)]) = h;
             }
     };
+    const std::false_type high{};
+    const std::true_type low{};
 
     // rows 16 b .. of a matrix whose rows run along k, k-step s
     const auto row_operand = [&](const _Float16* m, int pitch, int b, int s) {
@@ -207,29 +216,43 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(OrthoArgs a,
                 *reinterpret_cast<H4*>(&bm[m * AP + n]) = h;
             }
         __syncthreads();
-        // B X, its wave's columns: X's rows run along n, so its operands are read transposed
+        // B X, its wave's columns: X's rows run along n, so its operands are read transposed.
+        // First with X's float16, then with what that loses, in the same place: the columns
+        // are the wave's own here, so its own order is enough.
         f32x4_t y[RB][CB];
 #pragma unroll
         for (int i = 0; i < RB; ++i)
 #pragma unroll
             for (int j = 0; j < CB; ++j) y[i][j] = f32x4_t{};
+#pragma unroll 1
+        for (int half_of_x = 0; half_of_x < 2; ++half_of_x) {
+            if (half_of_x) {
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+                put_x(low);
+                asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
 #pragma unroll
-        for (int s = 0; s < P / 32; ++s) {
-            Op right[CB];
+                for (int i = 0; i < RB; ++i)
 #pragma unroll
-            for (int j = 0; j < CB; ++j) {
-                i16x4_t half[2];
-#pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    half[t] = lds_read_tr16((const GR_LDS unsigned char*)&xh[(32 * s + 8 * g4 + 4 * t + (r16 >> 2)) * XP +
-                                                                             (wave * CB + j) * 16 + 4 * (r16 & 3)]);
-                right[j] = __builtin_bit_cast(Op, __builtin_shufflevector(half[0], half[1], 0, 1, 2, 3, 4, 5, 6, 7));
+                    for (int j = 0; j < CB; ++j) y[i][j] *= kLowScale;
             }
 #pragma unroll
-            for (int i = 0; i < RB; ++i) {
-                const Op left = row_operand(bm, AP, i, s);
+            for (int s = 0; s < P / 32; ++s) {
+                Op right[CB];
 #pragma unroll
-                for (int j = 0; j < CB; ++j) y[i][j] = In::mfma(right[j], left, y[i][j]);
+                for (int j = 0; j < CB; ++j) {
+                    i16x4_t half[2];
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+                        half[t] = lds_read_tr16((const GR_LDS unsigned char*)&xh[(32 * s + 8 * g4 + 4 * t + (r16 >> 2)) * XP +
+                                                                                 (wave * CB + j) * 16 + 4 * (r16 & 3)]);
+                    right[j] = __builtin_bit_cast(Op, __builtin_shufflevector(half[0], half[1], 0, 1, 2, 3, 4, 5, 6, 7));
+                }
+#pragma unroll
+                for (int i = 0; i < RB; ++i) {
+                    const Op left = row_operand(bm, AP, i, s);
+#pragma unroll
+                    for (int j = 0; j < CB; ++j) y[i][j] = In::mfma(right[j], left, y[i][j]);
+                }
             }
         }
 #pragma unroll
@@ -238,7 +261,7 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(OrthoArgs a,
 #pragma unroll
             for (int j = 0; j < CB; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[i][j][e] = fmaf(d, x[i][j][e], y[i][j][e] * (1.0f / kOrthoB));
+                for (int e = 0; e < 4; ++e) x[i][j][e] = fmaf(d, x[i][j][e], y[i][j][e] * (1.0f / (kOrthoB * kLowScale)));
         }
         __syncthreads();                                        // every wave has read xh
     };
@@ -246,7 +269,7 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(OrthoArgs a,
     if constexpr (!LONG) {
         start_x();
         for (int step = 0; step < c.steps; ++step) {
-            put_x();
+            put_x(high);
             __syncthreads();
             square(xh, XP, Q / 32);
             rest_of_step(c.v[3 * step], c.v[3 * step + 1], c.v[3 * step + 2]);
@@ -260,7 +283,7 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(OrthoArgs a,
         };
         if (part_of.first) {
             start_x();
-            if (!part_of.last) put_x();
+            if (!part_of.last) put_x(high);
         } else {
 #pragma unroll
             for (int i = 0; i < RB; ++i)
@@ -286,9 +309,9 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(OrthoArgs a,
                         for (int b = 0; b < GR * GC; ++b) acc[b / GC][b % GC] += v[u][b];
                     }
             }
-            put_x();
+            put_x(high);
             rest_of_step(part_of.ca, part_of.cb, part_of.cc);
-            if (!part_of.last) put_x();
+            if (!part_of.last) put_x(high);
         }
         if (!part_of.last) {
             __syncthreads();

@@ -116,9 +116,17 @@ int gemm_relu_add_norm_backward(const void* dy, int64_t dy_stride, const void* d
  * (with A = X^T X on the right where rows > cols: the same matrix).  The singular vectors
  * stay, the singular values tend to 1.  coefficients: host memory, steps times a, b, c,
  * read before the call returns; steps <= 64.  dtype (g): F16, BF16 or F32.  out is dense
- * bfloat16 (batch x rows x cols).  The products' operands are rounded to float16, X itself
- * is kept in twice that: results are off by less than 1e-3 of their norm before they are
- * rounded.  Values of X and of b A + c A^2 past 2^8 in magnitude, and of A past 2^6, are
+ * bfloat16 (batch x rows x cols).  X is kept in two float16 (22 bits; fp32 where a call of a
+ * short side is one launch, or one a step), and b A + c A^2 multiplies both; A is made of
+ * the larger, and A's and b A + c A^2's values off their diagonals are rounded to float16 as
+ * operands.  What a result is off before it is rounded, as a share of its norm and whatever
+ * the singular values: with (3.4445, -4.7750, 2.0315) 3e-3 for up to 6 steps where the shorter
+ * side is at least 16 (5e-4 is usual) and 1e-2 for up to 5 below that; with (1.5, -0.5, 0) and
+ * (1.875, -1.25, 0.375), which converge, 1.5e-3 for up to 12 steps.  The former do not
+ * converge: their singular values keep moving, by factors of up to 1.6 further apart a step,
+ * which takes 3e-3 to 1.2e-2 after 10 steps.  Coefficients of larger slopes grow their
+ * roundings accordingly.  A singular value below 2^-22 of the norm is lost in X, as one below
+ * 2^-24 is in fp32, and many steps of a large a bring what is there instead up to 1.  Values of X and of b A + c A^2 past 2^8 in magnitude, and of A past 2^6, are
  * past float16's range here and give infinities and NaN; coefficients that keep the
  * singular values below 2 stay far from that.  A matrix of zeros gives zeros (with eps == 0 NaN, 0 / 0); a
  * NaN in g, or with at least one step an infinity, gives NaN all over its matrix.  The shorter side <= 2^16, the longer <= 2^22, rows x cols <=
