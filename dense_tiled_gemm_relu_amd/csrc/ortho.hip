@@ -106,7 +106,8 @@ template <class T> __global__ void __launch_bounds__(kThreads) ortho_start_kerne
     for (int k = 0; k < kOrthoParts; k += 64) s += k + lane < a.parts ? a.squares[batch * kOrthoParts + k + lane] : 0.0;
 #pragma unroll
     for (int step = 1; step < 64; step *= 2) s += __shfl_xor(s, step);
-    // the scale as an fp32 number times a power of two: it may be past fp32's range
+    // the scale as an fp32 number times a power of two: it may be past fp32's range, and
+    // values below the normal range take the power first, while they are exact
     int power;
     const float factor = (float)frexp((double)kOrthoX / (sqrt(s) + (double)a.eps), &power);
     _Float16* xh = static_cast<_Float16*>(a.xh) + batch * 2 * (size_t)a.P * (size_t)a.Q;
@@ -128,7 +129,7 @@ template <class T> __global__ void __launch_bounds__(kThreads) ortho_start_kerne
         float v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            v[e] = r0 + r < a.rows && c + e < a.cols ? ldexpf((float)raw[k][e] * factor, power) : 0.0f;
+            v[e] = r0 + r < a.rows && c + e < a.cols ? ldexpf((float)raw[k][e], power) * factor : 0.0f;
         if (tall) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) tile[r][c4 + e] = v[e];

@@ -108,7 +108,7 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(OrthoArgs a,
 #pragma unroll
             for (int k = 1; k < kSmallWaves; ++k) s += part[k];
         }
-        // the scale as an fp32 number times a power of two: it may be past fp32's range
+        // the scale as an fp32 number times a power of two, as in ortho_start_kernel
         const double scale = (double)kOrthoX / (sqrt(s) + (double)a.eps);
         int power;
         const float factor = (float)frexp(scale, &power);
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kSmallThreads) ortho_small_kernel(OrthoArgs a,
             for (int j = 0; j < CB; ++j) {
                 x[i][j] = *reinterpret_cast<const f32x4_t*>(raw + (16 * i + r16) * RP + column(j));
 #pragma unroll
-                for (int e = 0; e < 4; ++e) x[i][j][e] = ldexpf(x[i][j][e] * factor, power);
+                for (int e = 0; e < 4; ++e) x[i][j][e] = ldexpf(x[i][j][e], power) * factor;
             }
         __syncthreads();                                        // read, so xh may take its place
     };

@@ -136,3 +136,18 @@ def test_far_apart_singular_values_in_a_batch(m, n):
     for one, result in zip(g, got):
         want = exact(one, QUINTIC, 5)
         assert excess(result, want) <= documented(min(m, n), QUINTIC, 5) * want.norm()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("steps", [0, 5])
+@pytest.mark.parametrize("dtype,least", [(F16, 2.0 ** -24), (BF16, 2.0 ** -133), (F32, 2.0 ** -149)])
+@pytest.mark.parametrize("m,n", [(5, 7), (60, 100), (100, 60), (100, 250), (64, 1024), (700, 100), (200, 300), (300, 200)])
+def test_values_below_the_normal_range(m, n, dtype, least, steps):
+    # a power of two times whole numbers, all of them multiples of the type's smallest value:
+    # with eps 0 X is the same as without the factor, to the bit
+    gen = torch.Generator().manual_seed(m + n)
+    whole = torch.randint(-9, 10, (m, n), generator=gen).float()
+    tiny = (whole.to(F64) * least).to(dtype)
+    assert torch.equal(tiny.to(F64), whole.to(F64) * least)
+    got = gr.orthogonalize(tiny.cuda(), steps, eps=0.0)
+    assert torch.equal(got, gr.orthogonalize(whole.to(dtype).cuda(), steps, eps=0.0)) and got.any()
