@@ -346,12 +346,13 @@ Symmetric symmetric_config(const Linear& l, int64_t batch)
 // A = X X^T has the longest K and, of a short X, few tiles: its K is cut into parts where
 // the estimate says so (3001 x 1000, 136 tiles of 47 steps: 16 us in one part, 14 in three).  Two
 // workgroups that share a CU slow each other down from 0.55 of their time together.
+constexpr int kGramParts = 8;
 void split_gram(OrthoPlan& o, const Linear& l, int64_t batch)
 {
     const int64_t steps = ceil_div(l.K, kSplitStep), tiles = triangle(side_of(LIN_64, l)) * batch;
     const TileTime t = tile_time(LIN_64);
     double best = symmetric_time(o.gram, l, batch);
-    for (int64_t parts = 2; parts <= 8; ++parts) {
+    for (int64_t parts = 2; parts <= kGramParts; ++parts) {
         if (tiles > kNumCUs || tiles * parts > 2 * kNumCUs || steps < 4 * parts) break;
         const double share = t.alone + (1.0 - t.alone) * double(std::max<int64_t>(0, tiles * parts - kNumCUs)) / kNumCUs;
         const double time = share * (t.per_byte * double(l.K) * l.bytes / double(parts) + t.fixed) + 3000.0;
@@ -426,20 +427,21 @@ extern "C" const char* gemm_relu_orthogonalize_plan(int64_t batch, int64_t rows,
     if (ortho_is_small(std::min(rows, cols), std::max(rows, cols))) return "small";
     if (ortho_is_long(batch, std::min(rows, cols), std::max(rows, cols))) return "long";
     // every plan's name, kept for good: three products, of which two may name the tiles on
-    // their diagonal
-    constexpr int CFGS = LIN_64 + 1, DIAGONALS = 3;
+    // their diagonal, and the first the parts of its K instead (2 to kGramParts)
+    constexpr int CFGS = LIN_64 + 1, DIAGONALS = 3, PLAIN = CFGS * DIAGONALS;
     struct Names {
-        char text[CFGS * DIAGONALS][CFGS * DIAGONALS][CFGS][160];
+        char text[PLAIN + kGramParts - 1][PLAIN][CFGS][160];
         static int put(char* to, size_t room, int k)
         {
+            if (k >= PLAIN) return std::snprintf(to, room, "%s*%d,", linear_info(LIN_64).name, k - PLAIN + 2);
             static constexpr int diagonals[DIAGONALS] = {-1, LIN_128, LIN_64};
             const int d = diagonals[k % DIAGONALS];
             return std::snprintf(to, room, d < 0 ? "%s," : "%s/%s,", linear_info(k / DIAGONALS).name, d < 0 ? "" : linear_info(d).name);
         }
         Names()
         {
-            for (int a = 0; a < CFGS * DIAGONALS; ++a)
-                for (int b = 0; b < CFGS * DIAGONALS; ++b)
+            for (int a = 0; a < PLAIN + kGramParts - 1; ++a)
+                for (int b = 0; b < PLAIN; ++b)
                     for (int c = 0; c < CFGS; ++c) {
                         char* to = text[a][b][c];
                         size_t at = size_t(put(to, sizeof text[a][b][c], a));
@@ -451,7 +453,7 @@ extern "C" const char* gemm_relu_orthogonalize_plan(int64_t batch, int64_t rows,
     static const Names names;
     const OrthoPlan o = plan_ortho(batch, rows, cols);
     const auto index = [](const Symmetric& s) { return s.cfg * DIAGONALS + (s.diagonal < 0 ? 0 : s.diagonal == LIN_128 ? 1 : 2); };
-    return names.text[index(o.gram)][index(o.poly)][o.step];
+    return names.text[o.parts > 1 ? PLAIN + int(o.parts) - 2 : index(o.gram)][index(o.poly)][o.step];
 }
 
 extern "C" int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t g_batch_stride, void* out, int64_t batch,

@@ -139,7 +139,7 @@ int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t batch_strid
                             uint64_t workspace_bytes, void* stream);
 
 /* Configuration names of a step's products, "A,B,X" ("t/d" where a symmetric one's tiles on
- * the diagonal take another configuration d; "small" where one launch does all steps, "long" where one does a step, "none",
+ * the diagonal take another configuration d, "t*n" where A's K is cut into n parts; "small" where one launch does all steps, "long" where one does a step, "none",
  * "unsupported" and NULL as for the others).  The text stays valid.  Host-only. */
 const char* gemm_relu_orthogonalize_plan(int64_t batch, int64_t rows, int64_t cols);
 

@@ -11,12 +11,22 @@ def act_plan(rows, n, k):
     return gr.library().gemm_relu_act_plan(rows, n, k, gr.BF16).decode()
 
 
+def ortho_plan(batch, m, n):
+    return gr.library().gemm_relu_orthogonalize_plan(batch, m, n).decode()
+
+
 # odd rows, columns and K: the residual's, the bias's and K's ends inside a tile
 TILE_48X32 = [(37, 6837, 789), (226, 1628, 127), (134, 2649, 3846)]
+# batch, rows, columns, parts of A's K
+CUT = [(1, 300, 900, 3), (1, 1001, 300, 4), (3, 256, 1024, 4), (1, 320, 1600, 5), (1, 512, 2048, 7), (1, 129, 5000, 8),
+       (1, 16385, 64, 8), (1, 1000, 3001, 3)]
 
 
 def test_the_sizes_take_these_paths():
     assert all(act_plan(*size) == "k48x32x64_s3" for size in TILE_48X32)
+    assert all("*" not in ortho_plan(*size) for size in ((1, 129, 300), (1, 2100, 2100), (8, 1024, 2048)))
+    for batch, m, n, parts in CUT:
+        assert ortho_plan(batch, m, n).startswith("d64x64x64_s4*%d," % parts), (m, n, ortho_plan(batch, m, n))
 
 
 @pytest.mark.gpu
@@ -51,3 +61,53 @@ def test_48x32_tiles_on_integers(rows, n, k, dtype):
     for act, v in (("none", z), ("relu", z.clamp(min=0))):
         y = gr.matmul_act(x.to(dtype), w.to(dtype), b.to(dtype), act, r.to(dtype))
         assert torch.equal(y.to(F64), v + r)
+
+
+def scattered(m, n, k, seed):
+    """4^k entries of +-1, the others 0, so that the norm is 2^k."""
+    gen = torch.Generator().manual_seed(seed)
+    g = torch.zeros(m * n)
+    g[torch.randperm(m * n, generator=gen)[:4 ** k]] = (2 * torch.randint(0, 2, (4 ** k,), generator=gen) - 1).float()
+    return g.view(m, n).cuda()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch,m,n,parts", CUT)
+def test_products_cut_along_k(batch, m, n, parts):
+    # A and A^2 are whole numbers of at most 9 bits times a power of two, and B is a multiple
+    # of one of them: exactly one right result
+    k = 5 if min(m, n) > 64 else 4
+    g = torch.stack([scattered(m, n, k, 3 * i) for i in range(batch)])
+    g = g if batch > 1 else g[0]
+    for a, b, c in ((1.5, -0.5, 0.0), (1.0, 0.0, 4.0 ** k)):
+        got = gr.orthogonalize(g, 1, (a, b, c), 0.0)
+        for x, y in zip(g.view(batch, m, n).to(F64) / 2 ** k, got.view(batch, m, n).to(F64)):
+            x, y = (x.t(), y.t()) if m > n else (x, y)
+            gram = x @ x.t()
+            assert ((gram * 4 ** k) @ (gram * 4 ** k)).abs().max() < 2 ** 9
+            assert torch.equal(y, (a * x + (b * gram + c * gram @ gram) @ x).to(BF16).to(F64))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("batch,m,n,parts", CUT)
+def test_products_cut_along_k_in_a_graph_and_on_two_streams(batch, m, n, parts):
+    # the arrival counters stand in each call's own workspace and are left cleared
+    shape = (batch, m, n) if batch > 1 else (m, n)
+    g, other = rnd(1, *shape).to(BF16), rnd(2, *shape).to(BF16)
+    want, want2 = gr.orthogonalize(g), gr.orthogonalize(other)
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        a, b = gr.orthogonalize(g, stream=streams[0]), gr.orthogonalize(other, stream=streams[1])
+        torch.cuda.synchronize()
+        assert torch.equal(a, want) and torch.equal(b, want2)
+    graph, kept = torch.cuda.CUDAGraph(), g.clone()
+    with torch.cuda.graph(graph, stream=streams[0]):
+        out = gr.orthogonalize(g)
+    for k in range(4):
+        g.copy_(other if k % 2 else kept)
+        out.zero_()
+        gr.orthogonalize(other)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want2 if k % 2 else want), k
