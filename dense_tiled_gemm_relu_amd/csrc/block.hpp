@@ -68,7 +68,7 @@ struct AddNormArgs {
 };
 hipError_t launch_add_norm(const AddNormArgs& a, int dt, int wdt, hipStream_t stream);
 // strips of rows the backward pass sums on their own before launch_join
-int add_norm_strips(int64_t rows, int64_t cols, int bytes);
+int add_norm_strips(int64_t rows);
 hipError_t launch_add_norm_backward(const AddNormArgs& a, int dt, int wdt, hipStream_t stream);
 
 // ---- orthogonalisation (ortho.hip)

@@ -207,15 +207,14 @@ extern "C" int gemm_relu_add_norm(const void* x, int64_t x_stride, const void* r
 }
 
 // the strips' sums, then two sums a row
-static uint64_t add_norm_sums(int64_t rows, int64_t cols, int bytes)
+static uint64_t add_norm_sums(int64_t rows, int64_t cols)
 {
-    return uint64_t(round_up(int64_t(add_norm_strips(rows, cols, bytes)) * kNormSums * cols * 4, 256));
+    return uint64_t(round_up(int64_t(add_norm_strips(rows)) * kNormSums * cols * 4, 256));
 }
 extern "C" int64_t gemm_relu_add_norm_backward_workspace(int64_t rows, int64_t cols)
 {
     if (!size_ok(rows) || !size_ok(cols)) return GEMM_RELU_EINVAL;
-    // of the type that leaves more strips
-    return int64_t(std::max(add_norm_sums(rows, cols, 2), add_norm_sums(rows, cols, 4))) + rows * 2 * 4;
+    return int64_t(add_norm_sums(rows, cols)) + rows * 2 * 4;
 }
 
 extern "C" int gemm_relu_add_norm_backward(const void* dy, int64_t dy_stride, const void* ds, int64_t ds_stride, const void* x,
@@ -256,7 +255,7 @@ extern "C" int gemm_relu_add_norm_backward(const void* dy, int64_t dy_stride, co
     a.dgate = dgate;
     a.db = dbias;
     a.partial = static_cast<float*>(workspace);
-    a.row_sums = reinterpret_cast<float*>(static_cast<char*>(workspace) + add_norm_sums(rows, cols, e));
+    a.row_sums = reinterpret_cast<float*>(static_cast<char*>(workspace) + add_norm_sums(rows, cols));
     a.x_stride = x_stride;
     a.r_stride = residual_stride;
     a.gate_stride = gate ? gate_stride : 0;
@@ -279,7 +278,7 @@ extern "C" int gemm_relu_add_norm_backward(const void* dy, int64_t dy_stride, co
         j.results = kMaxResults;
         j.sums = kNormSums;
         j.cols = int(cols);
-        j.strips = add_norm_strips(rows, cols, e);
+        j.strips = add_norm_strips(rows);
         err = launch_join(j, wdtype, st);
     }
     return finish(err, st);

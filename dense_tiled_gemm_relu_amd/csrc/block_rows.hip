@@ -761,8 +761,10 @@ hipError_t launch_add_norm(const AddNormArgs& a, int dt, int wdt, hipStream_t st
     });
 }
 
-// Workgroups of the backward pass, each of which leaves one strip of sums: one a CU.
-int add_norm_strips(int64_t rows, int64_t cols, int bytes)
+// Workgroups of the backward pass, each of which leaves one strip of sums: one a CU, whatever
+// the rows' length.  (Of short rows a workgroup takes up to 16 at a time, so that of a few
+// hundred rows some have none and leave zeros.)
+int add_norm_strips(int64_t rows)
 {
     return rows == 0 ? 0 : even_grid(rows, 1, 256);
 }
@@ -770,7 +772,7 @@ int add_norm_strips(int64_t rows, int64_t cols, int bytes)
 hipError_t launch_add_norm_backward(const AddNormArgs& a, int dt, int wdt, hipStream_t stream)
 {
     if (a.rows == 0) return hipSuccess;
-    const int strips = add_norm_strips(a.rows, a.cols, elem_size(dt));
+    const int strips = add_norm_strips(a.rows);
     return with_types(dt, wdt, [&](auto x, auto w) {
         using T = decltype(x);
         using W = decltype(w);
