@@ -158,8 +158,9 @@ typedef float Stats __attribute__((ext_vector_type(4), aligned(4)));       // a 
 // stays in registers, gate, post_weight and scale as one product.  One wave a row and four
 // rows a workgroup, or `waves` waves a row: one chunk a thread (two where 16 waves would
 // not hold the row).  Bound by HBM where there is one norm (16384 x 8192 bf16 194 us, 5.5
-// TB/s); with norms on both sides the vector unit works as long (4097 x 3001 fp16 27 us, 3.6
-// TB/s).
+// TB/s); with layer norms on both sides the waves wait half of their time, a row's four
+// barriers among it, and the vector unit is busy for the other half (40 instructions an
+// element; 4097 x 3001 fp16 27 us, 3.6 TB/s).
 template <class T, class W, bool ONE, int V>
 __global__ void __launch_bounds__(ONE ? kThreads : 1024) add_norm_kernel(AddNormArgs a, int waves)
 {
@@ -318,9 +319,11 @@ __global__ void __launch_bounds__(ONE ? kThreads : 1024) add_norm_kernel(AddNorm
 // rate.  16-bit rows of more than 1024 chunks have more than LDS holds: their sums over
 // rows are left to add_norm_strip_any_kernel.  A chunk
 // moved back inside the row has its weights cleared where its neighbour owns the element:
-// the row's sums then need no test, and only what it owns is stored.  Bound by HBM, with
-// the vector unit close behind: 16384 x 4096 bf16, eight streams, 200 us (5.4 TB/s; 440
-// with the sums in registers, which spill); 4097 x 3001 fp16 37 us, 4.0 TB/s.
+// the row's sums then need no test, and only what it owns is stored.  Bound by HBM:
+// 16384 x 4096 bf16, eight streams, 200 us (5.4 TB/s; 440 with the sums in registers, which
+// spill); with layer norms on both sides by its waits, more than half of the waves' time, the
+// vector unit busy for 38 % (45 instructions an element; 4097 x 3001 fp16 37 us, 4.0 TB/s: six
+// waves a row, so 12 of the 16 that fit).
 template <class T, class W, int V>
 __global__ void __launch_bounds__(1024) add_norm_backward_kernel(AddNormArgs a, int waves)
 {
@@ -557,7 +560,11 @@ __global__ void __launch_bounds__(1024) add_norm_backward_kernel(AddNormArgs a, 
     }
 }
 
-// ---- rows of any length: one workgroup a row, read once per use
+// ---- rows of any length: one workgroup a row, read once per use.  Forward, x and the residual
+// are read three times for a root mean square norm of s, four for a layer norm, and x
+// once or twice more for a norm of its own: 1024 x 65536 bf16, rms, 463 us forward and 862 backward
+// (its bytes' share 101 and 127), with post norm and gate 676 and 2142; 2048 x 32768 fp32 552
+// and 873, 822 and 2043.
 template <class T, class W> struct AnyRow {
     const AddNormArgs& a;
     const T *x, *r;

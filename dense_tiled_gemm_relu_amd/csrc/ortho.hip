@@ -176,8 +176,8 @@ __global__ void __launch_bounds__(kThreads) ortho_copy_kernel(OrthoArgs a)
 // ------------------------------------------------------------ the products
 // B X is one product over 2 P values of K: [B / kLowScale, B] [xl; xh], the lesser terms first
 // (xl holds kLowScale times what xh loses, B / kLowScale loses nothing that counts beside B
-// xh).  What a step of 8192 x 8192 takes: A 476 us and A^2 511 (half of their products; 1150
-// and 1075 TFLOP/s for those), B X 1664 (1320 TFLOP/s; 895 without xl), whose epilogue
+// xh).  What a step of 8192 x 8192 takes: A 475 us and A^2 509 (half of their products; 1160
+// and 1080 TFLOP/s for those), B X 1652 (1330 TFLOP/s; 895 without xl), whose epilogue
 // reads and writes 8 bytes an element while the matrix units wait: one tile fills a CU.  8 x
 // 1024 x 2048: 43, 35 and 88 us (63 without xl), of which 25 are such an epilogue (one round
 // of tiles); with X in fp32 it was the same.

@@ -48,8 +48,10 @@ const char* gemm_relu_act_plan(int64_t rows, int64_t n, int64_t k, int dtype);
  * bias_dtype) may be NULL.  dz is rounded to dtype before the products (the sum over
  * rows takes it as it is); with F16 and an activation but max(z, 0), whose slopes pass
  * 1, half of it is, so that no finite dy gives an infinite dz: below 2^-13 it is then
- * a multiple of 2^-23.  max(z, 0) has slope 0 at 0.  rows and n <= 2^30, else
- * GEMM_RELU_EUNSUPPORTED (from the workspace function too).
+ * a multiple of 2^-23.  max(z, 0) has slope 0 at 0.  The lower tail of gelu's distribution
+ * function, here and in gemm_relu_act, is within 6e-6 of itself for |z| < 8.  rows and n <=
+ * 2^30, else GEMM_RELU_EUNSUPPORTED (from the workspace function too), and so are
+ * matrices dz of 2^23 or more tiles of 64 x 64 (from the call).
  */
 int64_t gemm_relu_act_backward_workspace(int64_t rows, int64_t n, int64_t k);
 int gemm_relu_act_backward(const void* dy, int64_t dy_stride, const float* z, const void* x,
@@ -68,7 +70,9 @@ const char* gemm_relu_act_backward_plan(int64_t rows, int64_t n, int64_t k, int 
 /*
  * From one block to the next: the block's output x, normed first if post_weight is
  * given, gated and scaled, is added to the residual stream, whose sum the next block's
- * norm takes (rows past fp32's range: as gemm_relu_layer_norm).  For each row of x and residual (rows x cols),
+ * norm takes (rows past fp32's range: as gemm_relu_layer_norm; with eps 0, squares of values
+ * under 2^-63 lose digits, and a row of values under 2^-75 has an infinite 1 / deviation).  For
+ * each row of x and residual (rows x cols),
  *   t = norm(x) post_weight, or x without one,
  *   s = residual + scale gate t,
  *   y = norm(s) weight + bias.
