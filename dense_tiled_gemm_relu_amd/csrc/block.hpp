@@ -77,7 +77,8 @@ hipError_t launch_add_norm_backward(const AddNormArgs& a, int dt, int wdt, hipSt
 // diagonal times 2^10 and B = b A + c A^2 without its diagonal times 2^8; the scales keep
 // what is far below a matrix's norm inside float16's normal range (its smallest value of
 // full precision, 2^-14, is 2^-22 of X's and B's norm and 2^-24 of A's), and leave room
-// for norms of 2^8, 2^6 and 2^8.
+// for norms of 2^8, 2^6 and 2^8.  (What multiplies X's low half is B over kLowScale, a multiple of
+// 2^-21 of B's norm at the least: 2^-33 beside the rest.)
 constexpr float kOrthoX = 256.0f, kOrthoA = 1024.0f, kOrthoB = 256.0f;
 struct OrthoArgs {
     const void* g;              // batch x rows x cols

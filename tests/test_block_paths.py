@@ -111,3 +111,32 @@ def test_products_cut_along_k_in_a_graph_and_on_two_streams(batch, m, n, parts):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want2 if k % 2 else want), k
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("m,n", [(20001, 60001), (60001, 20001)])
+def test_matrices_past_32_bits(m, n):
+    # X's two halves are one operand of 2.4e9 values, 4.8 GB.  g is zero but for some rows and
+    # columns, the first and the last among them: exact there as above, and zero elsewhere
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("needs 40 GB")
+    gen = torch.Generator().manual_seed(5)
+    rows = torch.cat([torch.tensor([0, m - 1]), 1 + torch.randperm(m - 2, generator=gen)[:62]]).sort().values.cuda()
+    cols = torch.cat([torch.tensor([0, n - 1]), 1 + torch.randperm(n - 2, generator=gen)[:298]]).sort().values.cuda()
+    part = scattered(64, 300, 4, 11)
+    part[0, 0] = part[0, 299] = part[63, 0] = part[63, 299] = 0
+    at = part.view(-1).nonzero()[:4, 0]                      # four entries move to the corners
+    part.view(-1)[at] = 0
+    part[0, 0] = part[0, 299] = part[63, 0] = part[63, 299] = 1
+    assert part.norm() == 16
+    g = torch.zeros(m, n, dtype=BF16, device="cuda")
+    g[rows[:, None], cols[None, :]] = part.to(BF16)
+    x = part.to(F64) / 16
+    gram = x @ x.t()
+    assert ((256 * gram) @ (256 * gram)).abs().max() < 2 ** 9
+    for a, b, c in ((1.5, -0.5, 0.0), (1.0, 0.0, 256.0)):
+        got = gr.orthogonalize(g, 1, (a, b, c), 0.0)
+        inside = got[rows[:, None], cols[None, :]]
+        want = (a * x + (b * gram + c * gram @ gram) @ x).to(BF16)
+        assert torch.equal(inside, want)
+        assert int(got.count_nonzero()) == int(want.count_nonzero())
