@@ -373,7 +373,7 @@ OrthoPlan plan_ortho(int64_t batch, int64_t rows, int64_t cols)
     if (ortho_is_long(batch, o.p, o.q)) {
         const uint64_t parts = uint64_t(ortho_parts(o.q)) * uint64_t(batch), P = uint64_t(o.P);
         o.x[0] = uint64_t(batch) * kOrthoParts * 8;                     // X of the parts' lanes
-        o.a = o.x[0] + parts * P * kOrthoPart * 4;                        // two steps' sums
+        o.a = o.x[0] + parts * P * kOrthoPart * 4;                      // two steps' sums
         o.bytes = o.a + 2 * parts * P * P * 4;
         return o;
     }

@@ -130,11 +130,13 @@ int gemm_relu_add_norm_backward(const void* dy, int64_t dy_stride, const void* d
  * converge: their singular values keep moving, by factors of up to 1.6 further apart a step,
  * which takes 3e-3 to 1.2e-2 after 10 steps.  Coefficients of larger slopes grow their
  * roundings accordingly.  A singular value below 2^-22 of the norm is lost in X, as one below
- * 2^-24 is in fp32, and many steps of a large a bring what is there instead up to 1.  Values of X and of b A + c A^2 past 2^8 in magnitude, and of A past 2^6, are
- * past float16's range here and give infinities and NaN; coefficients that keep the
- * singular values below 2 stay far from that.  A matrix of zeros gives zeros (with eps == 0 NaN, 0 / 0); a
- * NaN in g, or with at least one step an infinity, gives NaN all over its matrix.  The shorter side <= 2^16, the longer <= 2^22, rows x cols <=
- * 2^34, batch <= 65535, else GEMM_RELU_EUNSUPPORTED.
+ * 2^-24 is in fp32, and many steps of a large a bring what is there instead up to 1.
+ * Values of X and of b A + c A^2 past 2^8 in magnitude, and of A past 2^6, are past
+ * float16's range here and give infinities and NaN; coefficients that keep the singular
+ * values below 2 stay far from that.  A matrix of zeros gives zeros (with eps == 0 NaN, 0 /
+ * 0); a NaN in g, or with at least one step an infinity, gives NaN all over its matrix.  The
+ * shorter side <= 2^16, the longer <= 2^22, rows x cols <= 2^34, batch <= 65535, else
+ * GEMM_RELU_EUNSUPPORTED.
  */
 int64_t gemm_relu_orthogonalize_workspace(int64_t batch, int64_t rows, int64_t cols);
 int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t batch_stride, void* out,
@@ -143,8 +145,9 @@ int gemm_relu_orthogonalize(const void* g, int64_t g_stride, int64_t batch_strid
                             uint64_t workspace_bytes, void* stream);
 
 /* Configuration names of a step's products, "A,B,X" ("t/d" where a symmetric one's tiles on
- * the diagonal take another configuration d, "t*n" where A's K is cut into n parts; "small" where one launch does all steps, "long" where one does a step, "none",
- * "unsupported" and NULL as for the others).  The text stays valid.  Host-only. */
+ * the diagonal take another configuration d, "t*n" where A's K is cut into n parts; "small"
+ * where one launch does all steps, "long" where one does a step, "none", "unsupported" and
+ * NULL as for the others).  The text stays valid.  Host-only. */
 const char* gemm_relu_orthogonalize_plan(int64_t batch, int64_t rows, int64_t cols);
 
 #ifdef __cplusplus

@@ -36,7 +36,7 @@ def schedules(p):
         yield QUINTIC, 6
         yield QUINTIC, 10
     yield CUBIC, 12
-    yield CONVERGING, 8
+    yield CONVERGING, 12
 
 
 def matrices(m, n, seed, device):
